@@ -369,6 +369,176 @@ NVFP4KV_API int nvfp4_extend_attention_paged(const nvfp4kv_cache *cache, const v
                                              int num_reqs, int max_q_len, int num_q_heads, float sm_scale, void *out,
                                              cudaStream_t stream);
 
+/*
+ * ------------------------------------------------------------------ latent cache
+ *
+ * Latent attention keeps ONE vector a token for all heads: a latent of 512
+ * values, from which every head's K (without its rotary part) and V are linear
+ * maps, and a rotary part of 64 values that all heads share.  A latent cache
+ * page holds P tokens, one slab per page (there are no kv heads):
+ *   pool = uint8[num_pages][416 * P], P/16 groups of 16 consecutive rows; a
+ *   group (6656 bytes) holds, for its rows r = 0..15:
+ *     codes   uint8[8][16][32]  byte i of [cb][r] = latent elements 64 cb + 2i
+ *                               (low nibble) and 64 cb + 2i + 1 (high nibble)
+ *     scales  uint8[16][32]     E4M3 scale of block b (elements 16b..16b+15) of
+ *                               row r at [r][(b/2 % 2) * 16 + b/4 * 2 + b % 2]
+ *     rotary  BF16[16][64]      16-byte chunk c (elements 8c..8c+7) of row r at
+ *                               chunk position c ^ (r % 8)
+ * 416 bytes a token: NVFP4 latents (a tensor scale g multiplies them) and the
+ * rotary part as it came.  Latent element = e2m1 * e4m3 * g.
+ */
+typedef struct {
+    void *pool;             /* device, uint8[num_pages][416 * page_size], 256-byte aligned */
+    int64_t num_pages;      /* >= 1 */
+    int32_t page_size;      /* P: 16, 32, 64 or 128 tokens */
+    int32_t latent_dim;     /* must be 512 */
+    int32_t rope_dim;       /* must be 64 */
+    float global_scale;     /* FP32 tensor scale g of the latents, a positive normal FP32 number */
+} nvfp4kv_latent_cache;
+
+/* Bytes of one page of a latent cache (416 * P); 0 if the descriptor is invalid. */
+NVFP4KV_API size_t nvfp4kv_latent_slab_bytes(const nvfp4kv_latent_cache *cache);
+
+/*
+ * Quantise BF16 latents into the latent cache and store the rotary parts.
+ *   latent         device BF16 [num_tokens][latent_stride], 512 values a token
+ *   rope           device BF16 [num_tokens][rope_stride], 64 values a token
+ *                  (both may be views of one wider row; 16-byte aligned,
+ *                  strides in elements, multiples of 8, >= 512 and >= 64)
+ *   slot_mapping   device int64 [num_tokens], as for nvfp4_kv_quantize_append
+ *                  (negative: skipped; >= num_pages * P: skipped and flagged).
+ * Scales and codes are the roundings nvfp4_kv_quantize_append makes (exact
+ * quotients, nearest even, saturating); the rotary values are stored as they
+ * are.  Two tokens writing one slot in one call is a caller error.
+ */
+NVFP4KV_API int nvfp4_latent_quantize_append(const nvfp4kv_latent_cache *cache, const void *latent,
+                                             int64_t latent_stride, const void *rope, int64_t rope_stride,
+                                             int64_t num_tokens, const int64_t *slot_mapping, cudaStream_t stream);
+
+/*
+ * Cached latents -> contiguous BF16 rows: the input of the up-projections whose
+ * outputs nvfp4_latent_extend_attention takes.
+ *   block_table, prefix_lens, cu_prefix_lens, total_prefix_tokens as for
+ *   nvfp4_prefix_dequant;
+ *   latent_ws      device BF16 [total_prefix_tokens][512]: the exact product
+ *                  e2m1 * e4m3 * g rounded once, nearest even
+ *   rope_ws        device BF16 [total_prefix_tokens][64]; both 16-byte aligned.
+ */
+NVFP4KV_API int nvfp4_latent_prefix_dequant(const nvfp4kv_latent_cache *cache, const int32_t *block_table,
+                                            int max_pages_per_seq, const int32_t *prefix_lens,
+                                            const int32_t *cu_prefix_lens, int num_reqs, int64_t total_prefix_tokens,
+                                            void *latent_ws, void *rope_ws, cudaStream_t stream);
+
+/* Workspace bytes nvfp4_latent_decode_attention needs for this shape and
+ * num_splits on the current device (0 if the arguments are invalid). */
+NVFP4KV_API size_t nvfp4kv_latent_decode_workspace_bytes(const nvfp4kv_latent_cache *cache, int batch, int num_heads,
+                                                         int num_splits);
+
+/*
+ * Latent decode attention, absorbed form: one query a sequence, the up-projection
+ * of K folded into the query and that of V left to the caller.
+ *   out[b][h] = sum_t softmax_t(sm_scale (q_latent[b][h] . c_t + q_rope[b][h] . r_t)) c_t
+ * over t < seq_lens[b], c_t the dequantised latent (512), r_t the rotary part (64).
+ *   q_latent      device BF16 [batch][num_heads][512], 16-byte aligned
+ *   q_rope        device BF16 [batch][num_heads][64], 16-byte aligned
+ *   block_table   device int32 [batch][max_pages_per_seq]
+ *   seq_lens      device int32 [batch] (clamped to the table and flagged; a
+ *                 page id outside the pool is flagged and read as zeros)
+ *   out           device BF16 [batch][num_heads][512], 16-byte aligned
+ *   workspace     device, >= nvfp4kv_latent_decode_workspace_bytes(...),
+ *                 256-byte aligned; calls that may overlap need one each
+ *   num_splits    CTAs a head tile's token range is cut into; 0 = auto.
+ * num_heads 1..128.  A sequence of length 0 yields zeros.
+ */
+NVFP4KV_API int nvfp4_latent_decode_attention(const nvfp4kv_latent_cache *cache, const void *q_latent,
+                                              const void *q_rope, int batch, int num_heads,
+                                              const int32_t *block_table, int max_pages_per_seq,
+                                              const int32_t *seq_lens, float sm_scale, void *out, void *workspace,
+                                              size_t workspace_bytes, int num_splits, cudaStream_t stream);
+
+/*
+ * Latent attention, expanded form, for a chunk: request r's new tokens attend to
+ * [its expanded prefix || the expanded chunk], causally in the chunk.  Head h's
+ * key is its 128 expanded values followed by the 64 rotary ones all heads share,
+ * its value is 128 expanded values:
+ *   out[t][h] = sum_j softmax_j(sm_scale (q[t][h][:128] . k_j[h] + q[t][h][128:] . r_j)) v_j[h].
+ *   q             device BF16 [total_q][num_heads][192]
+ *   k_prefix, v_prefix   device BF16, row of token j and head h at
+ *                 j * prefix_token_stride + h * prefix_head_stride (elements;
+ *                 k and v may be views of one up-projection output)
+ *   rope_prefix   device BF16 [total_prefix][64]
+ *   k_chunk, v_chunk     the same with the chunk_* strides, rows as q
+ *   rope_chunk    device BF16 [total_q][64]
+ *   cu_prefix_lens, cu_q_lens, total_*, max_q_len   as nvfp4_extend_attention
+ *   out           device BF16 [total_q][num_heads][128].
+ * Pointers 16-byte aligned, strides multiples of 8 elements, head strides >=
+ * 128.  BF16 products, FP32 sums on the tensor cores, probabilities in BF16.
+ * The prefix pointers may be NULL when total_prefix_tokens is 0.
+ */
+NVFP4KV_API int nvfp4_latent_extend_attention(const void *q, const void *k_prefix, const void *v_prefix,
+                                              int64_t prefix_token_stride, int64_t prefix_head_stride,
+                                              const void *rope_prefix, const int32_t *cu_prefix_lens,
+                                              int64_t total_prefix_tokens, const void *k_chunk, const void *v_chunk,
+                                              int64_t chunk_token_stride, int64_t chunk_head_stride,
+                                              const void *rope_chunk, const int32_t *cu_q_lens,
+                                              int64_t total_q_tokens, int num_reqs, int max_q_len, int num_heads,
+                                              float sm_scale, void *out, cudaStream_t stream);
+
+/*
+ * ------------------------------------------------------------------ cache eviction
+ */
+
+/* Workspace bytes nvfp4_accumulate_attention_weights needs for this shape on
+ * the current device (0 if the arguments are invalid). */
+NVFP4KV_API size_t nvfp4kv_weights_workspace_bytes(const nvfp4kv_cache *cache, int batch, int num_q_heads);
+
+/*
+ * Add the attention weights of one query per sequence to each cached token's
+ * score:
+ *   scores[b][h][t] += sum over the query heads j of kv head h of
+ *                      softmax_t(sm_scale * g_K * q[b][j] . k_t)[t],  t < seq_lens[b].
+ * Reads K only; other entries of scores are left as they are.
+ *   q, block_table, seq_lens, num_q_heads  as nvfp4_paged_decode_attention
+ *                 (a page id outside the pool is flagged and read as zeros)
+ *   scores        device float [batch][num_kv_heads][score_stride]; a sequence
+ *                 longer than score_stride is cut to it and flagged
+ *   workspace     device, >= nvfp4kv_weights_workspace_bytes(...), 256-byte
+ *                 aligned; calls that may overlap need one each.
+ * The weights are FP32; one addition per entry, so results do not depend on timing.
+ */
+NVFP4KV_API int nvfp4_accumulate_attention_weights(const nvfp4kv_cache *cache, const void *q, int batch,
+                                                   int num_q_heads, const int32_t *block_table,
+                                                   int max_pages_per_seq, const int32_t *seq_lens, float sm_scale,
+                                                   float *scores, int64_t score_stride, void *workspace,
+                                                   size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Evict all but `keep` tokens of every sequence and kv head into new pages.
+ * With n = seq_lens[b], new_lens[b] = min(n, keep) rows survive per kv head: all
+ * of them if n <= keep, else the first `sink`, the last `recent` and, of the
+ * others, those of largest score (ties to the lowest index; a NaN ranks below
+ * every number).  Heads may keep different tokens.  Their order is kept: row i
+ * of new_block_table's pages receives the old row kept[b][h][i], byte for byte.
+ *   scores        device float [batch][num_kv_heads][score_stride] (n is cut to
+ *                 score_stride and flagged)
+ *   keep          >= 1; sink, recent >= 0, sink + recent <= keep
+ *   block_table   device int32 [batch][max_pages_per_seq], read up to n
+ *   new_block_table  device int32 [batch][new_max_pages]: pages to write,
+ *                 each listed once and in no sequence's old table (the old
+ *                 pages are left as they are: they may be shared); rows that
+ *                 have no page are flagged and not written
+ *   new_lens      device int32 [batch], must not be seq_lens
+ *   kept          device int32 [batch][num_kv_heads][keep], -1 behind new_lens[b]
+ *   new_scores    device float [batch][num_kv_heads][new_score_stride], not
+ *                 scores: the kept scores, then zeros; new_score_stride >= keep.
+ * NVFP4 and FP8 pools.
+ */
+NVFP4KV_API int nvfp4_evict(const nvfp4kv_cache *cache, const float *scores, int64_t score_stride, int batch,
+                            const int32_t *block_table, int max_pages_per_seq, const int32_t *seq_lens,
+                            const int32_t *new_block_table, int new_max_pages, int keep, int recent, int sink,
+                            int32_t *new_lens, int32_t *kept, float *new_scores, int64_t new_score_stride,
+                            cudaStream_t stream);
+
 /* Synchronises `stream`, then reads and clears the current device's error
  * word.  Returns NVFP4KV_OK, NVFP4KV_EDEVICE_CHECK (some kernel skipped an
  * out-of-range index since the last check) or NVFP4KV_ECUDA. */

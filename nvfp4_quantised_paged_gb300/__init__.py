@@ -12,6 +12,14 @@ NVFP4 KV Cache" (section A2):
   quantize_append(cache, k, v, slot_mapping)             paths 1 and 2 (write)
   paged_decode_attention(cache, q, block_table, seq_lens) path 3 (decode)
   prefix_dequant(cache, block_table, prefix_lens, cu)     path 2 (extend)
+
+beside them a cache of latents (one shared vector a token) with its two
+attention forms, and the eviction of cached tokens by accumulated attention
+weight:
+
+  latent_quantize_append, latent_decode_attention (absorbed form),
+  latent_prefix_dequant, latent_extend_attention (expanded form)
+  accumulate_attention_weights, evict
 """
 
 from __future__ import annotations
@@ -29,6 +37,8 @@ LIB_PATH = os.path.join(HERE, "libnvfp4kv.so")
 DTYPE_NVFP4 = 0
 DTYPE_FP8_E4M3 = 1
 HEAD_DIM = 128
+LATENT_DIM = 512
+ROPE_DIM = 64
 
 STATUS = {0: "ok", -1: "invalid argument", -2: "unsupported configuration", -3: "CUDA error",
           -4: "a kernel skipped an out-of-range index"}
@@ -44,6 +54,11 @@ class _CacheDesc(ctypes.Structure):
     _fields_ = [("pool", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
                 ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("k_global_scale", ctypes.c_float), ("v_global_scale", ctypes.c_float)]
+
+
+class _LatentDesc(ctypes.Structure):
+    _fields_ = [("pool", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("latent_dim", ctypes.c_int32), ("rope_dim", ctypes.c_int32), ("global_scale", ctypes.c_float)]
 
 
 def _load_library():
@@ -74,6 +89,16 @@ def _load_library():
         "nvfp4_cascade_decode_attention": (i32, [D, P, i32, i32, P, i32, P, i32, P, f32, P, P, sz, i32, P]),
         "nvfp4kv_profile_decode": (i32, [P, P, i32, i32]),
         "nvfp4_paged_decode_attention_noalloc": (i32, [D, P, i32, i32, P, i32, P, f32, P, i32, P]),
+        "nvfp4kv_latent_slab_bytes": (sz, [P]),
+        "nvfp4_latent_quantize_append": (i32, [P, P, i64, P, i64, i64, P, P]),
+        "nvfp4_latent_prefix_dequant": (i32, [P, P, i32, P, P, i32, i64, P, P, P]),
+        "nvfp4kv_latent_decode_workspace_bytes": (sz, [P, i32, i32, i32]),
+        "nvfp4_latent_decode_attention": (i32, [P, P, P, i32, i32, P, i32, P, f32, P, P, sz, i32, P]),
+        "nvfp4_latent_extend_attention": (i32, [P, P, P, i64, i64, P, P, i64, P, P, i64, i64, P, P, i64, i32, i32, i32,
+                                                f32, P, P]),
+        "nvfp4kv_weights_workspace_bytes": (sz, [D, i32, i32]),
+        "nvfp4_accumulate_attention_weights": (i32, [D, P, i32, i32, P, i32, P, f32, P, i64, P, sz, P]),
+        "nvfp4_evict": (i32, [D, P, i64, i32, P, i32, P, P, i32, i32, i32, i32, P, P, P, i64, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -92,7 +117,10 @@ EXPORTED_SYMBOLS = ("nvfp4kv_version", "nvfp4kv_status_string", "nvfp4kv_slab_by
                     "nvfp4kv_selftest_bounded_wait", "nvfp4kv_calibrate_global_scales", "nvfp4_extend_attention",
                     "nvfp4_extend_attention_paged",
                     "nvfp4_paged_decode_attention_append", "nvfp4kv_cascade_workspace_bytes",
-                    "nvfp4_cascade_decode_attention")
+                    "nvfp4_cascade_decode_attention", "nvfp4kv_latent_slab_bytes", "nvfp4_latent_quantize_append",
+                    "nvfp4_latent_prefix_dequant", "nvfp4kv_latent_decode_workspace_bytes",
+                    "nvfp4_latent_decode_attention", "nvfp4_latent_extend_attention",
+                    "nvfp4kv_weights_workspace_bytes", "nvfp4_accumulate_attention_weights", "nvfp4_evict")
 
 NOALLOC_SCRATCH_BYTES = 64 << 20  # NVFP4KV_NOALLOC_SCRATCH_BYTES of the header
 
@@ -472,6 +500,333 @@ def extend_attention_paged(cache: PagedCache, q: torch.Tensor, block_table: torc
                                            _stream(stream))
     _check(rc, "nvfp4_extend_attention_paged")
     return out
+
+
+# ---------------------------------------------------------------- latent cache and eviction
+
+def _on_device(device: torch.device, *named):
+    """Every tensor lies on `device`, which is the current one (the library launches there)."""
+    for name, t in named:
+        if t.device != device:
+            raise ValueError("%s is on %s, the cache on %s" % (name, t.device, device))
+    if device.index != torch.cuda.current_device():
+        raise ValueError("the tensors are on %s, which is not the current device" % device)
+
+
+def _shape(t: torch.Tensor, name: str, shape):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+
+
+def _keep_until_done(stream: Optional[torch.cuda.Stream], *tensors):
+    """Tensors allocated here on the current stream, used on another one: their
+    memory is not given out again before that stream has passed this point."""
+    if stream is not None and stream != torch.cuda.current_stream():
+        stream.wait_stream(torch.cuda.current_stream())   # memory that earlier work here may still use
+        for t in tensors:
+            t.record_stream(stream)
+
+
+class LatentCache:
+    """A caller-owned pool of latent pages (uint8 [num_pages][416 * page_size]): 512
+    NVFP4 latent values and 64 BF16 rotary values a token."""
+
+    def __init__(self, num_pages: int, page_size: int, global_scale: float = 1.0, device="cuda",
+                 pool: Optional[torch.Tensor] = None):
+        self.num_pages, self.page_size, self.global_scale = int(num_pages), int(page_size), float(global_scale)
+        self.slab = latent_slab_bytes(self.page_size)
+        if pool is None:
+            pool = torch.zeros((self.num_pages, self.slab), dtype=torch.uint8, device=device)
+        _require(pool, "pool", torch.uint8)
+        if pool.numel() != self.num_pages * self.slab:
+            raise ValueError("pool has %d bytes, expected %d" % (pool.numel(), self.num_pages * self.slab))
+        self.pool = pool
+        self._desc = _LatentDesc(pool.data_ptr(), self.num_pages, self.page_size, LATENT_DIM, ROPE_DIM,
+                                 self.global_scale)
+
+    @property
+    def desc(self):
+        return ctypes.byref(self._desc)
+
+    @property
+    def num_slots(self) -> int:
+        return self.num_pages * self.page_size
+
+
+def latent_slab_bytes(page_size: int) -> int:
+    d = _LatentDesc(256, 1, int(page_size), LATENT_DIM, ROPE_DIM, 1.0)
+    n = _lib.nvfp4kv_latent_slab_bytes(ctypes.byref(d))
+    if n == 0:
+        raise NVFP4KVError(-2, "latent_slab_bytes(page_size=%d)" % page_size)
+    return int(n)
+
+
+def latent_quantize_append(cache: LatentCache, latent: torch.Tensor, k_rope: torch.Tensor, slot_mapping: torch.Tensor,
+                           stream: Optional[torch.cuda.Stream] = None):
+    """latent: BF16 [T][512], k_rope: BF16 [T][64] (rows may be strided: views of one
+    wider row); slot_mapping: int64 [T].  Quantises the latents, stores the rotary
+    parts as they are."""
+    _require(slot_mapping, "slot_mapping", torch.int64)
+    T = int(slot_mapping.shape[0])
+    for name, x, width in (("latent", latent, LATENT_DIM), ("k_rope", k_rope, ROPE_DIM)):
+        if not x.is_cuda or x.dtype != torch.bfloat16:
+            raise ValueError("%s must be a CUDA bfloat16 tensor" % name)
+        _shape(x, name, (T, width))
+        if T > 0 and x.stride(1) != 1:
+            raise ValueError("%s: each token must hold %d contiguous values" % (name, width))
+    _on_device(cache.pool.device, ("latent", latent), ("k_rope", k_rope), ("slot_mapping", slot_mapping))
+    # (a single row's stride says nothing: torch may give it any value)
+    sl = int(latent.stride(0)) if T > 1 else LATENT_DIM
+    sr = int(k_rope.stride(0)) if T > 1 else ROPE_DIM
+    rc = _lib.nvfp4_latent_quantize_append(cache.desc, _ptr(latent), sl, _ptr(k_rope), sr, T, _ptr(slot_mapping),
+                                           _stream(stream))
+    _check(rc, "nvfp4_latent_quantize_append")
+
+
+def latent_prefix_dequant(cache: LatentCache, block_table: torch.Tensor, prefix_lens: torch.Tensor,
+                          cu_prefix_lens: torch.Tensor, total_prefix_tokens: int,
+                          latent_ws: Optional[torch.Tensor] = None, rope_ws: Optional[torch.Tensor] = None,
+                          stream: Optional[torch.cuda.Stream] = None):
+    """Returns (latent_ws BF16 [total][512], rope_ws BF16 [total][64]): the cached
+    prefixes' rows, the input of the up-projections to per-head K and V."""
+    _require(block_table, "block_table", torch.int32)
+    _require(prefix_lens, "prefix_lens", torch.int32)
+    _require(cu_prefix_lens, "cu_prefix_lens", torch.int32)
+    R, total, dev = int(prefix_lens.shape[0]), int(total_prefix_tokens), cache.pool.device
+    _shape(cu_prefix_lens, "cu_prefix_lens", (R + 1,))
+    if block_table.dim() != 2 or block_table.shape[0] != R:
+        raise ValueError("block_table needs one row per request")
+    made = []
+    if latent_ws is None:
+        latent_ws = torch.empty((total, LATENT_DIM), dtype=torch.bfloat16, device=dev)
+        made.append(latent_ws)
+    if rope_ws is None:
+        rope_ws = torch.empty((total, ROPE_DIM), dtype=torch.bfloat16, device=dev)
+        made.append(rope_ws)
+    for name, x, width in (("latent_ws", latent_ws, LATENT_DIM), ("rope_ws", rope_ws, ROPE_DIM)):
+        _require(x, name, torch.bfloat16)
+        _shape(x, name, (total, width))
+    _on_device(dev, ("block_table", block_table), ("prefix_lens", prefix_lens), ("cu_prefix_lens", cu_prefix_lens),
+               ("latent_ws", latent_ws), ("rope_ws", rope_ws))
+    _keep_until_done(stream, *made)
+    rc = _lib.nvfp4_latent_prefix_dequant(cache.desc, _ptr(block_table), int(block_table.shape[1]), _ptr(prefix_lens),
+                                          _ptr(cu_prefix_lens), R, total, _ptr(latent_ws), _ptr(rope_ws),
+                                          _stream(stream))
+    _check(rc, "nvfp4_latent_prefix_dequant")
+    return latent_ws, rope_ws
+
+
+def latent_decode_workspace_bytes(cache: LatentCache, batch: int, num_heads: int, num_splits: int = 0) -> int:
+    n = _lib.nvfp4kv_latent_decode_workspace_bytes(cache.desc, int(batch), int(num_heads), int(num_splits))
+    if n == 0:
+        raise NVFP4KVError(-1, "latent_decode_workspace_bytes")
+    return int(n)
+
+
+def alloc_latent_decode_workspace(cache: LatentCache, batch: int, num_heads: int, num_splits: int = 0) -> torch.Tensor:
+    n = latent_decode_workspace_bytes(cache, batch, num_heads, num_splits)
+    return torch.empty(n, dtype=torch.uint8, device=cache.pool.device)
+
+
+def latent_decode_attention(cache: LatentCache, q_latent: torch.Tensor, q_rope: torch.Tensor,
+                            block_table: torch.Tensor, seq_lens: torch.Tensor, sm_scale: Optional[float] = None,
+                            out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                            num_splits: int = 0, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Absorbed form, one query a sequence.  q_latent: BF16 [B][H][512] (the queries
+    times the up-projection of K); q_rope: BF16 [B][H][64]; block_table int32
+    [B][max_pages]; seq_lens int32 [B] -> BF16 [B][H][512], each head's weighted
+    mean of the latents (its up-projection to V is left to the caller).  H <= 128;
+    sm_scale defaults to 1 / sqrt(128 + 64)."""
+    _require(q_latent, "q_latent", torch.bfloat16)
+    _require(q_rope, "q_rope", torch.bfloat16)
+    _require(block_table, "block_table", torch.int32)
+    _require(seq_lens, "seq_lens", torch.int32)
+    if q_latent.dim() != 3 or q_latent.shape[2] != LATENT_DIM:
+        raise ValueError("q_latent must be [batch][heads][512]")
+    B, H = int(q_latent.shape[0]), int(q_latent.shape[1])
+    _shape(q_rope, "q_rope", (B, H, ROPE_DIM))
+    _shape(seq_lens, "seq_lens", (B,))
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table needs one row per sequence")
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(HEAD_DIM + ROPE_DIM)
+    made = []
+    if out is None:
+        out = torch.empty_like(q_latent)
+        made.append(out)
+    else:
+        _require(out, "out", torch.bfloat16)
+        _shape(out, "out", q_latent.shape)
+    if workspace is None:
+        workspace = alloc_latent_decode_workspace(cache, B, H, num_splits)
+        made.append(workspace)
+    else:
+        _require(workspace, "workspace", torch.uint8)
+    _on_device(cache.pool.device, ("q_latent", q_latent), ("q_rope", q_rope), ("block_table", block_table),
+               ("seq_lens", seq_lens), ("out", out), ("workspace", workspace))
+    _keep_until_done(stream, *made)
+    rc = _lib.nvfp4_latent_decode_attention(cache.desc, _ptr(q_latent), _ptr(q_rope), B, H, _ptr(block_table),
+                                            int(block_table.shape[1]), _ptr(seq_lens), float(sm_scale), _ptr(out),
+                                            _ptr(workspace), workspace.numel(), int(num_splits), _stream(stream))
+    _check(rc, "nvfp4_latent_decode_attention")
+    return out
+
+
+def latent_extend_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Tensor, rope_prefix: torch.Tensor,
+                            cu_prefix_lens: torch.Tensor, k_chunk: torch.Tensor, v_chunk: torch.Tensor,
+                            rope_chunk: torch.Tensor, cu_q_lens: torch.Tensor, max_q_len: int,
+                            sm_scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                            stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Expanded form: each request's chunk attends to [its prefix || the chunk],
+    causally in the chunk.  q: BF16 [total_q][H][192], the last 64 the rotary part;
+    k_*, v_*: BF16 [rows][H][128], the up-projected latents (any token and head
+    strides that are multiples of 8: halves of one [rows][H][256] projection
+    output); rope_*: BF16 [rows][64], shared by the heads; cu_*: int32 [R+1];
+    max_q_len: bound on chunk lengths -> BF16 [total_q][H][128].  sm_scale > 0
+    defaults to 1 / sqrt(192)."""
+    _require(q, "q", torch.bfloat16)
+    if q.dim() != 3 or q.shape[2] != HEAD_DIM + ROPE_DIM:
+        raise ValueError("q must be [total_q][heads][192]")
+    _require(cu_prefix_lens, "cu_prefix_lens", torch.int32)
+    _require(cu_q_lens, "cu_q_lens", torch.int32)
+    TQ, H, R = int(q.shape[0]), int(q.shape[1]), int(cu_q_lens.shape[0]) - 1
+    _shape(cu_prefix_lens, "cu_prefix_lens", (R + 1,))
+    strides = []
+    for where, k, v, rope, rows in (("prefix", k_prefix, v_prefix, rope_prefix, None),
+                                    ("chunk", k_chunk, v_chunk, rope_chunk, TQ)):
+        rows = int(k.shape[0]) if rows is None else rows
+        for name, x in (("k_" + where, k), ("v_" + where, v)):
+            if not x.is_cuda or x.dtype != torch.bfloat16:
+                raise ValueError("%s must be a CUDA bfloat16 tensor" % name)
+            _shape(x, name, (rows, H, HEAD_DIM))
+            if rows > 0 and x.stride(2) != 1:
+                raise ValueError("%s: the 128 values of a head must be contiguous" % name)
+        # strides of axes of length 1 say nothing: torch may give them any value
+        st = int(k.stride(0)) if rows > 1 else H * HEAD_DIM
+        sh = int(k.stride(1)) if H > 1 else HEAD_DIM
+        if (rows > 1 and v.stride(0) != st) or (H > 1 and rows > 0 and v.stride(1) != sh):
+            raise ValueError("k_%s and v_%s must share their strides" % (where, where))
+        strides.append((st, sh))
+        _require(rope, "rope_" + where, torch.bfloat16)
+        _shape(rope, "rope_" + where, (rows, ROPE_DIM))
+    if out is None:
+        out = torch.empty((TQ, H, HEAD_DIM), dtype=torch.bfloat16, device=q.device)
+        _keep_until_done(stream, out)
+    else:
+        _require(out, "out", torch.bfloat16)
+        _shape(out, "out", (TQ, H, HEAD_DIM))
+    _on_device(q.device, ("k_prefix", k_prefix), ("v_prefix", v_prefix), ("rope_prefix", rope_prefix),
+               ("cu_prefix_lens", cu_prefix_lens), ("k_chunk", k_chunk), ("v_chunk", v_chunk),
+               ("rope_chunk", rope_chunk), ("cu_q_lens", cu_q_lens), ("out", out))
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(HEAD_DIM + ROPE_DIM)
+    (ps, ph), (cs, ch) = strides
+    rc = _lib.nvfp4_latent_extend_attention(_ptr(q), _ptr(k_prefix), _ptr(v_prefix), ps, ph, _ptr(rope_prefix),
+                                            _ptr(cu_prefix_lens), int(k_prefix.shape[0]), _ptr(k_chunk), _ptr(v_chunk),
+                                            cs, ch, _ptr(rope_chunk), _ptr(cu_q_lens), TQ, R, int(max_q_len), H,
+                                            float(sm_scale), _ptr(out), _stream(stream))
+    _check(rc, "nvfp4_latent_extend_attention")
+    return out
+
+
+def weights_workspace_bytes(cache: PagedCache, batch: int, num_q_heads: int) -> int:
+    n = _lib.nvfp4kv_weights_workspace_bytes(cache.desc, int(batch), int(num_q_heads))
+    if n == 0:
+        raise NVFP4KVError(-1, "weights_workspace_bytes")
+    return int(n)
+
+
+def alloc_weights_workspace(cache: PagedCache, batch: int, num_q_heads: int) -> torch.Tensor:
+    return torch.empty(weights_workspace_bytes(cache, batch, num_q_heads), dtype=torch.uint8, device=cache.pool.device)
+
+
+def accumulate_attention_weights(cache: PagedCache, q: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                                 scores: torch.Tensor, sm_scale: Optional[float] = None,
+                                 workspace: Optional[torch.Tensor] = None,
+                                 stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Adds to scores (float32 [B][Hkv][S], in place) the attention weights that the
+    queries q (BF16 [B][Hq][128]) put on every cached token: entry [b][h][t] grows
+    by the sum over kv head h's query heads of their softmax weight of token t <
+    seq_lens[b].  Returns scores."""
+    _require(q, "q", torch.bfloat16)
+    _require(block_table, "block_table", torch.int32)
+    _require(seq_lens, "seq_lens", torch.int32)
+    _require(scores, "scores", torch.float32)
+    if q.dim() != 3 or q.shape[2] != HEAD_DIM:
+        raise ValueError("q must be [batch][heads][128]")
+    B, Hq = int(q.shape[0]), int(q.shape[1])
+    _shape(seq_lens, "seq_lens", (B,))
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table needs one row per sequence")
+    if scores.dim() != 3 or tuple(scores.shape[:2]) != (B, cache.num_kv_heads):
+        raise ValueError("scores must be [batch][kv heads][tokens]")
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(HEAD_DIM)
+    if workspace is None:
+        workspace = alloc_weights_workspace(cache, B, Hq)
+        _keep_until_done(stream, workspace)
+    else:
+        _require(workspace, "workspace", torch.uint8)
+    _on_device(cache.pool.device, ("q", q), ("block_table", block_table), ("seq_lens", seq_lens), ("scores", scores),
+               ("workspace", workspace))
+    rc = _lib.nvfp4_accumulate_attention_weights(cache.desc, _ptr(q), B, Hq, _ptr(block_table),
+                                                 int(block_table.shape[1]), _ptr(seq_lens), float(sm_scale),
+                                                 _ptr(scores), int(scores.shape[2]), _ptr(workspace),
+                                                 workspace.numel(), _stream(stream))
+    _check(rc, "nvfp4_accumulate_attention_weights")
+    return scores
+
+
+def evict(cache: PagedCache, scores: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+          new_block_table: torch.Tensor, keep: int, recent: int = 0, sink: int = 0,
+          new_lens: Optional[torch.Tensor] = None, kept: Optional[torch.Tensor] = None,
+          new_scores: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+    """Keeps, for every sequence and kv head, the `keep` tokens of largest score (and
+    always the first `sink` and the last `recent`; ties to the lowest index), in
+    their order, and copies their rows into the pages of new_block_table (int32
+    [B][new pages]), none of which may be in use.  scores: float32 [B][Hkv][S].
+    Returns (new_lens int32 [B], kept int32 [B][Hkv][keep]: the old row of every new
+    one, -1 behind the last, new_scores float32 [B][Hkv][>= keep]: theirs, then zeros;
+    S or keep wide, the larger, by default)."""
+    _require(scores, "scores", torch.float32)
+    _require(block_table, "block_table", torch.int32)
+    _require(seq_lens, "seq_lens", torch.int32)
+    _require(new_block_table, "new_block_table", torch.int32)
+    B, Hkv, keep, dev = int(seq_lens.shape[0]), cache.num_kv_heads, int(keep), cache.pool.device
+    if keep < 1:
+        raise ValueError("keep must be at least 1")
+    if scores.dim() != 3 or tuple(scores.shape[:2]) != (B, Hkv):
+        raise ValueError("scores must be [batch][kv heads][tokens]")
+    for name, t in (("block_table", block_table), ("new_block_table", new_block_table)):
+        if t.dim() != 2 or t.shape[0] != B:
+            raise ValueError("%s needs one row per sequence" % name)
+    made = []
+    if new_lens is None:
+        new_lens = torch.empty(B, dtype=torch.int32, device=dev)
+        made.append(new_lens)
+    if kept is None:
+        kept = torch.empty((B, Hkv, keep), dtype=torch.int32, device=dev)
+        made.append(kept)
+    if new_scores is None:
+        new_scores = torch.empty((B, Hkv, max(int(scores.shape[2]), keep)), dtype=torch.float32, device=dev)
+        made.append(new_scores)
+    _require(new_lens, "new_lens", torch.int32)
+    _shape(new_lens, "new_lens", (B,))
+    _require(kept, "kept", torch.int32)
+    _shape(kept, "kept", (B, Hkv, keep))
+    _require(new_scores, "new_scores", torch.float32)
+    if new_scores.dim() != 3 or tuple(new_scores.shape[:2]) != (B, Hkv) or new_scores.shape[2] < keep:
+        raise ValueError("new_scores must be [batch][kv heads][at least keep]")
+    _on_device(dev, ("scores", scores), ("block_table", block_table), ("seq_lens", seq_lens),
+               ("new_block_table", new_block_table), ("new_lens", new_lens), ("kept", kept),
+               ("new_scores", new_scores))
+    _keep_until_done(stream, *made)
+    rc = _lib.nvfp4_evict(cache.desc, _ptr(scores), int(scores.shape[2]), B, _ptr(block_table),
+                          int(block_table.shape[1]), _ptr(seq_lens), _ptr(new_block_table),
+                          int(new_block_table.shape[1]), keep, int(recent), int(sink), _ptr(new_lens), _ptr(kept),
+                          _ptr(new_scores), int(new_scores.shape[2]), _stream(stream))
+    _check(rc, "nvfp4_evict")
+    return new_lens, kept, new_scores
 
 
 def check_device_errors(stream: Optional[torch.cuda.Stream] = None) -> int:

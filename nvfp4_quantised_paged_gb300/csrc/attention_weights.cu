@@ -1,0 +1,429 @@
+// attention_weights.cu -- the attention weight of every cached token, added to its score.
+//
+//   scores[b][h][t] += sum_j softmax_t(sm_scale * g_K * q_j . k_t)[t]
+// over the G query heads j of kv head h: what a policy that evicts tokens by
+// accumulated attention weight keeps.  K alone is needed (72 of a token's 144
+// NVFP4 bytes), but the softmax's denominators are known only after all of a
+// sequence, and the weights are held in FP32 (decode rounds its
+// probabilities to FP16, which a running sum would keep).
+//
+// Two kernels walk the same flat order of 64-token units (sequence, kv head,
+// unit), cut into one contiguous piece a warp:
+//   stats    running maximum and sum of 2^(s - m), kept by every thread for its
+//            own (token, head) positions and joined only where the warp leaves a
+//            (sequence, head) pair: one (m, l) partial per warp, pair and head;
+//   weights  joins the partials of a pair into L = m + log2 l, forms the scores'
+//            products again and adds sum_j 2^(s_j - L_j): no atomics, one
+//            addition per entry.
+// The scores come from mma.sync m16n8k16 with the 16 tokens of a group on M and
+// the heads on N.  The contraction's order is free, so thread j of a quad takes
+// the dimensions 32j .. 32j + 31 of its tokens: one 16-byte load of codes each,
+// coalesced over the warp, straight from the page to registers; e2m1 x e4m3 is
+// an exact FP16 value, and q is FP16 after a power-of-two pre-scale a head
+// (exact above 2^-29 of its largest value), undone in the FP32 score factor.
+#include <mutex>
+
+#include "common.cuh"
+#include "flat_plan.cuh"
+#include "kernels.h"
+#include "quantize.cuh"
+
+namespace nvfp4kv {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarpsW = kThreads / 32;
+constexpr int kUnit = 64;                     // tokens per unit
+constexpr int kGroupsW = kUnit / 16;
+constexpr float kNegInfW = -__builtin_huge_valf();
+
+struct WeightsArgs {
+    const uint8_t *pool;
+    int64_t num_pages;
+    int P, log2P, Hkv, G, Hq, B, max_pages;
+    int64_t slab;
+    const uint16_t *q;
+    const int32_t *block_table, *seq_lens;
+    int64_t cap;            // rows a sequence may have: min(table, score_stride)
+    float score_log2;       // sm_scale * g_K * log2(e)
+    float *scores;
+    int64_t score_stride;
+    float2 *part;           // [workers + B * Hkv][G]: (m, l) of warp w and pair p at w + p
+    int workers;
+    unsigned *err;
+};
+
+template <int DTYPE>
+struct RawUnit {  // one thread's share of a unit's K: tokens g and g + 8 of each group, 32 dimensions
+    uint4 code[kGroupsW][2][DTYPE == NVFP4KV_DTYPE_NVFP4 ? 1 : 2];
+    uint32_t scale[kGroupsW];   // two E4M3 bytes of token g (low half) and of token g + 8
+};
+
+template <int DTYPE>
+__device__ __forceinline__ void load_unit(const WeightsArgs &a, int b, int h, int t0, int n, int lane,
+                                          RawUnit<DTYPE> &r) {
+    const int g = lane >> 2, j = lane & 3;
+    int32_t page = -1;
+    if (lane < kGroupsW && t0 + 16 * lane < n) {
+        page = __ldg(a.block_table + (int64_t)b * a.max_pages + ((t0 + 16 * lane) >> a.log2P));
+        if (page < 0 || page >= a.num_pages) {
+            flag_error(a.err, kErrPage);
+            page = -1;
+        }
+    }
+    constexpr int kBytes = DTYPE == NVFP4KV_DTYPE_NVFP4 ? 2304 : 4096;
+#pragma unroll
+    for (int i = 0; i < kGroupsW; i++) {
+        const int32_t pg = __shfl_sync(0xffffffffu, page, i);
+        const int t = t0 + 16 * i;
+        const uint8_t *grp = a.pool + ((int64_t)pg * a.Hkv + h) * a.slab + ((t & (a.P - 1)) >> 4) * kBytes;
+        r.scale[i] = 0;
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+            const int row = g + 8 * e;
+            const bool ok = pg >= 0 && t + row < n;
+            if (DTYPE == NVFP4KV_DTYPE_NVFP4) {
+                r.code[i][e][0] = make_uint4(0, 0, 0, 0);
+                if (ok) {
+                    r.code[i][e][0] = __ldg(reinterpret_cast<const uint4 *>(grp + row * 64 + j * 16));
+                    r.scale[i] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(grp + 1024 + row * 8 + j * 2)) << (16 * e);
+                }
+            } else {
+#pragma unroll
+                for (int x = 0; x < (DTYPE == NVFP4KV_DTYPE_NVFP4 ? 1 : 2); x++) {
+                    r.code[i][e][x] = make_uint4(0, 0, 0, 0);
+                    if (ok) r.code[i][e][x] = __ldg(reinterpret_cast<const uint4 *>(grp + row * 128 + j * 32) + x);
+                }
+            }
+        }
+    }
+}
+
+// Scores (before the factor) of group i's 16 tokens: c[nt] = rows g, g + 8 x heads 8 nt + 2j, + 1.
+template <int DTYPE, int NT>
+__device__ __forceinline__ void group_scores(const RawUnit<DTYPE> &r, int i, const uint32_t (&qf)[NT][16],
+                                             float (&c)[NT][4]) {
+#pragma unroll
+    for (int x = 0; x < NT; x++) c[x][0] = c[x][1] = c[x][2] = c[x][3] = 0.f;
+    uint32_t f[2][16];   // token g / g + 8: f16 pairs of dimensions 32j + 2p, + 1
+#pragma unroll
+    for (int e = 0; e < 2; e++) {
+        if (DTYPE == NVFP4KV_DTYPE_NVFP4) {
+            const uint4 w = r.code[i][e][0];
+            e2m1x8_to_f16x2x4(w.x, f[e][0], f[e][1], f[e][2], f[e][3]);
+            e2m1x8_to_f16x2x4(w.y, f[e][4], f[e][5], f[e][6], f[e][7]);
+            e2m1x8_to_f16x2x4(w.z, f[e][8], f[e][9], f[e][10], f[e][11]);
+            e2m1x8_to_f16x2x4(w.w, f[e][12], f[e][13], f[e][14], f[e][15]);
+            const uint32_t s2 = e4m3x2_to_f16x2((r.scale[i] >> (16 * e)) & 0xffffu);
+            const uint32_t lo = __byte_perm(s2, s2, 0x1010), hi = __byte_perm(s2, s2, 0x3232);
+#pragma unroll
+            for (int p = 0; p < 8; p++) {
+                f[e][p] = hmul2(f[e][p], lo);
+                f[e][8 + p] = hmul2(f[e][8 + p], hi);
+            }
+        } else {
+            constexpr int kX = DTYPE == NVFP4KV_DTYPE_NVFP4 ? 1 : 2;
+#pragma unroll
+            for (int x = 0; x < kX; x++) {
+                const uint4 v = r.code[i][e][x];
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int p = 0; p < 4; p++) {
+                    f[e][8 * x + 2 * p] = e4m3x2_to_f16x2(w[p] & 0xffffu);
+                    f[e][8 * x + 2 * p + 1] = e4m3x2_to_f16x2(w[p] >> 16);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int s = 0; s < 8; s++)
+#pragma unroll
+        for (int x = 0; x < NT; x++)
+            mma_f16_16816(c[x], f[0][2 * s], f[1][2 * s], f[0][2 * s + 1], f[1][2 * s + 1], qf[x][2 * s], qf[x][2 * s + 1]);
+}
+
+// This thread's query fragments (heads 8 x + lane / 4, dimensions 32 (lane % 4) ..)
+// and the score factors of heads 8 x + 2 (lane % 4), + 1.
+template <int NT>
+__device__ __forceinline__ void load_query(const WeightsArgs &a, int b, int h, int lane, uint32_t (&qf)[NT][16],
+                                           float (&fac)[NT][2]) {
+    const int j = lane & 3;
+#pragma unroll
+    for (int x = 0; x < NT; x++) {
+        const int head = 8 * x + (lane >> 2);
+        uint32_t w[16], m = 0;
+        if (head < a.G) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(
+                a.q + ((int64_t)b * a.Hq + (int64_t)h * a.G + head) * kHeadDim + 32 * j);
+#pragma unroll
+            for (int p = 0; p < 4; p++) {
+                const uint4 v = __ldg(src + p);
+                w[4 * p] = v.x;
+                w[4 * p + 1] = v.y;
+                w[4 * p + 2] = v.z;
+                w[4 * p + 3] = v.w;
+            }
+        } else {
+#pragma unroll
+            for (int p = 0; p < 16; p++) w[p] = 0;
+        }
+#pragma unroll
+        for (int p = 0; p < 16; p++) m = max_u16x2(m, w[p] & 0x7fff7fffu);
+        m = max(m >> 16, m & 0xffffu);
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const int kq = m ? min(126, max(-126, 14 - ((int)(m >> 7) - 127))) : 0;   // largest |q| into [2^14, 2^15)
+        const float sc = __uint_as_float((uint32_t)(kq + 127) << 23);
+#pragma unroll
+        for (int p = 0; p < 16; p++) qf[x][p] = f32x2_to_f16x2(bf16_hi(w[p]) * sc, bf16_lo(w[p]) * sc);
+        const float f = a.score_log2 * __uint_as_float((uint32_t)(127 - kq) << 23);
+        fac[x][0] = __shfl_sync(0xffffffffu, f, 8 * j);
+        fac[x][1] = __shfl_sync(0xffffffffu, f, 8 * j + 4);
+    }
+}
+
+template <int DTYPE, int NT, bool kStats>
+__global__ void __launch_bounds__(kThreads) weights_kernel(WeightsArgs a) {
+    __shared__ FlatScratch<kThreads> scratch;
+    pdl_wait();   // lengths, q and the cache may come from earlier work; the weights kernel reads the partials
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int64_t worker = (int64_t)blockIdx.x * kWarpsW + (threadIdx.x >> 5);
+    auto rows = [&](int b) { return clamp_rows(__ldg(a.seq_lens + b), a.cap); };
+    auto units = [&](int b) { return (rows(b) + kUnit - 1) / kUnit; };
+    if (kStats && blockIdx.x == 0)
+        for (int b = threadIdx.x; b < a.B; b += kThreads) {
+            const int32_t n = a.seq_lens[b];
+            if (n < 0 || (int64_t)n > a.cap) flag_error(a.err, kErrSeqLen);
+        }
+    int b;
+    int64_t first, u0 = 0;
+    const int64_t total = flat_locate<kThreads>(
+        scratch, a.B, [&](int x) { return (int64_t)a.Hkv * units(x); },
+        [&](int64_t t) { return u0 = flat_begin(worker, t, a.workers); }, b, first);
+    const int64_t u1 = flat_begin(worker + 1, total, a.workers);
+    if (u0 >= u1) return;
+    int n = rows(b), nu = units(b);
+    int h = (int)((u0 - first) / nu), un = (int)((u0 - first) % nu);
+    uint32_t qf[NT][16];
+    float fac[NT][2], m[NT][2], l[NT][2];   // kStats: running maximum and sum; else m = L of the pair's heads
+    bool fresh = true;
+    for (int64_t u = u0; u < u1; u++) {
+        if (fresh) {
+            load_query<NT>(a, b, h, lane, qf, fac);
+            if (kStats) {
+#pragma unroll
+                for (int x = 0; x < NT; x++) {
+                    m[x][0] = m[x][1] = kNegInfW;
+                    l[x][0] = l[x][1] = 0.f;
+                }
+            } else {
+                // the pair's units [first + h nu, first + (h + 1) nu) were covered by these warps
+                const int64_t p = (int64_t)b * a.Hkv + h, p0 = first + (int64_t)h * nu;
+                const int64_t w0 = flat_piece(p0, total, a.workers), w1 = flat_piece(p0 + nu - 1, total, a.workers);
+                float mine[NT * 8];
+#pragma unroll
+                for (int hd = 0; hd < NT * 8; hd++) {
+                    mine[hd] = -kNegInfW;      // heads that do not exist: weight 2^-inf
+                    if (hd >= a.G) continue;   // uniform
+                    float mm = kNegInfW, ll = 0.f;
+                    for (int64_t w = w0 + lane; w <= w1; w += 32) {
+                        if (flat_begin(w, total, a.workers) == flat_begin(w + 1, total, a.workers)) continue;  // empty
+                        const float2 v = __ldcg(a.part + (w + p) * a.G + hd);
+                        const float mx = fmaxf(mm, v.x);
+                        if (mx != kNegInfW) ll = ll * ex2(mm - mx) + v.y * ex2(v.x - mx);
+                        mm = mx;
+                    }
+#pragma unroll
+                    for (int x = 16; x; x >>= 1) {
+                        const float om = __shfl_xor_sync(0xffffffffu, mm, x), ol = __shfl_xor_sync(0xffffffffu, ll, x);
+                        const float mx = fmaxf(mm, om);
+                        if (mx != kNegInfW) ll = ll * ex2(mm - mx) + ol * ex2(om - mx);
+                        mm = mx;
+                    }
+                    mine[hd] = mm + __log2f(ll);
+                }
+#pragma unroll
+                for (int x = 0; x < NT; x++) {
+                    m[x][0] = m[x][1] = 0.f;
+#pragma unroll
+                    for (int q = 0; q < 4; q++)
+                        if ((lane & 3) == q) {
+                            m[x][0] = mine[8 * x + 2 * q];
+                            m[x][1] = mine[8 * x + 2 * q + 1];
+                        }
+                }
+            }
+            fresh = false;
+        }
+        const int t0 = un * kUnit;
+        RawUnit<DTYPE> raw;
+        load_unit<DTYPE>(a, b, h, t0, n, lane, raw);
+        const int g = lane >> 2, j = lane & 3;
+        float *dst = a.scores + ((int64_t)b * a.Hkv + h) * a.score_stride + t0 + g + 8 * (j & 1);
+        float old[kGroupsW];
+        if (!kStats) {   // lanes j = 0 and 1 of a quad own tokens g and g + 8
+#pragma unroll
+            for (int i = 0; i < kGroupsW; i++) {
+                old[i] = 0.f;
+                if (j < 2 && t0 + 16 * i + g + 8 * j < n) old[i] = dst[16 * i];
+            }
+        }
+        float sc[kStats ? kGroupsW : 1][NT][4];
+#pragma unroll
+        for (int i = 0; i < kGroupsW; i++) {
+            float c[NT][4];
+            group_scores<DTYPE, NT>(raw, i, qf, c);
+            const bool ok0 = t0 + 16 * i + g < n, ok1 = t0 + 16 * i + g + 8 < n;
+            if (kStats) {
+#pragma unroll
+                for (int x = 0; x < NT; x++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        sc[kStats ? i : 0][x][e] = (e < 2 ? ok0 : ok1) ? c[x][e] * fac[x][e & 1] : kNegInfW;
+            } else {
+                float w0 = 0.f, w1 = 0.f;
+#pragma unroll
+                for (int x = 0; x < NT; x++) {
+                    w0 += ex2(fmaf(c[x][0], fac[x][0], -m[x][0])) + ex2(fmaf(c[x][1], fac[x][1], -m[x][1]));
+                    w1 += ex2(fmaf(c[x][2], fac[x][0], -m[x][0])) + ex2(fmaf(c[x][3], fac[x][1], -m[x][1]));
+                }
+                w0 += __shfl_xor_sync(0xffffffffu, w0, 1);
+                w1 += __shfl_xor_sync(0xffffffffu, w1, 1);
+                w0 += __shfl_xor_sync(0xffffffffu, w0, 2);
+                w1 += __shfl_xor_sync(0xffffffffu, w1, 2);
+                if (j < 2 && (j ? ok1 : ok0)) dst[16 * i] = old[i] + (j ? w1 : w0);
+            }
+        }
+        if (kStats) {
+#pragma unroll
+            for (int x = 0; x < NT; x++)
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    float mx = m[x][e];
+#pragma unroll
+                    for (int i = 0; i < kGroupsW; i++)
+                        mx = fmaxf(mx, fmaxf(sc[kStats ? i : 0][x][e], sc[kStats ? i : 0][x][e + 2]));
+                    if (mx != kNegInfW) {
+                        float s = l[x][e] * ex2(m[x][e] - mx);
+#pragma unroll
+                        for (int i = 0; i < kGroupsW; i++)
+                            s += ex2(sc[kStats ? i : 0][x][e] - mx) + ex2(sc[kStats ? i : 0][x][e + 2] - mx);
+                        l[x][e] = s;
+                        m[x][e] = mx;
+                    }
+                }
+        }
+        un++;
+        if (un == nu || u + 1 == u1) {
+            if (kStats) {   // this warp's partial of the pair: join the eight token rows of each head
+                const int64_t at = (worker + (int64_t)b * a.Hkv + h) * a.G;
+#pragma unroll
+                for (int x = 0; x < NT; x++)
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {
+                        float mm = m[x][e], ll = l[x][e];
+#pragma unroll
+                        for (int s = 4; s < 32; s <<= 1) {
+                            const float om = __shfl_xor_sync(0xffffffffu, mm, s), ol = __shfl_xor_sync(0xffffffffu, ll, s);
+                            const float mx = fmaxf(mm, om);
+                            if (mx != kNegInfW) ll = ll * ex2(mm - mx) + ol * ex2(om - mx);
+                            mm = mx;
+                        }
+                        const int hd = 8 * x + 2 * j + e;
+                        if (g == 0 && hd < a.G) a.part[at + hd] = make_float2(mm, ll);
+                    }
+            }
+            if (un == nu) {
+                fresh = true;
+                un = 0;
+                if (++h == a.Hkv && u + 1 < u1) {
+                    h = 0;
+                    first += (int64_t)a.Hkv * nu;
+                    do {
+                        b++;
+                        n = rows(b);
+                        nu = units(b);
+                    } while (nu == 0);   // u + 1 < u1 <= total: a later sequence has units
+                }
+            }
+        }
+    }
+}
+
+template <bool kStats>
+const void *weights_fn(int dtype, int nt) {
+    if (dtype == NVFP4KV_DTYPE_NVFP4)
+        return nt == 1 ? reinterpret_cast<const void *>(&weights_kernel<0, 1, kStats>)
+                       : reinterpret_cast<const void *>(&weights_kernel<0, 2, kStats>);
+    return nt == 1 ? reinterpret_cast<const void *>(&weights_kernel<1, 1, kStats>)
+                   : reinterpret_cast<const void *>(&weights_kernel<1, 2, kStats>);
+}
+
+constexpr int kMaxDevicesW = 64;
+std::mutex g_mu_w;
+int g_workers[kMaxDevicesW][2][2];
+
+}  // namespace
+
+int weights_workers(int dtype, int group, cudaError_t *status) {
+    const int nt = group <= 8 ? 1 : 2;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && (dev < 0 || dev >= kMaxDevicesW)) e = cudaErrorInvalidDevice;
+    int out = 0;
+    if (e == cudaSuccess) {
+        std::lock_guard<std::mutex> lock(g_mu_w);
+        int &w = g_workers[dev][dtype][nt - 1];
+        if (!w) {
+            int sms = 0, a = 0, b = 0;
+            e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+            if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&a, weights_fn<true>(dtype, nt), kThreads, 0);
+            if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, weights_fn<false>(dtype, nt), kThreads, 0);
+            if (e == cudaSuccess) w = sms * (a < b ? (a > 0 ? a : 1) : (b > 0 ? b : 1)) * kWarpsW;
+        }
+        out = w;
+    }
+    if (status) *status = e;
+    return e == cudaSuccess ? out : 0;
+}
+
+size_t weights_workspace_bytes(int batch, int num_q_heads, int num_kv_heads, int workers) {
+    return ((size_t)workers + (size_t)batch * num_kv_heads) * (num_q_heads / num_kv_heads) * sizeof(float2);
+}
+
+cudaError_t launch_weights(const nvfp4kv_cache &c, const void *q, int batch, int num_q_heads,
+                           const int32_t *block_table, int max_pages, const int32_t *seq_lens, float sm_scale,
+                           float *scores, int64_t score_stride, void *workspace, int workers, unsigned *err,
+                           cudaStream_t stream) {
+    WeightsArgs a;
+    a.pool = static_cast<const uint8_t *>(c.pool);
+    a.num_pages = c.num_pages;
+    a.P = c.page_size;
+    a.log2P = __builtin_ctz((unsigned)c.page_size);
+    a.Hkv = c.num_kv_heads;
+    a.G = num_q_heads / c.num_kv_heads;
+    a.Hq = num_q_heads;
+    a.B = batch;
+    a.max_pages = max_pages;
+    a.slab = (int64_t)(c.dtype == NVFP4KV_DTYPE_NVFP4 ? 144 : 256) * c.page_size;
+    a.q = static_cast<const uint16_t *>(q);
+    a.block_table = block_table;
+    a.seq_lens = seq_lens;
+    const int64_t table = (int64_t)max_pages * c.page_size;
+    a.cap = table < score_stride ? table : score_stride;
+    a.score_log2 = (float)((double)sm_scale * (double)c.k_global_scale * 1.4426950408889634);
+    a.scores = scores;
+    a.score_stride = score_stride;
+    a.part = static_cast<float2 *>(workspace);
+    a.workers = workers;
+    a.err = err;
+    const int nt = a.G <= 8 ? 1 : 2;
+    void *args[] = {&a};
+    cudaError_t e = launch_pdl(weights_fn<true>(c.dtype, nt), (unsigned)(workers / kWarpsW), kThreads, 0, stream, args);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(weights_fn<false>(c.dtype, nt), (unsigned)(workers / kWarpsW), kThreads, 0, stream, args);
+}
+
+}  // namespace nvfp4kv

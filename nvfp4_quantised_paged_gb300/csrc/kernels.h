@@ -72,4 +72,44 @@ cudaError_t launch_calibrate(const void *k, const void *v, int64_t num_tokens, i
 cudaError_t launch_bounded_wait_selftest(int arrive, uint32_t poll_limit, int *result, unsigned *err,
                                          cudaStream_t stream);
 
+// Latents and rotary parts into the latent cache; and back to BF16 rows.
+cudaError_t launch_latent_append(const nvfp4kv_latent_cache &c, const void *latent, int64_t latent_stride,
+                                 const void *rope, int64_t rope_stride, int64_t num_tokens,
+                                 const int64_t *slot_mapping, unsigned *err, cudaStream_t stream);
+cudaError_t launch_latent_dequant(const nvfp4kv_latent_cache &c, const int32_t *block_table, int max_pages,
+                                  const int32_t *prefix_lens, const int32_t *cu, int num_reqs, int64_t total,
+                                  void *latent_ws, void *rope_ws, unsigned *err, cudaStream_t stream);
+
+// Absorbed latent decode: CTAs per head tile of an auto split (0 on an error),
+// workspace bytes for `splits` of them, and the launch.
+int latent_decode_auto_splits(int num_heads, cudaError_t *status);
+size_t latent_decode_workspace_bytes(int batch, int num_heads, int splits);
+cudaError_t launch_latent_decode(const nvfp4kv_latent_cache &c, const void *q_latent, const void *q_rope, int batch,
+                                 int num_heads, const int32_t *block_table, int max_pages, const int32_t *seq_lens,
+                                 float sm_scale, void *out, void *workspace, int splits, unsigned *err,
+                                 cudaStream_t stream);
+
+// Expanded latent attention of a chunk over [prefix || chunk]; strides in elements.
+cudaError_t launch_latent_extend(const void *q, const void *k_prefix, const void *v_prefix, int64_t pre_token,
+                                 int64_t pre_head, const void *rope_prefix, const int32_t *cu_prefix,
+                                 int64_t total_prefix, const void *k_chunk, const void *v_chunk, int64_t new_token,
+                                 int64_t new_head, const void *rope_chunk, const int32_t *cu_q, int64_t total_q,
+                                 int num_reqs, int max_q_len, int num_heads, float sm_scale, void *out, unsigned *err,
+                                 cudaStream_t stream);
+
+// Attention weights added to the scores: warps that share the work (0 on an
+// error), workspace bytes, and the launch.
+int weights_workers(int dtype, int group, cudaError_t *status);
+size_t weights_workspace_bytes(int batch, int num_q_heads, int num_kv_heads, int workers);
+cudaError_t launch_weights(const nvfp4kv_cache &c, const void *q, int batch, int num_q_heads,
+                           const int32_t *block_table, int max_pages, const int32_t *seq_lens, float sm_scale,
+                           float *scores, int64_t score_stride, void *workspace, int workers, unsigned *err,
+                           cudaStream_t stream);
+
+cudaError_t launch_evict(const nvfp4kv_cache &c, const float *scores, int64_t score_stride, int batch,
+                         const int32_t *block_table, int max_pages, const int32_t *seq_lens,
+                         const int32_t *new_block_table, int new_max_pages, int keep, int recent, int sink,
+                         int32_t *new_lens, int32_t *kept, float *new_scores, int64_t new_score_stride, unsigned *err,
+                         cudaStream_t stream);
+
 }  // namespace nvfp4kv
