@@ -199,11 +199,16 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(WeightsArgs a) {
         }
     int b;
     int64_t first, u0 = 0;
+    int64_t pieces = a.workers;   // never more than there are units: no piece is empty
     const int64_t total = flat_locate<kThreads>(
         scratch, a.B, [&](int x) { return (int64_t)a.Hkv * units(x); },
-        [&](int64_t t) { return u0 = flat_begin(worker, t, a.workers); }, b, first);
-    const int64_t u1 = flat_begin(worker + 1, total, a.workers);
-    if (u0 >= u1) return;
+        [&](int64_t t) {
+            pieces = min(pieces, t);
+            return u0 = worker < pieces ? flat_begin(worker, t, pieces) : -1;
+        },
+        b, first);
+    if (worker >= pieces) return;
+    const int64_t u1 = flat_begin(worker + 1, total, pieces);
     int n = rows(b), nu = units(b);
     int h = (int)((u0 - first) / nu), un = (int)((u0 - first) % nu);
     uint32_t qf[NT][16];
@@ -221,7 +226,7 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(WeightsArgs a) {
             } else {
                 // the pair's units [first + h nu, first + (h + 1) nu) were covered by these warps
                 const int64_t p = (int64_t)b * a.Hkv + h, p0 = first + (int64_t)h * nu;
-                const int64_t w0 = flat_piece(p0, total, a.workers), w1 = flat_piece(p0 + nu - 1, total, a.workers);
+                const int64_t w0 = flat_piece(p0, total, pieces), w1 = flat_piece(p0 + nu - 1, total, pieces);
                 float mine[NT * 8];
 #pragma unroll
                 for (int hd = 0; hd < NT * 8; hd++) {
@@ -229,7 +234,6 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(WeightsArgs a) {
                     if (hd >= a.G) continue;   // uniform
                     float mm = kNegInfW, ll = 0.f;
                     for (int64_t w = w0 + lane; w <= w1; w += 32) {
-                        if (flat_begin(w, total, a.workers) == flat_begin(w + 1, total, a.workers)) continue;  // empty
                         const float2 v = __ldcg(a.part + (w + p) * a.G + hd);
                         const float mx = fmaxf(mm, v.x);
                         if (mx != kNegInfW) ll = ll * ex2(mm - mx) + v.y * ex2(v.x - mx);

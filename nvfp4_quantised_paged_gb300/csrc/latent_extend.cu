@@ -170,27 +170,31 @@ __global__ void __launch_bounds__(kEThreads, 1)
     const uint32_t tmem = tmem_base;
 
     if (warp == kSoftThreads / 32) {
-        // ---------------- load / MMA thread
-        if (lane == 0) {
+        // ---------------- load / MMA warp: the whole warp runs the loop and one elected lane
+        // issues, so that descriptors stay uniform values (issued under a divergent branch a
+        // product cost more than the tensor core's 64 clocks for it)
+        {
             constexpr uint32_t idesc_s = idesc_bf16_f32(128, kKeys, false);
             constexpr uint32_t idesc_o = idesc_bf16_f32(128, kHeadDim, true);
-            auto mma_s = [&](int w, int s) {  // S_w = Q_w K(slot s)^T over 192 dimensions, 16 at a time
-                const uint32_t sQ = sbase + kOffQ + w * kQBytes, sK = sbase + kOffK + s * kKTile;
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const bool leader = elect_one();
+            const uint64_t dQ = smem_desc_sw128(sbase + kOffQ, 16, 1024), dK = smem_desc_sw128(sbase + kOffK, 16, 1024);
+            const uint64_t dV = smem_desc_sw128(sbase + kOffV, kBlockBytes, 1024);
+            auto mma_s = [&](uint32_t w, uint32_t s) {  // S_w = Q_w K(slot s)^T over 192 dimensions, 16 at a time
+                const uint64_t q = dQ + w * (kQBytes / 16), k = dK + s * (kKTile / 16);
 #pragma unroll
                 for (int kk = 0; kk < 12; kk++) {
-                    const uint32_t off = (uint32_t)(kk >> 2) * kBlockBytes + (uint32_t)(kk & 3) * 32;
-                    tc_mma_bf16(tmem + 128u * w, smem_desc_sw128(sQ + off, 16, 1024),
-                                smem_desc_sw128(sK + off, 16, 1024), idesc_s, kk > 0);
+                    const uint32_t off = (uint32_t)(kk >> 2) * (kBlockBytes / 16) + (uint32_t)(kk & 3) * 2;
+                    tc_mma_bf16(tm + 128u * w, q + off, k + off, idesc_s, kk > 0);
                 }
                 tc_commit(&s_done[w]);
             };
-            auto mma_pv = [&](int w, int j) {  // O_w += P_w V over the tile's 128 keys
-                const uint32_t sV = sbase + kOffV;
+            auto mma_pv = [&](uint32_t w, int j) {  // O_w += P_w V over the tile's 128 keys
+                const uint32_t acc = j > 0 ? 1u : 0u;
 #pragma unroll
                 for (int kk = 0; kk < 8; kk++)  // P from TMEM: 8 columns = 16 keys
-                    tc_mma_bf16_tmem_a(tmem + kColO + 128u * w, tmem + 128u * w + kk * 8,
-                                       smem_desc_sw128(sV + kk * 16 * 128, kBlockBytes, 1024), idesc_o,
-                                       (j > 0 || kk > 0) ? 1u : 0u);
+                    tc_mma_bf16_tmem_a(tm + kColO + 128u * w, tm + 128u * w + kk * 8, dV + kk * 128, idesc_o,
+                                       kk > 0 ? 1u : acc);
                 tc_commit(&pv_done[w]);
             };
             // Issue whatever is ready, for either query tile (the order of extend_attention.cu):
@@ -213,18 +217,18 @@ __global__ void __launch_bounds__(kEThreads, 1)
                     finished = false;
                     if (!at_pv[w]) {
                         if (t > 0 && pv_seen[w] < t) {
-                            if (!mbar_test_wait(&pv_done[w], (uint32_t)((t - 1) & 1))) continue;
+                            if (!__all_sync(0xffffffffu, mbar_test_wait(&pv_done[w], (uint32_t)((t - 1) & 1)))) continue;
                             pv_seen[w] = t;
                             progress = true;
                         }
-                        if (!mbar_test_wait(&k_full[t & 1], (uint32_t)((t >> 1) & 1))) continue;
+                        if (!__all_sync(0xffffffffu, mbar_test_wait(&k_full[t & 1], (uint32_t)((t >> 1) & 1)))) continue;
                         tc_fence_after();
-                        mma_s(w, t & 1);
+                        if (leader) mma_s(w, t & 1);
                         at_pv[w] = true;
                     } else {
-                        if (!mbar_test_wait(&p_full[w], (uint32_t)(t & 1))) continue;
+                        if (!__all_sync(0xffffffffu, mbar_test_wait(&p_full[w], (uint32_t)(t & 1)))) continue;
                         tc_fence_after();
-                        mma_pv(w, t);
+                        if (leader) mma_pv(w, t);
                         at_pv[w] = false;
                         tw[w] = t + 1;
                     }
@@ -237,23 +241,23 @@ __global__ void __launch_bounds__(kEThreads, 1)
                     min_seen = min(min_seen, pv_seen[1]);
                 }
                 if (k_next < nt && min_tw >= k_next - 1) {
-                    load_k(k_next);
+                    if (leader) load_k(k_next);
                     k_next++;
                     progress = true;
                 }
                 if (v_next < nt && min_seen >= v_next) {
-                    load_v(v_next);
+                    if (leader) load_v(v_next);
                     v_next++;
                     progress = true;
                 }
                 if (progress) {
                     idle = 0;
-                } else if (++idle > kWaitLimitE || *abort_flag) {
+                } else if (++idle > kWaitLimitE || __any_sync(0xffffffffu, *abort_flag)) {
                     ok = false;
                     break;
                 }
             }
-            if (!ok) {
+            if (!ok && leader) {
                 *abort_flag = 1;
                 flag_error(a.err, kErrTimeout);
                 // no copy or product may still be running when the CTA frees its memory

@@ -39,6 +39,13 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_maj
 // The descriptor with the A operand MN-major as well (its rows contiguous).
 __host__ __device__ constexpr uint32_t idesc_a_mn_major(uint32_t idesc) { return idesc | (1u << 15); }
 
+// One lane of a converged warp (the same one each time).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+    return r != 0;
+}
+
 // D (+)= A B for kind::f16 (the instruction descriptor fixes the input type).
 __device__ __forceinline__ void tc_mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                             uint32_t accumulate) {
