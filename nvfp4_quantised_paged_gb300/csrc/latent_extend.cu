@@ -8,15 +8,18 @@
 //
 // The pipeline is extend_attention.cu's: one CTA = 256 chunk tokens of one head in
 // two 128-row query tiles, one softmax warpgroup each with one row (= TMEM lane) a
-// thread; one thread of warp 8 drives the TMA loads and the tcgen05 products, two
-// independent chains that the tensor core overlaps.  What differs:
+// thread; a warp per query tile issues its tcgen05 products, two independent chains that
+// the tensor core overlaps.  What differs:
 //   * S_w = Q_w K^T takes twelve K 16 steps, eight over K's two column blocks and
-//     four over the rotary block, a third column block of the K slot that its own
-//     tensor map fills: 48 KB a K slot and a query tile;
-//   * Q 96 KB + two K slots 96 KB leave room for one V slot (32 KB): V(j + 1) is
-//     requested when both O_w += P_w(j) V(j) are done, and is needed only after
-//     S(j + 1) and its softmax, so one slot costs little where one K slot would
-//     put every K load on the critical path;
+//     four over the rotary block, a third one that its own tensor map fills; a
+//     query tile is 48 KB, and a K/V tile 80 KB in five column blocks;
+//   * Q leaves room for eight blocks of 16 KB, not for two K/V tiles: they are a
+//     ring that the load warp fills in the order K(j) K(j) R(j) V(j) V(j) K(j + 1) ...,
+//     each slot as soon as the products that read it are done (whole slots of one
+//     V and two K tiles left V's load on the critical path: 277 us against
+//     @@RING@@ us for 4 x 512 tokens over up to 8,192, 32 heads).  V's two blocks
+//     need not be neighbours: O_w += P_w V runs as two N 64 products a step, which
+//     with P in TMEM cost what one of N 128 does (30 and 60 clocks);
 //   * rows of a V tile past the request's end are zeroed in shared memory before
 //     the product: they are other requests' rows or padding, and a NaN there times
 //     a probability of 0 would still be a NaN.
@@ -36,16 +39,16 @@ constexpr int kWGs = 2;
 constexpr int kQRows = 128;
 constexpr int kCtaRows = kWGs * kQRows;
 constexpr int kSoftThreads = kWGs * kQRows;
-constexpr int kEThreads = kSoftThreads + 32;   // + the load / MMA warp
+constexpr int kEThreads = kSoftThreads + 64;   // + the MMA warp and the load warp
 constexpr int kKeys = 128;
 constexpr int kQkDim = kHeadDim + kRopeDim;    // 192
 constexpr int kBlockBytes = 128 * 128;         // one column block: 128 rows of 64 BF16 values
-constexpr int kQBytes = 3 * kBlockBytes, kKTile = 3 * kBlockBytes, kVTile = 2 * kBlockBytes;
+constexpr int kQBytes = 3 * kBlockBytes;
+constexpr int kSlots = 8;                      // ring of column blocks: block 5 t + i of tile t (i = 0 1: K, 2: rotary, 3 4: V)
 constexpr int kOffQ = 0;
-constexpr int kOffK = kWGs * kQBytes;          // K slots [2]
-constexpr int kOffV = kOffK + 2 * kKTile;      // one V slot
-constexpr int kOffBar = kOffV + kVTile;
-constexpr int kNumBars = 10;                   // k_full[2] v_full s_done[2] p_full[2] pv_done[2] drain
+constexpr int kOffRing = kWGs * kQBytes;
+constexpr int kOffBar = kOffRing + kSlots * kBlockBytes;
+constexpr int kNumBars = kSlots + 11;          // k_full[2] v_full[2] empty[8] s_done[2] p_full[2] pv_done[2] drain
 constexpr int kOffTmem = kOffBar + kNumBars * 8;
 constexpr int kOffAbort = kOffTmem + 4;
 constexpr int kOffOrder = kOffBar + 256;       // int[256]: requests by decreasing prefix length
@@ -73,12 +76,21 @@ struct ExtendMaps {
     CUtensorMap k_pre, v_pre, r_pre, k_new, v_new, r_new;
 };
 
+// Bounded wait that polls without suspending the thread (these waits are on the critical path).
+__device__ __forceinline__ bool poll_wait(uint64_t *bar, uint32_t parity, const volatile int *abort_flag) {
+    for (uint32_t n = 0; n < 4 * kWaitLimitE; n++) {
+        if (mbar_test_wait(bar, parity)) return true;
+        if ((n & 255) == 255 && *abort_flag) return false;
+    }
+    return false;
+}
+
 __global__ void __launch_bounds__(kEThreads, 1)
     latent_extend_kernel(const __grid_constant__ ExtendMaps maps, ExtendArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kOffBar);
-    uint64_t *k_full = bars, *v_full = bars + 2, *s_done = bars + 3, *p_full = bars + 5, *pv_done = bars + 7;
-    uint64_t *drain = bars + 9;
+    uint64_t *k_full = bars, *v_full = bars + 2, *empty = bars + 4, *s_done = empty + kSlots, *p_full = s_done + 2;
+    uint64_t *pv_done = p_full + 2, *drain = pv_done + 2;
     uint32_t &tmem_base = *reinterpret_cast<uint32_t *>(smem + kOffTmem);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffAbort);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -138,29 +150,15 @@ __global__ void __launch_bounds__(kEThreads, 1)
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     auto tile_row = [&](int j) { return j < nt_pre ? p0 + j * kKeys : q0 + (j - nt_pre) * kKeys; };
-    auto load_k = [&](int j) {
-        const bool pre = j < nt_pre;
-        const uint32_t dst = sbase + kOffK + (j & 1) * kKTile;
-        mbar_arrive_expect_tx(&k_full[j & 1], kKTile);
-        tma_load_3d(dst, pre ? &maps.k_pre : &maps.k_new, 0, head, tile_row(j), &k_full[j & 1]);
-        tma_load_3d(dst + kBlockBytes, pre ? &maps.k_pre : &maps.k_new, 64, head, tile_row(j), &k_full[j & 1]);
-        tma_load_3d(dst + 2 * kBlockBytes, pre ? &maps.r_pre : &maps.r_new, 0, 0, tile_row(j), &k_full[j & 1]);
-    };
-    auto load_v = [&](int j) {
-        const CUtensorMap *m = j < nt_pre ? &maps.v_pre : &maps.v_new;
-        mbar_arrive_expect_tx(v_full, kVTile);
-        tma_load_3d(sbase + kOffV, m, 0, head, tile_row(j), v_full);
-        tma_load_3d(sbase + kOffV + kBlockBytes, m, 64, head, tile_row(j), v_full);
-    };
+    auto slot_of = [](uint32_t blk) { return blk % kSlots; };   // (fewer than 2^27 blocks: lengths are int32)
+    auto phase_of = [](uint32_t blk) { return (blk / kSlots) & 1u; };
 
     if (warp == 0) tc_alloc(&tmem_base, kTmemCols);
     if (tid == kSoftThreads) {
-        for (int j = 0; j < kNumBars; j++) mbar_init(&bars[j], j == 5 || j == 6 ? kQRows : 1);
+        for (int j = 0; j < kNumBars; j++)
+            mbar_init(&bars[j], &bars[j] >= empty && &bars[j] < s_done ? nwg : &bars[j] >= p_full && &bars[j] < pv_done ? kQRows : 1);
         *abort_flag = 0;
         fence_mbar_init();
-        load_k(0);
-        load_v(0);
-        if (nt > 1) load_k(1);
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // Q for the tensor core
@@ -170,105 +168,132 @@ __global__ void __launch_bounds__(kEThreads, 1)
     const uint32_t tmem = tmem_base;
 
     if (warp == kSoftThreads / 32) {
-        // ---------------- load / MMA warp: the whole warp runs the loop and one elected lane
+        // ---------------- MMA warp: the whole warp runs the loop and one elected lane
         // issues, so that descriptors stay uniform values (issued under a divergent branch a
         // product cost more than the tensor core's 64 clocks for it)
         {
             constexpr uint32_t idesc_s = idesc_bf16_f32(128, kKeys, false);
-            constexpr uint32_t idesc_o = idesc_bf16_f32(128, kHeadDim, true);
-            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            constexpr uint32_t idesc_o = idesc_bf16_f32(128, 64, true);
+            auto uniform = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
+            const uint32_t tm = uniform(tmem);
             const bool leader = elect_one();
-            const uint64_t dQ = smem_desc_sw128(sbase + kOffQ, 16, 1024), dK = smem_desc_sw128(sbase + kOffK, 16, 1024);
-            const uint64_t dV = smem_desc_sw128(sbase + kOffV, kBlockBytes, 1024);
-            auto mma_s = [&](uint32_t w, uint32_t s) {  // S_w = Q_w K(slot s)^T over 192 dimensions, 16 at a time
-                const uint64_t q = dQ + w * (kQBytes / 16), k = dK + s * (kKTile / 16);
+            const uint64_t dQ = smem_desc_sw128(sbase + kOffQ, 16, 1024);
+            const uint64_t dB = smem_desc_sw128(sbase + kOffRing, 16, 1024);   // slot 0, K-major and MN-major alike
+            auto mma_s = [&](int w, uint32_t blk) {  // S_w = Q_w K^T over 192 dimensions, 16 at a time
 #pragma unroll
-                for (int kk = 0; kk < 12; kk++) {
-                    const uint32_t off = (uint32_t)(kk >> 2) * (kBlockBytes / 16) + (uint32_t)(kk & 3) * 2;
-                    tc_mma_bf16(tm + 128u * w, q + off, k + off, idesc_s, kk > 0);
+                for (int i = 0; i < 3; i++) {
+                    const uint32_t slot = uniform(slot_of(blk + i));
+                    const uint64_t q = dQ + (w * (kQBytes / 16) + i * (kBlockBytes / 16)), k = dB + slot * (kBlockBytes / 16);
+                    if (leader) {
+#pragma unroll
+                        for (int kk = 0; kk < 4; kk++)
+                            tc_mma_bf16(tm + 128u * w, q + kk * 2, k + kk * 2, idesc_s, i + kk > 0);
+                        tc_commit(&empty[slot]);
+                        if (i == 2) tc_commit(&s_done[w]);
+                    }
                 }
-                tc_commit(&s_done[w]);
             };
-            auto mma_pv = [&](uint32_t w, int j) {  // O_w += P_w V over the tile's 128 keys
-                const uint32_t acc = j > 0 ? 1u : 0u;
+            auto mma_pv = [&](int w, uint32_t blk, uint32_t acc) {  // O_w += P_w V over 128 keys, 64 dimensions at a time
 #pragma unroll
-                for (int kk = 0; kk < 8; kk++)  // P from TMEM: 8 columns = 16 keys
-                    tc_mma_bf16_tmem_a(tm + kColO + 128u * w, tm + 128u * w + kk * 8, dV + kk * 128, idesc_o,
-                                       kk > 0 ? 1u : acc);
-                tc_commit(&pv_done[w]);
+                for (int i = 0; i < 2; i++) {
+                    const uint32_t slot = uniform(slot_of(blk + 3 + i));
+                    const uint64_t v = dB + slot * (kBlockBytes / 16);
+                    if (leader) {
+#pragma unroll
+                        for (int kk = 0; kk < 8; kk++)  // P from TMEM: 8 columns = 16 keys
+                            tc_mma_bf16_tmem_a(tm + kColO + 128u * w + 64u * i, tm + 128u * w + kk * 8, v + kk * 128, idesc_o,
+                                               kk > 0 ? 1u : acc);
+                        tc_commit(&empty[slot]);
+                        if (i == 1) tc_commit(&pv_done[w]);
+                    }
+                }
             };
-            // Issue whatever is ready, for either query tile (the order of extend_attention.cu):
-            //   S_w(t) once K(t) has landed and O_w += P_w(t - 1) V(t - 1) is complete;
-            //   O_w += P_w(t) V(t) once P_w(t) is stored (and, so, V(t) has landed: its threads waited for it);
-            //   K(t) into slot t % 2 once both S(t - 2) are done (their P V issued);
-            //   V(t) once both P(t - 1) V(t - 1) are complete.
-            int tw[kWGs] = {0, 0};
-            bool at_pv[kWGs] = {false, false};
-            int pv_seen[kWGs] = {0, 0};
-            int k_next = nt > 1 ? 2 : 1, v_next = 1;
-            bool ok = true;
-            uint32_t idle = 0;
-            for (;;) {
-                bool progress = false, finished = true;
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                const bool good = __all_sync(0xffffffffu, poll_wait(bar, parity, abort_flag));
+                tc_fence_after();
+                return good;
+            };
+            // The two query tiles take turns: O_0 += P_0(t) V(t), S_0(t + 1), O_1 += P_1(t) V(t),
+            // S_1(t + 1), so the softmax of one runs while the tensor core works for the other
+            // (issued as they became ready, the two fell into step and left it idle meanwhile).
+            // S_w(t + 1) goes over the columns of P_w(t) and waits for the product that reads
+            // it; whether the next K and V have landed is checked while that product runs.
+            bool ok = wait(&k_full[0], 0);
+            if (ok) {
+                mma_s(0, 0);
+                if (nwg > 1) mma_s(1, 0);
+            }
+            ok = ok && wait(&v_full[0], 0);
+            for (uint32_t t = 0, blk = 0; ok && t < (uint32_t)nt; t++, blk += 5) {
+                const bool more = t + 1 < (uint32_t)nt;
 #pragma unroll
                 for (int w = 0; w < kWGs; w++) {
-                    const int t = tw[w];
-                    if (w >= nwg || t >= nt) continue;
-                    finished = false;
-                    if (!at_pv[w]) {
-                        if (t > 0 && pv_seen[w] < t) {
-                            if (!__all_sync(0xffffffffu, mbar_test_wait(&pv_done[w], (uint32_t)((t - 1) & 1)))) continue;
-                            pv_seen[w] = t;
-                            progress = true;
-                        }
-                        if (!__all_sync(0xffffffffu, mbar_test_wait(&k_full[t & 1], (uint32_t)((t >> 1) & 1)))) continue;
-                        tc_fence_after();
-                        if (leader) mma_s(w, t & 1);
-                        at_pv[w] = true;
-                    } else {
-                        if (!__all_sync(0xffffffffu, mbar_test_wait(&p_full[w], (uint32_t)(t & 1)))) continue;
-                        tc_fence_after();
-                        if (leader) mma_pv(w, t);
-                        at_pv[w] = false;
-                        tw[w] = t + 1;
-                    }
-                    progress = true;
-                }
-                if (finished) break;
-                int min_tw = tw[0], min_seen = pv_seen[0];
-                if (nwg > 1) {
-                    min_tw = min(min_tw, tw[1]);
-                    min_seen = min(min_seen, pv_seen[1]);
-                }
-                if (k_next < nt && min_tw >= k_next - 1) {
-                    if (leader) load_k(k_next);
-                    k_next++;
-                    progress = true;
-                }
-                if (v_next < nt && min_seen >= v_next) {
-                    if (leader) load_v(v_next);
-                    v_next++;
-                    progress = true;
-                }
-                if (progress) {
-                    idle = 0;
-                } else if (++idle > kWaitLimitE || __any_sync(0xffffffffu, *abort_flag)) {
-                    ok = false;
-                    break;
+                    if (w >= nwg) break;
+                    ok = ok && wait(&p_full[w], t & 1);
+                    if (ok) mma_pv(w, blk, t > 0 ? 1u : 0u);
+                    if (!more) continue;
+                    if (w == 0) ok = ok && wait(&k_full[(t + 1) & 1], ((t + 1) >> 1) & 1);
+                    if (w == nwg - 1) ok = ok && wait(&v_full[(t + 1) & 1], ((t + 1) >> 1) & 1);
+                    ok = ok && wait(&pv_done[w], t & 1);
+                    if (ok) mma_s(w, blk + 5);
                 }
             }
             if (!ok && leader) {
+                if (!*abort_flag) flag_error(a.err, kErrTimeout);
                 *abort_flag = 1;
-                flag_error(a.err, kErrTimeout);
-                // no copy or product may still be running when the CTA frees its memory
-                for (int t = max(0, k_next - 2); t < k_next; t++)
-                    mbar_wait_bounded(&k_full[t & 1], (uint32_t)((t >> 1) & 1), kWaitLimitE, nullptr);
-                mbar_wait_bounded(v_full, (uint32_t)((v_next - 1) & 1), kWaitLimitE, nullptr);
-                tc_commit(drain);
+                tc_commit(drain);   // no product may still be running when the CTA frees its memory
                 mbar_wait_bounded(drain, 0, kWaitLimitE, nullptr);
             }
         }
         __syncwarp();
+    } else if (warp == kSoftThreads / 32 + 1) {
+        // ---------------- load warp: the blocks in order, each slot once its readers are done
+        const bool leader = elect_one();
+        uint32_t blk = 0;
+        bool ok = true;
+        for (int j = 0; ok && j < nt; j++) {
+            const bool pre = j < nt_pre;
+            const CUtensorMap *mk = pre ? &maps.k_pre : &maps.k_new, *mr = pre ? &maps.r_pre : &maps.r_new;
+            const CUtensorMap *mv = pre ? &maps.v_pre : &maps.v_new;
+            for (int i = 0; i < 5; i++, blk++) {
+                const uint32_t slot = slot_of(blk);
+                if (blk >= kSlots) {
+                    ok = __all_sync(0xffffffffu, spin_wait(&empty[slot], phase_of(blk - kSlots), abort_flag));
+                    if (!ok) break;
+                }
+                uint64_t *full = i < 3 ? &k_full[j & 1] : &v_full[j & 1];   // K and rotary blocks complete one phase, V's the other
+                if (leader) {
+                    if (i == 0 || i == 3) mbar_arrive_expect_tx(full, (i == 0 ? 3 : 2) * kBlockBytes);
+                    tma_load_3d(sbase + kOffRing + slot * kBlockBytes, i < 2 ? mk : i == 2 ? mr : mv,
+                                i == 1 || i == 4 ? 64 : 0, i == 2 ? 0 : head, tile_row(j), full);
+                }
+                __syncwarp();
+            }
+        }
+        if (!ok && leader) {
+            if (!*abort_flag) flag_error(a.err, kErrTimeout);
+            *abort_flag = 1;
+        }
+        // After an abort: request what is missing of the last K or V (its barrier counts whole
+        // ones; the slots' contents no longer matter), and wait until every copy has landed.
+        if (!ok) {
+            const uint32_t j = blk / 5;
+            const bool pre = (int)j < nt_pre;
+            for (uint32_t i = blk % 5; i != 0 && i != 3 && i < 5; i++) {
+                uint64_t *full = i < 3 ? &k_full[j & 1] : &v_full[j & 1];
+                const CUtensorMap *m = i < 2 ? (pre ? &maps.k_pre : &maps.k_new) : i == 2 ? (pre ? &maps.r_pre : &maps.r_new)
+                                                                                       : (pre ? &maps.v_pre : &maps.v_new);
+                if (leader)
+                    tma_load_3d(sbase + kOffRing + slot_of(5u * j + i) * kBlockBytes, m, i == 1 || i == 4 ? 64 : 0,
+                                i == 2 ? 0 : head, tile_row((int)j), full);
+                blk++;
+            }
+            for (uint32_t x = blk > 10 ? blk - 10 : 0; x < blk; x++) {
+                const uint32_t t = x / 5;
+                if (x % 5 == 0) mbar_wait_bounded(&k_full[t & 1], (t >> 1) & 1, kWaitLimitE, nullptr);
+                if (x % 5 == 3) mbar_wait_bounded(&v_full[t & 1], (t >> 1) & 1, kWaitLimitE, nullptr);
+            }
+        }
     } else if ((tid >> 7) < nwg) {
         // ---------------- softmax of this thread's query row
         const int w = tid >> 7;
@@ -280,7 +305,7 @@ __global__ void __launch_bounds__(kEThreads, 1)
         bool ok = true;
         for (int j = 0; j < nt; j++) {
             // S_w(j) done; its commit also covers O_w += P_w(j - 1) V(j - 1)
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&s_done[w], (uint32_t)(j & 1), kWaitLimitE, abort_flag));
+            ok = __all_sync(0xffffffffu, poll_wait(&s_done[w], (uint32_t)(j & 1), abort_flag));
             if (!ok) break;
             tc_fence_after();
             const bool pre = j < nt_pre;
@@ -369,21 +394,23 @@ __global__ void __launch_bounds__(kEThreads, 1)
             tc_st32(tmem + lane_base + colS, pw0);       // over scores 0 .. 31 (read already)
             tc_st32(tmem + lane_base + colS + 32, pw1);  // over scores 32 .. 63
             tc_wait_st();
-            // V(j) has landed; rows past the request's end (edge tiles only) become zeros.  Both
-            // warpgroups write them, each before its own product.
-            ok = __all_sync(0xffffffffu, spin_wait(v_full, (uint32_t)(j & 1), abort_flag));
-            if (!ok) break;
+            // Rows of V past the request's end (edge tiles only) become zeros once V(j) has
+            // landed.  Both warpgroups write them, each before its own product.
             const int there = (pre ? np : L) - base;   // rows of the tile that belong to the request
             if (there < kKeys) {
-                if ((tid & 127) >= there) {
-                    uint4 *z = reinterpret_cast<uint4 *>(smem + kOffV + (tid & 127) * 128);
+                const uint32_t blk = 5u * j + 3;
+                ok = spin_wait(&v_full[j & 1], (uint32_t)((j >> 1) & 1), abort_flag);
 #pragma unroll
-                    for (int c = 0; c < 8; c++) {
-                        z[c] = make_uint4(0u, 0u, 0u, 0u);
-                        z[kBlockBytes / 16 + c] = make_uint4(0u, 0u, 0u, 0u);
+                for (int i = 0; i < 2; i++) {
+                    uint4 *z = reinterpret_cast<uint4 *>(smem + kOffRing + slot_of(blk + i) * kBlockBytes + (tid & 127) * 128);
+                    if (ok && (tid & 127) >= there) {
+#pragma unroll
+                        for (int c = 0; c < 8; c++) z[c] = make_uint4(0u, 0u, 0u, 0u);
                     }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
             }
             tc_fence_before();
             mbar_arrive(&p_full[w]);
