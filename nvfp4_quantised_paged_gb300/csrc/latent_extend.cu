@@ -17,7 +17,7 @@
 //     ring that the load warp fills in the order K(j) K(j) R(j) V(j) V(j) K(j + 1) ...,
 //     each slot as soon as the products that read it are done (whole slots of one
 //     V and two K tiles left V's load on the critical path: 277 us against
-//     @@RING@@ us for 4 x 512 tokens over up to 8,192, 32 heads).  V's two blocks
+//     212 us for 4 x 512 tokens over up to 8,192, 32 heads).  V's two blocks
 //     need not be neighbours: O_w += P_w V runs as two N 64 products a step, which
 //     with P in TMEM cost what one of N 128 does (30 and 60 clocks);
 //   * rows of a V tile past the request's end are zeroed in shared memory before
@@ -25,6 +25,10 @@
 //     a probability of 0 would still be a NaN.
 // Bound by the tensor cores: 2 * (192 + 128) flops a (query, key, head), K and V
 // tiles shared by 256 queries through L2.  Every wait is bounded.
+#include <cooperative_groups.h>
+
+#include <mutex>
+
 #include "common.cuh"
 #include "extend_common.cuh"
 #include "kernels.h"
@@ -34,6 +38,8 @@
 namespace nvfp4kv {
 
 namespace {
+
+namespace cg = cooperative_groups;
 
 constexpr int kWGs = 2;
 constexpr int kQRows = 128;
@@ -53,6 +59,7 @@ constexpr int kOffTmem = kOffBar + kNumBars * 8;
 constexpr int kOffAbort = kOffTmem + 4;
 constexpr int kOffOrder = kOffBar + 256;       // int[256]: requests by decreasing prefix length
 constexpr int kOrderMax = 256;
+constexpr int kMaxSplit = 8;                   // CTAs of a cluster
 constexpr int kESmem = kOffOrder + 4 * kOrderMax;
 static_assert(kOffAbort + 4 <= kOffOrder && kESmem <= 227 * 1024, "shared memory of a CTA");
 // TMEM columns: S_w at 128w (FP32; P_w as BF16 pairs over its first 64 columns), O_w at 256 + 128w
@@ -70,6 +77,8 @@ struct ExtendArgs {
     uint16_t *out;                     // BF16 [total_q][H][128]
     unsigned *err;
 };
+
+constexpr int kMinTiles = 4;                   // K/V tiles a CTA of a cluster has at least, on average
 
 // K/V as 3-D maps [rows][heads][128] (any strides), the rotary rows as [rows][1][64]; boxes of 64 x 1 x 128.
 struct ExtendMaps {
@@ -126,12 +135,16 @@ __global__ void __launch_bounds__(kEThreads, 1)
         if (first_cta) flag_error(a.err, kErrSeqLen);
         L = a.max_q_len;
     }
-    const int row0 = blockIdx.x * kCtaRows;
-    if (row0 >= L) return;
+    // A cluster of C CTAs shares the query rows; each takes a contiguous part of the K/V tiles.
+    cg::cluster_group cluster = cg::this_cluster();
+    const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int row0 = (int)(blockIdx.x / C) * kCtaRows;
+    if (row0 >= L) return;                                      // (all of the cluster)
     const int nwg = row0 + kQRows < L ? 2 : 1;                  // query tiles holding rows
     const int t_last = min(row0 + kCtaRows, L) - 1;             // last chunk token of this CTA
     const int nt_pre = (np + kKeys - 1) / kKeys;
-    const int nt = nt_pre + t_last / kKeys + 1;
+    const int nt_all = nt_pre + t_last / kKeys + 1;
+    const int j0 = (int)((int64_t)nt_all * rank / C), nt = (int)((int64_t)nt_all * (rank + 1) / C) - j0;
     const uint32_t sbase = smem_u32(smem);
 
     // ---- query tiles: 128 rows x 24 chunks of 16 bytes each, by their warpgroups
@@ -218,12 +231,12 @@ __global__ void __launch_bounds__(kEThreads, 1)
             // (issued as they became ready, the two fell into step and left it idle meanwhile).
             // S_w(t + 1) goes over the columns of P_w(t) and waits for the product that reads
             // it; whether the next K and V have landed is checked while that product runs.
-            bool ok = wait(&k_full[0], 0);
-            if (ok) {
+            bool ok = nt == 0 || wait(&k_full[0], 0);
+            if (ok && nt > 0) {
                 mma_s(0, 0);
                 if (nwg > 1) mma_s(1, 0);
             }
-            ok = ok && wait(&v_full[0], 0);
+            ok = ok && (nt == 0 || wait(&v_full[0], 0));
             for (uint32_t t = 0, blk = 0; ok && t < (uint32_t)nt; t++, blk += 5) {
                 const bool more = t + 1 < (uint32_t)nt;
 #pragma unroll
@@ -252,7 +265,7 @@ __global__ void __launch_bounds__(kEThreads, 1)
         uint32_t blk = 0;
         bool ok = true;
         for (int j = 0; ok && j < nt; j++) {
-            const bool pre = j < nt_pre;
+            const bool pre = j0 + j < nt_pre;
             const CUtensorMap *mk = pre ? &maps.k_pre : &maps.k_new, *mr = pre ? &maps.r_pre : &maps.r_new;
             const CUtensorMap *mv = pre ? &maps.v_pre : &maps.v_new;
             for (int i = 0; i < 5; i++, blk++) {
@@ -265,7 +278,7 @@ __global__ void __launch_bounds__(kEThreads, 1)
                 if (leader) {
                     if (i == 0 || i == 3) mbar_arrive_expect_tx(full, (i == 0 ? 3 : 2) * kBlockBytes);
                     tma_load_3d(sbase + kOffRing + slot * kBlockBytes, i < 2 ? mk : i == 2 ? mr : mv,
-                                i == 1 || i == 4 ? 64 : 0, i == 2 ? 0 : head, tile_row(j), full);
+                                i == 1 || i == 4 ? 64 : 0, i == 2 ? 0 : head, tile_row(j0 + j), full);
                 }
                 __syncwarp();
             }
@@ -278,14 +291,14 @@ __global__ void __launch_bounds__(kEThreads, 1)
         // ones; the slots' contents no longer matter), and wait until every copy has landed.
         if (!ok) {
             const uint32_t j = blk / 5;
-            const bool pre = (int)j < nt_pre;
+            const bool pre = j0 + (int)j < nt_pre;
             for (uint32_t i = blk % 5; i != 0 && i != 3 && i < 5; i++) {
                 uint64_t *full = i < 3 ? &k_full[j & 1] : &v_full[j & 1];
                 const CUtensorMap *m = i < 2 ? (pre ? &maps.k_pre : &maps.k_new) : i == 2 ? (pre ? &maps.r_pre : &maps.r_new)
                                                                                        : (pre ? &maps.v_pre : &maps.v_new);
                 if (leader)
                     tma_load_3d(sbase + kOffRing + slot_of(5u * j + i) * kBlockBytes, m, i == 1 || i == 4 ? 64 : 0,
-                                i == 2 ? 0 : head, tile_row((int)j), full);
+                                i == 2 ? 0 : head, tile_row(j0 + (int)j), full);
                 blk++;
             }
             for (uint32_t x = blk > 10 ? blk - 10 : 0; x < blk; x++) {
@@ -308,8 +321,8 @@ __global__ void __launch_bounds__(kEThreads, 1)
             ok = __all_sync(0xffffffffu, poll_wait(&s_done[w], (uint32_t)(j & 1), abort_flag));
             if (!ok) break;
             tc_fence_after();
-            const bool pre = j < nt_pre;
-            const int base = pre ? j * kKeys : (j - nt_pre) * kKeys;
+            const bool pre = j0 + j < nt_pre;
+            const int base = pre ? (j0 + j) * kKeys : (j0 + j - nt_pre) * kKeys;
             const int visible = (pre ? np : token + 1) - base;   // keys [0, visible) of the tile are seen
             const bool edge = __any_sync(0xffffffffu, visible < kKeys);  // mask on edge tiles only
             // the row's 64 scores of half h (masked scores are -inf)
@@ -353,6 +366,9 @@ __global__ void __launch_bounds__(kEThreads, 1)
             // half 1 shows whether the max must move; only then does it go over the
             // scores in TMEM.  If it must (the first tile, rarely later), O and the
             // row sum are rescaled and P is formed again from the scores in TMEM.
+            // (a row that has seen no key yet, its part of the tiles lying behind it, has the
+            // maximum -inf: its probabilities are 2^(-inf - 0) = 0)
+            auto neg_m = [&]() { return m_run == kNegInfE ? 0.f : -m_run; };
             uint32_t pw0[32], pw1[32];
             float ls[4] = {0.f, 0.f, 0.f, 0.f};
             float smax;
@@ -360,13 +376,13 @@ __global__ void __launch_bounds__(kEThreads, 1)
                 float sc[64];
                 load_half(0, sc);
                 smax = half_max(sc);
-                make_p(sc, -m_run, pw0, ls);
+                make_p(sc, neg_m(), pw0, ls);
                 load_half(1, sc);
                 smax = fmaxf(smax, half_max(sc));
                 const float mx = smax * a.score_log2;  // the scale is positive
                 const bool need = mx > m_run + kRescale;
                 if (!__any_sync(0xffffffffu, need)) {
-                    make_p(sc, -m_run, pw1, ls);
+                    make_p(sc, neg_m(), pw1, ls);
                 } else {
                     const float m_new = need ? fmaxf(m_run, mx) : m_run;
                     const float alpha = need ? (m_run == kNegInfE ? 0.f : ex2(m_run - m_new)) : 1.f;
@@ -385,9 +401,9 @@ __global__ void __launch_bounds__(kEThreads, 1)
                     l_run *= alpha;
                     m_run = m_new;
                     ls[0] = ls[1] = ls[2] = ls[3] = 0.f;
-                    make_p(sc, -m_run, pw1, ls);
+                    make_p(sc, neg_m(), pw1, ls);
                     load_half(0, sc);
-                    make_p(sc, -m_run, pw0, ls);
+                    make_p(sc, neg_m(), pw0, ls);
                 }
             }
             l_run += (ls[0] + ls[1]) + (ls[2] + ls[3]);
@@ -415,12 +431,38 @@ __global__ void __launch_bounds__(kEThreads, 1)
             tc_fence_before();
             mbar_arrive(&p_full[w]);
         }
-        if (ok)
+        if (ok && nt > 0)
             ok = __all_sync(0xffffffffu,
                             mbar_wait_bounded(&pv_done[w], (uint32_t)((nt - 1) & 1), kWaitLimitE, abort_flag));
+        // (a part goes over the ring, which the other query tile's last product may still read)
+        if (ok && nt > 0 && C > 1 && nwg > 1)
+            ok = __all_sync(0xffffffffu,
+                            mbar_wait_bounded(&pv_done[1 - w], (uint32_t)((nt - 1) & 1), kWaitLimitE, abort_flag));
         if (!ok) {
             *abort_flag = 1;
             if (lane == 0) flag_error(a.err, kErrTimeout);
+        } else if (C > 1) {
+            // ---- this CTA's part: FP32 rows over the ring (16-byte chunk c of row r at c ^ (r % 32)), (m, l) over Q
+            tc_fence_after();
+            const int r = w * kQRows + (tid & 127);
+            reinterpret_cast<float2 *>(smem + kOffQ)[r] = make_float2(m_run, l_run);
+            float4 *row = reinterpret_cast<float4 *>(smem + kOffRing) + r * 32;
+#pragma unroll
+            for (int cblk = 0; cblk < 4; cblk++) {
+                uint32_t ov[32];
+                if (nt > 0) {
+                    tc_ld32(tmem + lane_base + colO + 32 * cblk, ov);
+                    tc_wait_ld();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; e++) ov[e] = 0;
+                }
+#pragma unroll
+                for (int e = 0; e < 8; e++)
+                    row[(8 * cblk + e) ^ (r & 31)] =
+                        make_float4(__uint_as_float(ov[4 * e]), __uint_as_float(ov[4 * e + 1]),
+                                    __uint_as_float(ov[4 * e + 2]), __uint_as_float(ov[4 * e + 3]));
+            }
         } else {
             // ---- O / l -> BF16 row of the output
             tc_fence_after();
@@ -450,6 +492,39 @@ __global__ void __launch_bounds__(kEThreads, 1)
     tc_fence_before();
     __syncthreads();
     if (warp == 0) tc_dealloc(tmem, kTmemCols);
+    if (C > 1) {
+        // ---- join the parts: this CTA the rank-th share of the rows, a warp per row, lane l dims 4l .. 4l + 3
+        cluster.sync();
+        const int nrows = min(kCtaRows, L - row0);
+        if (warp < kSoftThreads / 32) {
+            for (int r = kCtaRows / C * rank + warp; r < min(nrows, kCtaRows / C * (rank + 1)); r += kSoftThreads / 32) {
+                float2 ml = make_float2(kNegInfE, 0.f);
+                if (lane < C) ml = cluster.map_shared_rank(reinterpret_cast<float2 *>(smem + kOffQ), lane)[r];
+                float mx = ml.x;
+#pragma unroll
+                for (int x = kMaxSplit / 2; x; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+                mx = __shfl_sync(0xffffffffu, mx, 0);
+                const float f = ml.x == kNegInfE ? 0.f : ex2(ml.x - mx);
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                float l = 0.f;
+                for (int c = 0; c < C; c++) {
+                    const float4 v = (cluster.map_shared_rank(reinterpret_cast<float4 *>(smem + kOffRing), c) + r * 32)[lane ^ (r & 31)];
+                    const float fc = __shfl_sync(0xffffffffu, f, c);
+                    l += fc * __shfl_sync(0xffffffffu, ml.y, c);
+                    acc.x += fc * v.x;
+                    acc.y += fc * v.y;
+                    acc.z += fc * v.z;
+                    acc.w += fc * v.w;
+                }
+                const float inv = 1.f / l;
+                const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+                const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+                reinterpret_cast<uint2 *>(a.out + (((int64_t)q0 + row0 + r) * a.H + head) * kHeadDim)[lane] =
+                    make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+            }
+        }
+        cluster.sync();   // no CTA leaves while its part may be read
+    }
 }
 
 // [rows][heads][width] BF16 at `base` (strides in elements) as a 3-D map with 64 x 1 x 128 boxes.
@@ -474,17 +549,37 @@ cudaError_t launch_latent_extend(const void *q, const void *k_prefix, const void
                                  int64_t new_head, const void *rope_chunk, const int32_t *cu_q, int64_t total_q,
                                  int num_reqs, int max_q_len, int num_heads, float sm_scale, void *out, unsigned *err,
                                  cudaStream_t stream) {
+    static std::mutex mu;
     static bool attr_set[64] = {};
+    static int waves[64][3];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::unique_lock<std::mutex> lock(mu);
     if (!attr_set[dev]) {
         e = cudaFuncSetAttribute(reinterpret_cast<const void *>(&latent_extend_kernel),
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, kESmem);
         if (e != cudaSuccess) return e;
+        // clusters of 2, 4 and 8 CTAs that the device holds at once
+        for (int k = 0; k < 3; k++) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(2u << k);
+            cfg.blockDim = dim3(kEThreads);
+            cfg.dynamicSmemBytes = kESmem;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = 2u << k;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&waves[dev][k], reinterpret_cast<const void *>(&latent_extend_kernel), &cfg);
+            if (e != cudaSuccess) return e;
+        }
         attr_set[dev] = true;
     }
+    lock.unlock();
     ExtendMaps maps;
     if (!make_map(&maps.k_new, k_chunk, total_q, num_heads, kHeadDim, new_token, new_head) ||
         !make_map(&maps.v_new, v_chunk, total_q, num_heads, kHeadDim, new_token, new_head) ||
@@ -510,9 +605,30 @@ cudaError_t launch_latent_extend(const void *q, const void *k_prefix, const void
     a.score_log2 = (float)((double)sm_scale * 1.4426950408889634);
     a.out = static_cast<uint16_t *>(out);
     a.err = err;
-    dim3 grid((unsigned)ceil_div64(max_q_len, kCtaRows), (unsigned)num_heads, (unsigned)num_reqs);
-    latent_extend_kernel<<<grid, kEThreads, kESmem, stream>>>(maps, a);
-    return cudaGetLastError();
+    const int64_t qtiles = ceil_div64(max_q_len, kCtaRows), ctas = qtiles * num_heads * num_reqs;
+    const int64_t tiles = (total_prefix + (total_q < (int64_t)num_reqs * max_q_len ? total_q : (int64_t)num_reqs * max_q_len)) /
+                          num_reqs / kKeys;   // K/V tiles of an average request
+    // Clusters share the K/V tiles of a CTA while the grid stays one wave of them: 32 heads x 2
+    // query tiles of one request over 8,192 tokens take 148 us as 64 CTAs and 88 us as 64
+    // clusters of two (157 us as 64 of four, which are two waves); 256 CTAs that are two waves
+    // already take 219 us either way.
+    int split = 1;
+    for (int k = 0; k < 3; k++)
+        if (ctas <= waves[dev][k] && tiles >= (kMinTiles << (k + 1))) split = 2 << k;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(qtiles * split), (unsigned)num_heads, (unsigned)num_reqs);
+    cfg.blockDim = dim3(kEThreads);
+    cfg.dynamicSmemBytes = kESmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    void *args[] = {&maps, &a};
+    return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(&latent_extend_kernel), args);
 }
 
 }  // namespace nvfp4kv
