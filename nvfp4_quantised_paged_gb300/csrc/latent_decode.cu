@@ -16,19 +16,28 @@
 // exact for g = 1 above 2^-29 of its largest value) and into the output; the
 // rotary steps are BF16 into the same accumulator.
 //
-// One CTA per SM.  Eight warps do everything but issue the products:
-//   * warp w holds the raw bytes of the tile's w-th 16-token group in registers
-//     (13 16-byte loads a lane, requested a whole tile ahead, straight from the
-//     page) and expands them into the tile, two column blocks at a time: pair i as
-//     soon as O += of row block i of the previous tile has read it;
-//   * then they run the softmax of the 128 x N scores, one token a thread, the two
-//     warpgroups taking half the heads each: base 2 with a lazily moved maximum per
-//     head (a vote over the warpgroup; O^T is rescaled only when a score exceeds the
-//     maximum by 2^8), P = 2^(s - m + 7) in FP16 (the offset uses FP16's upper
-//     range: weights down to 2^-21 of the largest keep full precision) over the
-//     rotary tile, whose product is done; the row sums of the rounded P stay in
-//     registers, one (token, head) each, until the sequence ends.
-// One thread of warp 8 issues S^T as the pairs arrive and O^T per row block.
+// One CTA per SM.  Sixteen warps do everything but issue the products:
+//   * expanding: two warps per 16-token group, taking every other column block; lane (r,
+//     q) holds the raw bytes of block q (16 dims) of rows r and r + 8, loaded straight from
+//     the page in contiguous pieces, each requested again for the next tile as soon as it
+//     is used.  A block goes to the tile in shared memory, as soon as the previous tile's
+//     O^T row block that reads it is done, and to TMEM as the A operand of S^T (all
+//     column blocks up to 32 heads, four with 64; the rotary part to TMEM alone): an A
+//     operand in shared memory costs a product 4 KB of reads, at least 38 clocks at any
+//     N, one in TMEM 9 at N = 16, and shared memory's bandwidth is what bounds the tile.
+//     The store to TMEM takes a quad's registers as four columns each, so the dims of a
+//     column block lie there in another order (position 16 k + 4 q + e holds dim 16 q + 4
+//     k + e), and those of Q's blocks with them;
+//   * softmax: one token (= TMEM lane) a thread, the four warpgroups taking a quarter of
+//     the heads each: base 2 with a lazily moved maximum per head (a vote over the
+//     warpgroup; O^T is rescaled only when a score exceeds the maximum by 2^8), P =
+//     2^(s - m + 7) in FP16 (the offset uses FP16's upper range: weights down to 2^-21 of
+//     the largest keep full precision); the row sums of the rounded P stay in registers
+//     until the sequence ends.
+// One warp issues S^T a pair of column blocks at a time as they arrive, and O^T per row
+// block.  Separate warps for expanding and softmax, eight each, took longer: every step
+// of the chain (expand, S^T, softmax, O^T) slows down, and there is no room in shared
+// memory for a second tile that would let them overlap.
 //
 // Split: the batch's 128-token tiles form one flat range, cut equally over the
 // CTAs of a head tile (64 heads).  A sequence that lies in one CTA is normalised
@@ -47,35 +56,37 @@ namespace nvfp4kv {
 
 namespace {
 
-constexpr int kWorkers = 256;                 // expanding and softmax threads
+constexpr int kWorkers = 512;                 // warps 0 .. 15
 constexpr int kLThreads = kWorkers + 128;     // + the MMA warp's warpgroup (its other warps only meet the last barrier)
-// Launched with 168 registers a thread; the two working warpgroups then take 216
-// and the third gives back down to 72: 2 x 128 x 216 + 128 x 72 = 384 x 168.
-constexpr int kWorkRegs = 216, kMmaRegs = 72;
-static_assert(2 * 128 * kWorkRegs + 128 * kMmaRegs <= kLThreads * 168, "register split must fit the launch");
+// Launched with 96 registers a thread; then 512 x 104 + 128 x 64 = 640 x 96.
+constexpr int kWorkRegs = 104, kMmaRegs = 64;
+static_assert(kWorkers * kWorkRegs + 128 * kMmaRegs <= kLThreads * 96, "register split must fit the launch");
 constexpr int kTile = 128;                    // tokens per tile
 constexpr int kColBlock = kTile * 128;        // bytes of one column block (64 dims) of the tile
 constexpr int kTileBytes = 8 * kColBlock;
-constexpr uint32_t kWaitLimitL = 1u << 22;
+constexpr uint32_t kWaitLimitL = 1u << 24;
 constexpr float kNegInfL = -__builtin_huge_valf();
 constexpr float kRescaleL = 8.0f;
 constexpr float kPOffset = 7.0f;              // P = 2^(s - m + 7): at most 2^15
-constexpr int kNumBarsL = 12;                 // kv_full[5] s_done p_full pv_done[4] drain
 
 template <int N>
 struct LSmem {
+    static constexpr int kTmemCbs = N == 64 ? 4 : 8;      // column blocks of S^T's A operand that lie in TMEM
     static constexpr int kQBlock = N * 128;               // one column block of Q, [N][64]
     static constexpr int kQ = 0;                          // 8 FP16 blocks + the BF16 rotary block
-    static constexpr int kKV = 9 * kQBlock;
-    static constexpr int kRope = kKV + kTileBytes;        // BF16 [128][64]; P over it: FP16 [128 tokens][N]
-    static constexpr int kBar = kRope + kColBlock;
-    static constexpr int kMisc = kBar + kNumBarsL * 8;    // tmem base, abort
-    static constexpr int kM = kMisc + 16;                 // float m[N], fac[N], alpha[N]
-    static constexpr int kWarpMax = kM + 3 * N * 4;       // float [2][4][N / 2]
-    static constexpr int kWarpSum = kWarpMax + 4 * N * 4; // float [2][4][N / 2]
-    static constexpr int kBytes = kWarpSum + 4 * N * 4;
-    static constexpr uint32_t kCols = N == 64 ? 512 : N == 32 ? 256 : 128;   // O at 0 .. 4N, S at 4N .. 5N
-    static_assert(kKV % 1024 == 0 && kRope % 1024 == 0, "operand tiles need 1024-byte alignment");
+    static constexpr int kKV = 9 * kQBlock;               // the tile
+    static constexpr int kP = kKV + kTileBytes;           // FP16 [128 tokens][64], N heads used
+    static constexpr int kBar = kP + kColBlock;
+    static constexpr int kNumBars = 9;                    // kv_full[2] s_done p_full pv_done[4] drain
+    static constexpr int kMisc = kBar + kNumBars * 8;     // tmem base, abort
+    static constexpr int kM = (kMisc + 8 + 15) & ~15;     // float m[N], fac[N], alpha[N]
+    static constexpr int kWarpMax = kM + 3 * N * 4;       // float [4][4][N / 4]: warps' maxima, and row sums at the end
+    static constexpr int kBytes = kWarpMax + 4 * N * 4;
+    // TMEM columns
+    static constexpr uint32_t kColS = 4 * N, kColR = 5 * N, kColK = kColR + 32;   // O at 0
+    static constexpr uint32_t kCols = 512;
+    static_assert(kColK + 32 * kTmemCbs <= kCols, "TMEM columns");
+    static_assert(kKV % 1024 == 0 && kP % 1024 == 0, "operand tiles need 1024-byte alignment");
     static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
     static_assert(sizeof(FlatScratch<kLThreads>) <= kTileBytes, "the plan's scratch lies in the tile");
 };
@@ -96,10 +107,11 @@ struct LatentArgs {
     unsigned *err;
 };
 
+// Bounded wait that polls without suspending the thread (these waits are on the critical path).
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, const volatile int *abort_flag) {
     for (uint32_t n = 0; n < kWaitLimitL; n++) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if (*abort_flag) return false;
+        if (mbar_test_wait(bar, parity)) return true;
+        if ((n & 63) == 63 && *abort_flag) return false;
     }
     return false;
 }
@@ -107,7 +119,7 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, const v
 // The tiles of a CTA's range in order.
 struct TileIter {
     int b, t, nt, n;
-    int64_t left;   // tiles of the range from this one on
+    int left;       // tiles of the range from this one on
 };
 
 __device__ __forceinline__ void set_seq(const LatentArgs &a, TileIter &it) {
@@ -134,9 +146,9 @@ __device__ __forceinline__ void add_f16x2(float &s0, float &s1, uint32_t w) {
         : "r"(w), "h"(one));
 }
 
-// Barriers 1 and 2: the warpgroups; 3: both.
+// Barriers 1 .. 4: the working warpgroups; 5: all of them.
 __device__ __forceinline__ void group_sync(int wg) { asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory"); }
-__device__ __forceinline__ void workers_sync() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
+__device__ __forceinline__ void workers_sync() { asm volatile("bar.sync 5, 512;" ::: "memory"); }
 
 __device__ __forceinline__ bool group_any(int wg, bool p) {
     uint32_t r;
@@ -153,7 +165,7 @@ __device__ __forceinline__ int ordered(float x) {
 }
 __device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
 
-// v[c] (c < CW <= 32) summed over the warp's lanes: lane c returns column c's sum (lanes >= CW: a copy of c % CW's)
+// v[c] (c < CW <= 16) summed over the warp's lanes: lane c returns column c's sum (lanes >= CW: a copy of c % CW's)
 template <int CW>
 __device__ __forceinline__ float column_sums(float (&v)[CW], int lane) {
 #pragma unroll
@@ -176,10 +188,10 @@ __device__ __forceinline__ float column_sums(float (&v)[CW], int lane) {
 template <int N>
 __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs a) {
     using L = LSmem<N>;
-    constexpr int CW = N / 2;                     // heads per warpgroup
+    constexpr int CW = N / 4;                     // heads per warpgroup
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBar);
-    uint64_t *kv_full = bars, *s_done = bars + 5, *p_full = bars + 6, *pv_done = bars + 7, *drain = bars + 11;
+    uint64_t *kv_full = bars, *s_done = bars + 2, *p_full = bars + 3, *pv_done = bars + 4, *drain = bars + 8;
     uint32_t &tmem_base = *reinterpret_cast<uint32_t *>(smem + L::kMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 4);
     float *s_m = reinterpret_cast<float *>(smem + L::kM), *s_fac = s_m + N, *s_alpha = s_fac + N;
@@ -204,12 +216,13 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
     TileIter it;
     it.b = b0;
     it.t = (int)(u0 - first);
-    it.left = u1 - u0;
+    it.left = (int)(u1 - u0);   // (the host refuses 2^31 tiles)
     set_seq(a, it);
 
-    if (warp == 8) tc_alloc(&tmem_base, L::kCols);
+    if (warp == 16) tc_alloc(&tmem_base, L::kCols);
     if (tid == 0) {
-        for (int i = 0; i < kNumBarsL; i++) mbar_init(&bars[i], i < 5 || i == 6 ? kWorkers / 32 : 1);
+        for (int i = 0; i < L::kNumBars; i++)
+            mbar_init(&bars[i], i < 2 || i == 3 ? kWorkers / 32 : 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -217,61 +230,67 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base, sbase = smem_u32(smem);
-    constexpr uint32_t kColS = 4 * N;
-
-    if (warp >= 8) {
-        // ---------------- the MMA thread
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
+    if (warp >= 16) {
+        // ---------------- the MMA warp
         // The whole warp runs the loop and one elected lane issues, so that the compiler
         // sees the descriptors as uniform values: a product issued under a divergent
         // branch cost 70 to 110 clocks, more than the products themselves (38 at N = 16,
         // 47 at N = 64).
-        if (warp == 8) {
-            bool ok = true;
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
+        if (warp == 16) {
             constexpr uint32_t idesc_s = idesc_f16_f32(128, N, false), idesc_r = idesc_bf16_f32(128, N, false);
             constexpr uint32_t idesc_o = idesc_a_mn_major(idesc_f16_f32(128, N, true));
-            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            auto uniform = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
+            const uint32_t tm = uniform(tmem);
             const bool leader = elect_one();
             // operand descriptors; a step adds its byte offset / 16 to the address field
             const uint64_t dC = smem_desc_sw128(sbase + L::kKV, 16, 1024), dQ = smem_desc_sw128(sbase + L::kQ, 16, 1024);
-            const uint64_t dR = smem_desc_sw128(sbase + L::kRope, 16, 1024);   // rotary tile, and P over it
-            const uint64_t dV = smem_desc_sw128(sbase + L::kKV, kColBlock, 1024);
-            bool fresh = true;   // the tile is the range's first of its sequence
-            for (uint32_t j = 0; it.left > 0; j++) {
+            const uint64_t dP = smem_desc_sw128(sbase + L::kP, 16, 1024), dV = smem_desc_sw128(sbase + L::kKV, kColBlock, 1024);
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                const bool good = __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag));
+                tc_fence_after();
+                return good;
+            };
+            const uint32_t n = (uint32_t)it.left;
+            bool fresh = true, ok = true;   // fresh: the tile is the range's first of its sequence
+            for (uint32_t j = 0; j < n; j++) {
 #pragma unroll 1
-                for (uint32_t i = 0; i < 4; i++) {
-                    ok = ok && wait_bar(&kv_full[i], j & 1, abort_flag);
-                    tc_fence_after();
+                for (uint32_t i = 0; i < 4; i++) {   // column blocks 2 i, 2 i + 1 (and the rotary part, with the first)
+                    if (!(i & 1)) ok = ok && wait(&kv_full[i >> 1], j & 1);
+                    if (!ok) break;
+                    const uint64_t q = dQ + i * (2 * L::kQBlock / 16), c = dC + i * (2 * kColBlock / 16);
+                    const uint32_t t = tm + L::kColK + 64 * i;
                     if (leader) {
-                        const uint64_t dCi = dC + i * (2 * kColBlock / 16), dQi = dQ + i * (2 * L::kQBlock / 16);
+                        if (i == 0) {
 #pragma unroll
-                        for (int kk = 0; kk < 8; kk++) {
-                            const uint32_t half = kk >> 2, sub = (uint32_t)(kk & 3) * 2;
-                            tc_mma_bf16(tm + kColS, dCi + (half * (kColBlock / 16) + sub), dQi + (half * (L::kQBlock / 16) + sub),
-                                        idesc_s, i > 0 || kk > 0);
+                            for (int kk = 0; kk < 4; kk++)
+                                tc_mma_bf16_tmem_a(tm + L::kColS, tm + L::kColR + kk * 8, dQ + (8 * L::kQBlock / 16 + kk * 2),
+                                                   idesc_r, kk > 0);
                         }
+                        if (L::kTmemCbs == 8 || 2 * i < L::kTmemCbs) {
+#pragma unroll
+                            for (int kk = 0; kk < 8; kk++)
+                                tc_mma_bf16_tmem_a(tm + L::kColS, t + kk * 8,
+                                                   q + ((kk >> 2) * (L::kQBlock / 16) + (kk & 3) * 2), idesc_s, 1u);
+                        } else {
+#pragma unroll
+                            for (int kk = 0; kk < 8; kk++)
+                                tc_mma_bf16(tm + L::kColS, c + ((kk >> 2) * (kColBlock / 16) + (kk & 3) * 2),
+                                            q + ((kk >> 2) * (L::kQBlock / 16) + (kk & 3) * 2), idesc_s, 1u);
+                        }
+                        if (i == 3) tc_commit(s_done);
                     }
                 }
-                ok = ok && wait_bar(&kv_full[4], j & 1, abort_flag);
-                tc_fence_after();
-                if (leader) {
-#pragma unroll
-                    for (int kk = 0; kk < 4; kk++)
-                        tc_mma_bf16(tm + kColS, dR + kk * 2, dQ + (8 * L::kQBlock / 16 + kk * 2), idesc_r, 1u);
-                    tc_commit(s_done);
-                }
-                ok = ok && wait_bar(p_full, j & 1, abort_flag);
-                tc_fence_after();
-                if (!__all_sync(0xffffffffu, ok)) break;
+                ok = ok && wait(p_full, j & 1);
+                if (!ok) break;
                 if (leader) {
                     const uint32_t acc = fresh ? 0u : 1u;
 #pragma unroll 1
                     for (uint32_t mb = 0; mb < 4; mb++) {
-                        const uint64_t dVm = dV + mb * (2 * kColBlock / 16);
+                        const uint64_t v = dV + mb * (2 * kColBlock / 16);
 #pragma unroll
                         for (int kk = 0; kk < 8; kk++)   // 16 tokens: 2,048 bytes of a column block, and of P
-                            tc_mma_bf16(tm + mb * N, dVm + kk * 128, dR + kk * 128, idesc_o,
-                                        kk > 0 ? 1u : acc);
+                            tc_mma_bf16(tm + mb * N, v + kk * 128, dP + kk * 128, idesc_o, kk > 0 ? 1u : acc);
                         tc_commit(&pv_done[mb]);
                     }
                 }
@@ -279,7 +298,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
                 next_tile(a, it);
                 fresh = it.b != b;
             }
-            if (!__all_sync(0xffffffffu, ok) && leader) {
+            if (!ok && leader) {
                 if (!*abort_flag) flag_error(a.err, kErrTimeout);
                 *abort_flag = 1;
                 tc_commit(drain);   // no product may still read the CTA's memory when it ends
@@ -288,7 +307,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
         }
         __syncwarp();
     } else {
-        // ---------------- expanding and softmax warps
+        // ---------------- expanding and softmax
         // A wait that gave up sets the abort flag, which ends every other wait; the
         // warps then still run through their tiles (on meaningless values), so that
         // no barrier is left short of a warp.
@@ -298,150 +317,212 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
                 *abort_flag = 1;
                 flag_error(a.err, kErrTimeout);
             }
+            __syncwarp();
         };
-        const int wg = warp >> 2, row = 32 * (warp & 3) + lane;   // softmax: this thread's token (TMEM lane)
+        const int wg = warp >> 2, row = 32 * (warp & 3) + lane;   // softmax: head quarter, token
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-        const int er = lane >> 1, hb = lane & 1;                  // expanding: row of the group, half of a column block
-        uint4 code[8], scl, rope[4];
-        auto page_of = [&](const TileIter &x) -> int32_t {        // page of this warp's group (-1: none)
-            const int t = x.t * kTile + 16 * warp;
+        // expanding: group grp of the tile (its TMEM lanes are this warp's to reach), column blocks 2 i + par, rows
+        // er and er + 8, 16-value block eq of a column block
+        const int grp = 2 * (warp & 3) + (wg & 1), par = wg >> 1, er = lane >> 2, eq = lane & 3;
+        const uint32_t glanes = (uint32_t)(16 * grp) << 16;
+        uint2 raw[4][2];
+        uint4 scl[2], rope[2];
+        auto page_of = [&](const TileIter &x) -> int32_t {        // page of the group (-1: none)
+            const int t = x.t * kTile + 16 * grp;
             if (x.left <= 0 || t >= x.n) return -1;
             return __ldg(a.block_table + (int64_t)x.b * a.max_pages + (t >> a.log2P));
         };
-        auto load_tile = [&](const TileIter &x, int32_t page) {
-            const int t = x.t * kTile + 16 * warp;
-            const bool there = x.left > 0 && t < x.n;
-            const bool good = there && page >= 0 && page < a.num_pages;
-            if (there && !good && lane == 0) flag_error(a.err, kErrPage);
-            const uint8_t *grp = a.pool + (int64_t)(good ? page : 0) * ((int64_t)kLatentRow * a.P) +
-                                 (int64_t)((t & (a.P - 1)) >> 4) * kLatentGroup;
-            const bool rok = good && t + er < x.n;
-#pragma unroll
-            for (int cb = 0; cb < 8; cb++)
-                code[cb] = rok ? __ldg(reinterpret_cast<const uint4 *>(grp + cb * 512 + lane * 16)) : make_uint4(0, 0, 0, 0);
-            scl = rok ? __ldg(reinterpret_cast<const uint4 *>(grp + kLatentScales + lane * 16)) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int x4 = 0; x4 < 4; x4++)
-                rope[x4] = good && t + 4 * x4 + (lane >> 3) < x.n
-                               ? __ldg(reinterpret_cast<const uint4 *>(grp + kLatentRope + x4 * 512 + lane * 16))
-                               : make_uint4(0, 0, 0, 0);
-        };
-        TileIter nx = it;                       // the tile whose bytes are requested next
-        load_tile(nx, page_of(nx));
-        next_tile(a, nx);
-        int32_t npage = page_of(nx);            // its page, requested a tile earlier still
-        bool fresh = true;
-        int t_begin = it.t;                     // first tile of the current sequence in this range
-        float l[CW];
-        for (uint32_t j = 0; it.left > 0; j++) {
-            if (fresh) {
-                // ---- Q of the sequence: one warp per head, FP16 latent blocks and the BF16 rotary block
-                // (S of the previous sequence is done: its scores were read)
-                for (int hh = warp; hh < N; hh += 8) {
-                    const int h = h0 + hh;
-                    uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
-                    uint32_t xr = 0;
-                    if (h < a.H) {
-                        const int64_t at = (int64_t)it.b * a.H + h;
-                        const uint4 *src = reinterpret_cast<const uint4 *>(a.ql + at * kLatentDim) + lane * 2;
-                        x0 = __ldg(src);
-                        x1 = __ldg(src + 1);
-                        xr = __ldg(reinterpret_cast<const uint32_t *>(a.qr + at * kRopeDim) + lane);
-                    }
-                    const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-                    uint32_t ml = 0, mr = xr & 0x7fff7fffu;
-#pragma unroll
-                    for (int e = 0; e < 8; e++) ml = max_u16x2(ml, w[e] & 0x7fff7fffu);
-                    ml = __reduce_max_sync(0xffffffffu, max(ml >> 16, ml & 0xffffu));
-                    mr = __reduce_max_sync(0xffffffffu, max(mr >> 16, mr & 0xffffu));
-                    // 2^kq puts the largest |q g| into [2^14, 2^15), the rotary part below 2^127
-                    const uint32_t top = __float_as_uint(__uint_as_float(ml << 16) * a.g);
-                    int kq = top ? 14 - ((int)(top >> 23) - 127) : 0;
-                    kq = min(min(126, max(-126, kq)), 126 - ((int)(mr >> 7) - 127));
-                    kq = max(-126, kq);
-                    const float sc = __uint_as_float((uint32_t)(kq + 127) << 23);
-                    uint32_t f[8];
-#pragma unroll
-                    for (int e = 0; e < 8; e++)
-                        f[e] = f32x2_to_f16x2(bf16_hi(w[e]) * a.g * sc, bf16_lo(w[e]) * a.g * sc);
-                    uint8_t *q = smem + L::kQ + (lane >> 2) * L::kQBlock;      // lane: dims 16 lane .. 16 lane + 15
-                    *reinterpret_cast<uint4 *>(q + sw128_off(hh, (lane & 3) * 2)) = make_uint4(f[0], f[1], f[2], f[3]);
-                    *reinterpret_cast<uint4 *>(q + sw128_off(hh, (lane & 3) * 2 + 1)) = make_uint4(f[4], f[5], f[6], f[7]);
-                    *reinterpret_cast<uint32_t *>(smem + L::kQ + 8 * L::kQBlock + sw128_off(hh, lane >> 2) + (lane & 3) * 4) =
-                        f32x2_to_bf16x2(bf16_hi(xr) * sc, bf16_lo(xr) * sc);
-                    if (lane == 0) {
-                        s_fac[hh] = a.score_log2 * __uint_as_float((uint32_t)(127 - kq) << 23);
-                        s_m[hh] = kNegInfL;
-                    }
-                }
-#pragma unroll
-                for (int c = 0; c < CW; c++) l[c] = 0.f;
-                workers_sync();   // s_fac and s_m are written for all heads
+        // the group's address and how many of its rows exist (0: none, or a page out of range, flagged)
+        auto group_of = [&](const TileIter &x, int32_t page, int &rows) -> const uint8_t * {
+            const int t = x.t * kTile + 16 * grp;
+            rows = x.left > 0 ? x.n - t : 0;
+            if (rows > 0 && (page < 0 || page >= a.num_pages)) {
+                if (lane == 0) flag_error(a.err, kErrPage);
+                rows = 0;
             }
-            // ---- expand the tile, a pair of column blocks at a time
+            return a.pool + (int64_t)(rows > 0 ? page : 0) * ((int64_t)kLatentRow * a.P) +
+                   (int64_t)((t & (a.P - 1)) >> 4) * kLatentGroup;
+        };
+        auto load_block = [&](const uint8_t *p, int rows, int i) {
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                if (j > 0) wait(&pv_done[i], (j - 1) & 1);
-                const uint4 wv[2] = {code[2 * i], code[2 * i + 1]};
-                const uint32_t s4 = i == 0 ? scl.x : i == 1 ? scl.y : i == 2 ? scl.z : scl.w;
+            for (int e = 0; e < 2; e++)
+                raw[i][e] = er + 8 * e < rows
+                                ? __ldg(reinterpret_cast<const uint2 *>(p + (2 * i + par) * 512 + (er + 8 * e) * 32 + eq * 8))
+                                : make_uint2(0, 0);
+        };
+        auto load_scales = [&](const uint8_t *p, int rows) {      // byte 2 cb + eq % 2: of column block cb
 #pragma unroll
-                for (int c = 0; c < 2; c++) {
-                    const uint32_t s2 = e4m3x2_to_f16x2((s4 >> (16 * c)) & 0xffffu);
-                    const uint32_t lo = __byte_perm(s2, s2, 0x1010), hi = __byte_perm(s2, s2, 0x3232);
-                    uint32_t f[16];
-                    e2m1x8_to_f16x2x4(wv[c].x, f[0], f[1], f[2], f[3]);
-                    e2m1x8_to_f16x2x4(wv[c].y, f[4], f[5], f[6], f[7]);
-                    e2m1x8_to_f16x2x4(wv[c].z, f[8], f[9], f[10], f[11]);
-                    e2m1x8_to_f16x2x4(wv[c].w, f[12], f[13], f[14], f[15]);
+            for (int e = 0; e < 2; e++)
+                scl[e] = er + 8 * e < rows
+                             ? __ldg(reinterpret_cast<const uint4 *>(p + kLatentScales + (er + 8 * e) * 32 + (eq >> 1) * 16))
+                             : make_uint4(0, 0, 0, 0);
+        };
+        auto load_rope = [&](const uint8_t *p, int rows) {        // 16-byte chunk 4 par + eq
 #pragma unroll
-                    for (int e = 0; e < 8; e++) {
-                        f[e] = hmul2(f[e], lo);
-                        f[8 + e] = hmul2(f[8 + e], hi);
-                    }
-                    uint8_t *blk = smem + L::kKV + (2 * i + c) * kColBlock;
+            for (int e = 0; e < 2; e++)
+                rope[e] = er + 8 * e < rows ? __ldg(reinterpret_cast<const uint4 *>(
+                                                  p + kLatentRope + (er + 8 * e) * 128 + (((4 * par + eq) ^ er) << 4)))
+                                            : make_uint4(0, 0, 0, 0);
+        };
+        // Q of sequence b: one warp per head, FP16 latent blocks and the BF16 rotary block (the
+        // previous sequence's S^T are done: its scores were seen).
+        auto load_q = [&](int b) {
+#pragma unroll 2
+            for (int hh = warp; hh < N; hh += kWorkers / 32) {
+                const int h = h0 + hh;
+                uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
+                uint32_t xr = 0;
+                if (h < a.H) {
+                    const int64_t at = (int64_t)b * a.H + h;
+                    const uint4 *src = reinterpret_cast<const uint4 *>(a.ql + at * kLatentDim) + lane * 2;
+                    x0 = __ldg(src);
+                    x1 = __ldg(src + 1);
+                    xr = __ldg(reinterpret_cast<const uint32_t *>(a.qr + at * kRopeDim) + lane);
+                }
+                const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+                uint32_t ml = 0, mr = xr & 0x7fff7fffu;
+#pragma unroll
+                for (int e = 0; e < 8; e++) ml = max_u16x2(ml, w[e] & 0x7fff7fffu);
+                ml = __reduce_max_sync(0xffffffffu, max(ml >> 16, ml & 0xffffu));
+                mr = __reduce_max_sync(0xffffffffu, max(mr >> 16, mr & 0xffffu));
+                // 2^kq puts the largest |q g| into [2^14, 2^15), the rotary part below 2^127
+                const uint32_t top = __float_as_uint(__uint_as_float(ml << 16) * a.g);
+                int kq = top ? 14 - ((int)(top >> 23) - 127) : 0;
+                kq = min(min(126, max(-126, kq)), 126 - ((int)(mr >> 7) - 127));
+                kq = max(-126, kq);
+                const float sc = __uint_as_float((uint32_t)(kq + 127) << 23);
+                uint32_t f[8];
+#pragma unroll
+                for (int e = 0; e < 8; e++) f[e] = f32x2_to_f16x2(bf16_hi(w[e]) * a.g * sc, bf16_lo(w[e]) * a.g * sc);
+                uint8_t *q = smem + L::kQ + (lane >> 2) * L::kQBlock;      // lane: dims 16 lane .. 16 lane + 15
+                const int bq = lane & 3;
+                if ((lane >> 2) < L::kTmemCbs) {   // in the order of the block in TMEM
 #pragma unroll
                     for (int k = 0; k < 4; k++)
-                        *reinterpret_cast<uint4 *>(blk + sw128_off(16 * warp + er, 4 * hb + k)) =
-                            make_uint4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
+                        *reinterpret_cast<uint2 *>(q + sw128_off(hh, 2 * k + (bq >> 1)) + (bq & 1) * 8) =
+                            make_uint2(f[2 * k], f[2 * k + 1]);
+                } else {
+                    *reinterpret_cast<uint4 *>(q + sw128_off(hh, bq * 2)) = make_uint4(f[0], f[1], f[2], f[3]);
+                    *reinterpret_cast<uint4 *>(q + sw128_off(hh, bq * 2 + 1)) = make_uint4(f[4], f[5], f[6], f[7]);
                 }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&kv_full[i]);
+                // rotary dims 32 p + 8 q + 4 k + e (here d = 2 lane, + 1) at position 32 p + 16 k + 4 q + e
+                const int d = 2 * lane, pos = (d & 32) + ((d >> 2) & 1) * 16 + ((d >> 3) & 3) * 4 + (d & 3);
+                *reinterpret_cast<uint32_t *>(smem + L::kQ + 8 * L::kQBlock + sw128_off(hh, pos >> 3) + (pos & 7) * 2) =
+                    f32x2_to_bf16x2(bf16_hi(xr) * sc, bf16_lo(xr) * sc);
+                if (lane == 0) {
+                    s_fac[hh] = a.score_log2 * __uint_as_float((uint32_t)(127 - kq) << 23);
+                    s_m[hh] = kNegInfL;
+                }
             }
-            // the rotary tile, over the previous tile's P (row block 3, the last to read it, is done)
+            // (published to the tensor core with the first half of the tile)
+            workers_sync();   // s_fac and s_m are written for all heads
+        };
+        const uint32_t n = (uint32_t)it.left;
+        TileIter nx = it;                       // the tile whose bytes are requested next
+        {
+            int rows;
+            const uint8_t *p = group_of(nx, page_of(nx), rows);
 #pragma unroll
-            for (int x4 = 0; x4 < 4; x4++)
-                *reinterpret_cast<uint4 *>(smem + L::kRope + warp * 2048 + x4 * 512 + lane * 16) = rope[x4];
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&kv_full[4]);
-            // ---- request the next tile's bytes, and the page after that
-            load_tile(nx, npage);
-            next_tile(a, nx);
-            npage = page_of(nx);
-
-            // ---- softmax of this thread's token
+            for (int i = 0; i < 4; i++) load_block(p, rows, i);
+            load_scales(p, rows);
+            load_rope(p, rows);
+        }
+        next_tile(a, nx);
+        int32_t npage = page_of(nx);            // its page, requested a tile earlier still
+        bool fresh = true;                      // the range's first tile of its sequence
+        int t_begin = it.t;
+        float l[CW];
+        for (uint32_t j = 0; j < n; j++) {
+            if (fresh) {
+                load_q(it.b);
+#pragma unroll
+                for (int c = 0; c < CW; c++) l[c] = 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; i++) {       // ---- expand block eq of column block 2 i + par, rows er and er + 8
+                uint32_t f[2][8];
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    const uint32_t sw = i == 0 ? scl[e].x : i == 1 ? scl[e].y : i == 2 ? scl[e].z : scl[e].w;
+                    const uint32_t sb = (sw >> (16 * par + 8 * (eq & 1))) & 0xffu;
+                    const uint32_t s = e4m3x2_to_f16x2(sb * 0x101u);
+                    e2m1x8_to_f16x2x4(raw[i][e].x, f[e][0], f[e][1], f[e][2], f[e][3]);
+                    e2m1x8_to_f16x2x4(raw[i][e].y, f[e][4], f[e][5], f[e][6], f[e][7]);
+#pragma unroll
+                    for (int x = 0; x < 8; x++) f[e][x] = hmul2(f[e][x], s);
+                }
+                // (TMEM's copy is free: the previous tile's scores were seen)
+                if (L::kTmemCbs == 8 || 2 * i < L::kTmemCbs) {
+                    const uint32_t st[16] = {f[0][0], f[0][1], f[1][0], f[1][1], f[0][2], f[0][3], f[1][2], f[1][3],
+                                             f[0][4], f[0][5], f[1][4], f[1][5], f[0][6], f[0][7], f[1][6], f[1][7]};
+                    tc_st_16x256_x4(tmem + glanes + L::kColK + 32 * (2 * i + par), st);
+                }
+                if (i == 0) {
+                    const uint32_t st[8] = {rope[0].x, rope[0].y, rope[1].x, rope[1].y, rope[0].z, rope[0].w, rope[1].z, rope[1].w};
+                    tc_st_16x256_x2(tmem + glanes + L::kColR + 16 * par, st);
+                }
+                if (j > 0) wait(&pv_done[i], (j - 1) & 1);
+                uint8_t *blk = smem + L::kKV + (2 * i + par) * kColBlock;
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    const int tr = 16 * grp + er + 8 * e;
+                    *reinterpret_cast<uint4 *>(blk + sw128_off(tr, 2 * eq)) = make_uint4(f[e][0], f[e][1], f[e][2], f[e][3]);
+                    *reinterpret_cast<uint4 *>(blk + sw128_off(tr, 2 * eq + 1)) = make_uint4(f[e][4], f[e][5], f[e][6], f[e][7]);
+                }
+                if (i & 1) {   // half of the tile at a time: a fence takes about as long as an expanding step
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&kv_full[i >> 1]);
+                }
+            }
+            // Request the next tile's bytes, and the page after that.  Only here: a proxy fence waits
+            // for loads in flight, and no fence follows before the softmax is done.
+            {
+                int rows;
+                const uint8_t *p = group_of(nx, npage, rows);
+                load_scales(p, rows);
+                load_rope(p, rows);
+#pragma unroll
+                for (int i = 0; i < 4; i++) load_block(p, rows, i);
+                next_tile(a, nx);
+                npage = page_of(nx);
+            }
+            // ---- softmax of the token's scores for the warpgroup's heads.  S^T done says that the
+            // previous tile's O^T, issued before it, is done too: P and O^T may be written.
             wait(s_done, j & 1);
-            __syncwarp();
             tc_fence_after();
             const bool seen = it.t * kTile + row < it.n;
-            uint32_t sr[CW];
-            tc_ld(tmem + lanes + kColS + wg * CW, sr);
-            tc_wait_ld();
-            float sc[CW];
+            // The scores are read from TMEM in chunks of up to eight heads (the next tile's bytes hold
+            // the registers): once to see whether a maximum must move, again to form P.
+            constexpr int CH = CW < 8 ? CW : 8;
+            auto load_scores = [&](int c0, float (&sc)[CH]) {
+                uint32_t sr[CH];
+                tc_ld(tmem + lanes + L::kColS + wg * CW + c0, sr);
+                tc_wait_ld();
+#pragma unroll
+                for (int c = 0; c < CH; c++) sc[c] = seen ? __uint_as_float(sr[c]) * s_fac[wg * CW + c0 + c] : kNegInfL;
+            };
+            float sc[CH];
             bool need = false;
 #pragma unroll
-            for (int c = 0; c < CW; c++) {
-                sc[c] = seen ? __uint_as_float(sr[c]) * s_fac[wg * CW + c] : kNegInfL;
-                need |= sc[c] > s_m[wg * CW + c] + kRescaleL;
+            for (int c0 = 0; c0 < CW; c0 += CH) {
+                load_scores(c0, sc);
+#pragma unroll
+                for (int c = 0; c < CH; c++) need |= sc[c] > s_m[wg * CW + c0 + c] + kRescaleL;
             }
             if (group_any(wg, need)) {
                 float *wmax = reinterpret_cast<float *>(smem + L::kWarpMax) + wg * 4 * CW;
                 int mine = 0;
 #pragma unroll
-                for (int c = 0; c < CW; c++) {
-                    const int mx = __reduce_max_sync(0xffffffffu, ordered(sc[c]));
-                    if (lane == c) mine = mx;
+                for (int c0 = 0; c0 < CW; c0 += CH) {
+                    if (CW > CH) load_scores(c0, sc);
+#pragma unroll
+                    for (int c = 0; c < CH; c++) {
+                        const int mx = __reduce_max_sync(0xffffffffu, ordered(sc[c]));
+                        if (lane == c0 + c) mine = mx;
+                    }
                 }
                 if (lane < CW) wmax[(warp & 3) * CW + lane] = unordered(mine);
                 group_sync(wg);
@@ -454,7 +535,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
                 group_sync(wg);
 #pragma unroll
                 for (int c = 0; c < CW; c++) l[c] *= s_alpha[wg * CW + c];
-                if (!fresh) {   // O^T holds earlier tiles, complete: rescale this warp's lanes of the warpgroup's heads
+                if (!fresh) {   // O^T holds the earlier tiles: rescale the warpgroup's heads
 #pragma unroll 1
                     for (int mb = 0; mb < 4; mb++) {
                         uint32_t ov[CW];
@@ -469,18 +550,22 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
                 }
             }
 #pragma unroll
-            for (int k = 0; k < CW / 8; k++) {
-                uint32_t pw[4];
+            for (int c0 = 0; c0 < CW; c0 += CH) {
+                if (CW > CH) load_scores(c0, sc);
+                uint32_t pw[CH / 2];
 #pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const int c = 8 * k + 2 * e;
+                for (int e = 0; e < CH / 2; e++) {
+                    const int c = c0 + 2 * e;
                     const float m0 = s_m[wg * CW + c], m1 = s_m[wg * CW + c + 1];
-                    pw[e] = f32x2_to_f16x2(ex2(sc[c + 1] - (m1 == kNegInfL ? 0.f : m1 - kPOffset)),
-                                           ex2(sc[c] - (m0 == kNegInfL ? 0.f : m0 - kPOffset)));
+                    pw[e] = f32x2_to_f16x2(ex2(sc[2 * e + 1] - (m1 == kNegInfL ? 0.f : m1 - kPOffset)),
+                                           ex2(sc[2 * e] - (m0 == kNegInfL ? 0.f : m0 - kPOffset)));
                     add_f16x2(l[c], l[c + 1], pw[e]);
                 }
-                *reinterpret_cast<uint4 *>(smem + L::kRope + sw128_off(row, wg * (CW / 8) + k)) =
-                    make_uint4(pw[0], pw[1], pw[2], pw[3]);
+                if (CW == 4)   // eight bytes a thread: two warpgroups share a 16-byte chunk
+                    *reinterpret_cast<uint2 *>(smem + L::kP + sw128_off(row, wg >> 1) + (wg & 1) * 8) = make_uint2(pw[0], pw[1]);
+                else
+                    *reinterpret_cast<uint4 *>(smem + L::kP + sw128_off(row, (wg * CW + c0) / 8)) =
+                        make_uint4(pw[0], pw[1], pw[CH / 2 - 2], pw[CH / 2 - 1]);
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             tc_fence_before();
@@ -492,11 +577,11 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
             next_tile(a, it);
             fresh = it.left <= 0 || it.b != cur.b;
             if (!fresh) continue;
+#pragma unroll 1
             for (int i = 0; i < 4; i++) wait(&pv_done[i], j & 1);
-            __syncwarp();
             tc_fence_after();
             {
-                float *wsum = reinterpret_cast<float *>(smem + L::kWarpSum) + wg * 4 * CW;
+                float *wsum = reinterpret_cast<float *>(smem + L::kWarpMax) + wg * 4 * CW;
                 const float s = column_sums<CW>(l, lane);
                 if (lane < CW) wsum[(warp & 3) * CW + lane] = s;
                 group_sync(wg);
@@ -535,7 +620,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) tc_dealloc(tmem, L::kCols);
+    if (warp == 16) tc_dealloc(tmem, L::kCols);
 }
 
 // Joins the partials of the sequences that several CTAs covered (and zeroes those
