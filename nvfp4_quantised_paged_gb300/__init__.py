@@ -504,24 +504,55 @@ def extend_attention_paged(cache: PagedCache, q: torch.Tensor, block_table: torc
 
 # ---------------------------------------------------------------- latent cache and eviction
 
-def _on_device(device: torch.device, *named):
-    """Every tensor lies on `device`, which is the current one (the library launches there)."""
-    for name, t in named:
-        if t.device != device:
-            raise ValueError("%s is on %s, the cache on %s" % (name, t.device, device))
-    if device.index != torch.cuda.current_device():
-        raise ValueError("the tensors are on %s, which is not the current device" % device)
+# (the calls below are short: their checks are written to cost little on the host)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
-def _shape(t: torch.Tensor, name: str, shape):
-    if tuple(t.shape) != tuple(shape):
+def _complain(t, name: str, dtype: torch.dtype, shape, dev: int):
+    """The error that the failed check of _want describes."""
+    if not isinstance(t, torch.Tensor) or t.get_device() < 0:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.get_device() != dev:
+        raise ValueError("%s is on cuda:%d, the call's other tensors on cuda:%d" % (name, t.get_device(), dev))
+    if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    raise ValueError("%s must be contiguous" % name)
+
+
+def _want(t, name: str, dtype: torch.dtype, shape, dev: int) -> int:
+    """Checks a contiguous CUDA tensor (shape None: any) and returns its address."""
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev
+            or not t.is_contiguous() or (shape is not None and t.shape != shape)):
+        _complain(t, name, dtype, shape, dev)
+    return t.data_ptr()
+
+
+def _want_table(t, name: str, rows: int, dev: int) -> int:
+    p = _want(t, name, torch.int32, None, dev)
+    if t.dim() != 2 or t.shape[0] != rows:
+        raise ValueError("%s must be [%d][pages], a row per sequence" % (name, rows))
+    return p
+
+
+def _launch_stream(dev: int, stream: Optional[torch.cuda.Stream]) -> int:
+    """The stream handle of a call whose tensors lie on device dev: the current
+    device (the library launches there), and the stream on it."""
+    if _current_device() != dev:
+        raise ValueError("the tensors are on cuda:%d, which is not the current device" % dev)
+    if stream is None:
+        return _raw_stream(dev)
+    if stream.device.index != dev:
+        raise ValueError("the stream is on %s, the tensors on cuda:%d" % (stream.device, dev))
+    return stream.cuda_stream
 
 
 def _keep_until_done(stream: Optional[torch.cuda.Stream], *tensors):
     """Tensors allocated here on the current stream, used on another one: their
     memory is not given out again before that stream has passed this point."""
-    if stream is not None and stream != torch.cuda.current_stream():
+    if stream is not None and tensors and stream.cuda_stream != _raw_stream(stream.device.index):
         stream.wait_stream(torch.cuda.current_stream())   # memory that earlier work here may still use
         for t in tensors:
             t.record_stream(stream)
@@ -543,10 +574,7 @@ class LatentCache:
         self.pool = pool
         self._desc = _LatentDesc(pool.data_ptr(), self.num_pages, self.page_size, LATENT_DIM, ROPE_DIM,
                                  self.global_scale)
-
-    @property
-    def desc(self):
-        return ctypes.byref(self._desc)
+        self.desc = ctypes.byref(self._desc)
 
     @property
     def num_slots(self) -> int:
@@ -561,26 +589,32 @@ def latent_slab_bytes(page_size: int) -> int:
     return int(n)
 
 
+def _rows(t, name: str, T: int, width: int, dev: int):
+    """Address and row stride of BF16 [T][width] whose rows may be strided."""
+    if (not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.get_device() != dev
+            or t.shape != (T, width) or (T > 0 and t.stride(1) != 1)):
+        if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.get_device() == dev and t.shape == (T, width):
+            raise ValueError("%s: each token must hold %d contiguous values" % (name, width))
+        _complain(t, name, torch.bfloat16, (T, width), dev)
+    # (a single row's stride says nothing: torch may give it any value)
+    return t.data_ptr(), t.stride(0) if T > 1 else width
+
+
 def latent_quantize_append(cache: LatentCache, latent: torch.Tensor, k_rope: torch.Tensor, slot_mapping: torch.Tensor,
                            stream: Optional[torch.cuda.Stream] = None):
     """latent: BF16 [T][512], k_rope: BF16 [T][64] (rows may be strided: views of one
     wider row); slot_mapping: int64 [T].  Quantises the latents, stores the rotary
     parts as they are."""
-    _require(slot_mapping, "slot_mapping", torch.int64)
-    T = int(slot_mapping.shape[0])
-    for name, x, width in (("latent", latent, LATENT_DIM), ("k_rope", k_rope, ROPE_DIM)):
-        if not x.is_cuda or x.dtype != torch.bfloat16:
-            raise ValueError("%s must be a CUDA bfloat16 tensor" % name)
-        _shape(x, name, (T, width))
-        if T > 0 and x.stride(1) != 1:
-            raise ValueError("%s: each token must hold %d contiguous values" % (name, width))
-    _on_device(cache.pool.device, ("latent", latent), ("k_rope", k_rope), ("slot_mapping", slot_mapping))
-    # (a single row's stride says nothing: torch may give it any value)
-    sl = int(latent.stride(0)) if T > 1 else LATENT_DIM
-    sr = int(k_rope.stride(0)) if T > 1 else ROPE_DIM
-    rc = _lib.nvfp4_latent_quantize_append(cache.desc, _ptr(latent), sl, _ptr(k_rope), sr, T, _ptr(slot_mapping),
-                                           _stream(stream))
-    _check(rc, "nvfp4_latent_quantize_append")
+    dev = cache.pool.get_device()
+    sp = _want(slot_mapping, "slot_mapping", torch.int64, None, dev)
+    T = slot_mapping.numel()
+    if slot_mapping.dim() != 1:
+        raise ValueError("slot_mapping must be [tokens]")
+    lp, ls = _rows(latent, "latent", T, LATENT_DIM, dev)
+    rp, rs = _rows(k_rope, "k_rope", T, ROPE_DIM, dev)
+    rc = _lib.nvfp4_latent_quantize_append(cache.desc, lp, ls, rp, rs, T, sp, _launch_stream(dev, stream))
+    if rc:
+        _check(rc, "nvfp4_latent_quantize_append")
 
 
 def latent_prefix_dequant(cache: LatentCache, block_table: torch.Tensor, prefix_lens: torch.Tensor,
@@ -589,30 +623,25 @@ def latent_prefix_dequant(cache: LatentCache, block_table: torch.Tensor, prefix_
                           stream: Optional[torch.cuda.Stream] = None):
     """Returns (latent_ws BF16 [total][512], rope_ws BF16 [total][64]): the cached
     prefixes' rows, the input of the up-projections to per-head K and V."""
-    _require(block_table, "block_table", torch.int32)
-    _require(prefix_lens, "prefix_lens", torch.int32)
-    _require(cu_prefix_lens, "cu_prefix_lens", torch.int32)
-    R, total, dev = int(prefix_lens.shape[0]), int(total_prefix_tokens), cache.pool.device
-    _shape(cu_prefix_lens, "cu_prefix_lens", (R + 1,))
-    if block_table.dim() != 2 or block_table.shape[0] != R:
-        raise ValueError("block_table needs one row per request")
+    dev, total = cache.pool.get_device(), int(total_prefix_tokens)
+    pp = _want(prefix_lens, "prefix_lens", torch.int32, None, dev)
+    R = prefix_lens.numel()
+    cp = _want(cu_prefix_lens, "cu_prefix_lens", torch.int32, (R + 1,), dev)
+    bp = _want_table(block_table, "block_table", R, dev)
+    s = _launch_stream(dev, stream)
     made = []
     if latent_ws is None:
-        latent_ws = torch.empty((total, LATENT_DIM), dtype=torch.bfloat16, device=dev)
+        latent_ws = torch.empty((total, LATENT_DIM), dtype=torch.bfloat16, device=cache.pool.device)
         made.append(latent_ws)
     if rope_ws is None:
-        rope_ws = torch.empty((total, ROPE_DIM), dtype=torch.bfloat16, device=dev)
+        rope_ws = torch.empty((total, ROPE_DIM), dtype=torch.bfloat16, device=cache.pool.device)
         made.append(rope_ws)
-    for name, x, width in (("latent_ws", latent_ws, LATENT_DIM), ("rope_ws", rope_ws, ROPE_DIM)):
-        _require(x, name, torch.bfloat16)
-        _shape(x, name, (total, width))
-    _on_device(dev, ("block_table", block_table), ("prefix_lens", prefix_lens), ("cu_prefix_lens", cu_prefix_lens),
-               ("latent_ws", latent_ws), ("rope_ws", rope_ws))
+    lp = _want(latent_ws, "latent_ws", torch.bfloat16, (total, LATENT_DIM), dev)
+    rp = _want(rope_ws, "rope_ws", torch.bfloat16, (total, ROPE_DIM), dev)
     _keep_until_done(stream, *made)
-    rc = _lib.nvfp4_latent_prefix_dequant(cache.desc, _ptr(block_table), int(block_table.shape[1]), _ptr(prefix_lens),
-                                          _ptr(cu_prefix_lens), R, total, _ptr(latent_ws), _ptr(rope_ws),
-                                          _stream(stream))
-    _check(rc, "nvfp4_latent_prefix_dequant")
+    rc = _lib.nvfp4_latent_prefix_dequant(cache.desc, bp, block_table.shape[1], pp, cp, R, total, lp, rp, s)
+    if rc:
+        _check(rc, "nvfp4_latent_prefix_dequant")
     return latent_ws, rope_ws
 
 
@@ -637,39 +666,51 @@ def latent_decode_attention(cache: LatentCache, q_latent: torch.Tensor, q_rope: 
     [B][max_pages]; seq_lens int32 [B] -> BF16 [B][H][512], each head's weighted
     mean of the latents (its up-projection to V is left to the caller).  H <= 128;
     sm_scale defaults to 1 / sqrt(128 + 64)."""
-    _require(q_latent, "q_latent", torch.bfloat16)
-    _require(q_rope, "q_rope", torch.bfloat16)
-    _require(block_table, "block_table", torch.int32)
-    _require(seq_lens, "seq_lens", torch.int32)
+    dev = cache.pool.get_device()
+    qp = _want(q_latent, "q_latent", torch.bfloat16, None, dev)
     if q_latent.dim() != 3 or q_latent.shape[2] != LATENT_DIM:
         raise ValueError("q_latent must be [batch][heads][512]")
-    B, H = int(q_latent.shape[0]), int(q_latent.shape[1])
-    _shape(q_rope, "q_rope", (B, H, ROPE_DIM))
-    _shape(seq_lens, "seq_lens", (B,))
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError("block_table needs one row per sequence")
-    if sm_scale is None:
-        sm_scale = 1.0 / math.sqrt(HEAD_DIM + ROPE_DIM)
+    B, H, _ = q_latent.shape
+    rp = _want(q_rope, "q_rope", torch.bfloat16, (B, H, ROPE_DIM), dev)
+    lp = _want(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    bp = _want_table(block_table, "block_table", B, dev)
+    s = _launch_stream(dev, stream)
     made = []
     if out is None:
         out = torch.empty_like(q_latent)
         made.append(out)
-    else:
-        _require(out, "out", torch.bfloat16)
-        _shape(out, "out", q_latent.shape)
     if workspace is None:
         workspace = alloc_latent_decode_workspace(cache, B, H, num_splits)
         made.append(workspace)
-    else:
-        _require(workspace, "workspace", torch.uint8)
-    _on_device(cache.pool.device, ("q_latent", q_latent), ("q_rope", q_rope), ("block_table", block_table),
-               ("seq_lens", seq_lens), ("out", out), ("workspace", workspace))
+    op = _want(out, "out", torch.bfloat16, (B, H, LATENT_DIM), dev)
+    wp = _want(workspace, "workspace", torch.uint8, None, dev)
     _keep_until_done(stream, *made)
-    rc = _lib.nvfp4_latent_decode_attention(cache.desc, _ptr(q_latent), _ptr(q_rope), B, H, _ptr(block_table),
-                                            int(block_table.shape[1]), _ptr(seq_lens), float(sm_scale), _ptr(out),
-                                            _ptr(workspace), workspace.numel(), int(num_splits), _stream(stream))
-    _check(rc, "nvfp4_latent_decode_attention")
+    rc = _lib.nvfp4_latent_decode_attention(cache.desc, qp, rp, B, H, bp, block_table.shape[1], lp,
+                                            _LATENT_SCALE if sm_scale is None else float(sm_scale), op, wp,
+                                            workspace.numel(), int(num_splits), s)
+    if rc:
+        _check(rc, "nvfp4_latent_decode_attention")
     return out
+
+
+_LATENT_SCALE = 1.0 / math.sqrt(HEAD_DIM + ROPE_DIM)
+
+
+def _heads(k, v, where: str, rows: int, H: int, dev: int):
+    """Addresses and (token, head) strides of BF16 K and V [rows][H][128], which share them."""
+    shape = (rows, H, HEAD_DIM)
+    for name, x in (("k_", k), ("v_", v)):
+        if (not isinstance(x, torch.Tensor) or x.dtype is not torch.bfloat16 or x.get_device() != dev
+                or x.shape != shape or (rows > 0 and x.stride(2) != 1)):
+            if isinstance(x, torch.Tensor) and x.dtype is torch.bfloat16 and x.get_device() == dev and x.shape == shape:
+                raise ValueError("%s%s: the 128 values of a head must be contiguous" % (name, where))
+            _complain(x, name + where, torch.bfloat16, shape, dev)
+    # strides of axes of length 1 say nothing: torch may give them any value
+    st = k.stride(0) if rows > 1 else H * HEAD_DIM
+    sh = k.stride(1) if H > 1 else HEAD_DIM
+    if (rows > 1 and v.stride(0) != st) or (H > 1 and rows > 0 and v.stride(1) != sh):
+        raise ValueError("k_%s and v_%s must share their strides" % (where, where))
+    return k.data_ptr(), v.data_ptr(), st, sh
 
 
 def latent_extend_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Tensor, rope_prefix: torch.Tensor,
@@ -684,48 +725,29 @@ def latent_extend_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: t
     output); rope_*: BF16 [rows][64], shared by the heads; cu_*: int32 [R+1];
     max_q_len: bound on chunk lengths -> BF16 [total_q][H][128].  sm_scale > 0
     defaults to 1 / sqrt(192)."""
-    _require(q, "q", torch.bfloat16)
-    if q.dim() != 3 or q.shape[2] != HEAD_DIM + ROPE_DIM:
-        raise ValueError("q must be [total_q][heads][192]")
-    _require(cu_prefix_lens, "cu_prefix_lens", torch.int32)
-    _require(cu_q_lens, "cu_q_lens", torch.int32)
-    TQ, H, R = int(q.shape[0]), int(q.shape[1]), int(cu_q_lens.shape[0]) - 1
-    _shape(cu_prefix_lens, "cu_prefix_lens", (R + 1,))
-    strides = []
-    for where, k, v, rope, rows in (("prefix", k_prefix, v_prefix, rope_prefix, None),
-                                    ("chunk", k_chunk, v_chunk, rope_chunk, TQ)):
-        rows = int(k.shape[0]) if rows is None else rows
-        for name, x in (("k_" + where, k), ("v_" + where, v)):
-            if not x.is_cuda or x.dtype != torch.bfloat16:
-                raise ValueError("%s must be a CUDA bfloat16 tensor" % name)
-            _shape(x, name, (rows, H, HEAD_DIM))
-            if rows > 0 and x.stride(2) != 1:
-                raise ValueError("%s: the 128 values of a head must be contiguous" % name)
-        # strides of axes of length 1 say nothing: torch may give them any value
-        st = int(k.stride(0)) if rows > 1 else H * HEAD_DIM
-        sh = int(k.stride(1)) if H > 1 else HEAD_DIM
-        if (rows > 1 and v.stride(0) != st) or (H > 1 and rows > 0 and v.stride(1) != sh):
-            raise ValueError("k_%s and v_%s must share their strides" % (where, where))
-        strides.append((st, sh))
-        _require(rope, "rope_" + where, torch.bfloat16)
-        _shape(rope, "rope_" + where, (rows, ROPE_DIM))
+    dev = q.get_device()
+    qp = _want(q, "q", torch.bfloat16, None, dev)
+    if dev < 0 or q.dim() != 3 or q.shape[2] != HEAD_DIM + ROPE_DIM:
+        raise ValueError("q must be a CUDA tensor [total_q][heads][192]")
+    TQ, H, _ = q.shape
+    np_ = _want(cu_q_lens, "cu_q_lens", torch.int32, None, dev)
+    R = cu_q_lens.numel() - 1
+    pp = _want(cu_prefix_lens, "cu_prefix_lens", torch.int32, (R + 1,), dev)
+    TP = k_prefix.shape[0]
+    k0, v0, ps, ph = _heads(k_prefix, v_prefix, "prefix", TP, H, dev)
+    k1, v1, cs, ch = _heads(k_chunk, v_chunk, "chunk", TQ, H, dev)
+    r0 = _want(rope_prefix, "rope_prefix", torch.bfloat16, (TP, ROPE_DIM), dev)
+    r1 = _want(rope_chunk, "rope_chunk", torch.bfloat16, (TQ, ROPE_DIM), dev)
+    s = _launch_stream(dev, stream)
     if out is None:
         out = torch.empty((TQ, H, HEAD_DIM), dtype=torch.bfloat16, device=q.device)
         _keep_until_done(stream, out)
-    else:
-        _require(out, "out", torch.bfloat16)
-        _shape(out, "out", (TQ, H, HEAD_DIM))
-    _on_device(q.device, ("k_prefix", k_prefix), ("v_prefix", v_prefix), ("rope_prefix", rope_prefix),
-               ("cu_prefix_lens", cu_prefix_lens), ("k_chunk", k_chunk), ("v_chunk", v_chunk),
-               ("rope_chunk", rope_chunk), ("cu_q_lens", cu_q_lens), ("out", out))
-    if sm_scale is None:
-        sm_scale = 1.0 / math.sqrt(HEAD_DIM + ROPE_DIM)
-    (ps, ph), (cs, ch) = strides
-    rc = _lib.nvfp4_latent_extend_attention(_ptr(q), _ptr(k_prefix), _ptr(v_prefix), ps, ph, _ptr(rope_prefix),
-                                            _ptr(cu_prefix_lens), int(k_prefix.shape[0]), _ptr(k_chunk), _ptr(v_chunk),
-                                            cs, ch, _ptr(rope_chunk), _ptr(cu_q_lens), TQ, R, int(max_q_len), H,
-                                            float(sm_scale), _ptr(out), _stream(stream))
-    _check(rc, "nvfp4_latent_extend_attention")
+    op = _want(out, "out", torch.bfloat16, (TQ, H, HEAD_DIM), dev)
+    rc = _lib.nvfp4_latent_extend_attention(qp, k0, v0, ps, ph, r0, pp, TP, k1, v1, cs, ch, r1, np_, TQ, R,
+                                            int(max_q_len), H, _LATENT_SCALE if sm_scale is None else float(sm_scale),
+                                            op, s)
+    if rc:
+        _check(rc, "nvfp4_latent_extend_attention")
     return out
 
 
@@ -748,33 +770,30 @@ def accumulate_attention_weights(cache: PagedCache, q: torch.Tensor, block_table
     queries q (BF16 [B][Hq][128]) put on every cached token: entry [b][h][t] grows
     by the sum over kv head h's query heads of their softmax weight of token t <
     seq_lens[b].  Returns scores."""
-    _require(q, "q", torch.bfloat16)
-    _require(block_table, "block_table", torch.int32)
-    _require(seq_lens, "seq_lens", torch.int32)
-    _require(scores, "scores", torch.float32)
+    dev = cache.pool.get_device()
+    qp = _want(q, "q", torch.bfloat16, None, dev)
     if q.dim() != 3 or q.shape[2] != HEAD_DIM:
         raise ValueError("q must be [batch][heads][128]")
-    B, Hq = int(q.shape[0]), int(q.shape[1])
-    _shape(seq_lens, "seq_lens", (B,))
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError("block_table needs one row per sequence")
-    if scores.dim() != 3 or tuple(scores.shape[:2]) != (B, cache.num_kv_heads):
+    B, Hq, _ = q.shape
+    lp = _want(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    bp = _want_table(block_table, "block_table", B, dev)
+    cp = _want(scores, "scores", torch.float32, None, dev)
+    if scores.dim() != 3 or scores.shape[0] != B or scores.shape[1] != cache.num_kv_heads:
         raise ValueError("scores must be [batch][kv heads][tokens]")
-    if sm_scale is None:
-        sm_scale = 1.0 / math.sqrt(HEAD_DIM)
+    s = _launch_stream(dev, stream)
     if workspace is None:
         workspace = alloc_weights_workspace(cache, B, Hq)
         _keep_until_done(stream, workspace)
-    else:
-        _require(workspace, "workspace", torch.uint8)
-    _on_device(cache.pool.device, ("q", q), ("block_table", block_table), ("seq_lens", seq_lens), ("scores", scores),
-               ("workspace", workspace))
-    rc = _lib.nvfp4_accumulate_attention_weights(cache.desc, _ptr(q), B, Hq, _ptr(block_table),
-                                                 int(block_table.shape[1]), _ptr(seq_lens), float(sm_scale),
-                                                 _ptr(scores), int(scores.shape[2]), _ptr(workspace),
-                                                 workspace.numel(), _stream(stream))
-    _check(rc, "nvfp4_accumulate_attention_weights")
+    wp = _want(workspace, "workspace", torch.uint8, None, dev)
+    rc = _lib.nvfp4_accumulate_attention_weights(cache.desc, qp, B, Hq, bp, block_table.shape[1], lp,
+                                                 _HEAD_SCALE if sm_scale is None else float(sm_scale), cp,
+                                                 scores.shape[2], wp, workspace.numel(), s)
+    if rc:
+        _check(rc, "nvfp4_accumulate_attention_weights")
     return scores
+
+
+_HEAD_SCALE = 1.0 / math.sqrt(HEAD_DIM)
 
 
 def evict(cache: PagedCache, scores: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
@@ -788,44 +807,39 @@ def evict(cache: PagedCache, scores: torch.Tensor, block_table: torch.Tensor, se
     Returns (new_lens int32 [B], kept int32 [B][Hkv][keep]: the old row of every new
     one, -1 behind the last, new_scores float32 [B][Hkv][>= keep]: theirs, then zeros;
     S or keep wide, the larger, by default)."""
-    _require(scores, "scores", torch.float32)
-    _require(block_table, "block_table", torch.int32)
-    _require(seq_lens, "seq_lens", torch.int32)
-    _require(new_block_table, "new_block_table", torch.int32)
-    B, Hkv, keep, dev = int(seq_lens.shape[0]), cache.num_kv_heads, int(keep), cache.pool.device
+    dev, Hkv, keep = cache.pool.get_device(), cache.num_kv_heads, int(keep)
+    lp = _want(seq_lens, "seq_lens", torch.int32, None, dev)
+    B = seq_lens.numel()
+    cp = _want(scores, "scores", torch.float32, None, dev)
+    if scores.dim() != 3 or scores.shape[0] != B or scores.shape[1] != Hkv:
+        raise ValueError("scores must be [batch][kv heads][tokens]")
     if keep < 1:
         raise ValueError("keep must be at least 1")
-    if scores.dim() != 3 or tuple(scores.shape[:2]) != (B, Hkv):
-        raise ValueError("scores must be [batch][kv heads][tokens]")
-    for name, t in (("block_table", block_table), ("new_block_table", new_block_table)):
-        if t.dim() != 2 or t.shape[0] != B:
-            raise ValueError("%s needs one row per sequence" % name)
-    made = []
+    S = scores.shape[2]
+    bp = _want_table(block_table, "block_table", B, dev)
+    np_ = _want_table(new_block_table, "new_block_table", B, dev)
+    s = _launch_stream(dev, stream)
+    where, made = cache.pool.device, []
     if new_lens is None:
-        new_lens = torch.empty(B, dtype=torch.int32, device=dev)
+        new_lens = torch.empty(B, dtype=torch.int32, device=where)
         made.append(new_lens)
     if kept is None:
-        kept = torch.empty((B, Hkv, keep), dtype=torch.int32, device=dev)
+        kept = torch.empty((B, Hkv, keep), dtype=torch.int32, device=where)
         made.append(kept)
     if new_scores is None:
-        new_scores = torch.empty((B, Hkv, max(int(scores.shape[2]), keep)), dtype=torch.float32, device=dev)
+        new_scores = torch.empty((B, Hkv, max(S, keep)), dtype=torch.float32, device=where)
         made.append(new_scores)
-    _require(new_lens, "new_lens", torch.int32)
-    _shape(new_lens, "new_lens", (B,))
-    _require(kept, "kept", torch.int32)
-    _shape(kept, "kept", (B, Hkv, keep))
-    _require(new_scores, "new_scores", torch.float32)
-    if new_scores.dim() != 3 or tuple(new_scores.shape[:2]) != (B, Hkv) or new_scores.shape[2] < keep:
+    nlp = _want(new_lens, "new_lens", torch.int32, (B,), dev)
+    kp = _want(kept, "kept", torch.int32, (B, Hkv, keep), dev)
+    nsp = _want(new_scores, "new_scores", torch.float32, None, dev)
+    if (new_scores.dim() != 3 or new_scores.shape[0] != B or new_scores.shape[1] != Hkv
+            or new_scores.shape[2] < keep):
         raise ValueError("new_scores must be [batch][kv heads][at least keep]")
-    _on_device(dev, ("scores", scores), ("block_table", block_table), ("seq_lens", seq_lens),
-               ("new_block_table", new_block_table), ("new_lens", new_lens), ("kept", kept),
-               ("new_scores", new_scores))
     _keep_until_done(stream, *made)
-    rc = _lib.nvfp4_evict(cache.desc, _ptr(scores), int(scores.shape[2]), B, _ptr(block_table),
-                          int(block_table.shape[1]), _ptr(seq_lens), _ptr(new_block_table),
-                          int(new_block_table.shape[1]), keep, int(recent), int(sink), _ptr(new_lens), _ptr(kept),
-                          _ptr(new_scores), int(new_scores.shape[2]), _stream(stream))
-    _check(rc, "nvfp4_evict")
+    rc = _lib.nvfp4_evict(cache.desc, cp, S, B, bp, block_table.shape[1], lp, np_, new_block_table.shape[1], keep,
+                          int(recent), int(sink), nlp, kp, nsp, new_scores.shape[2], s)
+    if rc:
+        _check(rc, "nvfp4_evict")
     return new_lens, kept, new_scores
 
 
