@@ -61,16 +61,12 @@ struct RawUnit {  // one thread's share of a unit's K: tokens g and g + 8 of eac
 };
 
 template <int DTYPE>
-__device__ __forceinline__ void load_unit(const WeightsArgs &a, int b, int h, int t0, int n, int lane,
+__device__ __forceinline__ void load_unit(const WeightsArgs &a, int h, int t0, int n, int32_t page, int lane,
                                           RawUnit<DTYPE> &r) {
     const int g = lane >> 2, j = lane & 3;
-    int32_t page = -1;
-    if (lane < kGroupsW && t0 + 16 * lane < n) {
-        page = __ldg(a.block_table + (int64_t)b * a.max_pages + ((t0 + 16 * lane) >> a.log2P));
-        if (page < 0 || page >= a.num_pages) {
-            flag_error(a.err, kErrPage);
-            page = -1;
-        }
+    if (lane < kGroupsW && t0 + 16 * lane < n && (page < 0 || page >= a.num_pages)) {
+        flag_error(a.err, kErrPage);
+        page = -1;
     }
     constexpr int kBytes = DTYPE == NVFP4KV_DTYPE_NVFP4 ? 2304 : 4096;
 #pragma unroll
@@ -97,6 +93,26 @@ __device__ __forceinline__ void load_unit(const WeightsArgs &a, int b, int h, in
                 }
             }
         }
+    }
+}
+
+template <int DTYPE>
+__device__ __forceinline__ void load_whole(const WeightsArgs &a, int h, int t0, int32_t page, int lane,
+                                           RawUnit<DTYPE> &r) {
+    constexpr int kBytes = DTYPE == NVFP4KV_DTYPE_NVFP4 ? 2304 : 4096, kX = DTYPE == NVFP4KV_DTYPE_NVFP4 ? 1 : 2;
+    const int g = lane >> 2, j = lane & 3;
+    const uint8_t *grp = a.pool + ((int64_t)page * a.Hkv + h) * a.slab + ((t0 & (a.P - 1)) >> 4) * kBytes;
+    const uint8_t *code = grp + g * (64 * kX) + j * (16 * kX), *scale = grp + 1024 + g * 8 + j * 2;
+#pragma unroll
+    for (int i = 0; i < kGroupsW; i++) {
+#pragma unroll
+        for (int e = 0; e < 2; e++)
+#pragma unroll
+            for (int x = 0; x < kX; x++)
+                r.code[i][e][x] = __ldg(reinterpret_cast<const uint4 *>(code + i * kBytes + e * 512 * kX) + x);
+        if (DTYPE == NVFP4KV_DTYPE_NVFP4)
+            r.scale[i] = (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(scale + i * kBytes)) |
+                         ((uint32_t)__ldg(reinterpret_cast<const uint16_t *>(scale + i * kBytes + 64)) << 16);
     }
 }
 
@@ -183,8 +199,34 @@ __device__ __forceinline__ void load_query(const WeightsArgs &a, int b, int h, i
     }
 }
 
+// A warp's units in order.
+struct UnitIter {
+    int b, h, t, n;   // sequence, kv head, first token, the sequence's rows
+    int64_t left;     // units of the piece from this one on
+};
+
+__device__ __forceinline__ void next_unit(const WeightsArgs &a, UnitIter &it) {
+    it.left--;
+    it.t += kUnit;
+    if (it.t < it.n) return;
+    it.t = 0;
+    if (++it.h < a.Hkv || it.left <= 0) return;
+    it.h = 0;
+    do {              // left > 0: a later sequence has units
+        it.b++;
+        it.n = clamp_rows(__ldg(a.seq_lens + it.b), a.cap);
+    } while (it.n == 0);
+}
+
+// Page of the unit's lane-th group (lanes 0 .. kGroupsW - 1).
+__device__ __forceinline__ int32_t unit_page(const WeightsArgs &a, const UnitIter &it, int lane) {
+    const int t = it.t + 16 * lane;
+    if (lane >= kGroupsW || it.left <= 0 || t >= it.n) return -1;
+    return __ldg(a.block_table + (int64_t)it.b * a.max_pages + (t >> a.log2P));
+}
+
 template <int DTYPE, int NT, bool kStats>
-__global__ void __launch_bounds__(kThreads) weights_kernel(WeightsArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) weights_kernel(WeightsArgs a) {
     __shared__ FlatScratch<kThreads> scratch;
     pdl_wait();   // lengths, q and the cache may come from earlier work; the weights kernel reads the partials
     pdl_launch_dependents();
@@ -209,12 +251,33 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(WeightsArgs a) {
         b, first);
     if (worker >= pieces) return;
     const int64_t u1 = flat_begin(worker + 1, total, pieces);
-    int n = rows(b), nu = units(b);
-    int h = (int)((u0 - first) / nu), un = (int)((u0 - first) % nu);
+    UnitIter it;
+    it.b = b;
+    it.n = rows(b);
+    const int nu0 = units(b);
+    it.h = (int)((u0 - first) / nu0);
+    it.t = (int)((u0 - first) % nu0) * kUnit;
+    it.left = u1 - u0;
     uint32_t qf[NT][16];
     float fac[NT][2], m[NT][2], l[NT][2];   // kStats: running maximum and sum; else m = L of the pair's heads
     bool fresh = true;
-    for (int64_t u = u0; u < u1; u++) {
+    int64_t u = u0;                         // position in the flat order
+    UnitIter nx = it;                       // its pages are requested one unit ahead
+    int32_t npage = unit_page(a, nx, lane);
+    for (; it.left > 0; u++) {
+        RawUnit<DTYPE> raw;
+        // a whole unit on one page (pages of 64 tokens or more): no masks, one address
+        const bool whole = it.t + kUnit <= it.n && a.P >= kUnit;
+        const int32_t page0 = __shfl_sync(0xffffffffu, npage, 0);
+        const bool fast = whole && page0 >= 0 && page0 < a.num_pages;
+        if (fast)
+            load_whole<DTYPE>(a, it.h, it.t, page0, lane, raw);
+        else
+            load_unit<DTYPE>(a, it.h, it.t, it.n, npage, lane, raw);
+        next_unit(a, nx);
+        npage = unit_page(a, nx, lane);
+        b = it.b;
+        const int h = it.h, n = it.n, t0 = it.t;
         if (fresh) {
             load_query<NT>(a, b, h, lane, qf, fac);
             if (kStats) {
@@ -224,8 +287,9 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(WeightsArgs a) {
                     l[x][0] = l[x][1] = 0.f;
                 }
             } else {
-                // the pair's units [first + h nu, first + (h + 1) nu) were covered by these warps
-                const int64_t p = (int64_t)b * a.Hkv + h, p0 = first + (int64_t)h * nu;
+                // the pair's units [p0, p0 + nu) were covered by these warps
+                const int nu = (n + kUnit - 1) / kUnit;
+                const int64_t p = (int64_t)b * a.Hkv + h, p0 = u - t0 / kUnit;
                 const int64_t w0 = flat_piece(p0, total, pieces), w1 = flat_piece(p0 + nu - 1, total, pieces);
                 float mine[NT * 8];
 #pragma unroll
@@ -259,11 +323,7 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(WeightsArgs a) {
                         }
                 }
             }
-            fresh = false;
         }
-        const int t0 = un * kUnit;
-        RawUnit<DTYPE> raw;
-        load_unit<DTYPE>(a, b, h, t0, n, lane, raw);
         const int g = lane >> 2, j = lane & 3;
         float *dst = a.scores + ((int64_t)b * a.Hkv + h) * a.score_stride + t0 + g + 8 * (j & 1);
         float old[kGroupsW];
@@ -271,7 +331,7 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(WeightsArgs a) {
 #pragma unroll
             for (int i = 0; i < kGroupsW; i++) {
                 old[i] = 0.f;
-                if (j < 2 && t0 + 16 * i + g + 8 * j < n) old[i] = dst[16 * i];
+                if (j < 2 && (fast || t0 + 16 * i + g + 8 * j < n)) old[i] = dst[16 * i];
             }
         }
         float sc[kStats ? kGroupsW : 1][NT][4];
@@ -279,7 +339,7 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(WeightsArgs a) {
         for (int i = 0; i < kGroupsW; i++) {
             float c[NT][4];
             group_scores<DTYPE, NT>(raw, i, qf, c);
-            const bool ok0 = t0 + 16 * i + g < n, ok1 = t0 + 16 * i + g + 8 < n;
+            const bool ok0 = fast || t0 + 16 * i + g < n, ok1 = fast || t0 + 16 * i + g + 8 < n;
             if (kStats) {
 #pragma unroll
                 for (int x = 0; x < NT; x++)
@@ -319,39 +379,25 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(WeightsArgs a) {
                     }
                 }
         }
-        un++;
-        if (un == nu || u + 1 == u1) {
-            if (kStats) {   // this warp's partial of the pair: join the eight token rows of each head
-                const int64_t at = (worker + (int64_t)b * a.Hkv + h) * a.G;
+        next_unit(a, it);
+        fresh = it.left <= 0 || it.b != b || it.h != h;
+        if (kStats && fresh) {   // this warp's partial of the pair: join the eight token rows of each head
+            const int64_t at = (worker + (int64_t)b * a.Hkv + h) * a.G;
 #pragma unroll
-                for (int x = 0; x < NT; x++)
+            for (int x = 0; x < NT; x++)
 #pragma unroll
-                    for (int e = 0; e < 2; e++) {
-                        float mm = m[x][e], ll = l[x][e];
+                for (int e = 0; e < 2; e++) {
+                    float mm = m[x][e], ll = l[x][e];
 #pragma unroll
-                        for (int s = 4; s < 32; s <<= 1) {
-                            const float om = __shfl_xor_sync(0xffffffffu, mm, s), ol = __shfl_xor_sync(0xffffffffu, ll, s);
-                            const float mx = fmaxf(mm, om);
-                            if (mx != kNegInfW) ll = ll * ex2(mm - mx) + ol * ex2(om - mx);
-                            mm = mx;
-                        }
-                        const int hd = 8 * x + 2 * j + e;
-                        if (g == 0 && hd < a.G) a.part[at + hd] = make_float2(mm, ll);
+                    for (int s = 4; s < 32; s <<= 1) {
+                        const float om = __shfl_xor_sync(0xffffffffu, mm, s), ol = __shfl_xor_sync(0xffffffffu, ll, s);
+                        const float mx = fmaxf(mm, om);
+                        if (mx != kNegInfW) ll = ll * ex2(mm - mx) + ol * ex2(om - mx);
+                        mm = mx;
                     }
-            }
-            if (un == nu) {
-                fresh = true;
-                un = 0;
-                if (++h == a.Hkv && u + 1 < u1) {
-                    h = 0;
-                    first += (int64_t)a.Hkv * nu;
-                    do {
-                        b++;
-                        n = rows(b);
-                        nu = units(b);
-                    } while (nu == 0);   // u + 1 < u1 <= total: a later sequence has units
+                    const int hd = 8 * x + 2 * j + e;
+                    if (g == 0 && hd < a.G) a.part[at + hd] = make_float2(mm, ll);
                 }
-            }
         }
     }
 }

@@ -120,6 +120,63 @@ __device__ __forceinline__ uint32_t e2m1_code_exact(float a, float den, float g)
     return fix_code(c, 7u, a, den, g, [](uint32_t k) { return e2m1_magnitude(k); });
 }
 
+// Tensor scales of ordinary size take a shorter way to the same roundings: the
+// quotient is estimated as a * rcp(den g), within a relative 2^-22 (reciprocal one
+// unit in the last place, two roundings; neither den g nor its reciprocal leaves the
+// normal range for den in [2^-9, 2688]), and rounded twice, at (1 - 2^-20) and (1 +
+// 2^-20) times the estimate.  Where both give one code, so does the exact quotient
+// between them; where they differ (one midpoint lies between), the midpoint is
+// compared exactly, as above.
+constexpr float kPlainScaleMin = 0x1p-60f, kPlainScaleMax = 0x1p60f;
+constexpr float kBelow = 1.0f - 0x1p-20f, kAbove = 1.0f + 0x1p-20f;
+
+__device__ __forceinline__ bool plain_scale(float g) { return g >= kPlainScaleMin && g <= kPlainScaleMax; }
+
+__device__ __forceinline__ uint32_t e4m3_code_between(float a, float den, float g) {
+    const float q = a * rcp_approx(den * g);
+    const uint32_t c2 = f32x2_to_e4m3x2(q * kAbove, q * kBelow);
+    const uint32_t lo = c2 & 0x7fu, hi = (c2 >> 8) & 0x7fu;
+    if (lo == hi) return lo;
+    const float d = __fmaf_rn(0.5f * (e4m3_magnitude(lo) + e4m3_magnitude(hi)) * den, g, -a);
+    return d < 0.0f || (d == 0.0f && (hi & 1u) == 0) ? hi : lo;
+}
+
+// Eight floats -> one word of eight E2M1 codes (element 2i in the low nibble of byte i).
+__device__ __forceinline__ uint32_t f32x8_to_e2m1x8(const float2 &a, const float2 &b, const float2 &c, const float2 &d) {
+    uint32_t r;
+    asm("{ .reg .b8 p, q, s, t;\n"
+        "  cvt.rn.satfinite.e2m1x2.f32 p, %2, %1; cvt.rn.satfinite.e2m1x2.f32 q, %4, %3;\n"
+        "  cvt.rn.satfinite.e2m1x2.f32 s, %6, %5; cvt.rn.satfinite.e2m1x2.f32 t, %8, %7;\n"
+        "  mov.b32 %0, {p, q, s, t}; }"
+        : "=r"(r)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y), "f"(d.x), "f"(d.y));
+    return r;
+}
+
+// Eight values (the BF16 pairs w[0..3]) -> the codes of x / (sd g).
+__device__ __forceinline__ uint32_t e2m1x8_between(const uint32_t *w, float sd, float g, float r) {
+    float2 lo[4], hi[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const float2 y = mul2(make_float2(bf16_lo(w[i]), bf16_hi(w[i])), r);
+        lo[i] = mul2(y, kBelow);
+        hi[i] = mul2(y, kAbove);
+    }
+    uint32_t c = f32x8_to_e2m1x8(lo[0], lo[1], lo[2], lo[3]);
+    const uint32_t up = f32x8_to_e2m1x8(hi[0], hi[1], hi[2], hi[3]), diff = c ^ up;
+    if (diff) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            if (!((diff >> (4 * i)) & 0xfu)) continue;
+            const float a = fabsf((i & 1) ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]));
+            const uint32_t k = (c >> (4 * i)) & 7u;   // the code below the midpoint; the one above is k + 1
+            const float d = __fmaf_rn(0.5f * (e2m1_magnitude(k) + e2m1_magnitude(k + 1)) * sd, g, -a);
+            if (d < 0.0f || (d == 0.0f && (k & 1u))) c = (c & ~(0xfu << (4 * i))) | (up & (0xfu << (4 * i)));
+        }
+    }
+    return c;
+}
+
 // The e2m1 * e4m3 (or e4m3) value p, exact in FP32, times g, rounded once to
 // BF16 (nearest-even; subnormal steps of 2^-133; infinity on overflow).
 // hi = fl(p g) and lo = p g - hi exactly (an FMA, exact while p g >= 2^-118);
@@ -161,7 +218,9 @@ __device__ __forceinline__ void quantize_block16(const uint4 &a, const uint4 &b,
     const bool tiny = !kUnitScale && g < kTinyTensorScale;   // decide at (x, g) 2^64: same quotients
     const float gs = tiny ? g * kTinyRescale : g;
     if (tiny) amax *= kTinyRescale;
+    const bool plain = !kUnitScale && plain_scale(g) && amax_bits <= 0x7f80u;   // (NaN: the general way)
     const uint32_t s = kUnitScale ? f32x2_to_e4m3x2(0.0f, __fmul_rn(amax, kOneSixth)) & 0xffu
+                       : plain    ? e4m3_code_between(amax, 6.0f, g)
                                   : e4m3_code_exact(amax, 6.0f, gs);
     scale_byte = s;
     const float sd = __half2float(__ushort_as_half((uint16_t)(e4m3x2_to_f16x2(s) & 0xffffu)));
@@ -184,6 +243,10 @@ __device__ __forceinline__ void quantize_block16(const uint4 &a, const uint4 &b,
         }
         packed[0] = f16x2x4_to_e2m1x8(h[0], h[1], h[2], h[3]);
         packed[1] = f16x2x4_to_e2m1x8(h[4], h[5], h[6], h[7]);
+    } else if (plain) {
+        const float r = rcp_approx(sd * g);
+        packed[0] = e2m1x8_between(w, sd, g, r);
+        packed[1] = e2m1x8_between(w + 4, sd, g, r);
     } else {
         const float xs = tiny ? kTinyRescale : 1.0f;
 #pragma unroll
@@ -211,6 +274,14 @@ __device__ __forceinline__ uint32_t f32x2_to_bf16x2(float hi, float lo) {
 template <bool kUnit>
 __device__ __forceinline__ uint32_t f16x2_to_bf16x2_scaled(uint32_t x, float g) {
     if (kUnit) return f32x2_to_bf16x2(f16_hi(x), f16_lo(x));
+    if (plain_scale(g)) {
+        // No product of a nonzero value leaves FP32's normal range; its FP32 rounding decides
+        // the BF16 one unless it sits exactly on a midpoint, where the exact product may lie
+        // to either side.
+        const float lo = f16_lo(x) * g, hi = f16_hi(x) * g;
+        if ((__float_as_uint(lo) & 0xffffu) != 0x8000u && (__float_as_uint(hi) & 0xffffu) != 0x8000u)
+            return f32x2_to_bf16x2(hi, lo);
+    }
     return bf16_of_product(f16_lo(x), g) | (bf16_of_product(f16_hi(x), g) << 16);
 }
 
