@@ -15,11 +15,13 @@
 //   weights  joins the partials of a pair into L = m + log2 l, forms the scores'
 //            products again and adds sum_j 2^(s_j - L_j): no atomics, one
 //            addition per entry.
-// The scores come from mma.sync m16n8k16 with the 16 tokens of a group on M and
-// the heads on N.  The contraction's order is free, so thread j of a quad takes
-// the dimensions 32j .. 32j + 31 of its tokens: one 16-byte load of codes each,
-// coalesced over the warp, straight from the page to registers; e2m1 x e4m3 is
-// an exact FP16 value, and q is FP16 after a power-of-two pre-scale a head
+// Every warp has a ring of three 64-token stages that it fills itself with bulk
+// copies of the groups' K halves, two units ahead (loads to registers left the
+// warps waiting for memory a third of the time, and held 36 registers).  The
+// scores come from mma.sync m16n8k16 with the 16 tokens of a group on M and the
+// heads on N.  The contraction's order is free, so thread j of a quad takes the
+// dimensions 32j .. 32j + 31 of its tokens: 16 contiguous bytes of codes a token;
+// e2m1 x e4m3 is an exact FP16 value, and q is FP16 after a power-of-two pre-scale a head
 // (exact above 2^-29 of its largest value), undone in the FP32 score factor.
 #include <mutex>
 
@@ -36,7 +38,17 @@ constexpr int kThreads = 256;
 constexpr int kWarpsW = kThreads / 32;
 constexpr int kUnit = 64;                     // tokens per unit
 constexpr int kGroupsW = kUnit / 16;
+constexpr int kStagesW = 3;                   // ring stages of a warp
+constexpr uint32_t kWaitLimitW = 1u << 24;
 constexpr float kNegInfW = -__builtin_huge_valf();
+
+template <int DTYPE>
+struct KHalf {   // a group's K bytes: NVFP4 codes [16][64] and scales [16][8], or FP8 [16][128]
+    static constexpr int kGroup = DTYPE == NVFP4KV_DTYPE_NVFP4 ? 2304 : 4096;
+    static constexpr int kBytes = DTYPE == NVFP4KV_DTYPE_NVFP4 ? 1152 : 2048;
+    static constexpr int kStage = kGroupsW * kBytes;
+    static constexpr int kSmem = kWarpsW * kStagesW * kStage;
+};
 
 struct WeightsArgs {
     const uint8_t *pool;
@@ -54,84 +66,23 @@ struct WeightsArgs {
     unsigned *err;
 };
 
-template <int DTYPE>
-struct RawUnit {  // one thread's share of a unit's K: tokens g and g + 8 of each group, 32 dimensions
-    uint4 code[kGroupsW][2][DTYPE == NVFP4KV_DTYPE_NVFP4 ? 1 : 2];
-    uint32_t scale[kGroupsW];   // two E4M3 bytes of token g (low half) and of token g + 8
-};
-
-template <int DTYPE>
-__device__ __forceinline__ void load_unit(const WeightsArgs &a, int h, int t0, int n, int32_t page, int lane,
-                                          RawUnit<DTYPE> &r) {
-    const int g = lane >> 2, j = lane & 3;
-    if (lane < kGroupsW && t0 + 16 * lane < n && (page < 0 || page >= a.num_pages)) {
-        flag_error(a.err, kErrPage);
-        page = -1;
-    }
-    constexpr int kBytes = DTYPE == NVFP4KV_DTYPE_NVFP4 ? 2304 : 4096;
-#pragma unroll
-    for (int i = 0; i < kGroupsW; i++) {
-        const int32_t pg = __shfl_sync(0xffffffffu, page, i);
-        const int t = t0 + 16 * i;
-        const uint8_t *grp = a.pool + ((int64_t)pg * a.Hkv + h) * a.slab + ((t & (a.P - 1)) >> 4) * kBytes;
-        r.scale[i] = 0;
-#pragma unroll
-        for (int e = 0; e < 2; e++) {
-            const int row = g + 8 * e;
-            const bool ok = pg >= 0 && t + row < n;
-            if (DTYPE == NVFP4KV_DTYPE_NVFP4) {
-                r.code[i][e][0] = make_uint4(0, 0, 0, 0);
-                if (ok) {
-                    r.code[i][e][0] = __ldg(reinterpret_cast<const uint4 *>(grp + row * 64 + j * 16));
-                    r.scale[i] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(grp + 1024 + row * 8 + j * 2)) << (16 * e);
-                }
-            } else {
-#pragma unroll
-                for (int x = 0; x < (DTYPE == NVFP4KV_DTYPE_NVFP4 ? 1 : 2); x++) {
-                    r.code[i][e][x] = make_uint4(0, 0, 0, 0);
-                    if (ok) r.code[i][e][x] = __ldg(reinterpret_cast<const uint4 *>(grp + row * 128 + j * 32) + x);
-                }
-            }
-        }
-    }
-}
-
-template <int DTYPE>
-__device__ __forceinline__ void load_whole(const WeightsArgs &a, int h, int t0, int32_t page, int lane,
-                                           RawUnit<DTYPE> &r) {
-    constexpr int kBytes = DTYPE == NVFP4KV_DTYPE_NVFP4 ? 2304 : 4096, kX = DTYPE == NVFP4KV_DTYPE_NVFP4 ? 1 : 2;
-    const int g = lane >> 2, j = lane & 3;
-    const uint8_t *grp = a.pool + ((int64_t)page * a.Hkv + h) * a.slab + ((t0 & (a.P - 1)) >> 4) * kBytes;
-    const uint8_t *code = grp + g * (64 * kX) + j * (16 * kX), *scale = grp + 1024 + g * 8 + j * 2;
-#pragma unroll
-    for (int i = 0; i < kGroupsW; i++) {
-#pragma unroll
-        for (int e = 0; e < 2; e++)
-#pragma unroll
-            for (int x = 0; x < kX; x++)
-                r.code[i][e][x] = __ldg(reinterpret_cast<const uint4 *>(code + i * kBytes + e * 512 * kX) + x);
-        if (DTYPE == NVFP4KV_DTYPE_NVFP4)
-            r.scale[i] = (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(scale + i * kBytes)) |
-                         ((uint32_t)__ldg(reinterpret_cast<const uint16_t *>(scale + i * kBytes + 64)) << 16);
-    }
-}
-
-// Scores (before the factor) of group i's 16 tokens: c[nt] = rows g, g + 8 x heads 8 nt + 2j, + 1.
+// Scores (before the factor) of 16 tokens whose K half lies at k: c[x] = rows g, g + 8 x heads 8 x + 2j, + 1.
 template <int DTYPE, int NT>
-__device__ __forceinline__ void group_scores(const RawUnit<DTYPE> &r, int i, const uint32_t (&qf)[NT][16],
-                                             float (&c)[NT][4]) {
+__device__ __forceinline__ void group_scores(const uint8_t *k, int lane, const uint32_t (&qf)[NT][16], float (&c)[NT][4]) {
+    const int g = lane >> 2, j = lane & 3;
 #pragma unroll
     for (int x = 0; x < NT; x++) c[x][0] = c[x][1] = c[x][2] = c[x][3] = 0.f;
     uint32_t f[2][16];   // token g / g + 8: f16 pairs of dimensions 32j + 2p, + 1
 #pragma unroll
     for (int e = 0; e < 2; e++) {
+        const int row = g + 8 * e;
         if (DTYPE == NVFP4KV_DTYPE_NVFP4) {
-            const uint4 w = r.code[i][e][0];
+            const uint4 w = *reinterpret_cast<const uint4 *>(k + row * 64 + j * 16);
             e2m1x8_to_f16x2x4(w.x, f[e][0], f[e][1], f[e][2], f[e][3]);
             e2m1x8_to_f16x2x4(w.y, f[e][4], f[e][5], f[e][6], f[e][7]);
             e2m1x8_to_f16x2x4(w.z, f[e][8], f[e][9], f[e][10], f[e][11]);
             e2m1x8_to_f16x2x4(w.w, f[e][12], f[e][13], f[e][14], f[e][15]);
-            const uint32_t s2 = e4m3x2_to_f16x2((r.scale[i] >> (16 * e)) & 0xffffu);
+            const uint32_t s2 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(k + 1024 + row * 8 + j * 2));
             const uint32_t lo = __byte_perm(s2, s2, 0x1010), hi = __byte_perm(s2, s2, 0x3232);
 #pragma unroll
             for (int p = 0; p < 8; p++) {
@@ -139,10 +90,9 @@ __device__ __forceinline__ void group_scores(const RawUnit<DTYPE> &r, int i, con
                 f[e][8 + p] = hmul2(f[e][8 + p], hi);
             }
         } else {
-            constexpr int kX = DTYPE == NVFP4KV_DTYPE_NVFP4 ? 1 : 2;
 #pragma unroll
-            for (int x = 0; x < kX; x++) {
-                const uint4 v = r.code[i][e][x];
+            for (int x = 0; x < 2; x++) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(k + row * 128 + j * 32 + x * 16);
                 const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int p = 0; p < 4; p++) {
@@ -227,7 +177,11 @@ __device__ __forceinline__ int32_t unit_page(const WeightsArgs &a, const UnitIte
 
 template <int DTYPE, int NT, bool kStats>
 __global__ void __launch_bounds__(kThreads, 2) weights_kernel(WeightsArgs a) {
+    using H = KHalf<DTYPE>;
+    extern __shared__ __align__(128) uint8_t ring_all[];   // [warp][stage][group]
     __shared__ FlatScratch<kThreads> scratch;
+    __shared__ uint64_t bars[kWarpsW][kStagesW];
+    __shared__ int abort_all;
     pdl_wait();   // lengths, q and the cache may come from earlier work; the weights kernel reads the partials
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
@@ -249,6 +203,8 @@ __global__ void __launch_bounds__(kThreads, 2) weights_kernel(WeightsArgs a) {
             return u0 = worker < pieces ? flat_begin(worker, t, pieces) : -1;
         },
         b, first);
+    if (threadIdx.x == 0) abort_all = 0;
+    __syncthreads();
     if (worker >= pieces) return;
     const int64_t u1 = flat_begin(worker + 1, total, pieces);
     UnitIter it;
@@ -262,20 +218,60 @@ __global__ void __launch_bounds__(kThreads, 2) weights_kernel(WeightsArgs a) {
     float fac[NT][2], m[NT][2], l[NT][2];   // kStats: running maximum and sum; else m = L of the pair's heads
     bool fresh = true;
     int64_t u = u0;                         // position in the flat order
-    UnitIter nx = it;                       // its pages are requested one unit ahead
+    // The warp's ring: unit i of the piece into stage i % kStagesW, requested kStagesW - 1 units
+    // ahead (its pages one unit earlier still).
+    uint8_t *ring = ring_all + (threadIdx.x >> 5) * (kStagesW * H::kStage);
+    uint64_t *bar = bars[threadIdx.x >> 5];
+    const volatile int *abort_flag = &abort_all;
+    if (lane == 0) {
+        for (int i = 0; i < kStagesW; i++) mbar_init(&bar[i], 1);
+        fence_mbar_init();
+    }
+    __syncwarp();
+    auto request = [&](const UnitIter &x, int32_t page, int stage) {   // lane i < kGroupsW: group i
+        uint8_t *dst = ring + stage * H::kStage + lane * H::kBytes;
+        const int t = x.t + 16 * lane;
+        bool copy = x.left > 0 && lane < kGroupsW && t < x.n;
+        if (copy && (page < 0 || page >= a.num_pages)) {   // reads as zeros
+            flag_error(a.err, kErrPage);
+            for (int i = 0; i < H::kBytes / 16; i++) reinterpret_cast<uint4 *>(dst)[i] = make_uint4(0, 0, 0, 0);
+            copy = false;
+        }
+        const unsigned copies = __popc(__ballot_sync(0xffffffffu, copy));
+        if (lane == 0) mbar_arrive_expect_tx(&bar[stage], copies * H::kBytes);
+        __syncwarp();
+        if (copy)
+            bulk_g2s(dst, a.pool + ((int64_t)page * a.Hkv + x.h) * a.slab + ((t & (a.P - 1)) >> 4) * H::kGroup, H::kBytes,
+                     &bar[stage]);
+    };
+    UnitIter nx = it;
     int32_t npage = unit_page(a, nx, lane);
-    for (; it.left > 0; u++) {
-        RawUnit<DTYPE> raw;
-        // a whole unit on one page (pages of 64 tokens or more): no masks, one address
-        const bool whole = it.t + kUnit <= it.n && a.P >= kUnit;
-        const int32_t page0 = __shfl_sync(0xffffffffu, npage, 0);
-        const bool fast = whole && page0 >= 0 && page0 < a.num_pages;
-        if (fast)
-            load_whole<DTYPE>(a, it.h, it.t, page0, lane, raw);
-        else
-            load_unit<DTYPE>(a, it.h, it.t, it.n, npage, lane, raw);
+#pragma unroll
+    for (int i = 0; i < kStagesW - 1; i++) {
+        if (nx.left <= 0) break;
+        request(nx, npage, i);
         next_unit(a, nx);
         npage = unit_page(a, nx, lane);
+    }
+    int stage = 0, ahead = kStagesW - 1;
+    uint32_t parity = 0;
+    bool ok = true;
+    for (; it.left > 0; u++) {
+        if (nx.left > 0) {   // into the stage of the unit before this one, which the whole warp has read
+            __syncwarp();
+            request(nx, npage, ahead);
+            next_unit(a, nx);
+            npage = unit_page(a, nx, lane);
+        }
+        if (++ahead == kStagesW) ahead = 0;
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bar[stage], parity, kWaitLimitW, abort_flag));
+        if (!ok) break;
+        const uint8_t *unit = ring + stage * H::kStage;
+        if (++stage == kStagesW) {
+            stage = 0;
+            parity ^= 1;
+        }
+        const bool fast = it.t + kUnit <= it.n;   // a whole unit: no masks
         b = it.b;
         const int h = it.h, n = it.n, t0 = it.t;
         if (fresh) {
@@ -338,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 2) weights_kernel(WeightsArgs a) {
 #pragma unroll
         for (int i = 0; i < kGroupsW; i++) {
             float c[NT][4];
-            group_scores<DTYPE, NT>(raw, i, qf, c);
+            group_scores<DTYPE, NT>(unit + i * H::kBytes, lane, qf, c);
             const bool ok0 = fast || t0 + 16 * i + g < n, ok1 = fast || t0 + 16 * i + g + 8 < n;
             if (kStats) {
 #pragma unroll
@@ -400,6 +396,17 @@ __global__ void __launch_bounds__(kThreads, 2) weights_kernel(WeightsArgs a) {
                 }
         }
     }
+    if (!ok) {   // no copy may still be writing when the CTA's memory is freed
+        abort_all = 1;
+        if (lane == 0) flag_error(a.err, kErrTimeout);
+        for (int i = 0; i < kStagesW - 1 && it.left > nx.left; i++, it.left--) {
+            mbar_wait_bounded(&bar[stage], parity, kWaitLimitW, nullptr);
+            if (++stage == kStagesW) {
+                stage = 0;
+                parity ^= 1;
+            }
+        }
+    }
 }
 
 template <bool kStats>
@@ -410,6 +417,8 @@ const void *weights_fn(int dtype, int nt) {
     return nt == 1 ? reinterpret_cast<const void *>(&weights_kernel<1, 1, kStats>)
                    : reinterpret_cast<const void *>(&weights_kernel<1, 2, kStats>);
 }
+
+int weights_smem(int dtype) { return dtype == NVFP4KV_DTYPE_NVFP4 ? KHalf<0>::kSmem : KHalf<1>::kSmem; }
 
 constexpr int kMaxDevicesW = 64;
 std::mutex g_mu_w;
@@ -428,9 +437,13 @@ int weights_workers(int dtype, int group, cudaError_t *status) {
         int &w = g_workers[dev][dtype][nt - 1];
         if (!w) {
             int sms = 0, a = 0, b = 0;
+            const int smem = weights_smem(dtype);
+            const void *fa = weights_fn<true>(dtype, nt), *fb = weights_fn<false>(dtype, nt);
             e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-            if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&a, weights_fn<true>(dtype, nt), kThreads, 0);
-            if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, weights_fn<false>(dtype, nt), kThreads, 0);
+            if (e == cudaSuccess) e = cudaFuncSetAttribute(fa, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e == cudaSuccess) e = cudaFuncSetAttribute(fb, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&a, fa, kThreads, smem);
+            if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, fb, kThreads, smem);
             if (e == cudaSuccess) w = sms * (a < b ? (a > 0 ? a : 1) : (b > 0 ? b : 1)) * kWarpsW;
         }
         out = w;
@@ -471,9 +484,9 @@ cudaError_t launch_weights(const nvfp4kv_cache &c, const void *q, int batch, int
     a.err = err;
     const int nt = a.G <= 8 ? 1 : 2;
     void *args[] = {&a};
-    cudaError_t e = launch_pdl(weights_fn<true>(c.dtype, nt), (unsigned)(workers / kWarpsW), kThreads, 0, stream, args);
+    cudaError_t e = launch_pdl(weights_fn<true>(c.dtype, nt), (unsigned)(workers / kWarpsW), kThreads, (size_t)weights_smem(c.dtype), stream, args);
     if (e != cudaSuccess) return e;
-    return launch_pdl(weights_fn<false>(c.dtype, nt), (unsigned)(workers / kWarpsW), kThreads, 0, stream, args);
+    return launch_pdl(weights_fn<false>(c.dtype, nt), (unsigned)(workers / kWarpsW), kThreads, (size_t)weights_smem(c.dtype), stream, args);
 }
 
 }  // namespace nvfp4kv

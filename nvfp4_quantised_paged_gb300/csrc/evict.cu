@@ -1,22 +1,23 @@
 // evict.cu -- the tokens of largest score of every sequence and kv head, moved into new pages.
 //
 // Two kernels:
-//   select   one cluster of C CTAs per (sequence, kv head).  With n > keep rows
-//            the smallest kept key is found by a radix select over the scores'
-//            order-preserving 32-bit keys, 8 bits a round: each CTA counts its
-//            part of the rows in shared memory, the cluster adds the 256 counts
-//            up through distributed shared memory and every CTA picks the same
-//            digit.  Rows that must stay (the first `sink`, the last `recent`)
-//            have the largest key; ties at the border go to the lowest index.
-//            Then the kept indices are written in order: each warp counts and
-//            later compacts a contiguous part of the rows, its offset coming
-//            from one scan over the CTA's warps and one over the cluster.  Keys
-//            stay in shared memory between the rounds as far as they fit.
-//   move     one warp per 16-row group of the new pages gathers its rows and
-//            writes the group's contiguous bytes.
-// Both are bound by latency and HBM: 4 B of score per (row, head), then 144 B
-// read and written per kept row (256 B for FP8).  Nothing is atomic in global
-// memory, so the result does not depend on timing.
+//   select   finds the smallest kept key of each (sequence, kv head) with n > keep rows
+//            over the scores' order-preserving 32-bit keys.  Rows that must stay (the
+//            first `sink`, the last `recent`) have the largest key; ties at the border
+//            go to the lowest index; the kept indices are written in order.  Up to 32,768
+//            rows one CTA holds the keys in registers (select_one_kernel).  Longer
+//            segments take a cluster of up to eight CTAs and a radix select of 8 bits a
+//            round: each CTA counts its part of the rows in shared memory, the cluster
+//            adds the 256 counts up through distributed shared memory and every CTA picks
+//            the same digit; then each warp counts and compacts a contiguous part of the
+//            rows, its offset coming from one scan over the CTA's warps and one over the
+//            cluster.  Keys stay in shared memory between the rounds as far as they fit.
+//            (16 x 8 segments of up to 32,768 rows: 29 us with one CTA each, 66 us with
+//            clusters of four.)
+//   move     one warp per 16-row group of the new pages gathers its rows and writes the
+//            group's contiguous bytes: 36 us for 524,288 rows, which read 288 bytes of
+//            32-byte sectors each for their 144 and write 144: 6.3 TB/s.
+// Nothing is atomic in global memory, so the result does not depend on timing.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -33,6 +34,7 @@ constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kKeyCache = 16384;            // keys of a CTA's part kept in shared memory (64 KB)
 constexpr int kMaxCluster = 8;
+
 constexpr int kTargetCtasSel = 304;         // two CTAs per SM of a 152-SM GPU
 
 struct SelectArgs {
@@ -49,11 +51,252 @@ struct SelectArgs {
 };
 
 // Keys order as the scores do (-0 below +0 would split equal scores: both give
-// the key of 0); a NaN gets 0, below -inf.
+// the key of 0); a NaN gets 1, below -inf (0: no row).
 __device__ __forceinline__ uint32_t score_key(float x) {
-    if (x != x) return 0u;
+    if (x != x) return 1u;
     const uint32_t u = __float_as_uint(x + 0.0f);   // -0 + 0 = +0
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// What both selections write around the kept rows of a segment: its new length, -1
+// and score 0 behind it, and, where every row stays, all of it (true is returned).
+__device__ __forceinline__ bool select_edges(const SelectArgs &a, int seg, int n, int32_t len, int first, int step,
+                                             const float *src, int32_t *kept, float *dst) {
+    const int new_n = min(n, a.keep);
+    if (first == 0 && seg % a.Hkv == 0) {
+        a.new_lens[seg / a.Hkv] = new_n;
+        if (len < 0 || (int64_t)len > a.cap) flag_error(a.err, kErrSeqLen);
+    }
+    for (int i = new_n + first; i < a.keep; i += step) kept[i] = -1;
+    const int64_t end = a.new_score_stride;
+    int64_t i0 = new_n;                       // zeros: single ones up to a 16-byte boundary, then four at a time
+    while (i0 < end && (reinterpret_cast<uintptr_t>(dst + i0) & 15)) {
+        if (first == 0) dst[i0] = 0.f;
+        i0++;
+    }
+    for (int64_t i = i0 + 4 * (int64_t)first; i < end; i += 4 * (int64_t)step) {
+        if (i + 4 <= end) {
+            *reinterpret_cast<float4 *>(dst + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+        } else {
+            for (int64_t x = i; x < end; x++) dst[x] = 0.f;
+        }
+    }
+    if (n > a.keep) return false;
+    for (int i = first; i < n; i += step) {
+        kept[i] = i;
+        dst[i] = src[i];
+    }
+    return true;
+}
+
+// One CTA a segment of up to kOneRows rows: every thread holds PER consecutive
+// keys in registers, and the border key is found bit by bit, a count over the CTA
+// each (counting digits in shared memory took 40 clocks a warp and 32 keys).  Most
+// of the rows are left out of that search: 512 keys spread over the rows are a
+// sample whose ranks, found by one warp, give two keys between which the border
+// almost always lies; one count over all rows confirms it, and the few keys between
+// them are searched alone.  (Where they do not, all keys are.)  The search ends as soon
+// as a border splits off exactly the rows wanted.  A thread's kept rows are consecutive
+// too: one scan places them all.
+// 256 threads up to 8,192 rows (several CTAs an SM, cheaper sums), 1,024 beyond.
+constexpr int kOnePer = 33;                  // odd: consecutive keys of 32 threads lie in 32 banks
+constexpr int kOneSmall = 256, kOneLarge = 1024;
+constexpr int kOneSmallRows = kOneSmall * (kOnePer - 1), kOneRows = kOneLarge * (kOnePer - 1);
+constexpr int kListPer = 8;                  // keys a thread has of the list between the two borders
+constexpr int kSample = 512, kSamplePer = kSample / 32;
+constexpr int kSampleBits = 20;              // of a sample border that are found (sign, exponent, 11 of the fraction)
+
+// Sum of c over the CTA's T threads; buf alternates between calls.
+template <int T>
+__device__ __forceinline__ uint32_t cta_sum(uint32_t c, uint32_t (&s_count)[2][32], int buf) {
+    c = __reduce_add_sync(0xffffffffu, c);
+    if ((threadIdx.x & 31) == 0) s_count[buf][threadIdx.x >> 5] = c;
+    __syncthreads();
+    return __reduce_add_sync(0xffffffffu, (threadIdx.x & 31) < T / 32 ? s_count[buf][threadIdx.x & 31] : 0u);
+}
+
+// Exclusive sum of v over the CTA's threads before this one, and the total.
+template <int T>
+__device__ __forceinline__ uint32_t cta_scan(uint32_t v, uint32_t (&s_count)[2][32], uint32_t &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t incl = v;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, x);
+        if (lane >= x) incl += y;
+    }
+    __syncthreads();                          // s_count is read
+    if (lane == 31) s_count[0][warp] = incl;
+    __syncthreads();
+    uint32_t w = lane < T / 32 ? s_count[0][lane] : 0u;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, w, x);
+        if (lane >= x) w += y;
+    }
+    total = __shfl_sync(0xffffffffu, w, 31);
+    const uint32_t before = __shfl_sync(0xffffffffu, w, warp ? warp - 1 : 0);
+    __syncthreads();                          // s_count may be written again
+    return (warp ? before : 0u) + incl - v;
+}
+
+// The largest border with at least `want` >= 1 of the CTA's keys (K a thread) not below it;
+// exact: there are just `want`.  The border has the bits of `border` above bit `top`.
+template <int T, int K>
+__device__ __forceinline__ uint32_t find_border(const uint32_t (&k)[K], uint32_t want, uint32_t border, int top,
+                                                uint32_t (&s_count)[2][32], bool &exact) {
+    exact = false;
+    for (int bit = top; bit >= 0; bit--) {
+        const uint32_t trial = border | (1u << bit);
+        uint32_t c = 0;
+#pragma unroll
+        for (int i = 0; i < K; i++) c += k[i] >= trial;
+        c = cta_sum<T>(c, s_count, bit & 1);
+        if (c >= want) border = trial;
+        if (c == want) {
+            exact = true;
+            break;
+        }
+    }
+    return border;
+}
+
+template <int T, int PER>
+__device__ __forceinline__ void select_rows(const SelectArgs &a, int n, int per, int32_t *kept, uint32_t *s_keys,
+                                            uint32_t (&s_count)[2][32]) {
+    const int t0 = (int)threadIdx.x * per, last = n - a.recent;
+    const uint32_t keep = (uint32_t)a.keep;
+    auto key_at = [&](int t) { return t < a.sink || t >= last ? 0xffffffffu : score_key(__uint_as_float(s_keys[t])); };
+    uint32_t k[PER];
+#pragma unroll
+    for (int i = 0; i < PER; i++) k[i] = i < per && t0 + i < n ? key_at(t0 + i) : 0u;   // (0: below every border)
+    uint32_t border = 0;
+    bool exact = false, found = false;
+    if (PER > 5) {
+        if (threadIdx.x < 64) {
+            // sample ranks r -+ d around the border's expected one: warp 0 finds the upper border, warp 1 the lower
+            const int lane = (int)threadIdx.x & 31, low = (int)threadIdx.x >> 5;
+            uint32_t x[kSamplePer];
+#pragma unroll
+            for (int i = 0; i < kSamplePer; i++) x[i] = key_at((int)((int64_t)n * (i * 32 + lane) / kSample));
+            const int r = (int)((int64_t)keep * kSample / n), d = 4 + (int)(3.0f * sqrtf((float)r));
+            const uint32_t want = (uint32_t)(low ? min(r + d, kSample) : max(r - d, 0));
+            uint32_t found_at = 0;
+            for (int bit = 31; bit > 31 - kSampleBits; bit--) {
+                const uint32_t trial = found_at | (1u << bit);
+                uint32_t c[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int i = 0; i < kSamplePer; i++) c[i & 3] += x[i] >= trial;
+                if (__reduce_add_sync(0xffffffffu, (c[0] + c[1]) + (c[2] + c[3])) >= want) found_at = trial;
+            }
+            // (the upper one no lower than the sample's border; no carry: the low bits are 0)
+            if (lane == 0) s_count[1][low] = low ? found_at : found_at + ((1u << (32 - kSampleBits)) - 1u);
+        }
+        __syncthreads();
+        const uint32_t hi = s_count[1][0], lo = s_count[1][1];
+        uint32_t c = 0;
+#pragma unroll
+        for (int i = 0; i < PER; i++) c += (k[i] >= hi ? 1u : 0u) + (k[i] >= lo ? 0x10000u : 0u);
+        c = cta_sum<T>(c, s_count, 0);           // (both at most kOneRows)
+        const uint32_t c_hi = c & 0xffffu, c_lo = c >> 16;
+        if (lo > 0 && c_hi < keep && keep <= c_lo && c_lo - c_hi <= T * kListPer) {
+            uint32_t own = 0, total;
+#pragma unroll
+            for (int i = 0; i < PER; i++) own += k[i] - lo < hi - lo;   // lo <= key < hi
+            uint32_t at = cta_scan<T>(own, s_count, total);
+#pragma unroll
+            for (int i = 0; i < PER; i++)
+                if (k[i] - lo < hi - lo) s_keys[at++] = k[i];   // (every thread has read its keys)
+            __syncthreads();
+            uint32_t x[kListPer];
+#pragma unroll
+            for (int i = 0; i < kListPer; i++)
+                x[i] = threadIdx.x + i * T < total ? s_keys[threadIdx.x + i * T] : 0u;
+            const uint32_t diff = lo ^ (hi - 1u);
+            const int top = diff ? 31 - __clz((int)diff) : -1;
+            border = lo & ~(top >= 0 ? (top == 31 ? 0xffffffffu : (2u << top) - 1u) : 0u);
+            border = find_border<T>(x, keep - c_hi, border, top, s_count, exact);
+            found = true;
+        }
+    }
+    if (!found) {
+        __syncthreads();
+        border = find_border<T>(k, keep, 0u, 31, s_count, exact);
+    }
+    // rows above the border stay, and of those equal to it the first keep - (rows above)
+    const uint32_t from = exact ? border : border + 1u;   // (no overflow: a border of all ones is exact or never tried)
+    uint32_t gt = 0, eq = 0;
+#pragma unroll
+    for (int i = 0; i < PER; i++) {
+        gt += k[i] >= from;
+        eq += k[i] == border;
+    }
+    if (exact) eq = 0;
+    uint32_t total;                           // (both counts fit 16 bits: at most kOneRows)
+    const uint32_t before = cta_scan<T>(gt | (eq << 16), s_count, total);
+    total &= 0xffffu;
+    const uint32_t need = keep - total;       // 0 if the border was exact
+    const uint32_t eqs = before >> 16;
+    uint32_t at = (before & 0xffffu) + min(eqs, need);
+    uint32_t ties = eqs < need ? need - eqs : 0u;         // of this thread's ties, the first so many stay
+    uint64_t take = 0;
+#pragma unroll
+    for (int i = 0; i < PER; i++) {
+        const bool tie = !exact && k[i] == border && ties > 0;
+        ties -= tie;
+        if (k[i] >= from || tie) take |= 1ull << i;
+    }
+    while (take) {                            // (one step a kept row of the fullest thread, not one a row)
+        kept[at++] = t0 + __ffsll((long long)take) - 1;
+        take &= take - 1;
+    }
+}
+
+// dst[i] = src[kept[i]] for this CTA's rows i in [c0, c1), written by its threads before (loads beside the
+// compaction would stop each of its steps).
+template <int T>
+__device__ __forceinline__ void gather_scores(uint32_t c0, uint32_t c1, const float *src, const int32_t *kept, float *dst) {
+    __syncthreads();
+    for (uint32_t i = c0 + threadIdx.x; i < c1; i += T * 4) {
+        int t[4];
+#pragma unroll
+        for (int e = 0; e < 4; e++) t[e] = i + e * T < c1 ? kept[i + e * T] : 0;
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+            if (i + e * T < c1) dst[i + e * T] = __ldg(src + t[e]);
+    }
+}
+
+template <int T>
+__global__ void __launch_bounds__(T) select_one_kernel(SelectArgs a) {
+    extern __shared__ __align__(16) uint32_t s_keys[];   // the scores' bits; later the keys between two borders
+    __shared__ uint32_t s_count[2][32];
+    pdl_launch_dependents();                        // (the move waits for this grid to complete)
+    const int seg = (int)blockIdx.x, tid = threadIdx.x;
+    const int32_t len = a.seq_lens[seg / a.Hkv];
+    const int n = clamp_rows(len, a.cap);
+    const float *src = a.scores + (int64_t)seg * a.score_stride;
+    int32_t *kept = a.kept + (int64_t)seg * a.keep;
+    float *dst = a.new_scores + (int64_t)seg * a.new_score_stride;
+    if (select_edges(a, seg, n, len, tid, T, src, kept, dst)) return;
+    // the scores by asynchronous copies, all in flight at once
+    if ((a.score_stride & 3) == 0 && (reinterpret_cast<uintptr_t>(a.scores) & 15) == 0) {
+        for (int t = 4 * tid; t < n; t += 4 * T)   // (a last one may pass n, not the row)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(s_keys + t)), "l"(src + t) : "memory");
+    } else {
+        for (int t = tid; t < n; t += T)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(s_keys + t)), "l"(src + t) : "memory");
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    const int per = ((n + T - 1) / T) | 1;
+    if (per <= 5)
+        select_rows<T, 5>(a, n, per, kept, s_keys, s_count);
+    else if (per <= 17)
+        select_rows<T, 17>(a, n, per, kept, s_keys, s_count);
+    else
+        select_rows<T, kOnePer>(a, n, per, kept, s_keys, s_count);
+    gather_scores<T>(0, (uint32_t)a.keep, src, kept, dst);
 }
 
 __global__ void __launch_bounds__(kSelThreads) select_kernel(SelectArgs a) {
@@ -63,33 +306,18 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(SelectArgs a) {
     __shared__ uint32_t s_warp[kSelWarps][2];       // kept-for-sure and border keys of each warp's part
     __shared__ uint32_t s_cta[2];                   // their sums; read by the cluster
     __shared__ uint32_t s_digit[2];
+    pdl_launch_dependents();
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), C = (int)cluster.num_blocks();
     const int seg = (int)blockIdx.y;                // b * Hkv + h
-    const int b = seg / a.Hkv;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int32_t len = a.seq_lens[b];
+    const int32_t len = a.seq_lens[seg / a.Hkv];
     const int n = clamp_rows(len, a.cap);
     const float *src = a.scores + (int64_t)seg * a.score_stride;
     int32_t *kept = a.kept + (int64_t)seg * a.keep;
     float *dst = a.new_scores + (int64_t)seg * a.new_score_stride;
-    const int new_n = min(n, a.keep);
-    if (rank == 0 && tid == 0 && seg % a.Hkv == 0) {
-        a.new_lens[b] = new_n;
-        if (len < 0 || (int64_t)len > a.cap) flag_error(a.err, kErrSeqLen);
-    }
-    // behind the kept rows: -1 and score 0
-    for (int64_t i = new_n + (int64_t)rank * kSelThreads + tid; i < a.new_score_stride; i += (int64_t)C * kSelThreads) {
-        dst[i] = 0.f;
-        if (i < a.keep) kept[i] = -1;
-    }
-    if (n <= a.keep) {                              // uniform over the cluster: every row stays
-        for (int i = rank * kSelThreads + tid; i < n; i += C * kSelThreads) {
-            kept[i] = i;
-            dst[i] = src[i];
-        }
-        return;
-    }
+    if (select_edges(a, seg, n, len, rank * kSelThreads + tid, C * kSelThreads, src, kept, dst))
+        return;                                     // uniform over the cluster
     // this CTA's rows [r0, r1), this warp's [w0, w1)
     const int per = (n + C - 1) / C;
     const int r0 = min(n, rank * per), r1 = min(n, r0 + per);
@@ -189,6 +417,15 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(SelectArgs a) {
         at += s_warp[w][0];
         eq_before += s_warp[w][1];
     }
+    // this CTA's kept rows [c0, c1)
+    uint32_t c0 = 0, c_eq = 0;
+    for (int r = 0; r < rank; r++) {
+        const uint32_t *o = cluster.map_shared_rank(s_cta, r);
+        c0 += o[0];
+        c_eq += o[1];
+    }
+    const uint32_t c1 = c0 + s_cta[0] + min(c_eq + s_cta[1], need);
+    c0 += min(c_eq, need);
     at += min(eq_before, need);
     cluster.sync();                                 // no CTA leaves while its counts may be read
     for (int t = w0; t < w1; t += 32) {
@@ -198,14 +435,11 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(SelectArgs a) {
         const unsigned eqs = __ballot_sync(0xffffffffu, in && k == prefix);
         const bool take = in && (k > prefix || (k == prefix && eq_before + (uint32_t)__popc(eqs & below) < need));
         const unsigned takes = __ballot_sync(0xffffffffu, take);
-        if (take) {
-            const uint32_t i = at + (uint32_t)__popc(takes & below);
-            kept[i] = t + lane;
-            dst[i] = __ldg(src + t + lane);
-        }
+        if (take) kept[at + (uint32_t)__popc(takes & below)] = t + lane;
         at += (uint32_t)__popc(takes);
         eq_before += (uint32_t)__popc(eqs);
     }
+    gather_scores<kSelThreads>(c0, c1, src, kept, dst);
 }
 
 struct MoveArgs {
@@ -324,6 +558,9 @@ cudaError_t launch_evict(const nvfp4kv_cache &c, const float *scores, int64_t sc
     if (!attr_set[dev]) {
         e = cudaFuncSetAttribute(reinterpret_cast<const void *>(&select_kernel),
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, kKeyCache * 4);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(reinterpret_cast<const void *>(&select_one_kernel<kOneLarge>),
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, kOneRows * 4);
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
     }
@@ -344,6 +581,7 @@ cudaError_t launch_evict(const nvfp4kv_cache &c, const float *scores, int64_t sc
     a.new_score_stride = new_score_stride;
     a.err = err;
     const int64_t segs = (int64_t)batch * c.num_kv_heads;
+    const bool one = a.cap <= kOneRows;
     // CTAs a segment: enough to fill the GPU when there are few segments, none with less than 1,024 rows at hand
     int cluster = 1;
     while (cluster < kMaxCluster && segs * cluster < kTargetCtasSel && a.cap >= 2048 * (int64_t)cluster) cluster *= 2;
@@ -361,7 +599,17 @@ cudaError_t launch_evict(const nvfp4kv_cache &c, const float *scores, int64_t sc
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     void *args[] = {&a};
-    e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(&select_kernel), args);
+    const void *fn = reinterpret_cast<const void *>(&select_kernel);
+    if (one) {
+        const bool small = a.cap <= kOneSmallRows;
+        fn = small ? reinterpret_cast<const void *>(&select_one_kernel<kOneSmall>)
+                   : reinterpret_cast<const void *>(&select_one_kernel<kOneLarge>);
+        cfg.gridDim = dim3((unsigned)segs);
+        cfg.blockDim = dim3(small ? kOneSmall : kOneLarge);
+        cfg.dynamicSmemBytes = ((size_t)a.cap + 3) / 4 * 16;
+        cfg.numAttrs = 0;
+    }
+    e = cudaLaunchKernelExC(&cfg, fn, args);
     if (e != cudaSuccess) return e;
 
     MoveArgs m;
