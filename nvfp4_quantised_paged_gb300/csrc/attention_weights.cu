@@ -152,7 +152,7 @@ __device__ __forceinline__ void load_query(const WeightsArgs &a, int b, int h, i
 // A warp's units in order.
 struct UnitIter {
     int b, h, t, n;   // sequence, kv head, first token, the sequence's rows
-    int64_t left;     // units of the piece from this one on
+    int left;         // units of the piece from this one on
 };
 
 __device__ __forceinline__ void next_unit(const WeightsArgs &a, UnitIter &it) {
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 2) weights_kernel(WeightsArgs a) {
     pdl_wait();   // lengths, q and the cache may come from earlier work; the weights kernel reads the partials
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int64_t worker = (int64_t)blockIdx.x * kWarpsW + (threadIdx.x >> 5);
+    const unsigned worker = blockIdx.x * kWarpsW + (threadIdx.x >> 5);
     auto rows = [&](int b) { return clamp_rows(__ldg(a.seq_lens + b), a.cap); };
     auto units = [&](int b) { return (rows(b) + kUnit - 1) / kUnit; };
     if (kStats && blockIdx.x == 0)
@@ -194,30 +194,30 @@ __global__ void __launch_bounds__(kThreads, 2) weights_kernel(WeightsArgs a) {
             if (n < 0 || (int64_t)n > a.cap) flag_error(a.err, kErrSeqLen);
         }
     int b;
-    int64_t first, u0 = 0;
-    int64_t pieces = a.workers;   // never more than there are units: no piece is empty
-    const int64_t total = flat_locate<kThreads>(
-        scratch, a.B, [&](int x) { return (int64_t)a.Hkv * units(x); },
-        [&](int64_t t) {
-            pieces = min(pieces, t);
-            return u0 = worker < pieces ? flat_begin(worker, t, pieces) : -1;
+    unsigned first, u0 = 0, u1 = 0;
+    const unsigned total = flat_locate<kThreads>(
+        scratch, a.B, [&](int x) { return a.Hkv * units(x); },
+        [&](unsigned t) {
+            const FlatCut cut(t, a.workers);
+            u0 = cut.begin(worker);
+            u1 = cut.begin(worker + 1);
+            return u0 < u1 ? u0 : kFlatNone;
         },
         b, first);
     if (threadIdx.x == 0) abort_all = 0;
     __syncthreads();
-    if (worker >= pieces) return;
-    const int64_t u1 = flat_begin(worker + 1, total, pieces);
+    if (u0 >= u1) return;   // more warps than units
     UnitIter it;
     it.b = b;
     it.n = rows(b);
     const int nu0 = units(b);
-    it.h = (int)((u0 - first) / nu0);
-    it.t = (int)((u0 - first) % nu0) * kUnit;
-    it.left = u1 - u0;
+    it.h = (int)((u0 - first) / (unsigned)nu0);
+    it.t = (int)((u0 - first) % (unsigned)nu0) * kUnit;
+    it.left = (int)(u1 - u0);
     uint32_t qf[NT][16];
     float fac[NT][2], m[NT][2], l[NT][2];   // kStats: running maximum and sum; else m = L of the pair's heads
     bool fresh = true;
-    int64_t u = u0;                         // position in the flat order
+    unsigned u = u0;                        // position in the flat order
     // The warp's ring: unit i of the piece into stage i % kStagesW, requested kStagesW - 1 units
     // ahead (its pages one unit earlier still).
     uint8_t *ring = ring_all + (threadIdx.x >> 5) * (kStagesW * H::kStage);
@@ -285,15 +285,16 @@ __global__ void __launch_bounds__(kThreads, 2) weights_kernel(WeightsArgs a) {
             } else {
                 // the pair's units [p0, p0 + nu) were covered by these warps
                 const int nu = (n + kUnit - 1) / kUnit;
-                const int64_t p = (int64_t)b * a.Hkv + h, p0 = u - t0 / kUnit;
-                const int64_t w0 = flat_piece(p0, total, pieces), w1 = flat_piece(p0 + nu - 1, total, pieces);
+                const FlatCut cut(total, a.workers);
+                const int64_t p = (int64_t)b * a.Hkv + h;
+                const unsigned p0 = u - t0 / kUnit, w0 = cut.piece(p0), w1 = cut.piece(p0 + nu - 1);
                 float mine[NT * 8];
 #pragma unroll
                 for (int hd = 0; hd < NT * 8; hd++) {
                     mine[hd] = -kNegInfW;      // heads that do not exist: weight 2^-inf
                     if (hd >= a.G) continue;   // uniform
                     float mm = kNegInfW, ll = 0.f;
-                    for (int64_t w = w0 + lane; w <= w1; w += 32) {
+                    for (unsigned w = w0 + lane; w <= w1; w += 32) {
                         const float2 v = __ldcg(a.part + (w + p) * a.G + hd);
                         const float mx = fmaxf(mm, v.x);
                         if (mx != kNegInfW) ll = ll * ex2(mm - mx) + v.y * ex2(v.x - mx);

@@ -185,6 +185,10 @@ __device__ __forceinline__ float column_sums(float (&v)[CW], int lane) {
     return s;
 }
 
+__device__ __forceinline__ int seq_tiles(const LatentArgs &a, int b) {
+    return (clamp_rows(__ldg(a.seq_lens + b), a.cap) + kTile - 1) / kTile;
+}
+
 template <int N>
 __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs a) {
     using L = LSmem<N>;
@@ -197,28 +201,6 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
     float *s_m = reinterpret_cast<float *>(smem + L::kM), *s_fac = s_m + N, *s_alpha = s_fac + N;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h0 = blockIdx.y * N;
-    pdl_wait();               // everything read or written may belong to earlier work of the stream
-    pdl_launch_dependents();
-
-    if (blockIdx.x == 0 && blockIdx.y == 0)
-        for (int b = tid; b < a.B; b += kLThreads) {
-            const int32_t n = a.seq_lens[b];
-            if (n < 0 || (int64_t)n > a.cap) flag_error(a.err, kErrSeqLen);
-        }
-    int b0;
-    int64_t first, u0 = 0;
-    const int64_t total = flat_locate<kLThreads>(
-        *reinterpret_cast<FlatScratch<kLThreads> *>(smem + L::kKV), a.B,
-        [&](int b) { return (int64_t)((clamp_rows(__ldg(a.seq_lens + b), a.cap) + kTile - 1) / kTile); },
-        [&](int64_t t) { return u0 = flat_begin(blockIdx.x, t, a.splits); }, b0, first);
-    const int64_t u1 = flat_begin((int64_t)blockIdx.x + 1, total, a.splits);
-    if (u0 >= u1) return;
-    TileIter it;
-    it.b = b0;
-    it.t = (int)(u0 - first);
-    it.left = (int)(u1 - u0);   // (the host refuses 2^31 tiles)
-    set_seq(a, it);
-
     if (warp == 16) tc_alloc(&tmem_base, L::kCols);
     if (tid == 0) {
         for (int i = 0; i < L::kNumBars; i++)
@@ -226,9 +208,41 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
         *abort_flag = 0;
         fence_mbar_init();
     }
+    pdl_wait();               // everything read or written may belong to earlier work of the stream
+    pdl_launch_dependents();
+
+    int b0;
+    unsigned first, u0 = 0, u1 = 0;
+    flat_locate<kLThreads>(
+        *reinterpret_cast<FlatScratch<kLThreads> *>(smem + L::kKV), a.B, [&](int b) { return seq_tiles(a, b); },
+        [&](unsigned total) {
+            const FlatCut cut(total, a.splits);
+            u0 = cut.begin(blockIdx.x);
+            u1 = cut.begin(blockIdx.x + 1);
+            return u0 < u1 ? u0 : kFlatNone;
+        },
+        b0, first);
+    if (warp > 16) {   // (idle otherwise) lengths out of range, and the rows of sequences of length 0
+        for (int b = blockIdx.x; b < a.B; b += a.splits) {
+            const int32_t n = __ldg(a.seq_lens + b);
+            if (tid == kWorkers + 32 && blockIdx.y == 0 && (n < 0 || (int64_t)n > a.cap)) flag_error(a.err, kErrSeqLen);
+            if (n > 0) continue;
+            uint4 *dst = reinterpret_cast<uint4 *>(a.out + ((int64_t)b * a.H + h0) * kLatentDim);
+            for (int i = tid - kWorkers - 32; i < min(N, a.H - h0) * (kLatentDim / 8); i += 96) dst[i] = make_uint4(0, 0, 0, 0);
+        }
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (u0 >= u1) {           // more CTAs than tiles
+        if (warp == 16) tc_dealloc(tmem_base, L::kCols);
+        return;
+    }
+    TileIter it;
+    it.b = b0;
+    it.t = (int)(u0 - first);
+    it.left = (int)(u1 - u0);
+    set_seq(a, it);
     const uint32_t tmem = tmem_base, sbase = smem_u32(smem);
     if (warp >= 16) {
         // ---------------- the MMA warp
@@ -364,21 +378,33 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
                                                   p + kLatentRope + (er + 8 * e) * 128 + (((4 * par + eq) ^ er) << 4)))
                                             : make_uint4(0, 0, 0, 0);
         };
-        // Q of sequence b: one warp per head, FP16 latent blocks and the BF16 rotary block (the
-        // previous sequence's S^T are done: its scores were seen).
-        auto load_q = [&](int b) {
-#pragma unroll 2
-            for (int hh = warp; hh < N; hh += kWorkers / 32) {
-                const int h = h0 + hh;
-                uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
-                uint32_t xr = 0;
+        // Q of sequence b: a warp per head (N / 16 heads each), FP16 latent blocks and the BF16 rotary
+        // block, requested two heads at a time (the next tile's bytes hold the registers).
+        constexpr int QH = N / (kWorkers / 32), QB = QH < 2 ? QH : 2;
+        uint4 qv[QB][2];
+        uint32_t qx[QB];
+        auto fetch_q = [&](int b, int k0) {
+#pragma unroll
+            for (int k = 0; k < QB; k++) {
+                const int h = h0 + warp + (k0 + k) * (kWorkers / 32);
+                qv[k][0] = qv[k][1] = make_uint4(0, 0, 0, 0);
+                qx[k] = 0;
                 if (h < a.H) {
                     const int64_t at = (int64_t)b * a.H + h;
                     const uint4 *src = reinterpret_cast<const uint4 *>(a.ql + at * kLatentDim) + lane * 2;
-                    x0 = __ldg(src);
-                    x1 = __ldg(src + 1);
-                    xr = __ldg(reinterpret_cast<const uint32_t *>(a.qr + at * kRopeDim) + lane);
+                    qv[k][0] = __ldg(src);
+                    qv[k][1] = __ldg(src + 1);
+                    qx[k] = __ldg(reinterpret_cast<const uint32_t *>(a.qr + at * kRopeDim) + lane);
                 }
+            }
+        };
+        // (The previous sequence's S^T are done: its scores were seen.)
+        auto store_q = [&](int k0) {
+#pragma unroll
+            for (int k = 0; k < QB; k++) {
+                const int hh = warp + (k0 + k) * (kWorkers / 32);
+                const uint4 x0 = qv[k][0], x1 = qv[k][1];
+                const uint32_t xr = qx[k];
                 const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
                 uint32_t ml = 0, mr = xr & 0x7fff7fffu;
 #pragma unroll
@@ -414,17 +440,17 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
                     s_m[hh] = kNegInfL;
                 }
             }
-            // (published to the tensor core with the first half of the tile)
-            workers_sync();   // s_fac and s_m are written for all heads
         };
         const uint32_t n = (uint32_t)it.left;
         TileIter nx = it;                       // the tile whose bytes are requested next
         {
+            const int32_t page = page_of(nx);
+            fetch_q(it.b, 0);
             int rows;
-            const uint8_t *p = group_of(nx, page_of(nx), rows);
+            const uint8_t *p = group_of(nx, page, rows);
+            load_scales(p, rows);
 #pragma unroll
             for (int i = 0; i < 4; i++) load_block(p, rows, i);
-            load_scales(p, rows);
             load_rope(p, rows);
         }
         next_tile(a, nx);
@@ -434,7 +460,15 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
         float l[CW];
         for (uint32_t j = 0; j < n; j++) {
             if (fresh) {
-                load_q(it.b);
+                if (j > 0) fetch_q(it.b, 0);
+                store_q(0);
+#pragma unroll 1
+                for (int k0 = QB; k0 < QH; k0 += QB) {
+                    fetch_q(it.b, k0);
+                    store_q(k0);
+                }
+                // (published to the tensor core with the first half of the tile)
+                workers_sync();   // s_fac and s_m are written for all heads
 #pragma unroll
                 for (int c = 0; c < CW; c++) l[c] = 0.f;
             }
@@ -491,7 +525,8 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
             }
             // ---- softmax of the token's scores for the warpgroup's heads.  S^T done says that the
             // previous tile's O^T, issued before it, is done too: P and O^T may be written.
-            wait(s_done, j & 1);
+            if (warp == 0) wait(s_done, j & 1);   // one warp polls: sixteen would take shared memory's time from S^T
+            workers_sync();
             tc_fence_after();
             const bool seen = it.t * kTile + row < it.n;
             // The scores are read from TMEM in chunks of up to eight heads (the next tile's bytes hold
@@ -623,65 +658,60 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
     if (warp == 16) tc_dealloc(tmem, L::kCols);
 }
 
-// Joins the partials of the sequences that several CTAs covered (and zeroes those
-// of length 0): one CTA per (sequence, head), thread t owns dims 4t .. 4t + 3.
-constexpr int kJoinThreads = 128;
+// Joins the partials of the sequences that several CTAs covered: one CTA per (sequence,
+// head), thread t of a group of 128 owns dims 4 t .. 4 t + 3, and the groups (as many as
+// the launch has) take the partials in turn, four at a time.
+constexpr int kJoinGroup = 128, kJoinGroups = 4;
 
-__global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(LatentArgs a) {
-    __shared__ int64_t s_sum[2][kJoinThreads / 32];
-    const int b = blockIdx.y, h = blockIdx.x, tid = threadIdx.x;
+__global__ void __launch_bounds__(kJoinGroup *kJoinGroups) latent_join_kernel(LatentArgs a) {
+    __shared__ unsigned s_sum[2][kJoinGroup * kJoinGroups / 32];
+    __shared__ float2 s_ml[kJoinGroups];
+    __shared__ float4 s_acc[kJoinGroups - 1][kJoinGroup];
+    const int b = blockIdx.y, h = blockIdx.x, tid = threadIdx.x, t = tid & (kJoinGroup - 1), grp = tid / kJoinGroup;
+    const int groups = blockDim.x / kJoinGroup;
     pdl_wait();
-    auto tiles = [&](int x) { return (int64_t)((clamp_rows(__ldg(a.seq_lens + x), a.cap) + kTile - 1) / kTile); };
-    int64_t before = 0, all = 0;
-    for (int x = tid; x < a.B; x += kJoinThreads) {
-        const int64_t t = tiles(x);
-        all += t;
-        if (x < b) before += t;
+    const int nt = seq_tiles(a, b);
+    unsigned before = 0, all = 0;
+    for (int x = tid; x < a.B; x += blockDim.x) {
+        const unsigned n = seq_tiles(a, x);
+        all += n;
+        if (x < b) before += n;
     }
-#pragma unroll
-    for (int x = 16; x; x >>= 1) {
-        all += __shfl_xor_sync(0xffffffffu, all, x);
-        before += __shfl_xor_sync(0xffffffffu, before, x);
-    }
+    all = __reduce_add_sync(0xffffffffu, all);
+    before = __reduce_add_sync(0xffffffffu, before);
     if ((tid & 31) == 0) {
         s_sum[0][tid >> 5] = all;
         s_sum[1][tid >> 5] = before;
     }
     __syncthreads();
     all = before = 0;
-    for (int w = 0; w < kJoinThreads / 32; w++) {
+    for (int w = 0; w < (int)blockDim.x / 32; w++) {
         all += s_sum[0][w];
         before += s_sum[1][w];
     }
-    const int64_t nt = tiles(b);
-    uint2 *dst = reinterpret_cast<uint2 *>(a.out + ((int64_t)b * a.H + h) * kLatentDim) + tid;
-    if (nt == 0) {
-        *dst = make_uint2(0, 0);
-        return;
-    }
-    const int64_t c0 = flat_piece(before, all, a.splits), c1 = flat_piece(before + nt - 1, all, a.splits);
+    if (nt == 0) return;    // zeroed already
+    const FlatCut cut(all, a.splits);
+    const int c0 = cut.piece(before), c1 = cut.piece(before + nt - 1);
     if (c0 == c1) return;   // written by its CTA
     float m = kNegInfL, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int64_t c = c0; c <= c1; c += 4) {
-        float2 ml[4];
-        float4 v[4];
+    constexpr int U = 4;
+    for (int c = c0 + grp; c <= c1; c += U * groups) {
+        float2 ml[U];
+        float4 v[U];
 #pragma unroll
-        for (int k = 0; k < 4; k++) {
+        for (int k = 0; k < U; k++) {
             ml[k] = make_float2(kNegInfL, 0.f);
             v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (c + k <= c1) {   // every CTA between c0 and c1 holds tiles of the sequence (none is empty between two that do)
-                const int64_t cc = c + k;
-                if (flat_begin(cc, all, a.splits) < flat_begin(cc + 1, all, a.splits)) {
-                    const int64_t at = (cc + b) * a.H + h;
-                    ml[k] = __ldcg(a.part_ml + at);
-                    v[k] = __ldcg(reinterpret_cast<const float4 *>(a.part_acc + at * kLatentDim) + tid);
-                }
+            if (c + k * groups <= c1) {
+                const int64_t at = (int64_t)(c + k * groups + b) * a.H + h;
+                ml[k] = __ldcg(a.part_ml + at);
+                v[k] = __ldcg(reinterpret_cast<const float4 *>(a.part_acc + at * kLatentDim) + t);
             }
         }
         float mx = m;
 #pragma unroll
-        for (int k = 0; k < 4; k++) mx = fmaxf(mx, ml[k].x);
+        for (int k = 0; k < U; k++) mx = fmaxf(mx, ml[k].x);
         const float f0 = m == kNegInfL ? 0.f : ex2(m - mx);
         l *= f0;
         acc.x *= f0;
@@ -689,7 +719,7 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(LatentArgs a)
         acc.z *= f0;
         acc.w *= f0;
 #pragma unroll
-        for (int k = 0; k < 4; k++) {
+        for (int k = 0; k < U; k++) {
             const float f = ml[k].x == kNegInfL ? 0.f : ex2(ml[k].x - mx);
             l += f * ml[k].y;
             acc.x += f * v[k].x;
@@ -699,8 +729,34 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(LatentArgs a)
         }
         m = mx;
     }
+    if (groups > 1) {
+        if (t == 0) s_ml[grp] = make_float2(m, l);
+        if (grp > 0) s_acc[grp - 1][t] = acc;
+        __syncthreads();
+        if (grp > 0) return;
+        float mx = m;
+        for (int g = 1; g < groups; g++) mx = fmaxf(mx, s_ml[g].x);
+        const float f0 = m == kNegInfL ? 0.f : ex2(m - mx);
+        l *= f0;
+        acc.x *= f0;
+        acc.y *= f0;
+        acc.z *= f0;
+        acc.w *= f0;
+        for (int g = 1; g < groups; g++) {
+            const float2 o = s_ml[g];
+            if (o.x == kNegInfL) continue;
+            const float f = ex2(o.x - mx);
+            const float4 v = s_acc[g - 1][t];
+            l += f * o.y;
+            acc.x += f * v.x;
+            acc.y += f * v.y;
+            acc.z += f * v.z;
+            acc.w += f * v.w;
+        }
+    }
     const float inv = a.g / l;
-    *dst = make_uint2(f32x2_to_bf16x2(acc.y * inv, acc.x * inv), f32x2_to_bf16x2(acc.w * inv, acc.z * inv));
+    reinterpret_cast<uint2 *>(a.out + ((int64_t)b * a.H + h) * kLatentDim)[t] =
+        make_uint2(f32x2_to_bf16x2(acc.y * inv, acc.x * inv), f32x2_to_bf16x2(acc.w * inv, acc.z * inv));
 }
 
 int tile_heads(int H) { return H <= 16 ? 16 : H <= 32 ? 32 : 64; }
@@ -790,9 +846,11 @@ cudaError_t launch_latent_decode(const nvfp4kv_latent_cache &c, const void *q_la
     a.err = err;
     void *args[] = {&a};
     e = launch_pdl(fn, dim3((unsigned)splits, (unsigned)tiles), kLThreads, (size_t)smem, stream, args);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || splits == 1 || a.cap <= kTile) return e;   // no sequence can have been split
+    // A group of threads per four partials of a sequence, if its length is the batch's average
+    const int partials = (splits + batch - 1) / batch + 1, groups = partials <= 4 ? 1 : partials <= 8 ? 2 : kJoinGroups;
     return launch_pdl(reinterpret_cast<const void *>(&latent_join_kernel), dim3((unsigned)num_heads, (unsigned)batch),
-                      kJoinThreads, 0, stream, args);
+                      (unsigned)(kJoinGroup * groups), 0, stream, args);
 }
 
 }  // namespace nvfp4kv
