@@ -430,8 +430,8 @@ int nvfp4_latent_decode_attention(const nvfp4kv_latent_cache *cache, const void 
         !aligned(block_table, 4) || !aligned(seq_lens, 4))
         return NVFP4KV_EINVAL;
     if ((int64_t)max_pages_per_seq * cache->page_size > kMaxRows) return NVFP4KV_EUNSUPPORTED;
-    if ((int64_t)batch * (((int64_t)max_pages_per_seq * cache->page_size + 127) / 128) >= ((int64_t)1 << 31))
-        return NVFP4KV_EUNSUPPORTED;   // 128-token tiles, counted in 32 bits
+    if ((int64_t)batch * (((int64_t)max_pages_per_seq * cache->page_size + 127) / 128 + 1) >= ((int64_t)1 << 31))
+        return NVFP4KV_EUNSUPPORTED;   // 128-token tiles and a unit a sequence, counted in 32 bits
     cudaError_t e = cudaSuccess;
     const int splits = num_splits ? num_splits : latent_decode_auto_splits(num_heads, &e);
     if (e != cudaSuccess || splits <= 0) return NVFP4KV_ECUDA;

@@ -67,11 +67,13 @@ constexpr int kTileBytes = 8 * kColBlock;
 constexpr uint32_t kWaitLimitL = 1u << 24;
 constexpr float kNegInfL = -__builtin_huge_valf();
 constexpr float kRescaleL = 8.0f;
+constexpr int kSeqUnits = 1;                  // what a sequence's start costs a CTA, in tiles
 constexpr float kPOffset = 7.0f;              // P = 2^(s - m + 7): at most 2^15
 
 template <int N>
 struct LSmem {
-    static constexpr int kTmemCbs = N == 64 ? 4 : 8;      // column blocks of S^T's A operand that lie in TMEM
+    static constexpr int kSmemCbs = N == 64 ? 4 : 0;      // column blocks of S^T's A operand in shared memory (the first)
+    static constexpr int kTmemCbs = 8 - kSmemCbs;         // ... and in TMEM
     static constexpr int kQBlock = N * 128;               // one column block of Q, [N][64]
     static constexpr int kQ = 0;                          // 8 FP16 blocks + the BF16 rotary block
     static constexpr int kKV = 9 * kQBlock;               // the tile
@@ -79,8 +81,8 @@ struct LSmem {
     static constexpr int kBar = kP + kColBlock;
     static constexpr int kNumBars = 9;                    // kv_full[2] s_done p_full pv_done[4] drain
     static constexpr int kMisc = kBar + kNumBars * 8;     // tmem base, abort
-    static constexpr int kM = (kMisc + 8 + 15) & ~15;     // float m[N], fac[N], alpha[N]
-    static constexpr int kWarpMax = kM + 3 * N * 4;       // float [4][4][N / 4]: warps' maxima, and row sums at the end
+    static constexpr int kM = (kMisc + 8 + 15) & ~15;     // float m[N], fac[N], alpha[N], off[N]
+    static constexpr int kWarpMax = kM + 4 * N * 4;       // float [4][4][N / 4]: warps' maxima, and row sums at the end
     static constexpr int kBytes = kWarpMax + 4 * N * 4;
     // TMEM columns
     static constexpr uint32_t kColS = 4 * N, kColR = 5 * N, kColK = kColR + 32;   // O at 0
@@ -119,7 +121,7 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, const v
 // The tiles of a CTA's range in order.
 struct TileIter {
     int b, t, nt, n;
-    int left;       // tiles of the range from this one on
+    int left;       // units of the range from this one on
 };
 
 __device__ __forceinline__ void set_seq(const LatentArgs &a, TileIter &it) {
@@ -131,6 +133,8 @@ __device__ __forceinline__ void next_tile(const LatentArgs &a, TileIter &it) {
     it.left--;
     if (++it.t < it.nt || it.left <= 0) return;
     it.t = 0;
+    it.left -= kSeqUnits;
+    if (it.left <= 0) return;
     do {            // left > 0: a later sequence has tiles
         it.b++;
         set_seq(a, it);
@@ -185,8 +189,16 @@ __device__ __forceinline__ float column_sums(float (&v)[CW], int lane) {
     return s;
 }
 
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 __device__ __forceinline__ int seq_tiles(const LatentArgs &a, int b) {
     return (clamp_rows(__ldg(a.seq_lens + b), a.cap) + kTile - 1) / kTile;
+}
+
+// Units of sequence b in the flat order: its tiles, after kSeqUnits that stand for its start.
+__device__ __forceinline__ unsigned seq_units(const LatentArgs &a, int b) {
+    const int nt = seq_tiles(a, b);
+    return nt ? nt + kSeqUnits : 0;
 }
 
 template <int N>
@@ -198,7 +210,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
     uint64_t *kv_full = bars, *s_done = bars + 2, *p_full = bars + 3, *pv_done = bars + 4, *drain = bars + 8;
     uint32_t &tmem_base = *reinterpret_cast<uint32_t *>(smem + L::kMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 4);
-    float *s_m = reinterpret_cast<float *>(smem + L::kM), *s_fac = s_m + N, *s_alpha = s_fac + N;
+    float *s_m = reinterpret_cast<float *>(smem + L::kM), *s_fac = s_m + N, *s_alpha = s_fac + N, *s_off = s_alpha + N;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h0 = blockIdx.y * N;
     if (warp == 16) tc_alloc(&tmem_base, L::kCols);
@@ -214,7 +226,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
     int b0;
     unsigned first, u0 = 0, u1 = 0;
     flat_locate<kLThreads>(
-        *reinterpret_cast<FlatScratch<kLThreads> *>(smem + L::kKV), a.B, [&](int b) { return seq_tiles(a, b); },
+        *reinterpret_cast<FlatScratch<kLThreads> *>(smem + L::kKV), a.B, [&](int b) { return seq_units(a, b); },
         [&](unsigned total) {
             const FlatCut cut(total, a.splits);
             u0 = cut.begin(blockIdx.x);
@@ -234,14 +246,14 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (u0 >= u1) {           // more CTAs than tiles
+    TileIter it;
+    it.b = b0;
+    it.t = max(0, (int)(u0 - first) - kSeqUnits);
+    it.left = (int)(u1 - u0) - max(0, (int)(first + kSeqUnits - u0));
+    if (u0 >= u1 || it.left <= 0) {   // a range without tiles
         if (warp == 16) tc_dealloc(tmem_base, L::kCols);
         return;
     }
-    TileIter it;
-    it.b = b0;
-    it.t = (int)(u0 - first);
-    it.left = (int)(u1 - u0);
     set_seq(a, it);
     const uint32_t tmem = tmem_base, sbase = smem_u32(smem);
     if (warp >= 16) {
@@ -265,15 +277,14 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
                 tc_fence_after();
                 return good;
             };
-            const uint32_t n = (uint32_t)it.left;
             bool fresh = true, ok = true;   // fresh: the tile is the range's first of its sequence
-            for (uint32_t j = 0; j < n; j++) {
+            for (uint32_t j = 0; it.left > 0; j++) {
 #pragma unroll 1
                 for (uint32_t i = 0; i < 4; i++) {   // column blocks 2 i, 2 i + 1 (and the rotary part, with the first)
                     if (!(i & 1)) ok = ok && wait(&kv_full[i >> 1], j & 1);
                     if (!ok) break;
                     const uint64_t q = dQ + i * (2 * L::kQBlock / 16), c = dC + i * (2 * kColBlock / 16);
-                    const uint32_t t = tm + L::kColK + 64 * i;
+                    const uint32_t t = tm + L::kColK + 32 * (2 * i - L::kSmemCbs);
                     if (leader) {
                         if (i == 0) {
 #pragma unroll
@@ -281,7 +292,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
                                 tc_mma_bf16_tmem_a(tm + L::kColS, tm + L::kColR + kk * 8, dQ + (8 * L::kQBlock / 16 + kk * 2),
                                                    idesc_r, kk > 0);
                         }
-                        if (L::kTmemCbs == 8 || 2 * i < L::kTmemCbs) {
+                        if (L::kSmemCbs == 0 || 2 * i >= L::kSmemCbs) {
 #pragma unroll
                             for (int kk = 0; kk < 8; kk++)
                                 tc_mma_bf16_tmem_a(tm + L::kColS, t + kk * 8,
@@ -381,11 +392,9 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
         // Q of sequence b: a warp per head (N / 16 heads each), FP16 latent blocks and the BF16 rotary
         // block, requested two heads at a time (the next tile's bytes hold the registers).
         constexpr int QH = N / (kWorkers / 32), QB = QH < 2 ? QH : 2;
-        uint4 qv[QB][2];
-        uint32_t qx[QB];
-        auto fetch_q = [&](int b, int k0) {
+        auto fetch_q = [&](int b, int k0, auto &qv, auto &qx) {
 #pragma unroll
-            for (int k = 0; k < QB; k++) {
+            for (int k = 0; k < (int)(sizeof(qx) / 4); k++) {
                 const int h = h0 + warp + (k0 + k) * (kWorkers / 32);
                 qv[k][0] = qv[k][1] = make_uint4(0, 0, 0, 0);
                 qx[k] = 0;
@@ -398,10 +407,16 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
                 }
             }
         };
+        auto prefetch_q = [&](int b) {          // to L2, the whole tile's heads: 128-byte lines, one a thread
+            const int lines = min(N, a.H - h0) * 8;
+            for (int i = tid; i < lines; i += kWorkers)
+                prefetch_l2(a.ql + ((int64_t)b * a.H + h0) * kLatentDim + 64 * i);
+            if (tid < lines / 8) prefetch_l2(a.qr + ((int64_t)b * a.H + h0 + tid) * kRopeDim);
+        };
         // (The previous sequence's S^T are done: its scores were seen.)
-        auto store_q = [&](int k0) {
+        auto store_q = [&](int k0, auto &qv, auto &qx) {
 #pragma unroll
-            for (int k = 0; k < QB; k++) {
+            for (int k = 0; k < (int)(sizeof(qx) / 4); k++) {
                 const int hh = warp + (k0 + k) * (kWorkers / 32);
                 const uint4 x0 = qv[k][0], x1 = qv[k][1];
                 const uint32_t xr = qx[k];
@@ -422,7 +437,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
                 for (int e = 0; e < 8; e++) f[e] = f32x2_to_f16x2(bf16_hi(w[e]) * a.g * sc, bf16_lo(w[e]) * a.g * sc);
                 uint8_t *q = smem + L::kQ + (lane >> 2) * L::kQBlock;      // lane: dims 16 lane .. 16 lane + 15
                 const int bq = lane & 3;
-                if ((lane >> 2) < L::kTmemCbs) {   // in the order of the block in TMEM
+                if ((lane >> 2) >= L::kSmemCbs) {   // in the order of the block in TMEM
 #pragma unroll
                     for (int k = 0; k < 4; k++)
                         *reinterpret_cast<uint2 *>(q + sw128_off(hh, 2 * k + (bq >> 1)) + (bq & 1) * 8) =
@@ -438,37 +453,55 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
                 if (lane == 0) {
                     s_fac[hh] = a.score_log2 * __uint_as_float((uint32_t)(127 - kq) << 23);
                     s_m[hh] = kNegInfL;
+                    s_off[hh] = -kNegInfL;
                 }
             }
         };
-        const uint32_t n = (uint32_t)it.left;
-        TileIter nx = it;                       // the tile whose bytes are requested next
-        {
-            const int32_t page = page_of(nx);
-            fetch_q(it.b, 0);
-            int rows;
-            const uint8_t *p = group_of(nx, page, rows);
+        auto load_q = [&]() {   // (published to the tensor core with the first half of the tile)
+            uint4 qv[QB][2];
+            uint32_t qx[QB];
+#pragma unroll 1
+            for (int k0 = 0; k0 < QH; k0 += QB) {
+                fetch_q(it.b, k0, qv, qx);
+                store_q(k0, qv, qx);
+            }
+            workers_sync();   // s_fac and s_m are written for all heads
+        };
+        auto load_tile = [&](const uint8_t *p, int rows) {
             load_scales(p, rows);
 #pragma unroll
             for (int i = 0; i < 4; i++) load_block(p, rows, i);
             load_rope(p, rows);
+        };
+        TileIter nx = it;                       // the tile whose bytes are requested next
+        {   // the first tile and the first sequence's Q
+            uint4 qv[QH][2];
+            uint32_t qx[QH];
+            const int32_t page = page_of(nx);
+            fetch_q(it.b, 0, qv, qx);
+            int rows;
+            const uint8_t *p = group_of(nx, page, rows);
+            if (QB < QH) {   // the tile's bytes come to L2 while Q, which needs the registers, is laid out
+                if (rows > 0 && par == 0 && lane < kLatentGroup / 256) {
+                    prefetch_l2(p + lane * 256);
+                    prefetch_l2(p + lane * 256 + 128);
+                }
+                store_q(0, qv, qx);
+                load_tile(p, rows);
+            } else {
+                load_tile(p, rows);
+                store_q(0, qv, qx);
+            }
+            workers_sync();   // s_fac and s_m are written for all heads
         }
         next_tile(a, nx);
         int32_t npage = page_of(nx);            // its page, requested a tile earlier still
         bool fresh = true;                      // the range's first tile of its sequence
         int t_begin = it.t;
         float l[CW];
-        for (uint32_t j = 0; j < n; j++) {
+        for (uint32_t j = 0; it.left > 0; j++) {
             if (fresh) {
-                if (j > 0) fetch_q(it.b, 0);
-                store_q(0);
-#pragma unroll 1
-                for (int k0 = QB; k0 < QH; k0 += QB) {
-                    fetch_q(it.b, k0);
-                    store_q(k0);
-                }
-                // (published to the tensor core with the first half of the tile)
-                workers_sync();   // s_fac and s_m are written for all heads
+                if (j > 0) load_q();
 #pragma unroll
                 for (int c = 0; c < CW; c++) l[c] = 0.f;
             }
@@ -486,10 +519,10 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
                     for (int x = 0; x < 8; x++) f[e][x] = hmul2(f[e][x], s);
                 }
                 // (TMEM's copy is free: the previous tile's scores were seen)
-                if (L::kTmemCbs == 8 || 2 * i < L::kTmemCbs) {
+                if (2 * i >= L::kSmemCbs) {
                     const uint32_t st[16] = {f[0][0], f[0][1], f[1][0], f[1][1], f[0][2], f[0][3], f[1][2], f[1][3],
                                              f[0][4], f[0][5], f[1][4], f[1][5], f[0][6], f[0][7], f[1][6], f[1][7]};
-                    tc_st_16x256_x4(tmem + glanes + L::kColK + 32 * (2 * i + par), st);
+                    tc_st_16x256_x4(tmem + glanes + L::kColK + 32 * (2 * i + par - L::kSmemCbs), st);
                 }
                 if (i == 0) {
                     const uint32_t st[8] = {rope[0].x, rope[0].y, rope[1].x, rope[1].y, rope[0].z, rope[0].w, rope[1].z, rope[1].w};
@@ -503,8 +536,8 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
                     *reinterpret_cast<uint4 *>(blk + sw128_off(tr, 2 * eq)) = make_uint4(f[e][0], f[e][1], f[e][2], f[e][3]);
                     *reinterpret_cast<uint4 *>(blk + sw128_off(tr, 2 * eq + 1)) = make_uint4(f[e][4], f[e][5], f[e][6], f[e][7]);
                 }
-                if (i & 1) {   // half of the tile at a time: a fence takes about as long as an expanding step
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                if (i & 1) {   // half of the tile at a time; what S^T reads from TMEM needs no proxy fence (about 1,000 clocks)
+                    if (2 * i <= L::kSmemCbs) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     tc_wait_st();
                     tc_fence_before();
                     __syncwarp();
@@ -512,14 +545,11 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
                 }
             }
             // Request the next tile's bytes, and the page after that.  Only here: a proxy fence waits
-            // for loads in flight, and no fence follows before the softmax is done.
+            // for loads in flight, and the next one follows the softmax.
             {
                 int rows;
                 const uint8_t *p = group_of(nx, npage, rows);
-                load_scales(p, rows);
-                load_rope(p, rows);
-#pragma unroll
-                for (int i = 0; i < 4; i++) load_block(p, rows, i);
+                load_tile(p, rows);
                 next_tile(a, nx);
                 npage = page_of(nx);
             }
@@ -529,33 +559,49 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
             workers_sync();
             tc_fence_after();
             const bool seen = it.t * kTile + row < it.n;
-            // The scores are read from TMEM in chunks of up to eight heads (the next tile's bytes hold
-            // the registers): once to see whether a maximum must move, again to form P.
+            // d = s - m + 7, one multiply-add with the head's factor and offset 7 - m, read from TMEM in
+            // chunks of up to eight heads (the next tile's bytes hold the registers): once to see whether
+            // a maximum must move, and with more heads a thread again to form P.
             constexpr int CH = CW < 8 ? CW : 8;
-            auto load_scores = [&](int c0, float (&sc)[CH]) {
+            auto load_diffs = [&](int c0, float (&d)[CH]) {
                 uint32_t sr[CH];
                 tc_ld(tmem + lanes + L::kColS + wg * CW + c0, sr);
+                const float4 *fac = reinterpret_cast<const float4 *>(s_fac + wg * CW + c0);
+                const float4 *off = reinterpret_cast<const float4 *>(s_off + wg * CW + c0);
                 tc_wait_ld();
 #pragma unroll
-                for (int c = 0; c < CH; c++) sc[c] = seen ? __uint_as_float(sr[c]) * s_fac[wg * CW + c0 + c] : kNegInfL;
+                for (int x = 0; x < CH / 4; x++) {
+                    const float4 f = fac[x], o = off[x];
+                    d[4 * x] = fmaf(__uint_as_float(sr[4 * x]), f.x, o.x);
+                    d[4 * x + 1] = fmaf(__uint_as_float(sr[4 * x + 1]), f.y, o.y);
+                    d[4 * x + 2] = fmaf(__uint_as_float(sr[4 * x + 2]), f.z, o.z);
+                    d[4 * x + 3] = fmaf(__uint_as_float(sr[4 * x + 3]), f.w, o.w);
+                }
+                if (!seen) {
+#pragma unroll
+                    for (int c = 0; c < CH; c++) d[c] = kNegInfL;
+                }
             };
-            float sc[CH];
-            bool need = false;
+            float d[CH], top = kNegInfL;
 #pragma unroll
             for (int c0 = 0; c0 < CW; c0 += CH) {
-                load_scores(c0, sc);
+                load_diffs(c0, d);
 #pragma unroll
-                for (int c = 0; c < CH; c++) need |= sc[c] > s_m[wg * CW + c0 + c] + kRescaleL;
+                for (int c = 0; c < CH; c++) top = fmaxf(top, d[c]);
             }
-            if (group_any(wg, need)) {
+            const bool moves = group_any(wg, top > kRescaleL + kPOffset);
+            if (moves) {
                 float *wmax = reinterpret_cast<float *>(smem + L::kWarpMax) + wg * 4 * CW;
                 int mine = 0;
 #pragma unroll
                 for (int c0 = 0; c0 < CW; c0 += CH) {
-                    if (CW > CH) load_scores(c0, sc);
+                    uint32_t sr[CH];
+                    tc_ld(tmem + lanes + L::kColS + wg * CW + c0, sr);
+                    tc_wait_ld();
 #pragma unroll
                     for (int c = 0; c < CH; c++) {
-                        const int mx = __reduce_max_sync(0xffffffffu, ordered(sc[c]));
+                        const float sc = seen ? __uint_as_float(sr[c]) * s_fac[wg * CW + c0 + c] : kNegInfL;
+                        const int mx = __reduce_max_sync(0xffffffffu, ordered(sc));
                         if (lane == c0 + c) mine = mx;
                     }
                 }
@@ -566,6 +612,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
                     const float mo = s_m[wg * CW + lane], mn = fmaxf(mo, mx);
                     s_alpha[wg * CW + lane] = mo == kNegInfL ? 0.f : ex2(mo - mn);
                     s_m[wg * CW + lane] = mn;
+                    s_off[wg * CW + lane] = mn == kNegInfL ? 0.f : kPOffset - mn;
                 }
                 group_sync(wg);
 #pragma unroll
@@ -584,17 +631,15 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
                     tc_wait_st();
                 }
             }
+            if (CW == CH && moves) load_diffs(0, d);
 #pragma unroll
             for (int c0 = 0; c0 < CW; c0 += CH) {
-                if (CW > CH) load_scores(c0, sc);
+                if (CW > CH) load_diffs(c0, d);
                 uint32_t pw[CH / 2];
 #pragma unroll
                 for (int e = 0; e < CH / 2; e++) {
-                    const int c = c0 + 2 * e;
-                    const float m0 = s_m[wg * CW + c], m1 = s_m[wg * CW + c + 1];
-                    pw[e] = f32x2_to_f16x2(ex2(sc[2 * e + 1] - (m1 == kNegInfL ? 0.f : m1 - kPOffset)),
-                                           ex2(sc[2 * e] - (m0 == kNegInfL ? 0.f : m0 - kPOffset)));
-                    add_f16x2(l[c], l[c + 1], pw[e]);
+                    pw[e] = f32x2_to_f16x2(ex2(d[2 * e + 1]), ex2(d[2 * e]));
+                    add_f16x2(l[c0 + 2 * e], l[c0 + 2 * e + 1], pw[e]);
                 }
                 if (CW == 4)   // eight bytes a thread: two warpgroups share a 16-byte chunk
                     *reinterpret_cast<uint2 *>(smem + L::kP + sw128_off(row, wg >> 1) + (wg & 1) * 8) = make_uint2(pw[0], pw[1]);
@@ -612,6 +657,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
             next_tile(a, it);
             fresh = it.left <= 0 || it.b != cur.b;
             if (!fresh) continue;
+            if (it.left > 0) prefetch_q(it.b);
 #pragma unroll 1
             for (int i = 0; i < 4; i++) wait(&pv_done[i], j & 1);
             tc_fence_after();
@@ -628,23 +674,32 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
                         m == kNegInfL ? m : m - kPOffset,
                         (wsum[lane] + wsum[CW + lane]) + (wsum[2 * CW + lane] + wsum[3 * CW + lane]));
                 }
-#pragma unroll 1
-                for (int mb = 0; mb < 4; mb++) {
-                    uint32_t ov[CW];
-                    tc_ld(tmem + lanes + mb * N + wg * CW, ov);
-                    tc_wait_ld();
-                    const int d = mb * 128 + row;
+                const int hw = h0 + wg * CW, nh = a.H - hw;     // the warpgroup's first head, and how many there are
+                if (whole) {
+                    float inv[CW];
 #pragma unroll
-                    for (int c = 0; c < CW; c++) {
-                        const int h = h0 + wg * CW + c;
-                        if (h >= a.H) continue;
-                        const float o = __uint_as_float(ov[c]);
-                        if (whole) {
-                            const float ls = (wsum[c] + wsum[CW + c]) + (wsum[2 * CW + c] + wsum[3 * CW + c]);
-                            a.out[((int64_t)cur.b * a.H + h) * kLatentDim + d] = __float2bfloat16_rn(o * (a.g / ls));
-                        } else {
-                            a.part_acc[(slot * a.H + h) * kLatentDim + d] = o;
-                        }
+                    for (int c = 0; c < CW; c++)
+                        inv[c] = a.g / ((wsum[c] + wsum[CW + c]) + (wsum[2 * CW + c] + wsum[3 * CW + c]));
+                    __nv_bfloat16 *dst = a.out + ((int64_t)cur.b * a.H + hw) * kLatentDim + row;
+#pragma unroll 1
+                    for (int mb = 0; mb < 4; mb++, dst += 128) {
+                        uint32_t ov[CW];
+                        tc_ld(tmem + lanes + mb * N + wg * CW, ov);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < CW; c++)
+                            if (c < nh) dst[c * kLatentDim] = __float2bfloat16_rn(__uint_as_float(ov[c]) * inv[c]);
+                    }
+                } else {
+                    float *dst = a.part_acc + (slot * a.H + hw) * kLatentDim + row;
+#pragma unroll 1
+                    for (int mb = 0; mb < 4; mb++, dst += 128) {
+                        uint32_t ov[CW];
+                        tc_ld(tmem + lanes + mb * N + wg * CW, ov);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < CW; c++)
+                            if (c < nh) dst[c * kLatentDim] = __uint_as_float(ov[c]);
                     }
                 }
                 tc_fence_before();
@@ -660,20 +715,24 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
 
 // Joins the partials of the sequences that several CTAs covered: one CTA per (sequence,
 // head), thread t of a group of 128 owns dims 4 t .. 4 t + 3, and the groups (as many as
-// the launch has) take the partials in turn, four at a time.
-constexpr int kJoinGroup = 128, kJoinGroups = 4;
+// the launch has) take the partials in turn, U at a time.  It waits for loads: U and the
+// groups are as large as one wave of CTAs allows (b8 h128: 8.7 us with U = 4 and four
+// groups in two waves).
+constexpr int kJoinGroup = 128, kJoinGroups = 8, kJoinWave = 152 * 8;   // groups of threads that run at once
 
+template <int U>
 __global__ void __launch_bounds__(kJoinGroup *kJoinGroups) latent_join_kernel(LatentArgs a) {
     __shared__ unsigned s_sum[2][kJoinGroup * kJoinGroups / 32];
     __shared__ float2 s_ml[kJoinGroups];
     __shared__ float4 s_acc[kJoinGroups - 1][kJoinGroup];
     const int b = blockIdx.y, h = blockIdx.x, tid = threadIdx.x, t = tid & (kJoinGroup - 1), grp = tid / kJoinGroup;
     const int groups = blockDim.x / kJoinGroup;
-    pdl_wait();
+    // The lengths may be read before the wait: the decode kernel lets this one start only
+    // after its own wait for everything before it, and does not write them.
     const int nt = seq_tiles(a, b);
     unsigned before = 0, all = 0;
     for (int x = tid; x < a.B; x += blockDim.x) {
-        const unsigned n = seq_tiles(a, x);
+        const unsigned n = seq_units(a, x);
         all += n;
         if (x < b) before += n;
     }
@@ -689,13 +748,13 @@ __global__ void __launch_bounds__(kJoinGroup *kJoinGroups) latent_join_kernel(La
         all += s_sum[0][w];
         before += s_sum[1][w];
     }
+    pdl_wait();
     if (nt == 0) return;    // zeroed already
     const FlatCut cut(all, a.splits);
-    const int c0 = cut.piece(before), c1 = cut.piece(before + nt - 1);
+    const int c0 = cut.piece(before + kSeqUnits), c1 = cut.piece(before + kSeqUnits + nt - 1);
     if (c0 == c1) return;   // written by its CTA
     float m = kNegInfL, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int U = 4;
     for (int c = c0 + grp; c <= c1; c += U * groups) {
         float2 ml[U];
         float4 v[U];
@@ -847,10 +906,13 @@ cudaError_t launch_latent_decode(const nvfp4kv_latent_cache &c, const void *q_la
     void *args[] = {&a};
     e = launch_pdl(fn, dim3((unsigned)splits, (unsigned)tiles), kLThreads, (size_t)smem, stream, args);
     if (e != cudaSuccess || splits == 1 || a.cap <= kTile) return e;   // no sequence can have been split
-    // A group of threads per four partials of a sequence, if its length is the batch's average
-    const int partials = (splits + batch - 1) / batch + 1, groups = partials <= 4 ? 1 : partials <= 8 ? 2 : kJoinGroups;
-    return launch_pdl(reinterpret_cast<const void *>(&latent_join_kernel), dim3((unsigned)num_heads, (unsigned)batch),
-                      (unsigned)(kJoinGroup * groups), 0, stream, args);
+    // The partials of a sequence of the batch's average length
+    const int partials = (splits + batch - 1) / batch + 1;
+    int groups = 1;
+    while (groups < kJoinGroups && groups * 8 < partials && (int64_t)batch * num_heads * groups * 2 <= kJoinWave) groups *= 2;
+    return launch_pdl(partials <= 4 ? reinterpret_cast<const void *>(&latent_join_kernel<4>)
+                                    : reinterpret_cast<const void *>(&latent_join_kernel<8>),
+                      dim3((unsigned)num_heads, (unsigned)batch), (unsigned)(kJoinGroup * groups), 0, stream, args);
 }
 
 }  // namespace nvfp4kv
