@@ -51,6 +51,17 @@ __device__ __forceinline__ float2 mul2(float2 a, float b) {
     return make_float2(__uint_as_float((uint32_t)d), __uint_as_float((uint32_t)(d >> 32)));
 }
 
+// a * b + c for a pair of floats, each rounded once.
+__device__ __forceinline__ float2 fma2(float2 a, float b, float2 c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(d)
+        : "l"((uint64_t)__float_as_uint(a.x) | ((uint64_t)__float_as_uint(a.y) << 32)),
+          "l"((uint64_t)__float_as_uint(b) | ((uint64_t)__float_as_uint(b) << 32)),
+          "l"((uint64_t)__float_as_uint(c.x) | ((uint64_t)__float_as_uint(c.y) << 32)));
+    return make_float2(__uint_as_float((uint32_t)d), __uint_as_float((uint32_t)(d >> 32)));
+}
+
 // Approximate reciprocal (the hardware's, at most one unit in the last place off).
 __device__ __forceinline__ float rcp_approx(float x) {
     float y;
@@ -126,7 +137,7 @@ __device__ __forceinline__ uint32_t e2m1_code_exact(float a, float den, float g)
 // normal range for den in [2^-9, 2688]), and rounded twice, at (1 - 2^-20) and (1 +
 // 2^-20) times the estimate.  Where both give one code, so does the exact quotient
 // between them; where they differ (one midpoint lies between), the midpoint is
-// compared exactly, as above.
+// compared exactly, as above.  Most blocks go a shorter way still (e2m1x8_corrected).
 constexpr float kPlainScaleMin = 0x1p-60f, kPlainScaleMax = 0x1p60f;
 constexpr float kBelow = 1.0f - 0x1p-20f, kAbove = 1.0f + 0x1p-20f;
 
@@ -175,6 +186,39 @@ __device__ __forceinline__ uint32_t e2m1x8_between(const uint32_t *w, float sd, 
         }
     }
     return c;
+}
+
+// Where a corrected quotient x / (sd g) decides every rounding of a block.  The midpoints
+// between codes are 1, 1.25, 1.5 or 1.75 times a power of two, so a border of the block is
+// such a multiple of step = sd g, and x, a BF16 number, is either exactly on it or at least
+// eight units (of FP32's last place) away, unless the border's bits below BF16's lie
+// within eight units of a BF16 number without being one: those blocks are refused.
+__device__ __forceinline__ bool borders_apart(float sd, float g, float step) {
+    const bool exact = __fmaf_rn(sd, g, -step) == 0.0f;
+    bool ok = true;
+#pragma unroll
+    for (int c = 4; c < 8; c++) {
+        const float y = 0.25f * c * step;
+        const uint32_t low = __float_as_uint(y) & 0xffffu;
+        const bool on = exact && low == 0 && (c == 4 || __fmaf_rn(0.25f * c, step, -y) == 0.0f);
+        ok = ok && (on || (low >= 8u && low <= 0xfff8u));
+    }
+    return ok;
+}
+
+// Eight values -> their codes under borders_apart.  One correction brings the quotient to
+// within 2^-23 of x / step, and to the midpoint itself where x is on a border (what is left
+// of the error is then far below half a unit), which rounds to even as it must.
+__device__ __forceinline__ uint32_t e2m1x8_corrected(const uint32_t *w, float step, float r) {
+    float2 q[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const uint32_t v = w[i] ^ 0x80008000u;
+        const float2 n = make_float2(bf16_lo(v), bf16_hi(v));   // -x: so signed, a zero keeps its sign
+        q[i] = mul2(n, -r);
+        q[i] = fma2(fma2(q[i], step, n), -r, q[i]);
+    }
+    return f32x8_to_e2m1x8(q[0], q[1], q[2], q[3]);
 }
 
 // The e2m1 * e4m3 (or e4m3) value p, exact in FP32, times g, rounded once to
@@ -244,9 +288,14 @@ __device__ __forceinline__ void quantize_block16(const uint4 &a, const uint4 &b,
         packed[0] = f16x2x4_to_e2m1x8(h[0], h[1], h[2], h[3]);
         packed[1] = f16x2x4_to_e2m1x8(h[4], h[5], h[6], h[7]);
     } else if (plain) {
-        const float r = rcp_approx(sd * g);
-        packed[0] = e2m1x8_between(w, sd, g, r);
-        packed[1] = e2m1x8_between(w + 4, sd, g, r);
+        const float step = sd * g, r = rcp_approx(step);
+        if (amax * r <= 8.0f && borders_apart(sd, g, step)) {
+            packed[0] = e2m1x8_corrected(w, step, r);
+            packed[1] = e2m1x8_corrected(w + 4, step, r);
+        } else {
+            packed[0] = e2m1x8_between(w, sd, g, r);
+            packed[1] = e2m1x8_between(w + 4, sd, g, r);
+        }
     } else {
         const float xs = tiny ? kTinyRescale : 1.0f;
 #pragma unroll
