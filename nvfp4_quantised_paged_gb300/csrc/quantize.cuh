@@ -348,6 +348,16 @@ __device__ __forceinline__ void nvfp4_block_to_bf16(uint2 codes, uint32_t sbyte,
     for (int i = 0; i < 8; i++) o[i] = f16x2_to_bf16x2_scaled<kUnit>(hmul2(f[i], s2), g);
 }
 
+// The same for half a block: 4 code bytes -> 4 BF16 pairs.
+template <bool kUnit>
+__device__ __forceinline__ void nvfp4_half_block_to_bf16(uint32_t codes, uint32_t sbyte, float g, uint32_t (&o)[4]) {
+    const uint32_t s2 = e4m3x2_to_f16x2(sbyte | (sbyte << 8));
+    uint32_t f[4];
+    e2m1x8_to_f16x2x4(codes, f[0], f[1], f[2], f[3]);
+#pragma unroll
+    for (int i = 0; i < 4; i++) o[i] = f16x2_to_bf16x2_scaled<kUnit>(hmul2(f[i], s2), g);
+}
+
 // L2 policy "evict last" (all of a request's lines), for st_u8_policy.
 __device__ __forceinline__ uint64_t l2_policy_evict_last() {
     uint64_t p;
