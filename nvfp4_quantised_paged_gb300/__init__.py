@@ -633,12 +633,17 @@ def latent_prefix_dequant(cache: LatentCache, block_table: torch.Tensor, prefix_
     if latent_ws is None:
         latent_ws = torch.empty((total, LATENT_DIM), dtype=torch.bfloat16, device=cache.pool.device)
         made.append(latent_ws)
+        lp = latent_ws.data_ptr()
+    else:
+        lp = _want(latent_ws, "latent_ws", torch.bfloat16, (total, LATENT_DIM), dev)
     if rope_ws is None:
         rope_ws = torch.empty((total, ROPE_DIM), dtype=torch.bfloat16, device=cache.pool.device)
         made.append(rope_ws)
-    lp = _want(latent_ws, "latent_ws", torch.bfloat16, (total, LATENT_DIM), dev)
-    rp = _want(rope_ws, "rope_ws", torch.bfloat16, (total, ROPE_DIM), dev)
-    _keep_until_done(stream, *made)
+        rp = rope_ws.data_ptr()
+    else:
+        rp = _want(rope_ws, "rope_ws", torch.bfloat16, (total, ROPE_DIM), dev)
+    if stream is not None:
+        _keep_until_done(stream, *made)
     rc = _lib.nvfp4_latent_prefix_dequant(cache.desc, bp, block_table.shape[1], pp, cp, R, total, lp, rp, s)
     if rc:
         _check(rc, "nvfp4_latent_prefix_dequant")
@@ -679,12 +684,15 @@ def latent_decode_attention(cache: LatentCache, q_latent: torch.Tensor, q_rope: 
     if out is None:
         out = torch.empty_like(q_latent)
         made.append(out)
+        op = out.data_ptr()
+    else:
+        op = _want(out, "out", torch.bfloat16, (B, H, LATENT_DIM), dev)
     if workspace is None:
         workspace = alloc_latent_decode_workspace(cache, B, H, num_splits)
         made.append(workspace)
-    op = _want(out, "out", torch.bfloat16, (B, H, LATENT_DIM), dev)
     wp = _want(workspace, "workspace", torch.uint8, None, dev)
-    _keep_until_done(stream, *made)
+    if stream is not None:
+        _keep_until_done(stream, *made)
     rc = _lib.nvfp4_latent_decode_attention(cache.desc, qp, rp, B, H, bp, block_table.shape[1], lp,
                                             _LATENT_SCALE if sm_scale is None else float(sm_scale), op, wp,
                                             workspace.numel(), int(num_splits), s)
@@ -741,8 +749,11 @@ def latent_extend_attention(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: t
     s = _launch_stream(dev, stream)
     if out is None:
         out = torch.empty((TQ, H, HEAD_DIM), dtype=torch.bfloat16, device=q.device)
-        _keep_until_done(stream, out)
-    op = _want(out, "out", torch.bfloat16, (TQ, H, HEAD_DIM), dev)
+        op = out.data_ptr()
+        if stream is not None:
+            _keep_until_done(stream, out)
+    else:
+        op = _want(out, "out", torch.bfloat16, (TQ, H, HEAD_DIM), dev)
     rc = _lib.nvfp4_latent_extend_attention(qp, k0, v0, ps, ph, r0, pp, TP, k1, v1, cs, ch, r1, np_, TQ, R,
                                             int(max_q_len), H, _LATENT_SCALE if sm_scale is None else float(sm_scale),
                                             op, s)
@@ -823,19 +834,26 @@ def evict(cache: PagedCache, scores: torch.Tensor, block_table: torch.Tensor, se
     if new_lens is None:
         new_lens = torch.empty(B, dtype=torch.int32, device=where)
         made.append(new_lens)
+        nlp = new_lens.data_ptr()
+    else:
+        nlp = _want(new_lens, "new_lens", torch.int32, (B,), dev)
     if kept is None:
         kept = torch.empty((B, Hkv, keep), dtype=torch.int32, device=where)
         made.append(kept)
+        kp = kept.data_ptr()
+    else:
+        kp = _want(kept, "kept", torch.int32, (B, Hkv, keep), dev)
     if new_scores is None:
         new_scores = torch.empty((B, Hkv, max(S, keep)), dtype=torch.float32, device=where)
         made.append(new_scores)
-    nlp = _want(new_lens, "new_lens", torch.int32, (B,), dev)
-    kp = _want(kept, "kept", torch.int32, (B, Hkv, keep), dev)
-    nsp = _want(new_scores, "new_scores", torch.float32, None, dev)
-    if (new_scores.dim() != 3 or new_scores.shape[0] != B or new_scores.shape[1] != Hkv
-            or new_scores.shape[2] < keep):
-        raise ValueError("new_scores must be [batch][kv heads][at least keep]")
-    _keep_until_done(stream, *made)
+        nsp = new_scores.data_ptr()
+    else:
+        nsp = _want(new_scores, "new_scores", torch.float32, None, dev)
+        if (new_scores.dim() != 3 or new_scores.shape[0] != B or new_scores.shape[1] != Hkv
+                or new_scores.shape[2] < keep):
+            raise ValueError("new_scores must be [batch][kv heads][at least keep]")
+    if stream is not None:
+        _keep_until_done(stream, *made)
     rc = _lib.nvfp4_evict(cache.desc, cp, S, B, bp, block_table.shape[1], lp, np_, new_block_table.shape[1], keep,
                           int(recent), int(sink), nlp, kp, nsp, new_scores.shape[2], s)
     if rc:

@@ -12,7 +12,8 @@
 // half a block, so that each store of the warp is 512 contiguous bytes (with a block a
 // lane, whose two stores half fill each sector, 65,536 tokens took 19.9 us, then 16.6),
 // and the stores are streaming ones (14.1): the rows, 75 MB, would push the cache's pages
-// out of L2.  The rotary part of the four tokens is one 16-byte chunk a lane.  All loads
+// out of L2, and so would the rows that append reads (append and expanding one after the
+// other, g 0.75: 46.4 us, with both streaming 41.1).  The rotary part of the four tokens is one 16-byte chunk a lane.  All loads
 // of the four tokens are issued before the first conversion.
 //
 // 65,536 tokens: append 14.7 us (7.0 TB/s; 21.6 with a tensor scale, whose roundings
@@ -50,6 +51,8 @@ __device__ __forceinline__ int scale_off(int r, int b) {
 
 template <bool kUnitScale>
 __global__ void __launch_bounds__(kThreads) latent_append_kernel(LatentAppendArgs a) {
+    pdl_wait();   // the rows, the slots and the pages may be earlier work's
+    pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
     const int64_t t0 = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kTokens;
     if (t0 >= a.num_tokens) return;
@@ -61,8 +64,8 @@ __global__ void __launch_bounds__(kThreads) latent_append_kernel(LatentAppendArg
         slot[j] = -1;
         if (j >= nt) continue;
         const uint4 *src = a.latent + (t0 + j) * a.latent_stride16 + lane * 2;
-        x0[j] = __ldg(src);
-        x1[j] = __ldg(src + 1);
+        x0[j] = __ldcs(src);
+        x1[j] = __ldcs(src + 1);
         slot[j] = __ldg(a.slots + t0 + j);
     }
     const int rj = lane >> 3, chunk = lane & 7;   // rotary: token and 16-byte chunk of this lane
@@ -104,6 +107,8 @@ struct LatentDequantArgs {
 
 template <bool kUnitScale>
 __global__ void __launch_bounds__(kThreads) latent_dequant_kernel(LatentDequantArgs a) {
+    pdl_wait();   // the rows, the slots and the pages may be earlier work's
+    pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
     const int64_t t0 = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kTokens;
     if (t0 >= a.total) return;
@@ -185,11 +190,10 @@ cudaError_t launch_latent_append(const nvfp4kv_latent_cache &c, const void *late
     a.slots = slot_mapping;
     a.g = c.global_scale;
     a.err = err;
-    if (c.global_scale == 1.0f)
-        latent_append_kernel<true><<<grid_of(num_tokens), kThreads, 0, stream>>>(a);
-    else
-        latent_append_kernel<false><<<grid_of(num_tokens), kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    void *args[] = {&a};
+    return launch_pdl(c.global_scale == 1.0f ? reinterpret_cast<const void *>(&latent_append_kernel<true>)
+                                             : reinterpret_cast<const void *>(&latent_append_kernel<false>),
+                      grid_of(num_tokens), kThreads, 0, stream, args);
 }
 
 cudaError_t launch_latent_dequant(const nvfp4kv_latent_cache &c, const int32_t *block_table, int max_pages,
@@ -210,11 +214,10 @@ cudaError_t launch_latent_dequant(const nvfp4kv_latent_cache &c, const int32_t *
     a.latent_ws = static_cast<uint4 *>(latent_ws);
     a.rope_ws = static_cast<uint4 *>(rope_ws);
     a.err = err;
-    if (c.global_scale == 1.0f)
-        latent_dequant_kernel<true><<<grid_of(total), kThreads, 0, stream>>>(a);
-    else
-        latent_dequant_kernel<false><<<grid_of(total), kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    void *args[] = {&a};
+    return launch_pdl(c.global_scale == 1.0f ? reinterpret_cast<const void *>(&latent_dequant_kernel<true>)
+                                             : reinterpret_cast<const void *>(&latent_dequant_kernel<false>),
+                      grid_of(total), kThreads, 0, stream, args);
 }
 
 }  // namespace nvfp4kv
