@@ -213,7 +213,6 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
     float *s_m = reinterpret_cast<float *>(smem + L::kM), *s_fac = s_m + N, *s_alpha = s_fac + N, *s_off = s_alpha + N;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h0 = blockIdx.y * N;
-    if (warp == 16) tc_alloc(&tmem_base, L::kCols);
     if (tid == 0) {
         for (int i = 0; i < L::kNumBars; i++)
             mbar_init(&bars[i], i < 2 || i == 3 ? kWorkers / 32 : 1);
@@ -222,6 +221,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
     }
     pdl_wait();               // everything read or written may belong to earlier work of the stream
     pdl_launch_dependents();
+    if (warp == 16) tc_alloc(&tmem_base, L::kCols);   // (after the wait: an earlier kernel may need the columns first)
 
     int b0;
     unsigned first, u0 = 0, u1 = 0;

@@ -70,6 +70,25 @@ def test_scores_match_the_formula(m, lens, Hq, Hkv, P, dtype, gk):
         assert np.array_equal(scores[b, :, n:].cpu().numpy(), old[b, :, n:].numpy())
 
 
+@pytest.mark.parametrize("B", [140, 300])
+def test_scores_of_many_sequences(m, B):
+    """More sequences than a warp, and than a CTA, scans at once: each as if it were alone."""
+    lens = np.random.RandomState(B).randint(0, 150, B).tolist()
+    w = workloads.make_decode("weights many", B, lens, 4, 1, 16)
+    cache, _ = fill_both(w, m)
+    q, bt, sl = w.q("cuda"), w.block_table.cuda(), w.seq_lens.cuda()
+    got = torch.zeros((B, 1, 160), device="cuda")
+    m.accumulate_attention_weights(cache, q, bt, sl, got)
+    torch.cuda.synchronize()
+    assert m.check_device_errors() == 0
+    # the number of warps that share a sequence changes the order of its denominator's sums: 2^-20
+    for b in list(range(0, B, 37)) + [B - 1]:
+        one = torch.zeros((1, 1, 160), device="cuda")
+        m.accumulate_attention_weights(cache, q[b:b + 1].contiguous(), bt[b:b + 1].contiguous(), sl[b:b + 1].contiguous(), one)
+        assert ((one[0] - got[b]).abs() <= 2.0**-20 * one[0]).all()
+    assert (got[:, 0].sum(-1).cpu() - 4.0 * (torch.tensor(lens) > 0)).abs().max() < 1e-4
+
+
 @pytest.mark.parametrize("scale", [-SM, 0.0, 8 * SM])
 def test_scores_with_other_scales(m, scale):
     w = workloads.make_decode("weights scale", 9, [200, 77], 8, 2, 64)

@@ -196,6 +196,21 @@ def test_decode_matches_the_formula(m, lens, H, P, g, splits):
     _check_decode(m, out, cache, bt, lens, P, q, qr, g)
 
 
+@pytest.mark.parametrize("B", [130, 700])
+def test_decode_of_many_sequences(m, B):
+    """More sequences than a warp, and than a CTA, scans at once; some empty, more splits than tiles."""
+    lens = np.random.RandomState(B).randint(0, 60, B).tolist()
+    cache, bt = _filled(m, [sum(lens)], 16, B)
+    rows = torch.randperm(cache.num_pages, generator=torch.Generator().manual_seed(B))
+    bt = np.stack([np.roll(rows.numpy(), i)[:4] for i in range(B)]).astype(np.int32)   # pages shared by several
+    q, qr = _rand((B, 16, 512), 1, 0.5), _rand((B, 16, 64), 2)
+    for splits in (0, 1500):
+        out = m.latent_decode_attention(cache, q, qr, _cuda(bt), _cuda(lens), num_splits=splits)
+        torch.cuda.synchronize()
+        assert m.check_device_errors() == 0
+        _check_decode(m, out, cache, bt, lens, 16, q, qr, 1.0)
+
+
 @pytest.mark.parametrize("H", [16, 64])
 def test_decode_with_rising_scores_rescales(m, H):
     """Keys whose scores grow along the sequence move the running maximum again and again."""
