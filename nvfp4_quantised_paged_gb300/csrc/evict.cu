@@ -20,6 +20,8 @@
 // Nothing is atomic in global memory, so the result does not depend on timing.
 #include <cooperative_groups.h>
 
+#include <mutex>
+
 #include "common.cuh"
 #include "flat_plan.cuh"
 #include "kernels.h"
@@ -271,6 +273,7 @@ template <int T>
 __global__ void __launch_bounds__(T) select_one_kernel(SelectArgs a) {
     extern __shared__ __align__(16) uint32_t s_keys[];   // the scores' bits; later the keys between two borders
     __shared__ uint32_t s_count[2][32];
+    pdl_wait();                                     // scores and lengths may be earlier work's
     pdl_launch_dependents();                        // (the move waits for this grid to complete)
     const int seg = (int)blockIdx.x, tid = threadIdx.x;
     const int32_t len = a.seq_lens[seg / a.Hkv];
@@ -278,15 +281,15 @@ __global__ void __launch_bounds__(T) select_one_kernel(SelectArgs a) {
     const float *src = a.scores + (int64_t)seg * a.score_stride;
     int32_t *kept = a.kept + (int64_t)seg * a.keep;
     float *dst = a.new_scores + (int64_t)seg * a.new_score_stride;
-    if (select_edges(a, seg, n, len, tid, T, src, kept, dst)) return;
-    // the scores by asynchronous copies, all in flight at once
-    if ((a.score_stride & 3) == 0 && (reinterpret_cast<uintptr_t>(a.scores) & 15) == 0) {
+    // the scores by asynchronous copies, all in flight at once, while what lies around the kept rows is written
+    if (n > a.keep && (a.score_stride & 3) == 0 && (reinterpret_cast<uintptr_t>(a.scores) & 15) == 0) {
         for (int t = 4 * tid; t < n; t += 4 * T)   // (a last one may pass n, not the row)
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(s_keys + t)), "l"(src + t) : "memory");
-    } else {
+    } else if (n > a.keep) {
         for (int t = tid; t < n; t += T)
             asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(s_keys + t)), "l"(src + t) : "memory");
     }
+    if (select_edges(a, seg, n, len, tid, T, src, kept, dst)) return;
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
     const int per = ((n + T - 1) / T) | 1;
@@ -306,6 +309,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(SelectArgs a) {
     __shared__ uint32_t s_warp[kSelWarps][2];       // kept-for-sure and border keys of each warp's part
     __shared__ uint32_t s_cta[2];                   // their sums; read by the cluster
     __shared__ uint32_t s_digit[2];
+    pdl_wait();
     pdl_launch_dependents();
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), C = (int)cluster.num_blocks();
@@ -550,11 +554,13 @@ cudaError_t launch_evict(const nvfp4kv_cache &c, const float *scores, int64_t sc
                          const int32_t *new_block_table, int new_max_pages, int keep, int recent, int sink,
                          int32_t *new_lens, int32_t *kept, float *new_scores, int64_t new_score_stride, unsigned *err,
                          cudaStream_t stream) {
+    static std::mutex mu;
     static bool attr_set[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::unique_lock<std::mutex> lock(mu);
     if (!attr_set[dev]) {
         e = cudaFuncSetAttribute(reinterpret_cast<const void *>(&select_kernel),
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, kKeyCache * 4);
@@ -564,6 +570,7 @@ cudaError_t launch_evict(const nvfp4kv_cache &c, const float *scores, int64_t sc
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
     }
+    lock.unlock();
     SelectArgs a;
     a.scores = scores;
     a.score_stride = score_stride;
@@ -591,13 +598,15 @@ cudaError_t launch_evict(const nvfp4kv_cache &c, const float *scores, int64_t sc
     const int64_t part = ceil_div64(a.cap, cluster);
     cfg.dynamicSmemBytes = (size_t)(part < kKeyCache ? part : kKeyCache) * 4;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)cluster;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     void *args[] = {&a};
     const void *fn = reinterpret_cast<const void *>(&select_kernel);
     if (one) {
@@ -607,7 +616,7 @@ cudaError_t launch_evict(const nvfp4kv_cache &c, const float *scores, int64_t sc
         cfg.gridDim = dim3((unsigned)segs);
         cfg.blockDim = dim3(small ? kOneSmall : kOneLarge);
         cfg.dynamicSmemBytes = ((size_t)a.cap + 3) / 4 * 16;
-        cfg.numAttrs = 0;
+        cfg.numAttrs = 1;
     }
     e = cudaLaunchKernelExC(&cfg, fn, args);
     if (e != cudaSuccess) return e;
