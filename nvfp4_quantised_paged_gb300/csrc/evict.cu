@@ -163,48 +163,79 @@ __device__ __forceinline__ uint32_t find_border(const uint32_t (&k)[K], uint32_t
     return border;
 }
 
+// The same for few keys a thread (`used` of them, the others are 0), two bits a step: the warp's counts of the three trials, up
+// to 32 K each, share a word (one bit a step took 4.0 us of the 32,768-row segments' 25).
+template <int T, int K>
+__device__ __forceinline__ uint32_t find_border_pairs(const uint32_t (&k)[K], int used, uint32_t want, uint32_t border,
+                                                      int top, uint32_t (&s_count)[2][32], bool &exact) {
+    static_assert(32 * K < 1024, "a warp's count must fit ten bits");
+    exact = false;
+    int buf = 0;
+    for (int bit = top & ~1; bit >= 0; bit -= 2, buf ^= 1) {
+        uint32_t c = 0;
+#pragma unroll
+        for (int i = 0; i < K; i++) {
+            if (i >= used) break;
+#pragma unroll
+            for (uint32_t x = 1; x < 4; x++) c += k[i] >= (border | (x << bit)) ? 1u << (10 * (x - 1)) : 0u;
+        }
+        c = __reduce_add_sync(0xffffffffu, c);
+        if ((threadIdx.x & 31) == 0) s_count[buf][threadIdx.x >> 5] = c;
+        __syncthreads();
+        c = (threadIdx.x & 31) < T / 32 ? s_count[buf][threadIdx.x & 31] : 0u;
+        const uint32_t c1 = __reduce_add_sync(0xffffffffu, c & 1023u), c2 = __reduce_add_sync(0xffffffffu, (c >> 10) & 1023u),
+                       c3 = __reduce_add_sync(0xffffffffu, c >> 20);
+        const uint32_t x = c3 >= want ? 3u : c2 >= want ? 2u : c1 >= want ? 1u : 0u;
+        border |= x << bit;
+        if ((x == 3 ? c3 : x == 2 ? c2 : x == 1 ? c1 : 0u) == want) {   // (want >= 1)
+            exact = true;
+            break;
+        }
+    }
+    return border;
+}
+
 template <int T, int PER>
 __device__ __forceinline__ void select_rows(const SelectArgs &a, int n, int per, int32_t *kept, uint32_t *s_keys,
                                             uint32_t (&s_count)[2][32]) {
     const int t0 = (int)threadIdx.x * per, last = n - a.recent;
     const uint32_t keep = (uint32_t)a.keep;
     auto key_at = [&](int t) { return t < a.sink || t >= last ? 0xffffffffu : score_key(__uint_as_float(s_keys[t])); };
+    if (PER > 5 && threadIdx.x < 64) {   // (while the other warps lay out their keys)
+        // sample ranks r -+ d around the border's expected one: warp 0 finds the upper border, warp 1 the lower
+        const int lane = (int)threadIdx.x & 31, low = (int)threadIdx.x >> 5;
+        uint32_t x[kSamplePer];
+#pragma unroll
+        for (int i = 0; i < kSamplePer; i++) x[i] = key_at((int)((int64_t)n * (i * 32 + lane) / kSample));
+        const int r = (int)((int64_t)keep * kSample / n), d = 4 + (int)(3.0f * sqrtf((float)r));
+        const uint32_t want = (uint32_t)(low ? min(r + d, kSample) : max(r - d, 0));
+        uint32_t found_at = 0;
+        for (int bit = 31; bit > 31 - kSampleBits; bit--) {
+            const uint32_t trial = found_at | (1u << bit);
+            uint32_t c[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < kSamplePer; i++) c[i & 3] += x[i] >= trial;
+            if (__reduce_add_sync(0xffffffffu, (c[0] + c[1]) + (c[2] + c[3])) >= want) found_at = trial;
+        }
+        // (the upper one no lower than the sample's border; no carry: the low bits are 0)
+        if (lane == 0) s_count[1][low] = low ? found_at : found_at + ((1u << (32 - kSampleBits)) - 1u);
+    }
     uint32_t k[PER];
 #pragma unroll
     for (int i = 0; i < PER; i++) k[i] = i < per && t0 + i < n ? key_at(t0 + i) : 0u;   // (0: below every border)
     uint32_t border = 0;
     bool exact = false, found = false;
     if (PER > 5) {
-        if (threadIdx.x < 64) {
-            // sample ranks r -+ d around the border's expected one: warp 0 finds the upper border, warp 1 the lower
-            const int lane = (int)threadIdx.x & 31, low = (int)threadIdx.x >> 5;
-            uint32_t x[kSamplePer];
-#pragma unroll
-            for (int i = 0; i < kSamplePer; i++) x[i] = key_at((int)((int64_t)n * (i * 32 + lane) / kSample));
-            const int r = (int)((int64_t)keep * kSample / n), d = 4 + (int)(3.0f * sqrtf((float)r));
-            const uint32_t want = (uint32_t)(low ? min(r + d, kSample) : max(r - d, 0));
-            uint32_t found_at = 0;
-            for (int bit = 31; bit > 31 - kSampleBits; bit--) {
-                const uint32_t trial = found_at | (1u << bit);
-                uint32_t c[4] = {0, 0, 0, 0};
-#pragma unroll
-                for (int i = 0; i < kSamplePer; i++) c[i & 3] += x[i] >= trial;
-                if (__reduce_add_sync(0xffffffffu, (c[0] + c[1]) + (c[2] + c[3])) >= want) found_at = trial;
-            }
-            // (the upper one no lower than the sample's border; no carry: the low bits are 0)
-            if (lane == 0) s_count[1][low] = low ? found_at : found_at + ((1u << (32 - kSampleBits)) - 1u);
-        }
         __syncthreads();
         const uint32_t hi = s_count[1][0], lo = s_count[1][1];
         uint32_t c = 0;
 #pragma unroll
         for (int i = 0; i < PER; i++) c += (k[i] >= hi ? 1u : 0u) + (k[i] >= lo ? 0x10000u : 0u);
+        const uint32_t own = (c >> 16) - (c & 0xffffu);   // lo <= key < hi
         c = cta_sum<T>(c, s_count, 0);           // (both at most kOneRows)
         const uint32_t c_hi = c & 0xffffu, c_lo = c >> 16;
         if (lo > 0 && c_hi < keep && keep <= c_lo && c_lo - c_hi <= T * kListPer) {
-            uint32_t own = 0, total;
-#pragma unroll
-            for (int i = 0; i < PER; i++) own += k[i] - lo < hi - lo;   // lo <= key < hi
+            uint32_t total;
             uint32_t at = cta_scan<T>(own, s_count, total);
 #pragma unroll
             for (int i = 0; i < PER; i++)
@@ -216,8 +247,8 @@ __device__ __forceinline__ void select_rows(const SelectArgs &a, int n, int per,
                 x[i] = threadIdx.x + i * T < total ? s_keys[threadIdx.x + i * T] : 0u;
             const uint32_t diff = lo ^ (hi - 1u);
             const int top = diff ? 31 - __clz((int)diff) : -1;
-            border = lo & ~(top >= 0 ? (top == 31 ? 0xffffffffu : (2u << top) - 1u) : 0u);
-            border = find_border<T>(x, keep - c_hi, border, top, s_count, exact);
+            border = top >= 0 ? lo & ~((4u << (top & ~1)) - 1u) : lo;   // (4 << 30: 0, all bits are open)
+            border = find_border_pairs<T>(x, ((int)total + T - 1) / T, keep - c_hi, border, top, s_count, exact);
             found = true;
         }
     }
@@ -227,13 +258,14 @@ __device__ __forceinline__ void select_rows(const SelectArgs &a, int n, int per,
     }
     // rows above the border stay, and of those equal to it the first keep - (rows above)
     const uint32_t from = exact ? border : border + 1u;   // (no overflow: a border of all ones is exact or never tried)
-    uint32_t gt = 0, eq = 0;
+    uint64_t take = 0, even = 0;
 #pragma unroll
     for (int i = 0; i < PER; i++) {
-        gt += k[i] >= from;
-        eq += k[i] == border;
+        if (k[i] >= from) take |= 1ull << i;
+        if (k[i] == border) even |= 1ull << i;
     }
-    if (exact) eq = 0;
+    if (exact) even = 0;
+    const uint32_t gt = (uint32_t)__popcll((long long)take), eq = (uint32_t)__popcll((long long)even);
     uint32_t total;                           // (both counts fit 16 bits: at most kOneRows)
     const uint32_t before = cta_scan<T>(gt | (eq << 16), s_count, total);
     total &= 0xffffu;
@@ -241,12 +273,10 @@ __device__ __forceinline__ void select_rows(const SelectArgs &a, int n, int per,
     const uint32_t eqs = before >> 16;
     uint32_t at = (before & 0xffffu) + min(eqs, need);
     uint32_t ties = eqs < need ? need - eqs : 0u;         // of this thread's ties, the first so many stay
-    uint64_t take = 0;
-#pragma unroll
-    for (int i = 0; i < PER; i++) {
-        const bool tie = !exact && k[i] == border && ties > 0;
-        ties -= tie;
-        if (k[i] >= from || tie) take |= 1ull << i;
+    while (even && ties > 0) {
+        take |= even & (0ull - even);
+        even &= even - 1;
+        ties--;
     }
     while (take) {                            // (one step a kept row of the fullest thread, not one a row)
         kept[at++] = t0 + __ffsll((long long)take) - 1;
