@@ -818,6 +818,9 @@ __global__ void __launch_bounds__(kJoinGroup *kJoinGroups) latent_join_kernel(La
         make_uint2(f32x2_to_bf16x2(acc.y * inv, acc.x * inv), f32x2_to_bf16x2(acc.w * inv, acc.z * inv));
 }
 
+// Heads of a CTA's tile.  More of them share an expanded tile: 32 sequences of 4,096 tokens
+// take 29.9 us with 32 heads in one tile and 41.6 us in two of 16, 41.3 us with 64 heads in
+// one tile and 49.8 us in two of 32 (69.5 against 87.7 us with 128 heads).
 int tile_heads(int H) { return H <= 16 ? 16 : H <= 32 ? 32 : 64; }
 
 const void *decode_fn(int n, int *smem) {
@@ -842,15 +845,24 @@ size_t align256l(size_t x) { return (x + 255) & ~(size_t)255; }
 
 }  // namespace
 
-int latent_decode_auto_splits(int num_heads, cudaError_t *status) {
-    int dev = 0, sms = 0;
+namespace {
+
+cudaError_t sm_count(int *sms) {
+    int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess && (dev < 0 || dev >= kMaxDevicesL)) e = cudaErrorInvalidDevice;
-    if (e == cudaSuccess) {
-        std::lock_guard<std::mutex> lock(g_mu_l);
-        if (!g_sms_l[dev]) e = cudaDeviceGetAttribute(&g_sms_l[dev], cudaDevAttrMultiProcessorCount, dev);
-        sms = g_sms_l[dev];
-    }
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(g_mu_l);
+    if (!g_sms_l[dev]) e = cudaDeviceGetAttribute(&g_sms_l[dev], cudaDevAttrMultiProcessorCount, dev);
+    *sms = g_sms_l[dev];
+    return e;
+}
+
+}  // namespace
+
+int latent_decode_auto_splits(int num_heads, cudaError_t *status) {
+    int sms = 0;
+    const cudaError_t e = sm_count(&sms);
     if (status) *status = e;
     if (e != cudaSuccess) return 0;
     const int n = tile_heads(num_heads), tiles = (num_heads + n - 1) / n;
@@ -867,11 +879,18 @@ cudaError_t launch_latent_decode(const nvfp4kv_latent_cache &c, const void *q_la
                                  int num_heads, const int32_t *block_table, int max_pages, const int32_t *seq_lens,
                                  float sm_scale, void *out, void *workspace, int splits, unsigned *err,
                                  cudaStream_t stream) {
-    const int n = tile_heads(num_heads), tiles = (num_heads + n - 1) / n;
-    int dev = 0, smem = 0;
+    int dev = 0, smem = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = sm_count(&sms);
     if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= kMaxDevicesL) return cudaErrorInvalidDevice;
+    // No more CTAs than there can be token tiles; and while there are SMs for it, smaller head
+    // tiles, whose steps are shorter (200 tokens: 10.7 us instead of 15.0 with 64 or 128 heads).
+    const int64_t cap = (int64_t)max_pages * c.page_size, most = batch * ((cap + kTile - 1) / kTile);
+    int n = tile_heads(num_heads);
+    for (int x = 16; x < n; x *= 2)
+        if (most * ((num_heads + x - 1) / x) <= sms) n = x;
+    const int tiles = (num_heads + n - 1) / n;
+    if (splits > most) splits = (int)most;
     const void *fn = decode_fn(n, &smem);
     {
         std::lock_guard<std::mutex> lock(g_mu_l);
@@ -892,7 +911,7 @@ cudaError_t launch_latent_decode(const nvfp4kv_latent_cache &c, const void *q_la
     a.max_pages = max_pages;
     a.block_table = block_table;
     a.seq_lens = seq_lens;
-    a.cap = (int64_t)max_pages * c.page_size;
+    a.cap = cap;
     a.ql = static_cast<const uint16_t *>(q_latent);
     a.qr = static_cast<const uint16_t *>(q_rope);
     a.score_log2 = (float)((double)sm_scale * 1.4426950408889634);

@@ -184,6 +184,11 @@ def _check_decode(m, out, cache, bt, lens, P, q, qr, g, sm=SM):
     ([513], 5, 16, 1.0, 7),
     ([40] * 30, 16, 16, 1.0, 0),
     ([40, 0] * 20, 40, 16, 1.0, 5),
+    ([300, 129, 0, 257] * 14, 32, 16, 1.0, 0),       # more tiles than SMs: head tiles of 32
+    ([300, 1, 280, 256] * 12, 64, 64, 0.75, 0),      # ... and of 64
+    ([260, 300, 40] * 14, 96, 32, 1.0, 0),
+    ([300, 200] * 20, 128, 128, 1.0, 0),
+    ([700] * 16, 40, 32, 1.0, 9),
 ])
 def test_decode_matches_the_formula(m, lens, H, P, g, splits):
     cache, bt = _filled(m, lens, P, 11 + H, g)
@@ -211,7 +216,7 @@ def test_decode_of_many_sequences(m, B):
         _check_decode(m, out, cache, bt, lens, 16, q, qr, 1.0)
 
 
-@pytest.mark.parametrize("H", [16, 64])
+@pytest.mark.parametrize("H", [16, 32, 64])
 def test_decode_with_rising_scores_rescales(m, H):
     """Keys whose scores grow along the sequence move the running maximum again and again."""
     P, n = 64, 1500
@@ -224,6 +229,12 @@ def test_decode_with_rising_scores_rescales(m, H):
     m.latent_quantize_append(cache, lat, rope, _cuda(_slots(bt[0], P, n), torch.int64))
     q = (g / 4).to(torch.bfloat16).expand(1, H, 512).contiguous()
     qr = _rand((1, H, 64), 8, 0.1)
+    for sm in (SM, -SM, 0.0):
+        for B in (1, 20):                     # (20: more tiles than SMs, larger head tiles)
+            out = m.latent_decode_attention(cache, q.expand(B, H, 512).contiguous(), qr.expand(B, H, 64).contiguous(),
+                                            _cuda(np.repeat(bt, B, 0)), _cuda([n] * B), sm_scale=sm, num_splits=2 * B)
+            torch.cuda.synchronize()
+            _check_decode(m, out[-1:], cache, bt, [n], P, q, qr, 1.0, sm)
     for sm in (SM, -SM, 0.0):
         out = m.latent_decode_attention(cache, q, qr, _cuda(bt), _cuda([n]), sm_scale=sm, num_splits=2)
         torch.cuda.synchronize()
