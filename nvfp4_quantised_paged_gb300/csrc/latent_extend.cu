@@ -78,7 +78,7 @@ struct ExtendArgs {
     unsigned *err;
 };
 
-constexpr int kMinTiles = 4;                   // K/V tiles a CTA of a cluster has at least, on average
+constexpr int kMinTiles = 4;                   // K/V tiles from which on clusters share them
 
 // K/V as 3-D maps [rows][heads][128] (any strides), the rotary rows as [rows][1][64]; boxes of 64 x 1 x 128.
 struct ExtendMaps {
@@ -611,10 +611,11 @@ cudaError_t launch_latent_extend(const void *q, const void *k_prefix, const void
     // Clusters share the K/V tiles of a CTA while the grid stays one wave of them: 32 heads x 2
     // query tiles of one request over 8,192 tokens take 148 us as 64 CTAs and 88 us as 64
     // clusters of two (157 us as 64 of four, which are two waves); 256 CTAs that are two waves
-    // already take 219 us either way.
+    // already take 219 us either way.  A tile a CTA is enough (8 heads, 64 queries over 1,100 tokens:
+    // 15.8 us in clusters of eight, 18.5 of four, 22.0 of two; over 300 tokens 16.7 of two, 15.5 alone).
     int split = 1;
     for (int k = 0; k < 3; k++)
-        if (ctas <= waves[dev][k] && tiles >= (kMinTiles << (k + 1))) split = 2 << k;
+        if (ctas <= waves[dev][k] && tiles >= (kMinTiles > (2 << k) ? kMinTiles : 2 << k)) split = 2 << k;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(qtiles * split), (unsigned)num_heads, (unsigned)num_reqs);
     cfg.blockDim = dim3(kEThreads);
