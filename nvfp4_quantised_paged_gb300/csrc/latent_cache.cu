@@ -6,18 +6,18 @@
 // dequant are bound by HBM: per token 1,152 B of BF16 on one side, 416 B of
 // cache on the other.
 //
-// One warp serves four tokens.  Appending, lane b is block b of each: the 32 lanes read
+// One warp serves four tokens (two where append rounds under a tensor scale).  Appending, lane b is block b of each: the 32 lanes read
 // one contiguous kilobyte of a token's BF16 row, store its codes in whole 32-byte
 // sectors (four lanes each) and its 32 scale bytes as one sector.  Expanding, a lane is
 // half a block, so that each store of the warp is 512 contiguous bytes (with a block a
 // lane, whose two stores half fill each sector, 65,536 tokens took 19.9 us, then 16.6),
 // and the stores are streaming ones (14.1): the rows, 75 MB, would push the cache's pages
 // out of L2, and so would the rows that append reads (append and expanding one after the
-// other, g 0.75: 46.4 us, with both streaming 41.1).  The rotary part of the four tokens is one 16-byte chunk a lane.  All loads
-// of the four tokens are issued before the first conversion.
+// other, g 0.75: 46.4 us, with both streaming 41.1, now 37.9).  The rotary parts are one 16-byte chunk a
+// lane.  All loads of the tokens are issued before the first conversion.
 //
-// 65,536 tokens: append 14.7 us (7.0 TB/s; 21.6 with a tensor scale, whose roundings
-// take their time), expanding 14.1 us (7.3 TB/s; 17.5).
+// 65,536 tokens: append 14.4 us (7.1 TB/s; 20.2 with a tensor scale, whose roundings
+// take their time), expanding 13.7 us (7.5 TB/s, part of it from L2; 17.1).
 #include "common.cuh"
 #include "kernels.h"
 #include "latent.cuh"
@@ -27,7 +27,7 @@ namespace nvfp4kv {
 
 namespace {
 
-constexpr int kTokens = 4;                 // tokens per warp
+constexpr int kTokens = 4;                 // tokens per warp, at most
 constexpr int kThreads = 256;
 
 struct LatentAppendArgs {
@@ -49,18 +49,24 @@ __device__ __forceinline__ int scale_off(int r, int b) {
     return kLatentScales + r * 32 + ((b >> 1) & 1) * 16 + (b >> 2) * 2 + (b & 1);
 }
 
+// Tokens a warp appends: the tensor scale's roundings take registers, and more warps an SM
+// make up for fewer tokens each (65,536 tokens: 20.2 us with two, 21.1 with four, 22.3 with
+// one; at scale 1 14.9, 14.4 and 15.8).
+constexpr int append_tokens(bool unit_scale) { return unit_scale ? kTokens : 2; }
+
 template <bool kUnitScale>
 __global__ void __launch_bounds__(kThreads) latent_append_kernel(LatentAppendArgs a) {
     pdl_wait();   // the rows, the slots and the pages may be earlier work's
     pdl_launch_dependents();
+    constexpr int NT = append_tokens(kUnitScale);
     const int lane = threadIdx.x & 31;
-    const int64_t t0 = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kTokens;
+    const int64_t t0 = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * NT;
     if (t0 >= a.num_tokens) return;
-    const int nt = (int)min((int64_t)kTokens, a.num_tokens - t0);
-    uint4 x0[kTokens], x1[kTokens], rp = make_uint4(0, 0, 0, 0);
-    int64_t slot[kTokens];
+    const int nt = (int)min((int64_t)NT, a.num_tokens - t0);
+    uint4 x0[NT], x1[NT], rp = make_uint4(0, 0, 0, 0);
+    int64_t slot[NT];
 #pragma unroll
-    for (int j = 0; j < kTokens; j++) {
+    for (int j = 0; j < NT; j++) {
         slot[j] = -1;
         if (j >= nt) continue;
         const uint4 *src = a.latent + (t0 + j) * a.latent_stride16 + lane * 2;
@@ -72,7 +78,7 @@ __global__ void __launch_bounds__(kThreads) latent_append_kernel(LatentAppendArg
     if (rj < nt) rp = __ldg(a.rope + (t0 + rj) * a.rope_stride16 + chunk);
     int64_t rslot = -1;
 #pragma unroll
-    for (int j = 0; j < kTokens; j++) {
+    for (int j = 0; j < NT; j++) {
         if (slot[j] >= a.num_slots) {
             if (lane == 0) flag_error(a.err, kErrSlot);
             slot[j] = -1;
@@ -170,7 +176,7 @@ __global__ void __launch_bounds__(kThreads) latent_dequant_kernel(LatentDequantA
     }
 }
 
-unsigned grid_of(int64_t tokens) { return (unsigned)ceil_div64(tokens, kTokens * (kThreads / 32)); }
+unsigned grid_of(int64_t tokens, int per_warp) { return (unsigned)ceil_div64(tokens, per_warp * (kThreads / 32)); }
 
 }  // namespace
 
@@ -193,7 +199,7 @@ cudaError_t launch_latent_append(const nvfp4kv_latent_cache &c, const void *late
     void *args[] = {&a};
     return launch_pdl(c.global_scale == 1.0f ? reinterpret_cast<const void *>(&latent_append_kernel<true>)
                                              : reinterpret_cast<const void *>(&latent_append_kernel<false>),
-                      grid_of(num_tokens), kThreads, 0, stream, args);
+                      grid_of(num_tokens, append_tokens(c.global_scale == 1.0f)), kThreads, 0, stream, args);
 }
 
 cudaError_t launch_latent_dequant(const nvfp4kv_latent_cache &c, const int32_t *block_table, int max_pages,
@@ -217,7 +223,7 @@ cudaError_t launch_latent_dequant(const nvfp4kv_latent_cache &c, const int32_t *
     void *args[] = {&a};
     return launch_pdl(c.global_scale == 1.0f ? reinterpret_cast<const void *>(&latent_dequant_kernel<true>)
                                              : reinterpret_cast<const void *>(&latent_dequant_kernel<false>),
-                      grid_of(total), kThreads, 0, stream, args);
+                      grid_of(total, kTokens), kThreads, 0, stream, args);
 }
 
 }  // namespace nvfp4kv
