@@ -471,9 +471,12 @@ NVFP4KV_API int nvfp4_latent_decode_attention(const nvfp4kv_latent_cache *cache,
  *   rope_chunk    device BF16 [total_q][64]
  *   cu_prefix_lens, cu_q_lens, total_*, max_q_len   as nvfp4_extend_attention
  *   out           device BF16 [total_q][num_heads][128].
- * Pointers 16-byte aligned, strides multiples of 8 elements, head strides >=
- * 128.  BF16 products, FP32 sums on the tensor cores, probabilities in BF16.
- * The prefix pointers may be NULL when total_prefix_tokens is 0.
+ * Pointers 16-byte aligned, strides multiples of 8 elements and >= 128,
+ * sm_scale > 0.  BF16 products, FP32 sums on the tensor cores, probabilities
+ * in BF16.  The prefix pointers may be NULL when total_prefix_tokens is 0.
+ * Rows of other requests and behind the last one may hold anything; a NaN or
+ * infinity in a value row of the request itself may reach the chunk's earlier
+ * tokens too (their probability of 0 times it is a NaN).
  */
 NVFP4KV_API int nvfp4_latent_extend_attention(const void *q, const void *k_prefix, const void *v_prefix,
                                               int64_t prefix_token_stride, int64_t prefix_head_stride,

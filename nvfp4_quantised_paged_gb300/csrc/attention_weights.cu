@@ -23,6 +23,11 @@
 // dimensions 32j .. 32j + 31 of its tokens: 16 contiguous bytes of codes a token;
 // e2m1 x e4m3 is an exact FP16 value, and q is FP16 after a power-of-two pre-scale a head
 // (exact above 2^-29 of its largest value), undone in the FP32 score factor.
+//
+// 16 sequences of up to 32,768 tokens, 64 query and 8 kv heads: 105 us (stats 47, weights
+// 58), of which one reading of K is 32 us.  Each pass is bound by unpacking: 170 to 195
+// instructions a 16-token group, half of the ALU's slots, at four warps a scheduler.
+// Three CTAs an SM (80 registers) took 122 us, 32-token units 132 us.
 #include <mutex>
 
 #include "common.cuh"

@@ -12,7 +12,7 @@
 //            the same digit; then each warp counts and compacts a contiguous part of the
 //            rows, its offset coming from one scan over the CTA's warps and one over the
 //            cluster.  Keys stay in shared memory between the rounds as far as they fit.
-//            (16 x 8 segments of up to 32,768 rows: 29 us with one CTA each, 66 us with
+//            (16 x 8 segments of up to 32,768 rows: 23 us with one CTA each, 66 us with
 //            clusters of four.)
 //   move     one warp per 16-row group of the new pages gathers its rows and writes the
 //            group's contiguous bytes: 36 us for 524,288 rows, which read 288 bytes of
@@ -37,7 +37,10 @@ constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kKeyCache = 16384;            // keys of a CTA's part kept in shared memory (64 KB)
 constexpr int kMaxCluster = 8;
 
-constexpr int kTargetCtasSel = 304;         // two CTAs per SM of a 152-SM GPU
+// CTAs that a launch of clusters aims at, two per SM of a 152-SM GPU.  (16 x 8 segments of
+// 40,000 rows: 107 us with 304, 171 us with 152, 118 us with 608; one segment: 24 us as a
+// cluster of eight, 164 us alone.)
+constexpr int kTargetCtasSel = 304;
 
 struct SelectArgs {
     const float *scores;

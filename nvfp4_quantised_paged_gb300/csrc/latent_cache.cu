@@ -6,15 +6,16 @@
 // dequant are bound by HBM: per token 1,152 B of BF16 on one side, 416 B of
 // cache on the other.
 //
-// One warp serves four tokens (two where append rounds under a tensor scale).  Appending, lane b is block b of each: the 32 lanes read
-// one contiguous kilobyte of a token's BF16 row, store its codes in whole 32-byte
-// sectors (four lanes each) and its 32 scale bytes as one sector.  Expanding, a lane is
-// half a block, so that each store of the warp is 512 contiguous bytes (with a block a
-// lane, whose two stores half fill each sector, 65,536 tokens took 19.9 us, then 16.6),
-// and the stores are streaming ones (14.1): the rows, 75 MB, would push the cache's pages
-// out of L2, and so would the rows that append reads (append and expanding one after the
-// other, g 0.75: 46.4 us, with both streaming 41.1, now 37.9).  The rotary parts are one 16-byte chunk a
-// lane.  All loads of the tokens are issued before the first conversion.
+// One warp serves four tokens (two where append rounds under a tensor scale).
+// Appending, lane b is block b of each: the 32 lanes read one contiguous kilobyte of a
+// token's BF16 row, store its codes in whole 32-byte sectors (four lanes each) and its 32
+// scale bytes as one sector.  Expanding, a lane is half a block, so that each store of the
+// warp is 512 contiguous bytes (with a block a lane, whose two stores half fill each
+// sector, 65,536 tokens took 19.9 us, then 16.6), and the stores are streaming ones
+// (14.1): the rows, 75 MB, would push the cache's pages out of L2, and so would the rows
+// that append reads (append and expanding one after the other, g 0.75: 46.4 us, with both
+// streaming 41.1, now 37.9).  The rotary parts are one 16-byte chunk a lane.  All loads of
+// the tokens are issued before the first conversion.
 //
 // 65,536 tokens: append 14.4 us (7.1 TB/s; 20.2 with a tensor scale, whose roundings
 // take their time), expanding 13.7 us (7.5 TB/s, part of it from L2; 17.1).

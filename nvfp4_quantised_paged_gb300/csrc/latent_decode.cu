@@ -22,14 +22,16 @@
 //     the page in contiguous pieces, each requested again for the next tile as soon as it
 //     is used.  A block goes to the tile in shared memory, as soon as the previous tile's
 //     O^T row block that reads it is done, and to TMEM as the A operand of S^T (all
-//     column blocks up to 32 heads, four with 64; the rotary part to TMEM alone): an A
+//     column blocks up to 32 heads, the last four with 64; the rotary part to TMEM alone): an A
 //     operand in shared memory costs a product 4 KB of reads, at least 38 clocks at any
 //     N, one in TMEM 9 at N = 16, and shared memory's bandwidth is what bounds the tile.
 //     The store to TMEM takes a quad's registers as four columns each, so the dims of a
 //     column block lie there in another order (position 16 k + 4 q + e holds dim 16 q + 4
 //     k + e), and those of Q's blocks with them;
+//     What S^T reads from TMEM is handed over without a proxy fence (about 1,000
+//     clocks); the tile's copy in shared memory is fenced with P, before O^T;
 //   * softmax: one token (= TMEM lane) a thread, the four warpgroups taking a quarter of
-//     the heads each: base 2 with a lazily moved maximum per head (a vote over the
+//     the heads each: s - m + 7 by one multiply-add, base 2 with a lazily moved maximum per head (a vote over the
 //     warpgroup; O^T is rescaled only when a score exceeds the maximum by 2^8), P =
 //     2^(s - m + 7) in FP16 (the offset uses FP16's upper range: weights down to 2^-21 of
 //     the largest keep full precision); the row sums of the rounded P stay in registers
@@ -39,10 +41,19 @@
 // of the chain (expand, S^T, softmax, O^T) slows down, and there is no room in shared
 // memory for a second tile that would let them overlap.
 //
-// Split: the batch's 128-token tiles form one flat range, cut equally over the
-// CTAs of a head tile (64 heads).  A sequence that lies in one CTA is normalised
-// and written there; others leave (m, l, O) partials that a second kernel joins.
-// Every wait is bounded.
+// Split: the batch's 128-token tiles form one flat range, cut equally over the CTAs of a
+// head tile; a sequence's start (its Q, the last one's output) counts as one tile more
+// (32 x 8,192 tokens, 16 heads: 35.1 us, 33.0 so).  A sequence that lies in one CTA is
+// normalised and written there; others leave (m, l, O) partials that a second kernel
+// joins.  Every wait is bounded.
+//
+// Measured (ragged lengths up to n): 32 sequences, n 8,192, 16 heads 32.2 us; 64, n 4,096,
+// 64 heads 56.2 us; 8, n 32,768, 128 heads 88.2 us (602 TFLOP/s); one of 77 tokens 7.7 us.
+// Of the first, 3.8 us pass until the first tile is expanded, 20 us in nine tiles of 4,300
+// clocks, 8 us in storing and joining partials.  A tile is bound by its expansion (1,024
+// conversions and as many packed multiplies a warp's width, 2,700 clocks with the stores)
+// and by shared memory's bandwidth: 128 KB written and 150 KB (N 16) to 300 KB (N 64) of
+// operands read at 128 bytes a clock.
 #include <mutex>
 
 #include "common.cuh"
@@ -536,7 +547,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
                     *reinterpret_cast<uint4 *>(blk + sw128_off(tr, 2 * eq)) = make_uint4(f[e][0], f[e][1], f[e][2], f[e][3]);
                     *reinterpret_cast<uint4 *>(blk + sw128_off(tr, 2 * eq + 1)) = make_uint4(f[e][4], f[e][5], f[e][6], f[e][7]);
                 }
-                if (i & 1) {   // half of the tile at a time; what S^T reads from TMEM needs no proxy fence (about 1,000 clocks)
+                if (i & 1) {   // half of the tile at a time (a quarter at a time: the same)
                     if (2 * i <= L::kSmemCbs) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     tc_wait_st();
                     tc_fence_before();
@@ -716,8 +727,8 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
 // Joins the partials of the sequences that several CTAs covered: one CTA per (sequence,
 // head), thread t of a group of 128 owns dims 4 t .. 4 t + 3, and the groups (as many as
 // the launch has) take the partials in turn, U at a time.  It waits for loads: U and the
-// groups are as large as one wave of CTAs allows (b8 h128: 8.7 us with U = 4 and four
-// groups in two waves).
+// groups are as large as one wave of CTAs allows (8 x 128 heads, 11 partials on average:
+// 4.9 us with U = 8, 8.7 us with U = 4 and four groups in two waves).
 constexpr int kJoinGroup = 128, kJoinGroups = 8, kJoinWave = 152 * 8;   // groups of threads that run at once
 
 template <int U>

@@ -160,10 +160,8 @@ __device__ __forceinline__ void tc_st_16x256_x4(uint32_t taddr, const uint32_t (
 // Overloads by the number of columns.
 __device__ __forceinline__ void tc_ld(uint32_t taddr, uint32_t (&r)[4]) { tc_ld4(taddr, r); }
 __device__ __forceinline__ void tc_st(uint32_t taddr, const uint32_t (&r)[4]) { tc_st4(taddr, r); }
-__device__ __forceinline__ void tc_ld(uint32_t taddr, uint32_t (&r)[32]) { tc_ld32(taddr, r); }
 __device__ __forceinline__ void tc_ld(uint32_t taddr, uint32_t (&r)[16]) { tc_ld16(taddr, r); }
 __device__ __forceinline__ void tc_ld(uint32_t taddr, uint32_t (&r)[8]) { tc_ld8(taddr, r); }
-__device__ __forceinline__ void tc_st(uint32_t taddr, const uint32_t (&r)[32]) { tc_st32(taddr, r); }
 __device__ __forceinline__ void tc_st(uint32_t taddr, const uint32_t (&r)[16]) { tc_st16(taddr, r); }
 __device__ __forceinline__ void tc_st(uint32_t taddr, const uint32_t (&r)[8]) { tc_st8(taddr, r); }
 
