@@ -505,8 +505,8 @@ int nvfp4_accumulate_attention_weights(const nvfp4kv_cache *cache, const void *q
         return NVFP4KV_EINVAL;
     if ((int64_t)max_pages_per_seq * cache->page_size > kMaxRows) return NVFP4KV_EUNSUPPORTED;
     const int64_t rows = std::min(score_stride, (int64_t)max_pages_per_seq * cache->page_size);
-    if ((int64_t)batch * cache->num_kv_heads > (((int64_t)1 << 31) - 1) / ((rows + 63) / 64))
-        return NVFP4KV_EUNSUPPORTED;   // 64-token units, counted in 32 bits
+    if ((int64_t)batch * cache->num_kv_heads > (((int64_t)1 << 31) - 1) / ((rows + kScoreUnit - 1) / kScoreUnit))
+        return NVFP4KV_EUNSUPPORTED;   // units, counted in 32 bits
     cudaError_t e = cudaSuccess;
     const int workers = weights_workers(cache->dtype, G, &e);
     if (e != cudaSuccess || workers <= 0) return NVFP4KV_ECUDA;

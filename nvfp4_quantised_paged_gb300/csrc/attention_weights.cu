@@ -7,7 +7,7 @@
 // sequence, and the weights are held in FP32 (decode rounds its
 // probabilities to FP16, which a running sum would keep).
 //
-// Two kernels walk the same flat order of 64-token units (sequence, kv head,
+// Two kernels walk the same flat order of 96-token units (sequence, kv head,
 // unit), cut into one contiguous piece a warp:
 //   stats    running maximum and sum of 2^(s - m), kept by every thread for its
 //            own (token, head) positions and joined only where the warp leaves a
@@ -15,19 +15,20 @@
 //   weights  joins the partials of a pair into L = m + log2 l, forms the scores'
 //            products again and adds sum_j 2^(s_j - L_j): no atomics, one
 //            addition per entry.
-// Every warp has a ring of three 64-token stages that it fills itself with bulk
-// copies of the groups' K halves, two units ahead (loads to registers left the
-// warps waiting for memory a third of the time, and held 36 registers).  The
+// Every warp has two 96-token stages that it fills itself with bulk copies of the
+// groups' K halves, a unit ahead (loads to registers left the warps waiting for
+// memory a third of the time, and held 36 registers; three stages of 64 tokens: 105
+// us for the case below, two 104, two of 80 tokens 102, two of 96 101).  The
 // scores come from mma.sync m16n8k16 with the 16 tokens of a group on M and the
 // heads on N.  The contraction's order is free, so thread j of a quad takes the
 // dimensions 32j .. 32j + 31 of its tokens: 16 contiguous bytes of codes a token;
 // e2m1 x e4m3 is an exact FP16 value, and q is FP16 after a power-of-two pre-scale a head
 // (exact above 2^-29 of its largest value), undone in the FP32 score factor.
 //
-// 16 sequences of up to 32,768 tokens, 64 query and 8 kv heads: 105 us (stats 47, weights
-// 58), of which one reading of K is 32 us.  Each pass is bound by unpacking: 170 to 195
+// 16 sequences of up to 32,768 tokens, 64 query and 8 kv heads: 99 us (stats 45, weights
+// 54), of which one reading of K is 32 us.  Each pass is bound by unpacking: some 160
 // instructions a 16-token group, half of the ALU's slots, at four warps a scheduler.
-// Three CTAs an SM (80 registers) took 122 us, 32-token units 132 us.
+// Three CTAs an SM (80 registers, 64-token units) took 122 us.
 #include <mutex>
 
 #include "common.cuh"
@@ -41,9 +42,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarpsW = kThreads / 32;
-constexpr int kUnit = 64;                     // tokens per unit
+constexpr int kUnit = kScoreUnit;                     // tokens per unit
 constexpr int kGroupsW = kUnit / 16;
-constexpr int kStagesW = 3;                   // ring stages of a warp
+constexpr int kStagesW = 2;                   // ring stages of a warp
 constexpr uint32_t kWaitLimitW = 1u << 24;
 constexpr float kNegInfW = -__builtin_huge_valf();
 
@@ -269,6 +270,19 @@ __global__ void __launch_bounds__(kThreads, 2) weights_kernel(WeightsArgs a) {
             npage = unit_page(a, nx, lane);
         }
         if (++ahead == kStagesW) ahead = 0;
+        const bool fast = it.t + kUnit <= it.n;   // a whole unit: no masks
+        b = it.b;
+        const int h = it.h, n = it.n, t0 = it.t;
+        const int g = lane >> 2, j = lane & 3;
+        float *dst = a.scores + ((int64_t)b * a.Hkv + h) * a.score_stride + t0 + g + 8 * (j & 1);
+        float old[kGroupsW];
+        if (!kStats) {   // lanes j = 0 and 1 of a quad own tokens g and g + 8
+#pragma unroll
+            for (int i = 0; i < kGroupsW; i++) {
+                old[i] = 0.f;
+                if (j < 2 && (fast || t0 + 16 * i + g + 8 * j < n)) old[i] = dst[16 * i];
+            }
+        }
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bar[stage], parity, kWaitLimitW, abort_flag));
         if (!ok) break;
         const uint8_t *unit = ring + stage * H::kStage;
@@ -276,9 +290,6 @@ __global__ void __launch_bounds__(kThreads, 2) weights_kernel(WeightsArgs a) {
             stage = 0;
             parity ^= 1;
         }
-        const bool fast = it.t + kUnit <= it.n;   // a whole unit: no masks
-        b = it.b;
-        const int h = it.h, n = it.n, t0 = it.t;
         if (fresh) {
             load_query<NT>(a, b, h, lane, qf, fac);
             if (kStats) {
@@ -324,16 +335,6 @@ __global__ void __launch_bounds__(kThreads, 2) weights_kernel(WeightsArgs a) {
                             m[x][1] = mine[8 * x + 2 * q + 1];
                         }
                 }
-            }
-        }
-        const int g = lane >> 2, j = lane & 3;
-        float *dst = a.scores + ((int64_t)b * a.Hkv + h) * a.score_stride + t0 + g + 8 * (j & 1);
-        float old[kGroupsW];
-        if (!kStats) {   // lanes j = 0 and 1 of a quad own tokens g and g + 8
-#pragma unroll
-            for (int i = 0; i < kGroupsW; i++) {
-                old[i] = 0.f;
-                if (j < 2 && (fast || t0 + 16 * i + g + 8 * j < n)) old[i] = dst[16 * i];
             }
         }
         float sc[kStats ? kGroupsW : 1][NT][4];

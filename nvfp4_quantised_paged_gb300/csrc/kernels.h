@@ -18,6 +18,9 @@ cudaError_t launch_prefix_dequant(const nvfp4kv_cache &c, const int32_t *block_t
                                   const int32_t *prefix_lens, const int32_t *cu, int num_reqs, int64_t total,
                                   void *k_ws, void *v_ws, unsigned *err, cudaStream_t stream);
 
+// Tokens of a unit of the scores' work (attention_weights.cu).
+constexpr int kScoreUnit = 96;
+
 // Number of decode CTAs an auto split uses (SM count x resident CTAs per SM).
 int decode_auto_grid(const nvfp4kv_cache &c, int group, cudaError_t *status);
 

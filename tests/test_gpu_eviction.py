@@ -37,6 +37,8 @@ def _k_of(w, pool, b):
     ([300, 256], 4, 1, 16, 0, 1.0),
     ([0, 63, 64, 65, 1], 16, 2, 32, 0, 1.0),
     ([1000, 17], 40, 8, 64, 0, 1.0),
+    ([95, 96, 97, 192, 193], 8, 2, 16, 0, 1.0),
+    ([385, 96, 95], 16, 1, 32, 1, 1.0),
     ([700, 129], 32, 2, 128, 0, 1.0),          # 16 heads a group
     ([500], 9, 1, 64, 0, 1.0),
     ([300, 40], 16, 2, 64, 1, 1.0),            # FP8 pool
