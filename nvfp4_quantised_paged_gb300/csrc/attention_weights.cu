@@ -25,8 +25,8 @@
 // e2m1 x e4m3 is an exact FP16 value, and q is FP16 after a power-of-two pre-scale a head
 // (exact above 2^-29 of its largest value), undone in the FP32 score factor.
 //
-// 16 sequences of up to 32,768 tokens, 64 query and 8 kv heads: 99 us (stats 45, weights
-// 54), of which one reading of K is 32 us.  Each pass is bound by unpacking: some 160
+// 16 sequences of up to 32,768 tokens, 64 query and 8 kv heads: 94 us (stats 45, the
+// rest weights), of which one reading of K is 32 us.  Each pass is bound by unpacking: some 160
 // instructions a 16-token group, half of the ALU's slots, at four warps a scheduler.
 // Three CTAs an SM (80 registers, 64-token units) took 122 us.
 #include <mutex>
@@ -188,8 +188,14 @@ __global__ void __launch_bounds__(kThreads, 2) weights_kernel(WeightsArgs a) {
     __shared__ FlatScratch<kThreads> scratch;
     __shared__ uint64_t bars[kWarpsW][kStagesW];
     __shared__ int abort_all;
-    pdl_wait();   // lengths, q and the cache may come from earlier work; the weights kernel reads the partials
-    pdl_launch_dependents();
+    // Lengths, q, the cache and the scores may come from earlier work, which is done when the stats
+    // kernel has passed its wait: it lets the weights kernel start only then, and that one has to
+    // wait again for the partials alone (2 x 300 tokens: 11.1 us, 9.3 so;
+    // 16 x 32,768: 99 and 94).
+    if (kStats) {
+        pdl_wait();
+        pdl_launch_dependents();
+    }
     const int lane = threadIdx.x & 31;
     const unsigned worker = blockIdx.x * kWarpsW + (threadIdx.x >> 5);
     auto rows = [&](int b) { return clamp_rows(__ldg(a.seq_lens + b), a.cap); };
@@ -212,7 +218,10 @@ __global__ void __launch_bounds__(kThreads, 2) weights_kernel(WeightsArgs a) {
         b, first);
     if (threadIdx.x == 0) abort_all = 0;
     __syncthreads();
-    if (u0 >= u1) return;   // more warps than units
+    if (u0 >= u1) {         // more warps than units
+        pdl_wait();         // (no CTA of the weights kernel ends before the stats kernel has)
+        return;
+    }
     UnitIter it;
     it.b = b;
     it.n = rows(b);
@@ -299,6 +308,7 @@ __global__ void __launch_bounds__(kThreads, 2) weights_kernel(WeightsArgs a) {
                     l[x][0] = l[x][1] = 0.f;
                 }
             } else {
+                pdl_wait();
                 // the pair's units [p0, p0 + nu) were covered by these warps
                 const int nu = (n + kUnit - 1) / kUnit;
                 const FlatCut cut(total, a.workers);

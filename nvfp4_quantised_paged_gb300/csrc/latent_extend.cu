@@ -103,6 +103,8 @@ __global__ void __launch_bounds__(kEThreads, 1)
     uint32_t &tmem_base = *reinterpret_cast<uint32_t *>(smem + kOffTmem);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffAbort);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    pdl_wait();               // everything read or written may belong to earlier work of the stream
+    pdl_launch_dependents();
     // Requests in order of decreasing prefix length: blockIdx.z is the rank (the longest CTAs start first).
     int r = blockIdx.z;
     if (gridDim.z <= kOrderMax) {
@@ -621,13 +623,15 @@ cudaError_t launch_latent_extend(const void *q, const void *k_prefix, const void
     cfg.blockDim = dim3(kEThreads);
     cfg.dynamicSmemBytes = kESmem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)split;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     void *args[] = {&maps, &a};
     return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(&latent_extend_kernel), args);
 }
