@@ -47,7 +47,7 @@
 // normalised and written there; others leave (m, l, O) partials that a second kernel
 // joins.  Every wait is bounded.
 //
-// Measured (ragged lengths up to n): 32 sequences, n 8,192, 16 heads 32.2 us; 64, n 4,096,
+// Measured (ragged lengths up to n): 32 sequences, n 8,192, 16 heads 30.9 us; 64, n 4,096,
 // 64 heads 56.2 us; 8, n 32,768, 128 heads 88.2 us (602 TFLOP/s); one of 77 tokens 7.7 us.
 // Of the first, 3.8 us pass until the first tile is expanded, 20 us in nine tiles of 4,300
 // clocks, 8 us in storing and joining partials.  A tile is bound by its expansion (1,024
@@ -68,10 +68,14 @@ namespace nvfp4kv {
 namespace {
 
 constexpr int kWorkers = 512;                 // warps 0 .. 15
-constexpr int kLThreads = kWorkers + 128;     // + the MMA warp's warpgroup (its other warps only meet the last barrier)
-// Launched with 96 registers a thread; then 512 x 104 + 128 x 64 = 640 x 96.
+// The MMA warp is alone up to 32 heads (17 warps, 96 registers a thread).  With 64 it is the
+// first of a warpgroup, whose other warps only meet the barriers, so that the working warps
+// can take some of its registers: launched with 96 a thread, then 512 x 104 + 128 x 64 = 640
+// x 96.  (A whole warpgroup with 16 or 32 heads: 32.2 against 30.9 us, 30.0 against 29.3.)
+template <int N>
+constexpr int kLThreads = kWorkers + (N == 64 ? 128 : 32);
 constexpr int kWorkRegs = 104, kMmaRegs = 64;
-static_assert(kWorkers * kWorkRegs + 128 * kMmaRegs <= kLThreads * 96, "register split must fit the launch");
+static_assert(kWorkers * kWorkRegs + 128 * kMmaRegs <= kLThreads<64> * 96, "register split must fit the launch");
 constexpr int kTile = 128;                    // tokens per tile
 constexpr int kColBlock = kTile * 128;        // bytes of one column block (64 dims) of the tile
 constexpr int kTileBytes = 8 * kColBlock;
@@ -101,7 +105,7 @@ struct LSmem {
     static_assert(kColK + 32 * kTmemCbs <= kCols, "TMEM columns");
     static_assert(kKV % 1024 == 0 && kP % 1024 == 0, "operand tiles need 1024-byte alignment");
     static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
-    static_assert(sizeof(FlatScratch<kLThreads>) <= kTileBytes, "the plan's scratch lies in the tile");
+    static_assert(sizeof(FlatScratch<kLThreads<N>>) <= kTileBytes, "the plan's scratch lies in the tile");
 };
 
 struct LatentArgs {
@@ -213,7 +217,7 @@ __device__ __forceinline__ unsigned seq_units(const LatentArgs &a, int b) {
 }
 
 template <int N>
-__global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs a) {
+__global__ void __launch_bounds__(kLThreads<N>, 1) latent_decode_kernel(LatentArgs a) {
     using L = LSmem<N>;
     constexpr int CW = N / 4;                     // heads per warpgroup
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -236,8 +240,8 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
 
     int b0;
     unsigned first, u0 = 0, u1 = 0;
-    flat_locate<kLThreads>(
-        *reinterpret_cast<FlatScratch<kLThreads> *>(smem + L::kKV), a.B, [&](int b) { return seq_units(a, b); },
+    flat_locate<kLThreads<N>>(
+        *reinterpret_cast<FlatScratch<kLThreads<N>> *>(smem + L::kKV), a.B, [&](int b) { return seq_units(a, b); },
         [&](unsigned total) {
             const FlatCut cut(total, a.splits);
             u0 = cut.begin(blockIdx.x);
@@ -245,13 +249,13 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
             return u0 < u1 ? u0 : kFlatNone;
         },
         b0, first);
-    if (warp > 16) {   // (idle otherwise) lengths out of range, and the rows of sequences of length 0
+    if (warp == 16) {   // lengths out of range, and the rows of sequences of length 0
         for (int b = blockIdx.x; b < a.B; b += a.splits) {
             const int32_t n = __ldg(a.seq_lens + b);
-            if (tid == kWorkers + 32 && blockIdx.y == 0 && (n < 0 || (int64_t)n > a.cap)) flag_error(a.err, kErrSeqLen);
+            if (lane == 0 && blockIdx.y == 0 && (n < 0 || (int64_t)n > a.cap)) flag_error(a.err, kErrSeqLen);
             if (n > 0) continue;
             uint4 *dst = reinterpret_cast<uint4 *>(a.out + ((int64_t)b * a.H + h0) * kLatentDim);
-            for (int i = tid - kWorkers - 32; i < min(N, a.H - h0) * (kLatentDim / 8); i += 96) dst[i] = make_uint4(0, 0, 0, 0);
+            for (int i = lane; i < min(N, a.H - h0) * (kLatentDim / 8); i += 32) dst[i] = make_uint4(0, 0, 0, 0);
         }
     }
     tc_fence_before();
@@ -273,7 +277,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
         // sees the descriptors as uniform values: a product issued under a divergent
         // branch cost 70 to 110 clocks, more than the products themselves (38 at N = 16,
         // 47 at N = 64).
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
+        if (N == 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
         if (warp == 16) {
             constexpr uint32_t idesc_s = idesc_f16_f32(128, N, false), idesc_r = idesc_bf16_f32(128, N, false);
             constexpr uint32_t idesc_o = idesc_a_mn_major(idesc_f16_f32(128, N, true));
@@ -347,7 +351,7 @@ __global__ void __launch_bounds__(kLThreads, 1) latent_decode_kernel(LatentArgs 
         // A wait that gave up sets the abort flag, which ends every other wait; the
         // warps then still run through their tiles (on meaningless values), so that
         // no barrier is left short of a warp.
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWorkRegs));
+        if (N == 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWorkRegs));
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             if (!wait_bar(bar, parity, abort_flag) && !*abort_flag) {
                 *abort_flag = 1;
@@ -934,7 +938,7 @@ cudaError_t launch_latent_decode(const nvfp4kv_latent_cache &c, const void *q_la
     a.splits = splits;
     a.err = err;
     void *args[] = {&a};
-    e = launch_pdl(fn, dim3((unsigned)splits, (unsigned)tiles), kLThreads, (size_t)smem, stream, args);
+    e = launch_pdl(fn, dim3((unsigned)splits, (unsigned)tiles), n == 64 ? kLThreads<64> : kLThreads<16>, (size_t)smem, stream, args);
     if (e != cudaSuccess || splits == 1 || a.cap <= kTile) return e;   // no sequence can have been split
     // The partials of a sequence of the batch's average length
     const int partials = (splits + batch - 1) / batch + 1;
