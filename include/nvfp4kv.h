@@ -444,7 +444,8 @@ NVFP4KV_API size_t nvfp4kv_latent_decode_workspace_bytes(const nvfp4kv_latent_ca
  *   block_table   device int32 [batch][max_pages_per_seq]
  *   seq_lens      device int32 [batch] (clamped to the table and flagged; a
  *                 page id outside the pool is flagged and read as zeros)
- *   out           device BF16 [batch][num_heads][512], 16-byte aligned
+ *   out           device BF16 [batch][num_heads][512], 16-byte aligned, not
+ *                 q_latent (several CTAs read a query)
  *   workspace     device, >= nvfp4kv_latent_decode_workspace_bytes(...),
  *                 256-byte aligned; calls that may overlap need one each
  *   num_splits    CTAs a head tile's token range is cut into; 0 = auto.

@@ -591,13 +591,14 @@ def latent_slab_bytes(page_size: int) -> int:
 
 def _rows(t, name: str, T: int, width: int, dev: int):
     """Address and row stride of BF16 [T][width] whose rows may be strided."""
-    if (not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.get_device() != dev
-            or t.shape != (T, width) or (T > 0 and t.stride(1) != 1)):
+    st = t.stride() if isinstance(t, torch.Tensor) else None
+    if (st is None or t.dtype is not torch.bfloat16 or t.get_device() != dev
+            or t.shape != (T, width) or (T > 0 and st[1] != 1)):
         if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.get_device() == dev and t.shape == (T, width):
             raise ValueError("%s: each token must hold %d contiguous values" % (name, width))
         _complain(t, name, torch.bfloat16, (T, width), dev)
     # (a single row's stride says nothing: torch may give it any value)
-    return t.data_ptr(), t.stride(0) if T > 1 else width
+    return t.data_ptr(), st[0] if T > 1 else width
 
 
 def latent_quantize_append(cache: LatentCache, latent: torch.Tensor, k_rope: torch.Tensor, slot_mapping: torch.Tensor,
@@ -706,17 +707,20 @@ _LATENT_SCALE = 1.0 / math.sqrt(HEAD_DIM + ROPE_DIM)
 
 def _heads(k, v, where: str, rows: int, H: int, dev: int):
     """Addresses and (token, head) strides of BF16 K and V [rows][H][128], which share them."""
-    shape = (rows, H, HEAD_DIM)
+    shape, strides = (rows, H, HEAD_DIM), []
     for name, x in (("k_", k), ("v_", v)):
-        if (not isinstance(x, torch.Tensor) or x.dtype is not torch.bfloat16 or x.get_device() != dev
-                or x.shape != shape or (rows > 0 and x.stride(2) != 1)):
-            if isinstance(x, torch.Tensor) and x.dtype is torch.bfloat16 and x.get_device() == dev and x.shape == shape:
+        st = x.stride() if isinstance(x, torch.Tensor) else None
+        if (st is None or x.dtype is not torch.bfloat16 or x.get_device() != dev or x.shape != shape
+                or (rows > 0 and st[2] != 1)):
+            if st is not None and x.dtype is torch.bfloat16 and x.get_device() == dev and x.shape == shape:
                 raise ValueError("%s%s: the 128 values of a head must be contiguous" % (name, where))
             _complain(x, name + where, torch.bfloat16, shape, dev)
+        strides.append(st)
+    sk, sv = strides
     # strides of axes of length 1 say nothing: torch may give them any value
-    st = k.stride(0) if rows > 1 else H * HEAD_DIM
-    sh = k.stride(1) if H > 1 else HEAD_DIM
-    if (rows > 1 and v.stride(0) != st) or (H > 1 and rows > 0 and v.stride(1) != sh):
+    st = sk[0] if rows > 1 else H * HEAD_DIM
+    sh = sk[1] if H > 1 else HEAD_DIM
+    if sk != sv and ((rows > 1 and sv[0] != st) or (H > 1 and rows > 0 and sv[1] != sh)):
         raise ValueError("k_%s and v_%s must share their strides" % (where, where))
     return k.data_ptr(), v.data_ptr(), st, sh
 

@@ -424,7 +424,8 @@ int nvfp4_latent_decode_attention(const nvfp4kv_latent_cache *cache, const void 
     if (num_heads > 128 || batch > 65535 || num_splits > 65535) return NVFP4KV_EUNSUPPORTED;
     if (!isfinite(sm_scale)) return NVFP4KV_EINVAL;
     if (batch == 0) return NVFP4KV_OK;
-    if (!q_latent || !q_rope || !block_table || !seq_lens || !out || !workspace || max_pages_per_seq < 1)
+    if (!q_latent || !q_rope || !block_table || !seq_lens || !out || !workspace || max_pages_per_seq < 1 ||
+        out == q_latent)
         return NVFP4KV_EINVAL;
     if (!aligned(q_latent, 16) || !aligned(q_rope, 16) || !aligned(out, 16) || !aligned(workspace, 256) ||
         !aligned(block_table, 4) || !aligned(seq_lens, 4))

@@ -80,8 +80,9 @@ def test_decode_refusals(m):
     need = lib.nvfp4kv_latent_decode_workspace_bytes(p, 2, 16, 3)
     # (splits + batch) (m, l) pairs of 16 heads, and their 512 sums, each part a multiple of 256
     assert need == (5 * 16 * 8 + 255) // 256 * 256 + 5 * 16 * 512 * 4
-    _refused(lib.nvfp4_latent_decode_attention, [p, A, A, 2, 16, A, 1, A, 0.1, A, A, need, 3, None],
-             [(1, None, -1), (1, odd, -1), (2, odd, -1), (3, -1, -1), (3, 70000, -2), (4, 0, -1), (4, 129, -2),
+    B = ctypes.c_void_p(8192)
+    _refused(lib.nvfp4_latent_decode_attention, [p, A, A, 2, 16, A, 1, A, 0.1, B, A, need, 3, None],
+             [(9, A, -1), (1, None, -1), (1, odd, -1), (2, odd, -1), (3, -1, -1), (3, 70000, -2), (4, 0, -1), (4, 129, -2),
               (5, None, -1), (6, 0, -1), (6, 1 << 27, -2), (7, None, -1), (8, float("inf"), -1),
               (8, float("nan"), -1), (9, odd, -1), (10, ctypes.c_void_p(4096 + 128), -1), (11, need - 1, -1), (12, -1, -1),
               (12, 70000, -2), (3, 0, 0)])
