@@ -315,6 +315,29 @@ def test_evict_flags_missing_pages(m):
     assert m.check_device_errors() == -4
 
 
+def test_pages_beyond_four_gigabytes(m):
+    """Scores and eviction in the last pages of a pool of more than 2^32 bytes."""
+    Hkv, P, lens, keep = 8, 128, [300, 200], 130
+    w = workloads.make_decode("far", 14, lens, 16, Hkv, P, extra_pages=4)
+    small, _ = fill_both(w, m)
+    bt = w.block_table.clone()
+    used = set(bt.flatten().tolist())
+    nt = torch.tensor([p for p in range(w.num_pages) if p not in used][:4], dtype=torch.int32).view(2, 2)
+    pages = (1 << 32) // (144 * P * Hkv) + 16
+    big = m.PagedCache(pages, P, Hkv, pool=torch.empty((pages, Hkv, 144 * P), dtype=torch.uint8, device="cuda"))
+    big.pool[pages - w.num_pages:] = small.pool.flip(0)
+    q, sl, got = w.q("cuda"), w.seq_lens.cuda(), []
+    for cache, far in ((small, False), (big, True)):
+        t, n = [torch.where(x >= 0, pages - 1 - x, x) if far else x for x in (bt, nt)]
+        sc = torch.zeros((2, Hkv, 300), device="cuda")
+        m.accumulate_attention_weights(cache, q, t.cuda(), sl, sc)
+        out = m.evict(cache, sc, t.cuda(), sl, n.cuda(), keep, recent=10, sink=2)
+        got.append((sc, *out, cache.pool[n.flatten().long().cuda()]))
+    torch.cuda.synchronize()
+    assert m.check_device_errors() == 0
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
 # ------------------------------------------------------------------ together
 
 def test_decode_score_evict_decode(m):

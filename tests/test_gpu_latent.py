@@ -324,6 +324,31 @@ def test_decode_on_other_streams_and_in_graphs(m):
     m.check_device_errors()
 
 
+def test_pages_beyond_four_gigabytes(m):
+    """The same rows in the last pages of a pool of more than 2^32 bytes: append, dequant and
+    decode give what they give in a small one."""
+    P, lens = 128, [300, 77]
+    small, bt = _filled(m, lens, P, 71)
+    pages = (1 << 32) // (416 * P) + 8
+    big = m.LatentCache(pages, P, pool=torch.empty((pages, 416 * P), dtype=torch.uint8, device="cuda"))
+    far = np.where(bt >= 0, pages - 1 - bt, -1).astype(np.int32)
+    for old, new in zip(bt[bt >= 0], far[far >= 0]):
+        big.pool[int(new)].fill_(0)
+        big.pool[int(new)] = small.pool[int(old)]
+    x = _rand((1, 576), 72)                   # one more token of sequence 1, into both
+    for cache, table in ((small, bt), (big, far)):
+        m.latent_quantize_append(cache, x[:, :512], x[:, 512:], _cuda([int(table[1, 0]) * P + 77], torch.int64))
+    lens[1] += 1
+    q, qr = _rand((2, 16, 512), 73, 0.5), _rand((2, 16, 64), 74)
+    got = []
+    for cache, table in ((small, bt), (big, far)):
+        o = m.latent_decode_attention(cache, q, qr, _cuda(table), _cuda(lens))
+        got.append((o, *m.latent_prefix_dequant(cache, _cuda(table), _cuda(lens), _cuda([0, 300, 378]), 378)))
+    torch.cuda.synchronize()
+    assert m.check_device_errors() == 0
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
 # ------------------------------------------------------------------ expanded extend
 
 def _extend(m, pre, new, H, seed, strided=True, max_q=None):
@@ -440,6 +465,30 @@ def test_extend_in_a_graph_and_on_another_stream(m):
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(other, out) and torch.equal(res, out)
+
+
+# ------------------------------------------------------------------ side by side
+
+def test_calls_on_several_streams_at_once(m):
+    """Decode calls of different head counts and extends on four streams, each with buffers of its
+    own, give what they give alone."""
+    lens = [900, 33, 400]
+    cache, bt = _filled(m, lens, 64, 81)
+    b, n = _cuda(bt), _cuda(lens)
+    qs = {H: (_rand((3, H, 512), H, 0.5), _rand((3, H, 64), H + 1)) for H in (16, 64, 128)}
+    want = {H: m.latent_decode_attention(cache, *q, b, n) for H, q in qs.items()}
+    ext, (q, kv, r0, r1, cp, cq) = _extend(m, [600, 40], [50, 129], 4, 9)
+    args = (q, kv[0], kv[1], r0, _cuda(cp), kv[2], kv[3], r1, _cuda(cq), 129)
+    torch.cuda.synchronize()
+    streams = {x: torch.cuda.Stream() for x in (16, 64, 128, "extend")}
+    got = []
+    for _ in range(6):
+        for H in qs:
+            got.append((want[H], m.latent_decode_attention(cache, *qs[H], b, n, stream=streams[H])))
+        got.append((ext, m.latent_extend_attention(*args, stream=streams["extend"])))
+    torch.cuda.synchronize()
+    assert m.check_device_errors() == 0
+    assert all(torch.equal(x, y) for x, y in got)
 
 
 # ------------------------------------------------------------------ together
