@@ -11,7 +11,8 @@
 //            adds the 256 counts up through distributed shared memory and every CTA picks
 //            the same digit; then each warp counts and compacts a contiguous part of the
 //            rows, its offset coming from one scan over the CTA's warps and one over the
-//            cluster.  Keys stay in shared memory between the rounds as far as they fit.
+//            cluster.  Keys stay in shared memory between the rounds as far as they fit;
+//            where they do not, a sample's borders take the place of the rounds here too.
 //            (16 x 8 segments of up to 32,768 rows: 23 us with one CTA each, 66 us with
 //            clusters of four.)
 //   move     one warp per 16-row group of the new pages gathers its rows and writes the
@@ -170,11 +171,11 @@ __device__ __forceinline__ uint32_t find_border(const uint32_t (&k)[K], uint32_t
 // to 32 K each, share a word (one bit a step took 4.0 us of the 32,768-row segments' 25).
 template <int T, int K>
 __device__ __forceinline__ uint32_t find_border_pairs(const uint32_t (&k)[K], int used, uint32_t want, uint32_t border,
-                                                      int top, uint32_t (&s_count)[2][32], bool &exact) {
+                                                      int top, uint32_t (&s_count)[2][32], bool &exact, int last = 0) {
     static_assert(32 * K < 1024, "a warp's count must fit ten bits");
     exact = false;
     int buf = 0;
-    for (int bit = top & ~1; bit >= 0; bit -= 2, buf ^= 1) {
+    for (int bit = top & ~1; bit >= last; bit -= 2, buf ^= 1) {
         uint32_t c = 0;
 #pragma unroll
         for (int i = 0; i < K; i++) {
@@ -335,6 +336,57 @@ __global__ void __launch_bounds__(T) select_one_kernel(SelectArgs a) {
     gather_scores<T>(0, (uint32_t)a.keep, src, kept, dst);
 }
 
+// find_border_pairs over the keys of a cluster's CTAs: the CTAs' counts are added up in
+// distributed shared memory, one cluster barrier a step.
+template <int K>
+__device__ __forceinline__ uint32_t find_border_cluster(cg::cluster_group &cluster, const uint32_t (&k)[K], uint32_t want,
+                                                        uint32_t border, int top, uint32_t (&s_count)[2][32],
+                                                        uint32_t (&s_step)[2][4], bool &exact) {
+    static_assert(32 * K < 1024, "a warp's count must fit ten bits");
+    const int lane = threadIdx.x & 31, C = (int)cluster.num_blocks();
+    exact = false;
+    int buf = 0;
+    for (int bit = top & ~1; bit >= 0; bit -= 2, buf ^= 1) {
+        uint32_t c = 0;
+#pragma unroll
+        for (int i = 0; i < K; i++)
+#pragma unroll
+            for (uint32_t x = 1; x < 4; x++) c += k[i] >= (border | (x << bit)) ? 1u << (10 * (x - 1)) : 0u;
+        c = __reduce_add_sync(0xffffffffu, c);
+        if (lane == 0) s_count[buf][threadIdx.x >> 5] = c;
+        __syncthreads();
+        if (threadIdx.x < 32) {
+            c = lane < kSelWarps ? s_count[buf][lane] : 0u;
+            const uint32_t c1 = __reduce_add_sync(0xffffffffu, c & 1023u), c2 = __reduce_add_sync(0xffffffffu, (c >> 10) & 1023u),
+                           c3 = __reduce_add_sync(0xffffffffu, c >> 20);
+            if (lane == 0) {
+                s_step[buf][1] = c1;
+                s_step[buf][2] = c2;
+                s_step[buf][3] = c3;
+            }
+        }
+        cluster.sync();                             // (a buffer is written again only after the next step's)
+        uint32_t n[4] = {0, 0, 0, 0};
+        const uint32_t *o = cluster.map_shared_rank(&s_step[0][0], lane < C ? lane : 0) + 4 * buf;
+#pragma unroll
+        for (int x = 1; x < 4; x++) n[x] = __reduce_add_sync(0xffffffffu, lane < C ? o[x] : 0u);
+        const uint32_t x = n[3] >= want ? 3u : n[2] >= want ? 2u : n[1] >= want ? 1u : 0u;
+        border |= x << bit;
+        if ((x == 3 ? n[3] : x == 2 ? n[2] : x == 1 ? n[1] : 0u) == want) {   // (want >= 1)
+            exact = true;
+            break;
+        }
+    }
+    return border;
+}
+
+constexpr int kSampleLong = 2 * kSelThreads;        // keys that place the borders of a cluster's rows
+constexpr int kSampleLast = 12;                     // bits of those borders that are left open
+constexpr int kListLong = kSelThreads * kListPer;   // keys between them that a CTA holds
+
+// kSampled: for launches in which a CTA may have more than kKeyCache rows.  (The other instance
+// needs less of an SM: 16 x 8 segments of 40,000 rows took 130 us with one for both, 108 so.)
+template <bool kSampled>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(SelectArgs a) {
     extern __shared__ uint32_t s_keys[];            // [kKeyCache]
     __shared__ uint32_t s_hist[256];                // this CTA's counts of a round; read by the cluster
@@ -366,7 +418,86 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(SelectArgs a) {
 
     uint32_t prefix = 0;                            // digits of the border key found so far
     uint32_t need = (uint32_t)a.keep;               // rows still to take among the keys with that prefix
-    for (int round = 0; round < 4; round++) {
+    // As in one CTA, a sample gives two keys between which the border almost always lies: one pass
+    // counts the keys above and lists those between, which are searched alone.  Where a CTA's keys
+    // all stay in shared memory, the rounds below are quicker (2 x 262,144 rows: 133 us by rounds, 83 so;
+    // 32 x 65,536: 46 and 61).
+    bool found = false;
+    if (kSampled && per > kKeyCache) {              // (uniform over the cluster)
+        __shared__ uint32_t s_list[kSampled ? kListLong : 1];     // keys between the sampled borders
+        __shared__ uint32_t s_count[2][32], s_step[2][4];
+        __shared__ uint32_t s_between, s_sums[2];   // this CTA's: keys between, (keys above, between); the last read by the cluster
+        uint32_t x[2];
+#pragma unroll
+        for (int i = 0; i < 2; i++) x[i] = make_key((int)((int64_t)n * (tid + i * kSelThreads) / kSampleLong));
+        const int r = (int)((int64_t)a.keep * kSampleLong / n), d = 4 + (int)(3.0f * sqrtf((float)r));
+        uint32_t hi = 0xffffffffu;
+        bool exact;
+        if (r > d)
+            hi = find_border_pairs<kSelThreads>(x, 2, (uint32_t)(r - d), 0u, 31, s_count, exact, kSampleLast) |
+                 ((1u << kSampleLast) - 1u);
+        __syncthreads();
+        const uint32_t lo = find_border_pairs<kSelThreads>(x, 2, (uint32_t)min(r + d, kSampleLong), 0u, 31, s_count, exact, kSampleLast);
+        if (tid == 0) s_between = 0;
+        __syncthreads();
+        uint32_t above = 0;
+        for (int tw = w0; tw < w1; tw += 128) {
+            uint32_t k[4];
+#pragma unroll
+            for (int e = 0; e < 4; e++) k[e] = tw + 32 * e + lane < w1 ? make_key(tw + 32 * e + lane) : 0u;   // (0: below lo)
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const int t = tw + 32 * e + lane;
+                if (t < w1 && t - r0 < kKeyCache) s_keys[t - r0] = k[e];   // read back by this thread only
+                above += k[e] >= hi;
+                const bool in = k[e] - lo < hi - lo;
+                const unsigned ins = __ballot_sync(0xffffffffu, in && lo > 0);
+                if (ins) {
+                    uint32_t at = 0;
+                    if (lane == 0) at = atomicAdd(&s_between, (uint32_t)__popc(ins));   // (their order says nothing)
+                    at = __shfl_sync(0xffffffffu, at, 0) + (uint32_t)__popc(ins & ((1u << lane) - 1u));
+                    if (in && at < (uint32_t)kListLong) s_list[at] = k[e];
+                }
+            }
+        }
+        above = cta_sum<kSelThreads>(above, s_count, 0);   // (its barrier: s_between and s_list are complete)
+        const uint32_t own = s_between;
+        if (tid == 0) {
+            s_sums[0] = above;
+            s_sums[1] = own <= (uint32_t)kListLong ? own : 0x1000000u;      // too many: no CTA goes on
+        }
+        cluster.sync();
+        const uint32_t *o = cluster.map_shared_rank(s_sums, lane < C ? lane : 0);
+        above = __reduce_add_sync(0xffffffffu, lane < C ? o[0] : 0u);
+        const uint32_t between = __reduce_add_sync(0xffffffffu, lane < C ? o[1] : 0u);
+        if (lo > 0 && between < 0x1000000u && above < need && need <= above + between) {
+            uint32_t k[kListPer];
+#pragma unroll
+            for (int i = 0; i < kListPer; i++) k[i] = tid + i * kSelThreads < (int)own ? s_list[tid + i * kSelThreads] : 0u;
+            const uint32_t diff = lo ^ (hi - 1u);
+            const int top = diff ? 31 - __clz((int)diff) : -1;
+            uint32_t border = top >= 0 ? lo & ~((4u << (top & ~1)) - 1u) : lo;   // (4 << 30: 0, all bits are open)
+            border = find_border_cluster(cluster, k, need - above, border, top, s_count, s_step, exact);
+            if (exact) {                            // just `keep` keys are not below the border
+                prefix = border - 1u;               // (border > 0: not every key is kept)
+                need = 0;
+            } else {                                // the border is a key, of which the first ones are taken
+                uint32_t c = 0;
+#pragma unroll
+                for (int i = 0; i < kListPer; i++) c += k[i] > border;
+                cluster.sync();                     // (s_sums is read)
+                c = cta_sum<kSelThreads>(c, s_count, 0);
+                if (tid == 0) s_sums[0] = c;
+                cluster.sync();
+                c = __reduce_add_sync(0xffffffffu, lane < C ? o[0] : 0u);
+                prefix = border;
+                need -= above + c;
+            }
+            found = true;
+        }
+        cluster.sync();                             // (s_sums and s_step are read)
+    }
+    for (int round = 0; round < 4 && !found; round++) {
         const int shift = 24 - 8 * round;
         if (tid < 256) s_hist[tid] = 0;
         __syncthreads();
@@ -423,12 +554,18 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(SelectArgs a) {
     }
     // keys above `prefix` all stay, `need` of those equal to it (in index order)
     uint32_t gt = 0, eq = 0;
-    for (int t = w0; t < w1; t += 32) {
-        const bool in = t + lane < w1;
-        const uint32_t k = in ? key_of(t + lane) : 0u;
-        gt += (uint32_t)__popc(__ballot_sync(0xffffffffu, in && k > prefix));
-        eq += (uint32_t)__popc(__ballot_sync(0xffffffffu, in && k == prefix));
+    for (int tw = w0; tw < w1; tw += 128) {
+        uint32_t k[4];
+#pragma unroll
+        for (int e = 0; e < 4; e++) k[e] = tw + 32 * e + lane < w1 ? key_of(tw + 32 * e + lane) : 0u;   // (0: no row's)
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            gt += k[e] > prefix;
+            eq += k[e] == prefix && k[e];
+        }
     }
+    gt = __reduce_add_sync(0xffffffffu, gt);
+    eq = __reduce_add_sync(0xffffffffu, eq);
     if (lane == 0) {
         s_warp[warp][0] = gt;
         s_warp[warp][1] = eq;
@@ -465,16 +602,22 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(SelectArgs a) {
     c0 += min(c_eq, need);
     at += min(eq_before, need);
     cluster.sync();                                 // no CTA leaves while its counts may be read
-    for (int t = w0; t < w1; t += 32) {
-        const bool in = t + lane < w1;
-        const uint32_t k = in ? key_of(t + lane) : 0u;
-        const unsigned below = (1u << lane) - 1u;
-        const unsigned eqs = __ballot_sync(0xffffffffu, in && k == prefix);
-        const bool take = in && (k > prefix || (k == prefix && eq_before + (uint32_t)__popc(eqs & below) < need));
-        const unsigned takes = __ballot_sync(0xffffffffu, take);
-        if (take) kept[at + (uint32_t)__popc(takes & below)] = t + lane;
-        at += (uint32_t)__popc(takes);
-        eq_before += (uint32_t)__popc(eqs);
+    const unsigned below = (1u << lane) - 1u;
+    for (int tw = w0; tw < w1; tw += 128) {
+        uint32_t k[4];
+#pragma unroll
+        for (int e = 0; e < 4; e++) k[e] = tw + 32 * e + lane < w1 ? key_of(tw + 32 * e + lane) : 0u;
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            const int t = tw + 32 * e + lane;
+            const bool in = t < w1;
+            const unsigned eqs = __ballot_sync(0xffffffffu, in && k[e] == prefix);
+            const bool take = in && (k[e] > prefix || (k[e] == prefix && eq_before + (uint32_t)__popc(eqs & below) < need));
+            const unsigned takes = __ballot_sync(0xffffffffu, take);
+            if (take) kept[at + (uint32_t)__popc(takes & below)] = t;
+            at += (uint32_t)__popc(takes);
+            eq_before += (uint32_t)__popc(eqs);
+        }
     }
     gather_scores<kSelThreads>(c0, c1, src, kept, dst);
 }
@@ -595,8 +738,11 @@ cudaError_t launch_evict(const nvfp4kv_cache &c, const float *scores, int64_t sc
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     std::unique_lock<std::mutex> lock(mu);
     if (!attr_set[dev]) {
-        e = cudaFuncSetAttribute(reinterpret_cast<const void *>(&select_kernel),
+        e = cudaFuncSetAttribute(reinterpret_cast<const void *>(&select_kernel<false>),
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, kKeyCache * 4);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(reinterpret_cast<const void *>(&select_kernel<true>),
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, kKeyCache * 4);
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(reinterpret_cast<const void *>(&select_one_kernel<kOneLarge>),
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, kOneRows * 4);
@@ -641,7 +787,8 @@ cudaError_t launch_evict(const nvfp4kv_cache &c, const float *scores, int64_t sc
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     void *args[] = {&a};
-    const void *fn = reinterpret_cast<const void *>(&select_kernel);
+    const void *fn = part > kKeyCache ? reinterpret_cast<const void *>(&select_kernel<true>)
+                                      : reinterpret_cast<const void *>(&select_kernel<false>);
     if (one) {
         const bool small = a.cap <= kOneSmallRows;
         fn = small ? reinterpret_cast<const void *>(&select_one_kernel<kOneSmall>)

@@ -226,7 +226,7 @@ def test_evict_keeps_the_largest(m, lens, Hkv, P, keep, recent, sink, dtype):
     _evict(m, lens, Hkv, P, keep, recent, sink, _scores((len(lens), Hkv, max(lens) + 5), sum(lens)), dtype)
 
 
-@pytest.mark.parametrize("n,keep", [(50, 20), (3000, 500), (20000, 3000), (40000, 5000)])   # each way of selecting
+@pytest.mark.parametrize("n,keep", [(50, 20), (3000, 500), (20000, 3000), (40000, 5000), (200000, 4000)])   # each way
 @pytest.mark.parametrize("kind", ["equal", "zeros", "two", "special", "rising", "falling", "narrow"])
 def test_evict_ties_and_special_values(m, n, keep, kind):
     t = torch.arange(n, dtype=torch.float32)
@@ -252,6 +252,13 @@ def test_evict_ties_and_special_values(m, n, keep, kind):
     else:                                      # keys that differ in the last bits alone
         x = (1.0 + torch.randint(0, 40, (n,), generator=g) * 2.0**-23).float()
     _evict(m, [n], 1, 128, keep, min(5, keep // 4), min(2, keep // 4), x.view(1, 1, n).cuda())
+
+
+@pytest.mark.parametrize("B,Hkv,n,keep", [(2, 2, 70000, 3000), (20, 8, 33000, 700), (40, 8, 33000, 90), (1, 1, 300000, 20)])
+def test_evict_long_segments(m, B, Hkv, n, keep):
+    """Clusters of eight, two and one CTA a segment, beside short segments; more keys than a CTA keeps."""
+    lens = [n] + [100] * (B - 1)
+    _evict(m, lens, Hkv, 128, keep, min(16, keep // 4), 3, _scores((B, Hkv, n + 1), B))
 
 
 def test_evict_unaligned_rows_and_own_buffers(m):
