@@ -48,7 +48,7 @@
 // joins.  Every wait is bounded.
 //
 // Measured (ragged lengths up to n): 32 sequences, n 8,192, 16 heads 30.9 us; 64, n 4,096,
-// 64 heads 56.2 us; 8, n 32,768, 128 heads 88.2 us (602 TFLOP/s); one of 77 tokens 7.7 us.
+// 64 heads 55.6 us; 8, n 32,768, 128 heads 86.1 us (617 TFLOP/s); one of 77 tokens 7.7 us.
 // Of the first, 3.8 us pass until the first tile is expanded, 20 us in nine tiles of 4,300
 // clocks, 8 us in storing and joining partials.  A tile is bound by its expansion (1,024
 // conversions and as many packed multiplies a warp's width, 2,700 clocks with the stores)
@@ -511,6 +511,15 @@ __global__ void __launch_bounds__(kLThreads<N>, 1) latent_decode_kernel(LatentAr
         }
         next_tile(a, nx);
         int32_t npage = page_of(nx);            // its page, requested a tile earlier still
+        // With 64 heads a tile the bytes of the tile after that are brought to L2 (64 sequences of up to
+        // 4,096 tokens: 58.1 us without, 56.1 so; with 16 heads it costs what it gains).
+        constexpr bool kAhead = N == 64;
+        TileIter pf = nx;
+        int32_t ppage = -1;
+        if (kAhead) {
+            if (pf.left > 0) next_tile(a, pf);
+            ppage = page_of(pf);
+        }
         bool fresh = true;                      // the range's first tile of its sequence
         int t_begin = it.t;
         float l[CW];
@@ -565,8 +574,21 @@ __global__ void __launch_bounds__(kLThreads<N>, 1) latent_decode_kernel(LatentAr
                 int rows;
                 const uint8_t *p = group_of(nx, npage, rows);
                 load_tile(p, rows);
-                next_tile(a, nx);
-                npage = page_of(nx);
+                if (kAhead) {
+                    if (par == 0 && ppage >= 0 && ppage < a.num_pages && lane < kLatentGroup / 256) {
+                        const uint8_t *group = a.pool + (int64_t)ppage * ((int64_t)kLatentRow * a.P) +
+                                               (int64_t)(((pf.t * kTile + 16 * grp) & (a.P - 1)) >> 4) * kLatentGroup;
+                        prefetch_l2(group + lane * 256);
+                        prefetch_l2(group + lane * 256 + 128);
+                    }
+                    nx = pf;
+                    npage = ppage;
+                    if (pf.left > 0) next_tile(a, pf);
+                    ppage = page_of(pf);
+                } else {
+                    next_tile(a, nx);
+                    npage = page_of(nx);
+                }
             }
             // ---- softmax of the token's scores for the warpgroup's heads.  S^T done says that the
             // previous tile's O^T, issued before it, is done too: P and O^T may be written.
