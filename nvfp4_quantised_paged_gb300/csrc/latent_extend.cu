@@ -195,33 +195,31 @@ __global__ void __launch_bounds__(kEThreads, 1)
             const uint64_t dQ = smem_desc_sw128(sbase + kOffQ, 16, 1024);
             const uint64_t dB = smem_desc_sw128(sbase + kOffRing, 16, 1024);   // slot 0, K-major and MN-major alike
             auto mma_s = [&](int w, uint32_t blk) {  // S_w = Q_w K^T over 192 dimensions, 16 at a time
+                if (!leader) return;
 #pragma unroll
                 for (int i = 0; i < 3; i++) {
-                    const uint32_t slot = uniform(slot_of(blk + i));
+                    const uint32_t slot = slot_of(blk + i);
                     const uint64_t q = dQ + (w * (kQBytes / 16) + i * (kBlockBytes / 16)), k = dB + slot * (kBlockBytes / 16);
-                    if (leader) {
 #pragma unroll
-                        for (int kk = 0; kk < 4; kk++)
-                            tc_mma_bf16(tm + 128u * w, q + kk * 2, k + kk * 2, idesc_s, i + kk > 0);
-                        tc_commit(&empty[slot]);
-                        if (i == 2) tc_commit(&s_done[w]);
-                    }
+                    for (int kk = 0; kk < 4; kk++)
+                        tc_mma_bf16(tm + 128u * w, q + kk * 2, k + kk * 2, idesc_s, i + kk > 0);
+                    tc_commit(&empty[slot]);
                 }
+                tc_commit(&s_done[w]);
             };
             auto mma_pv = [&](int w, uint32_t blk, uint32_t acc) {  // O_w += P_w V over 128 keys, 64 dimensions at a time
+                if (!leader) return;
 #pragma unroll
                 for (int i = 0; i < 2; i++) {
-                    const uint32_t slot = uniform(slot_of(blk + 3 + i));
+                    const uint32_t slot = slot_of(blk + 3 + i);
                     const uint64_t v = dB + slot * (kBlockBytes / 16);
-                    if (leader) {
 #pragma unroll
-                        for (int kk = 0; kk < 8; kk++)  // P from TMEM: 8 columns = 16 keys
-                            tc_mma_bf16_tmem_a(tm + kColO + 128u * w + 64u * i, tm + 128u * w + kk * 8, v + kk * 128, idesc_o,
-                                               kk > 0 ? 1u : acc);
-                        tc_commit(&empty[slot]);
-                        if (i == 1) tc_commit(&pv_done[w]);
-                    }
+                    for (int kk = 0; kk < 8; kk++)  // P from TMEM: 8 columns = 16 keys
+                        tc_mma_bf16_tmem_a(tm + kColO + 128u * w + 64u * i, tm + 128u * w + kk * 8, v + kk * 128, idesc_o,
+                                           kk > 0 ? 1u : acc);
+                    tc_commit(&empty[slot]);
                 }
+                tc_commit(&pv_done[w]);
             };
             auto wait = [&](uint64_t *bar, uint32_t parity) {
                 const bool good = __all_sync(0xffffffffu, poll_wait(bar, parity, abort_flag));
