@@ -47,10 +47,10 @@
 // normalised and written there; others leave (m, l, O) partials that a second kernel
 // joins.  Every wait is bounded.
 //
-// Measured (ragged lengths up to n): 32 sequences, n 8,192, 16 heads 30.9 us; 64, n 4,096,
-// 64 heads 55.6 us; 8, n 32,768, 128 heads 86.1 us (617 TFLOP/s); one of 77 tokens 7.7 us.
-// Of the first, 3.8 us pass until the first tile is expanded, 20 us in nine tiles of 4,300
-// clocks, 8 us in storing and joining partials.  A tile is bound by its expansion (1,024
+// Measured (ragged lengths up to n): 32 sequences, n 8,192, 16 heads 29.6 us; 64, n 4,096,
+// 64 heads 53.5 us; 8, n 32,768, 128 heads 81.1 us (655 TFLOP/s); one of 77 tokens 7.7 us.
+// Of the first, 3.8 us pass until the first tile is expanded, 19 us in nine tiles of 4,100
+// clocks, 7 us in storing and joining partials.  A tile is bound by its expansion (1,024
 // conversions and as many packed multiplies a warp's width, 2,700 clocks with the stores)
 // and by shared memory's bandwidth: 128 KB written and 150 KB (N 16) to 300 KB (N 64) of
 // operands read at 128 bytes a clock.

@@ -611,7 +611,7 @@ cudaError_t launch_latent_extend(const void *q, const void *k_prefix, const void
     // Clusters share the K/V tiles of a CTA while the grid stays one wave of them: 32 heads x 2
     // query tiles of one request over 8,192 tokens take 148 us as 64 CTAs and 88 us as 64
     // clusters of two (157 us as 64 of four, which are two waves); 256 CTAs that are two waves
-    // already take 219 us either way.  A tile a CTA is enough (8 heads, 64 queries over 1,100 tokens:
+    // already take the same either way.  A tile a CTA is enough (8 heads, 64 queries over 1,100 tokens:
     // 15.8 us in clusters of eight, 18.5 of four, 22.0 of two; over 300 tokens 16.7 of two, 15.5 alone).
     int split = 1;
     for (int k = 0; k < 3; k++)
