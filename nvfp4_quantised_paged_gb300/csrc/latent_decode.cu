@@ -294,9 +294,9 @@ __global__ void __launch_bounds__(kLThreads<N>, 1) latent_decode_kernel(LatentAr
             };
             bool fresh = true, ok = true;   // fresh: the tile is the range's first of its sequence
             for (uint32_t j = 0; it.left > 0; j++) {
-                // Half of the tile a step (unrolled by 1, 2 and 4: 32 sequences, n 8,192, 16 heads 30.9, 29.6 and
-                // 30.4 us; 8, n 32,768, 128 heads 85.9, 81.1 and 80.6).
-#pragma unroll 2
+                // (unrolled by 1, 2 and 4: 32 sequences, n 8,192, 16 heads 30.9, 29.6 and 30.4 us; 8, n 32,768,
+                // 128 heads 85.9, 81.1 and 80.6)
+#pragma unroll(N == 64 ? 4 : 2)
                 for (uint32_t i = 0; i < 4; i++) {   // column blocks 2 i, 2 i + 1 (and the rotary part, with the first)
                     if (!(i & 1)) ok = ok && wait(&kv_full[i >> 1], j & 1);
                     if (!ok) break;
