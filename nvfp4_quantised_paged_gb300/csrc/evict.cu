@@ -23,6 +23,7 @@
 
 #include <mutex>
 
+#include "border_search.cuh"
 #include "common.cuh"
 #include "flat_plan.cuh"
 #include "kernels.h"
@@ -167,36 +168,26 @@ __device__ __forceinline__ uint32_t find_border(const uint32_t (&k)[K], uint32_t
     return border;
 }
 
-// The same for few keys a thread (`used` of them, the others are 0), two bits a step: the warp's counts of the three trials, up
-// to 32 K each, share a word (one bit a step took 4.0 us of the 32,768-row segments' 25).
+// Counts of a step of search_pairs over the CTA, for few keys a thread (`used` of them, the others are 0): the warp's counts
+// of the three trials, up to 32 K each, share a word (one bit a step took 4.0 us of the 32,768-row segments' 25).
 template <int T, int K>
-__device__ __forceinline__ uint32_t find_border_pairs(const uint32_t (&k)[K], int used, uint32_t want, uint32_t border,
-                                                      int top, uint32_t (&s_count)[2][32], bool &exact, int last = 0) {
+__device__ __forceinline__ void count_pairs(const uint32_t (&k)[K], int used, uint32_t border, int bit, int buf,
+                                            uint32_t (&s_count)[2][32], uint32_t (&n)[4]) {
     static_assert(32 * K < 1024, "a warp's count must fit ten bits");
-    exact = false;
-    int buf = 0;
-    for (int bit = top & ~1; bit >= last; bit -= 2, buf ^= 1) {
-        uint32_t c = 0;
+    uint32_t c = 0;
 #pragma unroll
-        for (int i = 0; i < K; i++) {
-            if (i >= used) break;
+    for (int i = 0; i < K; i++) {
+        if (i >= used) break;
 #pragma unroll
-            for (uint32_t x = 1; x < 4; x++) c += k[i] >= (border | (x << bit)) ? 1u << (10 * (x - 1)) : 0u;
-        }
-        c = __reduce_add_sync(0xffffffffu, c);
-        if ((threadIdx.x & 31) == 0) s_count[buf][threadIdx.x >> 5] = c;
-        __syncthreads();
-        c = (threadIdx.x & 31) < T / 32 ? s_count[buf][threadIdx.x & 31] : 0u;
-        const uint32_t c1 = __reduce_add_sync(0xffffffffu, c & 1023u), c2 = __reduce_add_sync(0xffffffffu, (c >> 10) & 1023u),
-                       c3 = __reduce_add_sync(0xffffffffu, c >> 20);
-        const uint32_t x = c3 >= want ? 3u : c2 >= want ? 2u : c1 >= want ? 1u : 0u;
-        border |= x << bit;
-        if ((x == 3 ? c3 : x == 2 ? c2 : x == 1 ? c1 : 0u) == want) {   // (want >= 1)
-            exact = true;
-            break;
-        }
+        for (uint32_t x = 1; x < 4; x++) c += k[i] >= (border | (x << bit)) ? 1u << (10 * (x - 1)) : 0u;
     }
-    return border;
+    c = __reduce_add_sync(0xffffffffu, c);
+    if ((threadIdx.x & 31) == 0) s_count[buf][threadIdx.x >> 5] = c;
+    __syncthreads();
+    c = (threadIdx.x & 31) < T / 32 ? s_count[buf][threadIdx.x & 31] : 0u;
+    n[1] = __reduce_add_sync(0xffffffffu, c & 1023u);
+    n[2] = __reduce_add_sync(0xffffffffu, (c >> 10) & 1023u);
+    n[3] = __reduce_add_sync(0xffffffffu, c >> 20);
 }
 
 template <int T, int PER>
@@ -249,10 +240,10 @@ __device__ __forceinline__ void select_rows(const SelectArgs &a, int n, int per,
 #pragma unroll
             for (int i = 0; i < kListPer; i++)
                 x[i] = threadIdx.x + i * T < total ? s_keys[threadIdx.x + i * T] : 0u;
-            const uint32_t diff = lo ^ (hi - 1u);
-            const int top = diff ? 31 - __clz((int)diff) : -1;
-            border = top >= 0 ? lo & ~((4u << (top & ~1)) - 1u) : lo;   // (4 << 30: 0, all bits are open)
-            border = find_border_pairs<T>(x, ((int)total + T - 1) / T, keep - c_hi, border, top, s_count, exact);
+            const int used = ((int)total + T - 1) / T;
+            border = search_listed(lo, hi, keep - c_hi, exact, [&](uint32_t at_least, int bit, int step, uint32_t (&c)[4]) {
+                count_pairs<T>(x, used, at_least, bit, step & 1, s_count, c);
+            });
             found = true;
         }
     }
@@ -282,7 +273,7 @@ __device__ __forceinline__ void select_rows(const SelectArgs &a, int n, int per,
         even &= even - 1;
         ties--;
     }
-    while (take) {                            // (one step a kept row of the fullest thread, not one a row)
+    while (take && at < keep) {               // (one step a kept row of the fullest thread, not one a row)
         kept[at++] = t0 + __ffsll((long long)take) - 1;
         take &= take - 1;
     }
@@ -336,7 +327,7 @@ __global__ void __launch_bounds__(T) select_one_kernel(SelectArgs a) {
     gather_scores<T>(0, (uint32_t)a.keep, src, kept, dst);
 }
 
-// find_border_pairs over the keys of a cluster's CTAs: the CTAs' counts are added up in
+// search_pairs over the keys of a cluster's CTAs: the CTAs' counts are added up in
 // distributed shared memory, one cluster barrier a step.
 template <int K>
 __device__ __forceinline__ uint32_t find_border_cluster(cg::cluster_group &cluster, const uint32_t (&k)[K], uint32_t want,
@@ -431,13 +422,15 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(SelectArgs a) {
 #pragma unroll
         for (int i = 0; i < 2; i++) x[i] = make_key((int)((int64_t)n * (tid + i * kSelThreads) / kSampleLong));
         const int r = (int)((int64_t)a.keep * kSampleLong / n), d = 4 + (int)(3.0f * sqrtf((float)r));
+        auto count = [&](uint32_t border, int bit, int step, uint32_t (&c)[4]) {
+            count_pairs<kSelThreads>(x, 2, border, bit, step & 1, s_count, c);
+        };
         uint32_t hi = 0xffffffffu;
         bool exact;
         if (r > d)
-            hi = find_border_pairs<kSelThreads>(x, 2, (uint32_t)(r - d), 0u, 31, s_count, exact, kSampleLast) |
-                 ((1u << kSampleLast) - 1u);
+            hi = search_pairs(0u, 31, kSampleLast, (uint32_t)(r - d), exact, count) | ((1u << kSampleLast) - 1u);
         __syncthreads();
-        const uint32_t lo = find_border_pairs<kSelThreads>(x, 2, (uint32_t)min(r + d, kSampleLong), 0u, 31, s_count, exact, kSampleLast);
+        const uint32_t lo = search_pairs(0u, 31, kSampleLast, (uint32_t)min(r + d, kSampleLong), exact, count);
         if (tid == 0) s_between = 0;
         __syncthreads();
         uint32_t above = 0;

@@ -1,0 +1,52 @@
+"""Eviction where few rows go or the search has little to hold on to: the number of kept rows
+close to the number there are, in every selection, with guard areas around what is written."""
+
+import pytest
+import torch
+
+from test_gpu_eviction import _evict, _scores
+
+pytestmark = pytest.mark.gpu
+GUARD = 4096
+
+
+@pytest.fixture(scope="module")
+def m():
+    import nvfp4_quantised_paged_gb300 as mod
+    return mod
+
+
+def _guarded(shape, dtype, value):
+    """A buffer of `shape` inside a larger one filled with `value`; (the view, a check that the rest is untouched)."""
+    n = 1
+    for x in shape:
+        n *= x
+    whole = torch.full((n + 2 * GUARD,), value, dtype=dtype, device="cuda")
+
+    def intact():
+        return bool((whole[:GUARD] == value).all() and (whole[GUARD + n:] == value).all())
+    return whole[GUARD:GUARD + n].view(shape), intact
+
+
+def _run(m, lens, Hkv, keep, recent, sink, scores):
+    """Every output, kept and scores as narrow as they may be, checked against the plain form (in _evict)."""
+    B = len(lens)
+    kept, k_ok = _guarded((B, Hkv, keep), torch.int32, -77)
+    new_scores, s_ok = _guarded((B, Hkv, keep), torch.float32, -77.0)
+    new_lens, l_ok = _guarded((B,), torch.int32, -77)
+    _evict(m, lens, Hkv, 128, keep, recent, sink, scores, kept=kept, new_scores=new_scores, new_lens=new_lens)
+    assert k_ok() and s_ok() and l_ok()
+
+
+@pytest.mark.parametrize("recent,sink", [(256, 4), (0, 0)])
+@pytest.mark.parametrize("more", [1, 2, 8, 16])
+@pytest.mark.parametrize("keep", [2048, 4096, 8192, 32000])
+def test_a_few_rows_go(m, keep, more, recent, sink):
+    for seed in range(3):
+        _run(m, [keep + more] * 4, 2, keep, recent, sink, _scores((4, 2, keep + more), seed))
+
+
+def test_all_of_the_sampled_list_is_kept(m):
+    """Trimming a cache that is a token over its budget, many segments at once: in a tenth of them the
+    border falls on the lowest key between the sampled ones."""
+    _run(m, [2049] * 64, 8, 2048, 256, 4, _scores((64, 8, 2049), 5))
