@@ -327,48 +327,22 @@ __global__ void __launch_bounds__(T) select_one_kernel(SelectArgs a) {
     gather_scores<T>(0, (uint32_t)a.keep, src, kept, dst);
 }
 
-// search_pairs over the keys of a cluster's CTAs: the CTAs' counts are added up in
+// Counts of a step of search_pairs over the keys of a cluster's CTAs: theirs are added up in
 // distributed shared memory, one cluster barrier a step.
 template <int K>
-__device__ __forceinline__ uint32_t find_border_cluster(cg::cluster_group &cluster, const uint32_t (&k)[K], uint32_t want,
-                                                        uint32_t border, int top, uint32_t (&s_count)[2][32],
-                                                        uint32_t (&s_step)[2][4], bool &exact) {
-    static_assert(32 * K < 1024, "a warp's count must fit ten bits");
+__device__ __forceinline__ void count_pairs_cluster(cg::cluster_group &cluster, const uint32_t (&k)[K], uint32_t border,
+                                                    int bit, int buf, uint32_t (&s_count)[2][32],
+                                                    uint32_t (&s_step)[2][4], uint32_t (&n)[4]) {
     const int lane = threadIdx.x & 31, C = (int)cluster.num_blocks();
-    exact = false;
-    int buf = 0;
-    for (int bit = top & ~1; bit >= 0; bit -= 2, buf ^= 1) {
-        uint32_t c = 0;
+    count_pairs<kSelThreads>(k, K, border, bit, buf, s_count, n);
+    if (threadIdx.x == 0) {
 #pragma unroll
-        for (int i = 0; i < K; i++)
-#pragma unroll
-            for (uint32_t x = 1; x < 4; x++) c += k[i] >= (border | (x << bit)) ? 1u << (10 * (x - 1)) : 0u;
-        c = __reduce_add_sync(0xffffffffu, c);
-        if (lane == 0) s_count[buf][threadIdx.x >> 5] = c;
-        __syncthreads();
-        if (threadIdx.x < 32) {
-            c = lane < kSelWarps ? s_count[buf][lane] : 0u;
-            const uint32_t c1 = __reduce_add_sync(0xffffffffu, c & 1023u), c2 = __reduce_add_sync(0xffffffffu, (c >> 10) & 1023u),
-                           c3 = __reduce_add_sync(0xffffffffu, c >> 20);
-            if (lane == 0) {
-                s_step[buf][1] = c1;
-                s_step[buf][2] = c2;
-                s_step[buf][3] = c3;
-            }
-        }
-        cluster.sync();                             // (a buffer is written again only after the next step's)
-        uint32_t n[4] = {0, 0, 0, 0};
-        const uint32_t *o = cluster.map_shared_rank(&s_step[0][0], lane < C ? lane : 0) + 4 * buf;
-#pragma unroll
-        for (int x = 1; x < 4; x++) n[x] = __reduce_add_sync(0xffffffffu, lane < C ? o[x] : 0u);
-        const uint32_t x = n[3] >= want ? 3u : n[2] >= want ? 2u : n[1] >= want ? 1u : 0u;
-        border |= x << bit;
-        if ((x == 3 ? n[3] : x == 2 ? n[2] : x == 1 ? n[1] : 0u) == want) {   // (want >= 1)
-            exact = true;
-            break;
-        }
+        for (int x = 1; x < 4; x++) s_step[buf][x] = n[x];
     }
-    return border;
+    cluster.sync();                                 // (a buffer is written again only after the next step's)
+    const uint32_t *o = cluster.map_shared_rank(&s_step[0][0], lane < C ? lane : 0) + 4 * buf;
+#pragma unroll
+    for (int x = 1; x < 4; x++) n[x] = __reduce_add_sync(0xffffffffu, lane < C ? o[x] : 0u);
 }
 
 constexpr int kSampleLong = 2 * kSelThreads;        // keys that place the borders of a cluster's rows
@@ -467,10 +441,10 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(SelectArgs a) {
             uint32_t k[kListPer];
 #pragma unroll
             for (int i = 0; i < kListPer; i++) k[i] = tid + i * kSelThreads < (int)own ? s_list[tid + i * kSelThreads] : 0u;
-            const uint32_t diff = lo ^ (hi - 1u);
-            const int top = diff ? 31 - __clz((int)diff) : -1;
-            uint32_t border = top >= 0 ? lo & ~((4u << (top & ~1)) - 1u) : lo;   // (4 << 30: 0, all bits are open)
-            border = find_border_cluster(cluster, k, need - above, border, top, s_count, s_step, exact);
+            const uint32_t border =
+                search_listed(lo, hi, need - above, exact, [&](uint32_t at_least, int bit, int step, uint32_t (&c)[4]) {
+                    count_pairs_cluster(cluster, k, at_least, bit, step & 1, s_count, s_step, c);
+                });
             if (exact) {                            // just `keep` keys are not below the border
                 prefix = border - 1u;               // (border > 0: not every key is kept)
                 need = 0;
@@ -591,7 +565,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(SelectArgs a) {
         c0 += o[0];
         c_eq += o[1];
     }
-    const uint32_t c1 = c0 + s_cta[0] + min(c_eq + s_cta[1], need);
+    const uint32_t c1 = min(c0 + s_cta[0] + min(c_eq + s_cta[1], need), (uint32_t)a.keep);
     c0 += min(c_eq, need);
     at += min(eq_before, need);
     cluster.sync();                                 // no CTA leaves while its counts may be read
@@ -607,7 +581,8 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(SelectArgs a) {
             const unsigned eqs = __ballot_sync(0xffffffffu, in && k[e] == prefix);
             const bool take = in && (k[e] > prefix || (k[e] == prefix && eq_before + (uint32_t)__popc(eqs & below) < need));
             const unsigned takes = __ballot_sync(0xffffffffu, take);
-            if (take) kept[at + (uint32_t)__popc(takes & below)] = t;
+            const uint32_t to = at + (uint32_t)__popc(takes & below);
+            if (take && to < (uint32_t)a.keep) kept[to] = t;
             at += (uint32_t)__popc(takes);
             eq_before += (uint32_t)__popc(eqs);
         }

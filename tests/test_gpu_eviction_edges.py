@@ -50,3 +50,12 @@ def test_all_of_the_sampled_list_is_kept(m):
     """Trimming a cache that is a token over its budget, many segments at once: in a tenth of them the
     border falls on the lowest key between the sampled ones."""
     _run(m, [2049] * 64, 8, 2048, 256, 4, _scores((64, 8, 2049), 5))
+
+
+@pytest.mark.parametrize("B,Hkv,keep", [(2, 1, 140000), (16, 8, 33000), (40, 8, 33000)])
+def test_a_few_rows_of_long_segments_go(m, B, Hkv, keep):
+    """Clusters of eight, four and one CTA, with more keys than a CTA's shared memory holds in the
+    first and the last: one long segment, the others whole."""
+    for more in (1, 2, 8, 16):
+        for seed in range(2):
+            _run(m, [keep + more] + [50] * (B - 1), Hkv, keep, 64, 4, _scores((B, Hkv, keep + more), seed))
