@@ -29,7 +29,8 @@
 //     column block lie there in another order (position 16 k + 4 q + e holds dim 16 q + 4
 //     k + e), and those of Q's blocks with them;
 //     What S^T reads from TMEM is handed over without a proxy fence (about 1,000
-//     clocks); the tile's copy in shared memory is fenced with P, before O^T;
+//     clocks); Q, in shared memory, is fenced in the first tile of a sequence, the
+//     tile's copy in shared memory with P, before O^T;
 //   * softmax: one token (= TMEM lane) a thread, the four warpgroups taking a quarter of
 //     the heads each: s - m + 7 by one multiply-add, base 2 with a lazily moved maximum per head (a vote over the
 //     warpgroup; O^T is rescaled only when a score exceeds the maximum by 2^8), P =
@@ -474,7 +475,7 @@ __global__ void __launch_bounds__(kLThreads<N>, 1) latent_decode_kernel(LatentAr
                 }
             }
         };
-        auto load_q = [&]() {   // (published to the tensor core with the first half of the tile)
+        auto load_q = [&]() {   // (handed to the tensor core with the first half of the tile)
             uint4 qv[QB][2];
             uint32_t qx[QB];
 #pragma unroll 1
@@ -563,7 +564,9 @@ __global__ void __launch_bounds__(kLThreads<N>, 1) latent_decode_kernel(LatentAr
                     *reinterpret_cast<uint4 *>(blk + sw128_off(tr, 2 * eq + 1)) = make_uint4(f[e][4], f[e][5], f[e][6], f[e][7]);
                 }
                 if (i & 1) {   // half of the tile at a time (a quarter at a time: the same)
-                    if (2 * i <= L::kSmemCbs) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    // S^T reads shared memory through the async proxy: the column blocks that lie there, and Q,
+                    // which a sequence's first tile hands over with the first half
+                    if (2 * i <= L::kSmemCbs || (i == 1 && fresh)) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     tc_wait_st();
                     tc_fence_before();
                     __syncwarp();
