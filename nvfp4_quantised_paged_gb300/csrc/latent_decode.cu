@@ -14,7 +14,7 @@
 // and the MN-major A operand of the second.  e2m1 x e4m3 is an exact FP16 value;
 // the tensor scale is folded into q (FP16 after a power-of-two pre-scale a head,
 // exact for g = 1 above 2^-29 of its largest value) and into the output; the
-// rotary steps are BF16 into the same accumulator.
+// rotary steps are BF16, by the same pre-scale, into the same accumulator.
 //
 // One CTA per SM.  Sixteen warps do everything but issue the products:
 //   * expanding: two warps per 16-token group, taking every other column block; lane (r,
@@ -444,11 +444,12 @@ __global__ void __launch_bounds__(kLThreads<N>, 1) latent_decode_kernel(LatentAr
                 for (int e = 0; e < 8; e++) ml = max_u16x2(ml, w[e] & 0x7fff7fffu);
                 ml = __reduce_max_sync(0xffffffffu, max(ml >> 16, ml & 0xffffu));
                 mr = __reduce_max_sync(0xffffffffu, max(mr >> 16, mr & 0xffffu));
-                // 2^kq puts the largest |q g| into [2^14, 2^15), the rotary part below 2^127
+                // 2^kq puts the largest |q g| into [2^14, 2^15), but enlarges the rotary part to 2^64 at
+                // most: its products with keys below 2^57, 64 of them, stay in FP32 (a latent part that
+                // loses bits in FP16 then is below 2^-77 of the rotary one)
                 const uint32_t top = __float_as_uint(__uint_as_float(ml << 16) * a.g);
                 int kq = top ? 14 - ((int)(top >> 23) - 127) : 0;
-                kq = min(min(126, max(-126, kq)), 126 - ((int)(mr >> 7) - 127));
-                kq = max(-126, kq);
+                kq = max(-126, min(min(126, kq), max(0, 63 - ((int)(mr >> 7) - 127))));
                 const float sc = __uint_as_float((uint32_t)(kq + 127) << 23);
                 uint32_t f[8];
 #pragma unroll

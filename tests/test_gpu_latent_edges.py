@@ -30,3 +30,30 @@ def test_decode_of_many_short_sequences_in_one_cta(m, H):
         torch.cuda.synchronize()
         assert m.check_device_errors() == 0
         _check_decode(m, out, cache, bt, lens, 16, q, qr, 0.75)
+
+
+@pytest.mark.parametrize("H", [16, 32, 64])
+@pytest.mark.parametrize("s,t,r,g", [
+    (1e-36, 1.0, 1.0, 1.0),
+    (1e-30, 64.0, 1.0, 1.0),
+    (1.0, 1.0, 1.0, 2.0**-110),
+    (1.0, 4.0, 1.0, 2.0**-126),
+    (0.5, 1e-36, 1e6, 1.0),
+    (1e-38, 1e-4, 1e4, 1.0),
+])
+def test_decode_when_the_rotary_part_dwarfs_the_latent_one(m, H, s, t, r, g):
+    """Latent queries (or a tensor scale) so small that their pre-scale, which the rotary part
+    shares, must not push the rotary scores out of FP32."""
+    P, lens = 64, [200, 300] * (1 if H == 16 else 40)      # (more tiles than SMs: larger head tiles)
+    bt, pages = _table(lens, P, 5)
+    cache = m.LatentCache(pages, P, global_scale=g)
+    for b, n in enumerate(lens):
+        x = _rand((n, 576), 50 + b % 2)
+        x[:, 512:] *= r
+        m.latent_quantize_append(cache, x[:, :512], x[:, 512:], _cuda(_slots(bt[b], P, n), torch.int64))
+    q, qr = _rand((2, H, 512), 3, s), _rand((2, H, 64), 4, t)
+    out = m.latent_decode_attention(cache, q.repeat(len(lens) // 2, 1, 1), qr.repeat(len(lens) // 2, 1, 1), _cuda(bt),
+                                    _cuda(lens))
+    torch.cuda.synchronize()
+    assert m.check_device_errors() == 0
+    _check_decode(m, out[:2], cache, bt, lens[:2], P, q, qr, g)
