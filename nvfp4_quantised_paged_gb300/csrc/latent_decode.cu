@@ -85,6 +85,7 @@ constexpr float kNegInfL = -__builtin_huge_valf();
 constexpr float kRescaleL = 8.0f;
 constexpr int kSeqUnits = 1;                  // what a sequence's start costs a CTA, in tiles
 constexpr float kPOffset = 7.0f;              // P = 2^(s - m + 7): at most 2^15
+constexpr float kNoMax = 3.402823466e38f;     // the offset while every score was -inf: any other one moves the maximum, P of -inf is 0
 
 template <int N>
 struct LSmem {
@@ -472,7 +473,7 @@ __global__ void __launch_bounds__(kLThreads<N>, 1) latent_decode_kernel(LatentAr
                 if (lane == 0) {
                     s_fac[hh] = a.score_log2 * __uint_as_float((uint32_t)(127 - kq) << 23);
                     s_m[hh] = kNegInfL;
-                    s_off[hh] = -kNegInfL;
+                    s_off[hh] = kNoMax;
                 }
             }
         };
@@ -655,7 +656,7 @@ __global__ void __launch_bounds__(kLThreads<N>, 1) latent_decode_kernel(LatentAr
                     const float mo = s_m[wg * CW + lane], mn = fmaxf(mo, mx);
                     s_alpha[wg * CW + lane] = mo == kNegInfL ? 0.f : ex2(mo - mn);
                     s_m[wg * CW + lane] = mn;
-                    s_off[wg * CW + lane] = mn == kNegInfL ? 0.f : kPOffset - mn;
+                    s_off[wg * CW + lane] = mn == kNegInfL ? kNoMax : kPOffset - mn;
                 }
                 group_sync(wg);
 #pragma unroll
