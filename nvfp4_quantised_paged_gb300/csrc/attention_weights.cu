@@ -250,6 +250,7 @@ __global__ void __launch_bounds__(kThreads, 2) weights_kernel(WeightsArgs a) {
         if (copy && (page < 0 || page >= a.num_pages)) {   // reads as zeros
             flag_error(a.err, kErrPage);
             for (int i = 0; i < H::kBytes / 16; i++) reinterpret_cast<uint4 *>(dst)[i] = make_uint4(0, 0, 0, 0);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before a later unit's copy to the same place
             copy = false;
         }
         const unsigned copies = __popc(__ballot_sync(0xffffffffu, copy));

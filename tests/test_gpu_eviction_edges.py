@@ -1,9 +1,12 @@
 """Eviction where few rows go or the search has little to hold on to: the number of kept rows
-close to the number there are, in every selection, with guard areas around what is written."""
+close to the number there are, in every selection, with guard areas around what is written.
+Scores of sequences with missing pages, many units a warp."""
 
 import pytest
 import torch
 
+import workloads
+from gpu_common import fill_both
 from test_gpu_eviction import _evict, _scores
 
 pytestmark = pytest.mark.gpu
@@ -59,3 +62,22 @@ def test_a_few_rows_of_long_segments_go(m, B, Hkv, keep):
     for more in (1, 2, 8, 16):
         for seed in range(2):
             _run(m, [keep + more] + [50] * (B - 1), Hkv, keep, 64, 4, _scores((B, Hkv, keep + more), seed))
+
+
+@pytest.mark.parametrize("dtype,n", [(0, 120000), (1, 120000)])
+def test_scores_beside_many_missing_pages(m, dtype, n):
+    """Pages out of range between good ones, in sequences so long that a warp's ring goes round
+    several times: each reads as zeros, as a page of zeros does, and the pages after it are whole."""
+    w = workloads.make_decode("holes", 3, [n], 16, 8, 16, extra_pages=1)
+    cache, _ = fill_both(w, m, dtype=dtype)
+    zero = next(iter(set(range(w.num_pages)) - set(w.block_table.flatten().tolist())))
+    cache.pool[zero] = 0
+    holes = torch.rand(w.block_table.shape, generator=torch.Generator().manual_seed(1)) < 0.4
+    q, sl, got = w.q("cuda"), w.seq_lens.cuda(), []
+    for page in (zero, w.num_pages, -1):
+        scores = torch.zeros((1, 8, n), device="cuda")
+        m.accumulate_attention_weights(cache, q, torch.where(holes, page, w.block_table).to(torch.int32).cuda(), sl, scores)
+        torch.cuda.synchronize()
+        assert m.check_device_errors() == (0 if page == zero else -4)
+        got.append(scores)
+    assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
