@@ -414,10 +414,10 @@ __global__ void __launch_bounds__(kThreads, 2) weights_kernel(WeightsArgs a) {
                 }
         }
     }
-    if (!ok) {   // no copy may still be writing when the CTA's memory is freed
+    if (!ok) {   // no copy may still be writing when the CTA's memory is freed: units [it, nx) were requested
         abort_all = 1;
         if (lane == 0) flag_error(a.err, kErrTimeout);
-        for (int i = 0; i < kStagesW - 1 && it.left > nx.left; i++, it.left--) {
+        for (; it.left > nx.left; it.left--) {
             mbar_wait_bounded(&bar[stage], parity, kWaitLimitW, nullptr);
             if (++stage == kStagesW) {
                 stage = 0;

@@ -3,7 +3,7 @@
 The tensor core's products and the bulk copies access shared memory through the async proxy, so
 what ordinary stores put there has to be fenced by the storing threads before the other side
 goes on.  A missing fence shows in no output as long as the stores happen to land in time, so
-the source is read here."""
+the source is read here; so is what is waited for before a CTA's memory is freed."""
 
 import os
 import re
@@ -55,3 +55,20 @@ def test_zeros_in_place_of_a_page_are_fenced_before_the_next_copy():
     body = src[src.index("auto request = "):]
     body = body[body.index("flag_error(a.err, kErrPage)"):body.index("bulk_g2s(")]
     assert body.index("= make_uint4(0, 0, 0, 0)") < body.index("fence.proxy.async.shared::cta") < body.index("__syncwarp()")
+
+
+def test_scores_wait_for_every_copy_in_flight_when_they_give_up():
+    """After a wait that ran out, the units requested and not yet used, as many as the ring has stages,
+    are waited for before the CTA ends: the loop's header is run here."""
+    src = _source("attention_weights.cu")
+    stages = int(re.search(r"kStagesW = (\d+);", src).group(1))
+    body = src[src.index("if (!ok) {   // no copy"):]
+    init, cond, step = re.search(r"for \((.*?);(.*?);(.*?)\) \{", body).groups()
+    names = {"it.left": "left", "nx.left": "nx", "kStagesW": str(stages), "&&": "and"}
+    for a, b in names.items():
+        cond = cond.replace(a, b)
+    for outstanding in range(1, stages + 1):
+        left, waited = 10, 0
+        while eval(cond, {"left": left, "nx": 10 - outstanding, "i": waited}):
+            left, waited = left - 1, waited + 1
+        assert waited == outstanding
