@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kEThreads, 1)
             *abort_flag = 1;
         }
         // After an abort: request what is missing of the last K or V (its barrier counts whole
-        // ones; the slots' contents no longer matter), and wait until every copy has landed.
+        // ones; the slots' contents no longer matter).
         if (!ok) {
             const uint32_t j = blk / 5;
             const bool pre = j0 + (int)j < nt_pre;
@@ -301,11 +301,12 @@ __global__ void __launch_bounds__(kEThreads, 1)
                                 i == 2 ? 0 : head, tile_row(j0 + (int)j), full);
                 blk++;
             }
-            for (uint32_t x = blk > 10 ? blk - 10 : 0; x < blk; x++) {
-                const uint32_t t = x / 5;
-                if (x % 5 == 0) mbar_wait_bounded(&k_full[t & 1], (t >> 1) & 1, kWaitLimitE, nullptr);
-                if (x % 5 == 3) mbar_wait_bounded(&v_full[t & 1], (t >> 1) & 1, kWaitLimitE, nullptr);
-            }
+        }
+        // Whichever warp gave up, every copy has landed before the CTA's memory is freed.
+        for (uint32_t x = blk > 10 ? blk - 10 : 0; x < blk; x++) {
+            const uint32_t t = x / 5;
+            if (x % 5 == 0) mbar_wait_bounded(&k_full[t & 1], (t >> 1) & 1, kWaitLimitE, nullptr);
+            if (x % 5 == 3) mbar_wait_bounded(&v_full[t & 1], (t >> 1) & 1, kWaitLimitE, nullptr);
         }
     } else if ((tid >> 7) < nwg) {
         // ---------------- softmax of this thread's query row

@@ -72,3 +72,15 @@ def test_scores_wait_for_every_copy_in_flight_when_they_give_up():
         while eval(cond, {"left": left, "nx": 10 - outstanding, "i": waited}):
             left, waited = left - 1, waited + 1
         assert waited == outstanding
+
+
+# ------------------------------------------------------------------ latent extend: copies in flight
+
+def test_extend_waits_for_its_copies_whichever_warp_gives_up():
+    """The load warp may have requested everything when another warp's wait runs out: its last wait
+    stands on no condition."""
+    src = _source("latent_extend.cu")
+    body = src[src.index("// ---------------- load warp"):src.index("// ---------------- softmax of")]
+    for bar in ("k_full", "v_full"):
+        before = body[:body.index("mbar_wait_bounded(&%s[t & 1]" % bar)]
+        assert before.count("{") - before.count("}") == 1      # inside the loop over the blocks alone
