@@ -449,7 +449,10 @@ NVFP4KV_API size_t nvfp4kv_latent_decode_workspace_bytes(const nvfp4kv_latent_ca
  *   workspace     device, >= nvfp4kv_latent_decode_workspace_bytes(...),
  *                 256-byte aligned; calls that may overlap need one each
  *   num_splits    CTAs a head tile's token range is cut into; 0 = auto.
- * num_heads 1..128.  A sequence of length 0 yields zeros.
+ * num_heads 1..128, batch <= 65535.  A sequence of length 0 yields zeros; a token
+ * whose score is minus infinity counts nothing.  Queries are FP16 under a power
+ * of two per head, q_latent * g rounded to it once (exact for g = 1); the
+ * probabilities are FP16, the sums FP32.
  */
 NVFP4KV_API int nvfp4_latent_decode_attention(const nvfp4kv_latent_cache *cache, const void *q_latent,
                                               const void *q_rope, int batch, int num_heads,
@@ -535,7 +538,7 @@ NVFP4KV_API int nvfp4_accumulate_attention_weights(const nvfp4kv_cache *cache, c
  *   kept          device int32 [batch][num_kv_heads][keep], -1 behind new_lens[b]
  *   new_scores    device float [batch][num_kv_heads][new_score_stride], not
  *                 scores: the kept scores, then zeros; new_score_stride >= keep.
- * NVFP4 and FP8 pools.
+ * NVFP4 and FP8 pools; batch * num_kv_heads <= 65535.
  */
 NVFP4KV_API int nvfp4_evict(const nvfp4kv_cache *cache, const float *scores, int64_t score_stride, int batch,
                             const int32_t *block_table, int max_pages_per_seq, const int32_t *seq_lens,

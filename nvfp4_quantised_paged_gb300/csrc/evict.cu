@@ -14,7 +14,8 @@
 //            cluster.  Keys stay in shared memory between the rounds as far as they fit;
 //            where they do not, a sample's borders take the place of the rounds here too.
 //            (16 x 8 segments of up to 32,768 rows: 23 us with one CTA each, 66 us with
-//            clusters of four.)
+//            clusters of four.)  Which it is goes by the rows that the table and the score
+//            rows have room for: the lengths are on the device.
 //   move     one warp per 16-row group of the new pages gathers its rows and writes the
 //            group's contiguous bytes: 36 us for 524,288 rows, which read 288 bytes of
 //            32-byte sectors each for their 144 and write 144: 6.3 TB/s.

@@ -48,10 +48,11 @@
 // normalised and written there; others leave (m, l, O) partials that a second kernel
 // joins.  Every wait is bounded.
 //
-// Measured (ragged lengths up to n): 32 sequences, n 8,192, 16 heads 29.6 us; 64, n 4,096,
-// 64 heads 53.5 us; 8, n 32,768, 128 heads 81.1 us (655 TFLOP/s); one of 77 tokens 7.7 us.
-// Of the first, 3.8 us pass until the first tile is expanded, 19 us in nine tiles of 4,100
-// clocks, 7 us in storing and joining partials.  A tile is bound by its expansion (1,024
+// Measured (ragged lengths up to n, other pages each call): 32 sequences, n 8,192, 16 heads
+// 34.0 us (30.1 where the pages lie in L2); 64, n 4,096, 64 heads 53.5 us; 8, n 32,768, 128
+// heads 80.8 us (657 TFLOP/s); one of 77 tokens 7.4 us.  Of the first, in L2, some 4 us pass
+// until the first tile is expanded, 19 us in nine tiles of 4,100 clocks, 7 us in storing and
+// joining partials.  A tile is bound by its expansion (1,024
 // conversions and as many packed multiplies a warp's width, 2,700 clocks with the stores)
 // and by shared memory's bandwidth: 128 KB written and 150 KB (N 16) to 300 KB (N 64) of
 // operands read at 128 bytes a clock.
@@ -928,7 +929,8 @@ cudaError_t launch_latent_decode(const nvfp4kv_latent_cache &c, const void *q_la
     if (e == cudaSuccess) e = sm_count(&sms);
     if (e != cudaSuccess) return e;
     // No more CTAs than there can be token tiles; and while there are SMs for it, smaller head
-    // tiles, whose steps are shorter (200 tokens: 10.7 us instead of 15.0 with 64 or 128 heads).
+    // tiles, whose steps are shorter (200 tokens: 9.6 us instead of 14.3 with 64 or 128 heads).
+    // Both, and whether a join follows, go by the table's width: the lengths are on the device.
     const int64_t cap = (int64_t)max_pages * c.page_size, most = batch * ((cap + kTile - 1) / kTile);
     int n = tile_heads(num_heads);
     for (int x = 16; x < n; x *= 2)
