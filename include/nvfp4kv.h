@@ -546,6 +546,121 @@ NVFP4KV_API int nvfp4_evict(const nvfp4kv_cache *cache, const float *scores, int
                             int32_t *new_lens, int32_t *kept, float *new_scores, int64_t new_score_stride,
                             cudaStream_t stream);
 
+/*
+ * ------------------------------------------------------------------ speculative decoding
+ *
+ * A step over the cache: the drafted tokens' keys and values are appended behind each
+ * sequence (nvfp4_rope_quantize_append, which also rotates their queries),
+ * nvfp4_tree_attention attends from all drafts at once, and nvfp4_accept_tokens moves the
+ * accepted ones together.  Drafts are read back from the cache, quantised, so a draft sees
+ * exactly the rows that decoding token by token would.
+ */
+
+/* Head norms and rotary positions of nvfp4_rope_quantize_append; device pointers 16-byte aligned. */
+typedef struct {
+    const float *cos_sin;   /* device float [num_positions][rot_dim]: cosines of the rot_dim / 2 pairs, then sines */
+    int64_t num_positions;
+    int32_t rot_dim;        /* rotated values at the front of a head: 0, 32, 64, 96 or 128 */
+    int32_t adjacent;       /* pair i is values (2i, 2i + 1) if 1, (i, i + rot_dim / 2) if 0 */
+    int32_t num_axes;       /* 1..3 positions a token (text: 1; time, row and column of an image: 3) */
+    int32_t sections[3];    /* num_axes > 1: pairs of each axis, multiples of 4 that sum up to rot_dim / 2 */
+    const void *q_norm;     /* device BF16 [128]: weights of the queries' norm, or NULL: none */
+    const void *k_norm;     /* the same of the keys */
+    float eps;              /* of the norms, >= 0 */
+} nvfp4kv_rope;
+
+/*
+ * Normalise and rotate Q and K a head, and quantise K and V into the pool, in one pass.
+ * For every head x of Q (and K), with u = x w r, w = the norm's weights and
+ * r = 1 / sqrt(mean(x^2) + eps) (u = x without a norm), and for every rotated pair (a, b) of
+ * angle row (c, s) at the token's position on the pair's axis:
+ *   y_a = u_a c - u_b s,  y_b = u_b c + u_a s;   y = u elsewhere,
+ * rounded to BF16 once.  Q's y goes to q_out; K's y and V as they would by
+ * nvfp4_kv_quantize_append of that y (K's rounding to BF16 is the exact value's up to 2^-40
+ * of the pair's larger product, as a code may hang on it; Q's is formed in FP32).
+ *   q              device BF16 [num_tokens][q_stride], head h at h*128; NULL with num_q_heads 0
+ *   q_out          device BF16 [num_tokens][q_out_stride]; may be q itself with its stride,
+ *                  must not overlap q, k or v otherwise
+ *   k, v           device BF16 [num_tokens][kv_stride]; q, k and v may be views of one row
+ *   positions      device int32 [num_axes][num_tokens]; a token with one outside
+ *                  [0, num_positions) is skipped and flagged
+ *   slot_mapping   as nvfp4_kv_quantize_append; the query of a token with a negative slot is
+ *                  written all the same.
+ * Strides in elements, multiples of 8.  NVFP4 and FP8 pools.  num_tokens 0 is a no-op.
+ */
+NVFP4KV_API int nvfp4_rope_quantize_append(const nvfp4kv_cache *cache, const nvfp4kv_rope *rope, const void *q,
+                                           int64_t q_stride, void *q_out, int64_t q_out_stride, int num_q_heads,
+                                           const void *k, const void *v, int64_t kv_stride, int64_t num_tokens,
+                                           const int32_t *positions, const int64_t *slot_mapping,
+                                           cudaStream_t stream);
+
+/* Drafted tokens a sequence may have in one call. */
+#define NVFP4KV_MAX_DRAFTS 64
+
+/* Workspace bytes nvfp4_tree_attention needs for this shape and num_splits on
+ * the current device (0 if the arguments are invalid). */
+NVFP4KV_API size_t nvfp4kv_tree_workspace_bytes(const nvfp4kv_cache *cache, int batch, int num_q_heads, int max_q_len,
+                                                int num_splits);
+
+/*
+ * Attention of the drafted tokens of each sequence over the cache.
+ * Sequence b has d = cu_q_lens[b+1] - cu_q_lens[b] drafts, the last d of its n = seq_lens[b]
+ * cached tokens (they are counted in seq_lens, their rows are in the pages).  Draft i sees the
+ * base = n - d tokens before the drafts and draft j where bit j of its mask is set.  A draft's
+ * position is base + popcount(its mask) - 1, any other token's its index.  With
+ * s = sm_scale * g_K * q . k:
+ *   z = softcap > 0 ? softcap * tanh(s / softcap) : s
+ *   z += slopes[h] * (position of the key - position of the draft)       (slopes given)
+ *   only keys with position > position of the draft - window             (window > 0)
+ *   out = sum_t softmax_t(z) g_V v_t;  a draft that sees nothing yields zeros.
+ * One draft a sequence and a mask of 1 is decode attention with those options.
+ *   q             device BF16 [total_q][num_q_heads][128]: sequence b's drafts are rows
+ *                 cu_q_lens[b] .. cu_q_lens[b+1] - 1
+ *   cu_q_lens     device int32 [batch + 1], non-decreasing, within total_q_tokens
+ *   max_q_len     host bound on the drafts of a sequence, 1..NVFP4KV_MAX_DRAFTS (more are cut
+ *                 off and flagged)
+ *   tree_mask     device uint64 [total_q], bits behind the drafts ignored; NULL: a chain,
+ *                 draft i sees drafts 0..i
+ *   block_table, seq_lens  as nvfp4_paged_decode_attention; d > n > 0 is flagged and yields
+ *                 zeros; tokens of a page outside the pool are flagged and not seen
+ *   softcap >= 0 (0: none), window >= 0 (0: none), slopes device float [num_q_heads] or NULL
+ *   out           device BF16 [total_q][num_q_heads][128], not q; rows of no sequence are left
+ *                 as they are
+ *   workspace     device, >= nvfp4kv_tree_workspace_bytes(...), 256-byte aligned; calls that
+ *                 may overlap need one each
+ *   num_splits    CTAs that share the tokens of a row tile (128 rows of drafts x heads of a kv
+ *                 head); 0 = auto.
+ * NVFP4 pools only; at most 128 query heads a kv head.  Queries are FP16 under a power of two
+ * per row, the probabilities FP16, the sums FP32.  A NaN among a sequence's cached value rows
+ * may reach all of its drafts (a probability of 0 times it is a NaN).
+ */
+NVFP4KV_API int nvfp4_tree_attention(const nvfp4kv_cache *cache, const void *q, const int32_t *cu_q_lens,
+                                     int64_t total_q_tokens, int batch, int max_q_len, int num_q_heads,
+                                     const uint64_t *tree_mask, const int32_t *block_table, int max_pages_per_seq,
+                                     const int32_t *seq_lens, float sm_scale, float softcap, int window,
+                                     const float *slopes, void *out, void *workspace, size_t workspace_bytes,
+                                     int num_splits, cudaStream_t stream);
+
+/*
+ * Keep the accepted drafts of every sequence: row base + accepted[b][k] of its cached tokens
+ * becomes row base + k (all rows are read before one is written, so any order will do), for
+ * k < num_accepted[b], byte for byte in every kv head; base = seq_lens[b] - d with d drafts as in
+ * nvfp4_tree_attention.  new_lens[b] = base + num_accepted[b].
+ *   accepted      device int32 [batch][max_accepted], entries 0..d-1; the first that is none
+ *                 ends the list there and is flagged (as is a list longer than d or
+ *                 max_accepted)
+ *   num_accepted  device int32 [batch]
+ *   max_accepted  1..NVFP4KV_MAX_DRAFTS
+ *   new_lens      device int32 [batch], must not overlap seq_lens
+ * A sequence with d < 0, d > NVFP4KV_MAX_DRAFTS or d > seq_lens[b] is flagged and left as it is.
+ * A row with a page outside the pool is flagged and not moved.  NVFP4 and FP8 pools;
+ * batch <= 65535.
+ */
+NVFP4KV_API int nvfp4_accept_tokens(const nvfp4kv_cache *cache, const int32_t *block_table, int max_pages_per_seq,
+                                    const int32_t *seq_lens, const int32_t *cu_q_lens, int batch,
+                                    const int32_t *accepted, int max_accepted, const int32_t *num_accepted,
+                                    int32_t *new_lens, cudaStream_t stream);
+
 /* Synchronises `stream`, then reads and clears the current device's error
  * word.  Returns NVFP4KV_OK, NVFP4KV_EDEVICE_CHECK (some kernel skipped an
  * out-of-range index since the last check) or NVFP4KV_ECUDA. */

@@ -20,6 +20,11 @@ weight:
   latent_quantize_append, latent_decode_attention (absorbed form),
   latent_prefix_dequant, latent_extend_attention (expanded form)
   accumulate_attention_weights, evict
+
+and the cache side of speculative decoding, with the position rotation on the
+way into the cache:
+
+  rope_quantize_append, tree_attention, accept_tokens
 """
 
 from __future__ import annotations
@@ -39,6 +44,7 @@ DTYPE_FP8_E4M3 = 1
 HEAD_DIM = 128
 LATENT_DIM = 512
 ROPE_DIM = 64
+MAX_DRAFTS = 64  # NVFP4KV_MAX_DRAFTS of the header
 
 STATUS = {0: "ok", -1: "invalid argument", -2: "unsupported configuration", -3: "CUDA error",
           -4: "a kernel skipped an out-of-range index"}
@@ -59,6 +65,12 @@ class _CacheDesc(ctypes.Structure):
 class _LatentDesc(ctypes.Structure):
     _fields_ = [("pool", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
                 ("latent_dim", ctypes.c_int32), ("rope_dim", ctypes.c_int32), ("global_scale", ctypes.c_float)]
+
+
+class _RopeDesc(ctypes.Structure):
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("num_positions", ctypes.c_int64), ("rot_dim", ctypes.c_int32),
+                ("adjacent", ctypes.c_int32), ("num_axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 3),
+                ("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p), ("eps", ctypes.c_float)]
 
 
 def _load_library():
@@ -99,6 +111,10 @@ def _load_library():
         "nvfp4kv_weights_workspace_bytes": (sz, [D, i32, i32]),
         "nvfp4_accumulate_attention_weights": (i32, [D, P, i32, i32, P, i32, P, f32, P, i64, P, sz, P]),
         "nvfp4_evict": (i32, [D, P, i64, i32, P, i32, P, P, i32, i32, i32, i32, P, P, P, i64, P]),
+        "nvfp4_rope_quantize_append": (i32, [D, P, P, i64, P, i64, i32, P, P, i64, i64, P, P, P]),
+        "nvfp4kv_tree_workspace_bytes": (sz, [D, i32, i32, i32, i32]),
+        "nvfp4_tree_attention": (i32, [D, P, P, i64, i32, i32, i32, P, P, i32, P, f32, f32, i32, P, P, P, sz, i32, P]),
+        "nvfp4_accept_tokens": (i32, [D, P, i32, P, P, i32, P, i32, P, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -120,7 +136,9 @@ EXPORTED_SYMBOLS = ("nvfp4kv_version", "nvfp4kv_status_string", "nvfp4kv_slab_by
                     "nvfp4_cascade_decode_attention", "nvfp4kv_latent_slab_bytes", "nvfp4_latent_quantize_append",
                     "nvfp4_latent_prefix_dequant", "nvfp4kv_latent_decode_workspace_bytes",
                     "nvfp4_latent_decode_attention", "nvfp4_latent_extend_attention",
-                    "nvfp4kv_weights_workspace_bytes", "nvfp4_accumulate_attention_weights", "nvfp4_evict")
+                    "nvfp4kv_weights_workspace_bytes", "nvfp4_accumulate_attention_weights", "nvfp4_evict",
+                    "nvfp4_rope_quantize_append", "nvfp4kv_tree_workspace_bytes", "nvfp4_tree_attention",
+                    "nvfp4_accept_tokens")
 
 NOALLOC_SCRATCH_BYTES = 64 << 20  # NVFP4KV_NOALLOC_SCRATCH_BYTES of the header
 
@@ -863,6 +881,173 @@ def evict(cache: PagedCache, scores: torch.Tensor, block_table: torch.Tensor, se
     if rc:
         _check(rc, "nvfp4_evict")
     return new_lens, kept, new_scores
+
+
+# ---------------------------------------------------------------- speculative decoding
+
+def _head_rows(t, name: str, T: int, H: int, dev: int):
+    """Address and token stride of BF16 [T][H][128] whose tokens may be strided."""
+    st = t.stride() if isinstance(t, torch.Tensor) else None
+    if (st is None or t.dtype is not torch.bfloat16 or t.get_device() != dev or t.shape != (T, H, HEAD_DIM)
+            or (T > 0 and (st[2] != 1 or (H > 1 and st[1] != HEAD_DIM)))):
+        if st is not None and t.dtype is torch.bfloat16 and t.get_device() == dev and t.shape == (T, H, HEAD_DIM):
+            raise ValueError("%s: each token must hold %d contiguous values" % (name, H * HEAD_DIM))
+        _complain(t, name, torch.bfloat16, (T, H, HEAD_DIM), dev)
+    # (a single token's stride says nothing: torch may give it any value)
+    return t.data_ptr(), st[0] if T > 1 else H * HEAD_DIM
+
+
+def rope_quantize_append(cache: PagedCache, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
+                         positions: Optional[torch.Tensor], cos_sin: Optional[torch.Tensor],
+                         slot_mapping: torch.Tensor, q_norm: Optional[torch.Tensor] = None,
+                         k_norm: Optional[torch.Tensor] = None, eps: float = 1e-6, adjacent: bool = False,
+                         sections=None, q_out: Optional[torch.Tensor] = None,
+                         stream: Optional[torch.cuda.Stream] = None) -> Optional[torch.Tensor]:
+    """Norms (weights q_norm, k_norm: BF16 [128], or None) and rotation of every head of q (BF16
+    [T][Hq][128], or None) and k, and k and v (BF16 [T][Hkv][128]) quantised into the cache as
+    quantize_append would; q, k, v may be token-strided views of one projection's rows.
+    cos_sin: float32 [positions][R], cosines of the R / 2 pairs, then sines; R = 32, 64, 96 or 128
+    values at the front of a head are rotated (None: no rotation).  positions: int32 [T], or
+    [axes][T] with sections, the pairs of each axis.  adjacent: value 2i is paired with 2i + 1, else
+    i with i + R / 2.  Returns q_out, BF16 [T][Hq][128] (q itself may be passed)."""
+    dev, Hkv = cache.pool.get_device(), cache.num_kv_heads
+    sp = _want(slot_mapping, "slot_mapping", torch.int64, None, dev)
+    if slot_mapping.dim() != 1:
+        raise ValueError("slot_mapping must be [tokens]")
+    T = slot_mapping.numel()
+    kp, ks = _head_rows(k, "k", T, Hkv, dev)
+    vp, vs = _head_rows(v, "v", T, Hkv, dev)
+    if ks != vs:
+        raise ValueError("k and v must share a token stride")
+    rope = _RopeDesc(num_axes=1, adjacent=int(bool(adjacent)), eps=float(eps))
+    pp = 0
+    if cos_sin is not None:
+        rope.cos_sin = _want(cos_sin, "cos_sin", torch.float32, None, dev)
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be [positions][rotated values]")
+        rope.num_positions, rope.rot_dim = cos_sin.shape
+        if sections is None:
+            pp = _want(positions, "positions", torch.int32, None, dev)
+            if positions.numel() != T:
+                raise ValueError("positions must have %d entries" % T)
+        else:
+            rope.num_axes = len(sections)
+            if not 1 <= len(sections) <= 3 or sum(sections) * 2 != rope.rot_dim:
+                raise ValueError("sections must be one to three counts that sum up to half the rotated values")
+            rope.sections[:len(sections)] = [int(x) for x in sections]
+            pp = _want(positions, "positions", torch.int32, (len(sections), T), dev)
+    elif sections is not None:
+        raise ValueError("sections need cos_sin")
+    if q_norm is not None:
+        rope.q_norm = _want(q_norm, "q_norm", torch.bfloat16, (HEAD_DIM,), dev)
+    if k_norm is not None:
+        rope.k_norm = _want(k_norm, "k_norm", torch.bfloat16, (HEAD_DIM,), dev)
+    s = _launch_stream(dev, stream)
+    Hq = qp = qs = op = os_ = 0
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError("q must be [tokens][heads][128]")
+        Hq = q.shape[1]
+        qp, qs = _head_rows(q, "q", T, Hq, dev)
+        if q_out is None:
+            q_out = torch.empty((T, Hq, HEAD_DIM), dtype=torch.bfloat16, device=cache.pool.device)
+            op, os_ = q_out.data_ptr(), Hq * HEAD_DIM
+            if stream is not None:
+                _keep_until_done(stream, q_out)
+        else:
+            op, os_ = _head_rows(q_out, "q_out", T, Hq, dev)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    rc = _lib.nvfp4_rope_quantize_append(cache.desc, ctypes.addressof(rope), qp, qs, op, os_, Hq, kp, vp, ks, T, pp, sp, s)
+    if rc:
+        _check(rc, "nvfp4_rope_quantize_append")
+    return q_out
+
+
+def tree_workspace_bytes(cache: PagedCache, batch: int, num_q_heads: int, max_q_len: int, num_splits: int = 0) -> int:
+    n = _lib.nvfp4kv_tree_workspace_bytes(cache.desc, int(batch), int(num_q_heads), int(max_q_len), int(num_splits))
+    if n == 0:
+        raise NVFP4KVError(-1, "tree_workspace_bytes")
+    return int(n)
+
+
+def alloc_tree_workspace(cache: PagedCache, batch: int, num_q_heads: int, max_q_len: int,
+                         num_splits: int = 0) -> torch.Tensor:
+    return torch.empty(tree_workspace_bytes(cache, batch, num_q_heads, max_q_len, num_splits), dtype=torch.uint8,
+                       device=cache.pool.device)
+
+
+def tree_attention(cache: PagedCache, q: torch.Tensor, cu_q_lens: torch.Tensor, max_q_len: int,
+                   block_table: torch.Tensor, seq_lens: torch.Tensor, tree_mask: Optional[torch.Tensor] = None,
+                   sm_scale: Optional[float] = None, softcap: float = 0.0, window: int = 0,
+                   slopes: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None, num_splits: int = 0,
+                   stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Attention of each sequence's drafts (rows cu_q_lens[b] .. cu_q_lens[b+1] - 1 of q, BF16
+    [total_q][Hq][128]), which are the last of its seq_lens[b] cached tokens: draft i sees all
+    tokens before the drafts and draft j where bit j of its tree_mask (int64 [total_q]; None: a
+    chain) is set.  max_q_len: bound on the drafts of a sequence, at most 64.  softcap > 0 caps the
+    scores by a tanh, window > 0 limits how far back a draft sees, slopes (float32 [Hq]) times the
+    distance is added to the scores; a draft's position is that of its depth in the tree.
+    -> BF16 [total_q][Hq][128]."""
+    dev = cache.pool.get_device()
+    qp = _want(q, "q", torch.bfloat16, None, dev)
+    if q.dim() != 3 or q.shape[2] != HEAD_DIM:
+        raise ValueError("q must be [drafts][heads][128]")
+    TQ, Hq, _ = q.shape
+    lp = _want(seq_lens, "seq_lens", torch.int32, None, dev)
+    B = seq_lens.numel()
+    cp = _want(cu_q_lens, "cu_q_lens", torch.int32, (B + 1,), dev)
+    bp = _want_table(block_table, "block_table", B, dev)
+    mp = _want(tree_mask, "tree_mask", torch.int64, (TQ,), dev) if tree_mask is not None else 0
+    ap = _want(slopes, "slopes", torch.float32, (Hq,), dev) if slopes is not None else 0
+    s = _launch_stream(dev, stream)
+    made = []
+    if out is None:
+        out = torch.empty_like(q)
+        made.append(out)
+        op = out.data_ptr()
+    else:
+        op = _want(out, "out", torch.bfloat16, (TQ, Hq, HEAD_DIM), dev)
+    if workspace is None:
+        workspace = alloc_tree_workspace(cache, B, Hq, max_q_len, num_splits)
+        made.append(workspace)
+    wp = _want(workspace, "workspace", torch.uint8, None, dev)
+    if stream is not None:
+        _keep_until_done(stream, *made)
+    rc = _lib.nvfp4_tree_attention(cache.desc, qp, cp, TQ, B, int(max_q_len), Hq, mp, bp, block_table.shape[1], lp,
+                                   _HEAD_SCALE if sm_scale is None else float(sm_scale), float(softcap), int(window), ap,
+                                   op, wp, workspace.numel(), int(num_splits), s)
+    if rc:
+        _check(rc, "nvfp4_tree_attention")
+    return out
+
+
+def accept_tokens(cache: PagedCache, block_table: torch.Tensor, seq_lens: torch.Tensor, cu_q_lens: torch.Tensor,
+                  accepted: torch.Tensor, num_accepted: torch.Tensor, new_lens: Optional[torch.Tensor] = None,
+                  stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Moves the accepted drafts' rows together behind each sequence's prefix: draft accepted[b][k]
+    (int32 [B][at most 64]) becomes the k-th token after it, k < num_accepted[b] (int32 [B]).
+    seq_lens and cu_q_lens as in tree_attention.  Returns new_lens, int32 [B]."""
+    dev = cache.pool.get_device()
+    lp = _want(seq_lens, "seq_lens", torch.int32, None, dev)
+    B = seq_lens.numel()
+    cp = _want(cu_q_lens, "cu_q_lens", torch.int32, (B + 1,), dev)
+    bp = _want_table(block_table, "block_table", B, dev)
+    ap = _want_table(accepted, "accepted", B, dev)
+    np_ = _want(num_accepted, "num_accepted", torch.int32, (B,), dev)
+    s = _launch_stream(dev, stream)
+    if new_lens is None:
+        new_lens = torch.empty(B, dtype=torch.int32, device=cache.pool.device)
+        op = new_lens.data_ptr()
+        if stream is not None:
+            _keep_until_done(stream, new_lens)
+    else:
+        op = _want(new_lens, "new_lens", torch.int32, (B,), dev)
+    rc = _lib.nvfp4_accept_tokens(cache.desc, bp, block_table.shape[1], lp, cp, B, ap, accepted.shape[1], np_, op, s)
+    if rc:
+        _check(rc, "nvfp4_accept_tokens")
+    return new_lens
 
 
 def check_device_errors(stream: Optional[torch.cuda.Stream] = None) -> int:

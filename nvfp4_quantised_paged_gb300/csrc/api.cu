@@ -50,6 +50,9 @@ unsigned *error_word(cudaError_t *status) {
 
 constexpr int64_t kMaxRows = (int64_t)1 << 30;  // rows of a block table the kernels' 32-bit positions allow
 
+constexpr int kMaxTreeGroup = 128;              // query heads a kv head may have in the tree attention
+static_assert(kMaxDrafts == NVFP4KV_MAX_DRAFTS, "one mask bit a draft");
+
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // A tensor scale is a positive normal FP32 number (the exact-rounding argument of
@@ -543,6 +546,118 @@ int nvfp4_evict(const nvfp4kv_cache *cache, const float *scores, int64_t score_s
     return from_cuda(launch_evict(*cache, scores, score_stride, batch, block_table, max_pages_per_seq, seq_lens,
                                   new_block_table, new_max_pages, keep, recent, sink, new_lens, kept, new_scores,
                                   new_score_stride, err, stream));
+}
+
+int nvfp4_rope_quantize_append(const nvfp4kv_cache *cache, const nvfp4kv_rope *rope, const void *q, int64_t q_stride,
+                               void *q_out, int64_t q_out_stride, int num_q_heads, const void *k, const void *v,
+                               int64_t kv_stride, int64_t num_tokens, const int32_t *positions,
+                               const int64_t *slot_mapping, cudaStream_t stream) {
+    int rc = check_cache(cache);
+    if (rc) return rc;
+    if (!rope || num_q_heads < 0 || num_tokens < 0) return NVFP4KV_EINVAL;
+    if (rope->rot_dim < 0 || rope->rot_dim > kHeadDim || rope->rot_dim % 32) return NVFP4KV_EUNSUPPORTED;
+    if (rope->adjacent != 0 && rope->adjacent != 1) return NVFP4KV_EINVAL;
+    if (rope->num_axes < 1 || rope->num_axes > 3) return NVFP4KV_EUNSUPPORTED;
+    if (rope->num_axes > 1) {
+        int sum = 0;
+        for (int i = 0; i < rope->num_axes; i++) {
+            if (rope->sections[i] < 0 || rope->sections[i] > kHeadDim) return NVFP4KV_EINVAL;
+            if (rope->sections[i] % 4) return NVFP4KV_EUNSUPPORTED;
+            sum += rope->sections[i];
+        }
+        if (sum != rope->rot_dim / 2) return NVFP4KV_EINVAL;
+    }
+    if ((rope->q_norm || rope->k_norm) && !(isfinite(rope->eps) && rope->eps >= 0.0f)) return NVFP4KV_EINVAL;
+    if (!aligned(rope->q_norm, 16) || !aligned(rope->k_norm, 16)) return NVFP4KV_EINVAL;
+    if (num_tokens == 0) return NVFP4KV_OK;
+    if (rope->rot_dim > 0 &&
+        (!rope->cos_sin || !aligned(rope->cos_sin, 16) || rope->num_positions < 1 || !positions || !aligned(positions, 4)))
+        return NVFP4KV_EINVAL;
+    if (!k || !v || !slot_mapping || !aligned(k, 16) || !aligned(v, 16) || !aligned(slot_mapping, 8)) return NVFP4KV_EINVAL;
+    if (kv_stride < (int64_t)cache->num_kv_heads * kHeadDim || kv_stride % 8) return NVFP4KV_EINVAL;
+    if (num_q_heads > 0) {
+        const int64_t row = (int64_t)num_q_heads * kHeadDim;
+        if (!q || !q_out || !aligned(q, 16) || !aligned(q_out, 16)) return NVFP4KV_EINVAL;
+        if (q_stride < row || q_stride % 8 || q_out_stride < row || q_out_stride % 8) return NVFP4KV_EINVAL;
+        if (q_out == q && q_out_stride != q_stride) return NVFP4KV_EINVAL;
+    }
+    if (num_tokens > (((int64_t)1 << 31) - 1) / (num_q_heads + 2 * (int64_t)cache->num_kv_heads)) return NVFP4KV_EUNSUPPORTED;
+    cudaError_t e;
+    unsigned *err = error_word(&e);
+    if (!err) return NVFP4KV_ECUDA;
+    return from_cuda(launch_rope_append(*cache, *rope, q, q_stride, q_out, q_out_stride, num_q_heads, k, v, kv_stride,
+                                        num_tokens, positions, slot_mapping, err, stream));
+}
+
+size_t nvfp4kv_tree_workspace_bytes(const nvfp4kv_cache *cache, int batch, int num_q_heads, int max_q_len, int num_splits) {
+    if (check_cache(cache) || cache->dtype != NVFP4KV_DTYPE_NVFP4 || batch < 0 || num_q_heads < 1 ||
+        num_q_heads % cache->num_kv_heads || num_splits < 0 || max_q_len < 1 || max_q_len > kMaxDrafts)
+        return 0;
+    const int G = num_q_heads / cache->num_kv_heads;
+    if (G > kMaxTreeGroup) return 0;
+    const int64_t rows = (int64_t)max_q_len * G;
+    const int splits = num_splits ? num_splits : tree_auto_splits(rows, nullptr);
+    return splits > 0 ? tree_workspace_bytes(batch, cache->num_kv_heads, rows, splits) : 0;
+}
+
+int nvfp4_tree_attention(const nvfp4kv_cache *cache, const void *q, const int32_t *cu_q_lens, int64_t total_q_tokens,
+                         int batch, int max_q_len, int num_q_heads, const uint64_t *tree_mask,
+                         const int32_t *block_table, int max_pages_per_seq, const int32_t *seq_lens, float sm_scale,
+                         float softcap, int window, const float *slopes, void *out, void *workspace,
+                         size_t workspace_bytes, int num_splits, cudaStream_t stream) {
+    int rc = check_cache(cache);
+    if (rc) return rc;
+    if (cache->dtype != NVFP4KV_DTYPE_NVFP4) return NVFP4KV_EUNSUPPORTED;
+    if (batch < 0 || total_q_tokens < 0 || num_q_heads < 1 || num_q_heads % cache->num_kv_heads || num_splits < 0 ||
+        max_q_len < 1 || window < 0)
+        return NVFP4KV_EINVAL;
+    if (!isfinite(sm_scale) || !isfinite(softcap) || softcap < 0.0f) return NVFP4KV_EINVAL;
+    const int G = num_q_heads / cache->num_kv_heads;
+    if (max_q_len > kMaxDrafts || G > kMaxTreeGroup || batch > 65535 || cache->num_kv_heads > 65535)
+        return NVFP4KV_EUNSUPPORTED;
+    if (batch == 0 || total_q_tokens == 0) return NVFP4KV_OK;
+    if (!q || !cu_q_lens || !block_table || !seq_lens || !out || !workspace || max_pages_per_seq < 1) return NVFP4KV_EINVAL;
+    if (out == q) return NVFP4KV_EINVAL;   // several CTAs read a query
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 256) || !aligned(block_table, 4) ||
+        !aligned(seq_lens, 4) || !aligned(cu_q_lens, 4) || !aligned(tree_mask, 8) || !aligned(slopes, 4))
+        return NVFP4KV_EINVAL;
+    const int64_t cap = (int64_t)max_pages_per_seq * cache->page_size, most = ((int64_t)1 << 31) - 1;
+    if (cap > kMaxRows || total_q_tokens > most / num_q_heads) return NVFP4KV_EUNSUPPORTED;
+    // tiles, counted in 32 bits
+    if ((int64_t)batch * cache->num_kv_heads > most / ((cap + 127) / 128 + 1)) return NVFP4KV_EUNSUPPORTED;
+    cudaError_t e = cudaSuccess;
+    const int64_t rows = (int64_t)max_q_len * G;
+    const int splits = num_splits ? num_splits : tree_auto_splits(rows, &e);
+    if (e != cudaSuccess || splits <= 0) return NVFP4KV_ECUDA;
+    if (workspace_bytes < tree_workspace_bytes(batch, cache->num_kv_heads, rows, splits)) return NVFP4KV_EINVAL;
+    unsigned *err = error_word(&e);
+    if (!err) return NVFP4KV_ECUDA;
+    return from_cuda(launch_tree(*cache, q, cu_q_lens, total_q_tokens, batch, max_q_len, num_q_heads, tree_mask,
+                                 block_table, max_pages_per_seq, seq_lens, sm_scale, softcap, window, slopes, out,
+                                 workspace, splits, err, stream));
+}
+
+int nvfp4_accept_tokens(const nvfp4kv_cache *cache, const int32_t *block_table, int max_pages_per_seq,
+                        const int32_t *seq_lens, const int32_t *cu_q_lens, int batch, const int32_t *accepted,
+                        int max_accepted, const int32_t *num_accepted, int32_t *new_lens, cudaStream_t stream) {
+    int rc = check_cache(cache);
+    if (rc) return rc;
+    if (batch < 0 || max_accepted < 1) return NVFP4KV_EINVAL;
+    if (max_accepted > kMaxDrafts || batch > 65535) return NVFP4KV_EUNSUPPORTED;
+    if (batch == 0) return NVFP4KV_OK;
+    if (!block_table || !seq_lens || !cu_q_lens || !accepted || !num_accepted || !new_lens || max_pages_per_seq < 1)
+        return NVFP4KV_EINVAL;
+    if (!aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(cu_q_lens, 4) || !aligned(accepted, 4) ||
+        !aligned(num_accepted, 4) || !aligned(new_lens, 4))
+        return NVFP4KV_EINVAL;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(new_lens), y = reinterpret_cast<uintptr_t>(seq_lens);
+    if (x < y + 4 * (uintptr_t)batch && y < x + 4 * (uintptr_t)batch) return NVFP4KV_EINVAL;
+    if ((int64_t)max_pages_per_seq * cache->page_size > kMaxRows) return NVFP4KV_EUNSUPPORTED;
+    cudaError_t e;
+    unsigned *err = error_word(&e);
+    if (!err) return NVFP4KV_ECUDA;
+    return from_cuda(launch_accept(*cache, block_table, max_pages_per_seq, seq_lens, cu_q_lens, batch, accepted,
+                                   max_accepted, num_accepted, new_lens, err, stream));
 }
 
 int nvfp4kv_check_device_errors(cudaStream_t stream) {

@@ -17,6 +17,7 @@ namespace nvfp4kv {
 
 constexpr int kHeadDim = 128;
 constexpr int kBlock = 16;
+constexpr int kMaxDrafts = 64;   // drafted tokens a sequence (one mask bit each)
 
 // Bits of the per-device error word (see nvfp4kv_check_device_errors).
 enum : unsigned {
@@ -24,7 +25,9 @@ enum : unsigned {
     kErrPage = 2u,      // block_table entry outside [0, num_pages)
     kErrSeqLen = 4u,    // seq_len / prefix_len negative or beyond the table
     kErrTimeout = 8u,   // an mbarrier wait exceeded its iteration limit
-    kErrCuPrefix = 16u  // cu_prefix_lens inconsistent with prefix_lens
+    kErrCuPrefix = 16u, // cu_prefix_lens inconsistent with prefix_lens
+    kErrPosition = 32u, // position outside the rotation table
+    kErrDraft = 64u     // drafts that do not fit the call or the sequence, or an accepted index that is none of them
 };
 
 __device__ __forceinline__ void flag_error(unsigned *err, unsigned bit) { atomicOr(err, bit); }

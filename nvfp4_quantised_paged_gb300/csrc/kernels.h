@@ -115,4 +115,24 @@ cudaError_t launch_evict(const nvfp4kv_cache &c, const float *scores, int64_t sc
                          int32_t *new_lens, int32_t *kept, float *new_scores, int64_t new_score_stride, unsigned *err,
                          cudaStream_t stream);
 
+// Head norms and rotation of Q and K, K and V quantised into the pool; strides in elements.
+cudaError_t launch_rope_append(const nvfp4kv_cache &c, const nvfp4kv_rope &rope, const void *q, int64_t q_stride,
+                               void *q_out, int64_t q_out_stride, int num_q_heads, const void *k, const void *v,
+                               int64_t kv_stride, int64_t num_tokens, const int32_t *positions,
+                               const int64_t *slot_mapping, unsigned *err, cudaStream_t stream);
+
+// Attention of the drafted tokens: CTAs per row tile of an auto split for `rows` = max_q_len x
+// group rows a pair (0 on an error), workspace bytes for `splits` of them, and the launch.
+int tree_auto_splits(int64_t rows, cudaError_t *status);
+size_t tree_workspace_bytes(int batch, int num_kv_heads, int64_t rows, int splits);
+cudaError_t launch_tree(const nvfp4kv_cache &c, const void *q, const int32_t *cu_q, int64_t total_q, int batch,
+                        int max_q_len, int num_q_heads, const uint64_t *mask, const int32_t *block_table, int max_pages,
+                        const int32_t *seq_lens, float sm_scale, float softcap, int window, const float *slopes,
+                        void *out, void *workspace, int splits, unsigned *err, cudaStream_t stream);
+
+// The accepted drafts' rows moved together behind their prefixes.
+cudaError_t launch_accept(const nvfp4kv_cache &c, const int32_t *block_table, int max_pages, const int32_t *seq_lens,
+                          const int32_t *cu_q, int batch, const int32_t *accepted, int max_accept,
+                          const int32_t *num_accepted, int32_t *new_lens, unsigned *err, cudaStream_t stream);
+
 }  // namespace nvfp4kv
