@@ -12,7 +12,7 @@
 // A token costs 144 bytes a kv head and 512 flops a row: the cache's bytes bound it up to some
 // 128 rows, the tensor cores beyond.
 //
-// Tokens sit on the tensor core's M dimension in both products, rows on N (16, 32, 64 or 128),
+// Tokens sit on the tensor core's M dimension in both products, rows on N (16, 32 or 64),
 // so few rows cost little:
 //   S^T (128 tokens x N) = K Q^T     8 steps of M 128 x N x K 16, K as the A operand in TMEM
 //   O^T (128 dims x N) += V^T P^T    8 steps, V and P in shared memory, both MN-major
@@ -20,19 +20,22 @@
 // above 2^-29 of the row's largest value); the tensor scales go into the score's factor and
 // into the output.
 //
-// One CTA per SM, 18 warps:
-//   * sixteen workers expand a tile and run its softmax.  Expanding: one warp per 16-token
-//     group and operand; lane (r, q) holds the q-th 16 bytes of rows r and r + 8.  K goes to
-//     TMEM (the store takes a quad's registers as four columns each, so the dims lie there in
-//     another order: position 16 a + 4 q + e holds dim 32 q + 4 a + e, and Q's with them), V
-//     to a swizzled tile in shared memory.  Softmax: one token (= TMEM lane) a thread, the four
-//     warpgroups taking a quarter of the rows each; a lazily moved maximum per row (a vote over
-//     the warpgroup; O^T is rescaled only when a score exceeds it by 2^8), P = 2^(z - m + 7) in
-//     FP16, the sums of the rounded P in registers until the pair ends.
+// Two CTAs per SM, ten warps each:
+//   * eight workers expand a tile and run its softmax.  The first warpgroup expands K of the
+//     tile after this one, the second V of this one, a warp two 16-token groups; lane (r, q)
+//     holds the q-th 16 bytes of rows r and r + 8.  K goes to TMEM (the store takes a quad's
+//     registers as four columns each, so the dims lie there in another order: position 16 a +
+//     4 q + e holds dim 32 q + 4 a + e, and Q's with them), V to a swizzled tile in shared
+//     memory.  Softmax: one token (= TMEM lane) a thread, half of the rows a warpgroup; a lazily
+//     moved maximum per row (a vote over the warpgroup; O^T is rescaled only when a score exceeds
+//     it by 2^8), P = 2^(z - m + 7) in FP16, the sums of the rounded P in registers until the
+//     pair ends.
 //   * one warp copies raw tiles (8 groups of 2,304 bytes) into a ring, ahead of everything;
-//   * one warp issues the products.
-// Tile j + 1 is expanded before the softmax of tile j, whose scores are ready by then, and
-// O^T += V^T P^T of tile j runs while tile j + 2 is expanded: K, S, V and P are double.
+//   * one warp issues the products: O^T += V^T P^T of a tile and S^T of the next, handed over
+//     together and awaited together, so that a tile costs two waits and one vote.
+// The chain of a tile (wait, expand, softmax, products) is long beside its instructions: the
+// other CTA of the SM fills the gaps.  (One CTA of sixteen workers, with K, V and P double or
+// triple: 61 us for 32 sequences of up to 4,096 tokens, 32 query heads and 8 drafts.)
 //
 // Split: all pairs' 128-token tiles form one flat range (a pair's start counts as one tile
 // more), cut equally over the CTAs of a row tile.  A pair that lies in one CTA is normalised
@@ -50,8 +53,10 @@ namespace nvfp4kv {
 
 namespace {
 
-constexpr int kWorkersT = 512;                // warps 0 .. 15
-constexpr int kThreadsT = kWorkersT + 64;     // + the MMA warp (16) and the load warp (17)
+constexpr int kWorkersT = 256;                // warps 0 .. 7
+constexpr int kThreadsT = kWorkersT + 64;     // + the MMA warp (8) and the load warp (9)
+constexpr int kMmaWarp = kWorkersT / 32, kLoadWarp = kMmaWarp + 1;
+constexpr int kCtasT = 2;                     // CTAs an SM
 constexpr int kTileT = 128;                   // tokens a tile
 constexpr int kBlockT = kTileT * 128;         // bytes of a column block: 64 dims (or rows of P) of 128 tokens
 constexpr int kGroupT = 2304;                 // bytes of a 16-token group
@@ -65,27 +70,25 @@ constexpr int kPairUnits = 1;                 // what a pair's start costs a CTA
 
 template <int N>
 struct TSmem {
-    static constexpr int kPBlocks = N == 128 ? 2 : 1;
-    static constexpr int kStages = N == 128 ? 3 : 6;
+    static constexpr int kStages = N == 64 ? 2 : 3;
     static constexpr int kQBlock = N * 128;                       // a column block of Q, [N][64]
     static constexpr int kQ = 0;
-    static constexpr int kV = 2 * kQBlock > 4096 ? 2 * kQBlock : 4096;
-    static constexpr int kP = kV + 2 * 2 * kBlockT;               // V: two tiles of two column blocks
-    static constexpr int kRaw = kP + 2 * kPBlocks * kBlockT;      // P: two
+    static constexpr int kV = 2 * kQBlock;                        // two column blocks
+    static constexpr int kP = kV + 2 * kBlockT;                   // FP16 [128 tokens][64], N rows used
+    static constexpr int kRaw = kP + kBlockT;
     static constexpr int kBar = kRaw + kStages * kRawT;
-    // k_full[2] v_full[2] s_done[2] p_full[2] pv_done[2] drain raw_full[] raw_free[]
-    static constexpr int kNumBars = 11 + 2 * kStages;
+    static constexpr int kNumBars = 3 + 2 * kStages;              // ready done drain raw_full[] raw_free[]
     static constexpr int kMisc = kBar + 8 * kNumBars;             // tmem base, abort, valid[kStages]
     static constexpr int kM = (kMisc + 8 + 4 * kStages + 15) & ~15;   // float m[N], fac[N], alpha[N], off[N], slope[N], depth[N]
     static constexpr int kRow = kM + 6 * N * 4;                   // int row[N] (-1: none), draft[N]
-    static constexpr int kWarpMax = kRow + 2 * N * 4;             // float [4][4][N / 4]
+    static constexpr int kWarpMax = kRow + 2 * N * 4;             // float [2][4][N / 2]
     static constexpr int kMask = kWarpMax + 4 * N * 4;            // u64 mask[64], int depth[64]
     static constexpr int kBytes = kMask + 64 * 12;
-    // TMEM columns: O at 0, S[2], K[2]
-    static constexpr uint32_t kColS = N, kColK = 3 * N, kCols = 512;
-    static_assert(kColK + 128 <= kCols, "TMEM columns");
+    // TMEM columns: O at 0, S, K[2]
+    static constexpr uint32_t kColS = N, kColK = 2 * N, kCols = 256;
+    static_assert(kColK + 128 <= kCols && kCtasT * kCols <= 512, "TMEM columns");
     static_assert(kV % 1024 == 0 && kP % 1024 == 0 && kRaw % 1024 == 0 && kBar % 16 == 0 && kMask % 8 == 0, "alignment");
-    static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
+    static_assert(kCtasT * (kBytes + 1024) <= 228 * 1024, "shared memory of an SM");
     static_assert(sizeof(FlatScratch<kThreadsT>) <= 2 * kBlockT, "the plan's scratch lies in the V tile");
 };
 
@@ -134,23 +137,25 @@ __device__ __forceinline__ int pair_units(const TreeArgs &a, const Seq &s, int r
     return s.nt > 0 && s.d * a.G > r0 ? s.nt + kPairUnits : 0;
 }
 
-// The tiles of a CTA's range in order.
+// The pairs of a CTA's range in order, and of each its tiles [t, te) that lie in the range.
 struct TreeIter {
-    int b, kv, t;    // t: tile of the pair, from 0
+    int b, kv, t, te;
     Seq s;
-    int left;        // units of the range from this one on
+    int left;        // units of the range from tile t on
 };
 
-__device__ __forceinline__ void next_tile(const TreeArgs &a, TreeIter &it, int r0) {
-    it.left--;
-    if (++it.t < it.s.nt || it.left <= 0) return;
+__device__ __forceinline__ bool next_pair(const TreeArgs &a, TreeIter &it, int r0) {
+    it.left -= it.te - it.t + kPairUnits;
+    if (it.left <= 0) return false;
+    if (++it.kv == a.Hkv) {
+        it.kv = 0;
+        do {         // left > 0: a later sequence has tiles
+            it.s = seq_of(a, ++it.b);
+        } while (pair_units(a, it.s, r0) == 0);
+    }
     it.t = 0;
-    it.left -= kPairUnits;
-    if (it.left <= 0 || ++it.kv < a.Hkv) return;
-    it.kv = 0;
-    do {             // left > 0: a later sequence has tiles
-        it.s = seq_of(a, ++it.b);
-    } while (pair_units(a, it.s, r0) == 0);
+    it.te = min(it.s.nt, it.left);
+    return true;
 }
 
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, const volatile int *abort_flag) {
@@ -159,6 +164,12 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, const v
         if ((n & 63) == 63 && *abort_flag) return false;
     }
     return false;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
 // s0 += low FP16 of w, s1 += high FP16 of w
@@ -170,9 +181,9 @@ __device__ __forceinline__ void add_f16x2(float &s0, float &s1, uint32_t w) {
         : "r"(w), "h"(one));
 }
 
-// Barriers 1 .. 4: the working warpgroups; 5: all of them.
+// Barriers 1, 2: the working warpgroups; 3: both of them.
 __device__ __forceinline__ void group_sync(int wg) { asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory"); }
-__device__ __forceinline__ void workers_sync() { asm volatile("bar.sync 5, 512;" ::: "memory"); }
+__device__ __forceinline__ void workers_sync() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
 
 __device__ __forceinline__ bool group_any(int wg, bool p) {
     uint32_t r;
@@ -215,16 +226,15 @@ __device__ __forceinline__ void load_columns(uint32_t taddr, uint32_t (&r)[C]) {
     else tc_ld(taddr, r);
 }
 
-// OPT: the scores are capped or biased.
+// OPT: the scores are capped or biased, or their factor is not positive.
 template <int N, bool OPT>
-__global__ void __launch_bounds__(kThreadsT, 1) tree_kernel(TreeArgs a) {
+__global__ void __launch_bounds__(kThreadsT, kCtasT) tree_kernel(TreeArgs a) {
     using L = TSmem<N>;
-    constexpr int CW = N / 4;                     // rows per warpgroup
+    constexpr int CW = N / 2;                     // rows per warpgroup
     constexpr int S = L::kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBar);
-    uint64_t *k_full = bars, *v_full = bars + 2, *s_done = bars + 4, *p_full = bars + 6, *pv_done = bars + 8;
-    uint64_t *drain = bars + 10, *raw_full = bars + 11, *raw_free = raw_full + S;
+    uint64_t *ready = bars, *done = bars + 1, *drain = bars + 2, *raw_full = bars + 3, *raw_free = raw_full + S;
     uint32_t &tmem_base = *reinterpret_cast<uint32_t *>(smem + L::kMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 4);
     volatile int *s_valid = abort_flag + 1;
@@ -236,18 +246,14 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_kernel(TreeArgs a) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int r0 = blockIdx.y * N;
     if (tid == 0) {
-        for (int i = 0; i < 4; i++) mbar_init(&bars[i], i < 2 ? kWorkersT / 32 : kWorkersT / 64);
-        for (int i = 4; i < 11; i++) mbar_init(&bars[i], i == 6 || i == 7 ? kWorkersT / 32 : 1);
-        for (int i = 0; i < S; i++) {
-            mbar_init(&raw_full[i], 1);
-            mbar_init(&raw_free[i], kWorkersT / 32);
-        }
+        for (int i = 0; i < L::kNumBars; i++)
+            mbar_init(&bars[i], i == 0 || i >= 3 + S ? kWorkersT / 32 : 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
     pdl_wait();               // everything read or written may belong to earlier work of the stream
     pdl_launch_dependents();
-    if (warp == 16) tc_alloc(&tmem_base, L::kCols);
+    if (warp == kMmaWarp) tc_alloc(&tmem_base, L::kCols);
 
     int b0;
     unsigned first, u0 = 0, u1 = 0;
@@ -261,7 +267,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_kernel(TreeArgs a) {
             return u0 < u1 ? u0 : kFlatNone;
         },
         b0, first);
-    if (warp == 16 && blockIdx.y == 0) {   // what is out of range, and the rows of sequences without tokens
+    if (warp == kMmaWarp && blockIdx.y == 0) {   // what is out of range, and the rows of sequences without tokens
         for (int b = blockIdx.x; b < a.B; b += a.splits) {
             const Seq s = seq_of(a, b);
             const int32_t n = __ldg(a.seq_lens + b), q1 = __ldg(a.cu_q + b + 1);
@@ -280,68 +286,54 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_kernel(TreeArgs a) {
     tc_fence_after();
     TreeIter it = {};
     it.b = b0;
-    it.left = 0;
     if (u0 < u1) {
         it.s = seq_of(a, b0);
         const int per = it.s.nt + kPairUnits, rel = (int)(u0 - first), in = rel % per;
         it.kv = rel / per;
         it.t = max(0, in - kPairUnits);
         it.left = (int)(u1 - u0) - max(0, kPairUnits - in);
+        it.te = min(it.s.nt, it.t + it.left);
     }
     if (it.left <= 0) {   // a range without tiles
-        if (warp == 16) tc_dealloc(tmem_base, L::kCols);
+        if (warp == kMmaWarp) tc_dealloc(tmem_base, L::kCols);
         return;
     }
     const uint32_t tmem = tmem_base, sbase = smem_u32(smem);
-    if (warp == 16) {
+    if (warp == kMmaWarp) {
         // ---------------- the MMA warp: the whole warp runs the loop, one elected lane issues
         constexpr uint32_t idesc_s = idesc_f16_f32(128, N, false);
         constexpr uint32_t idesc_o = idesc_a_mn_major(idesc_f16_f32(128, N, true));
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         const bool leader = elect_one();
         // operand descriptors; a step adds its byte offset / 16 to the address field
-        const uint64_t dQ = smem_desc_sw128(sbase + L::kQ, 16, 1024);
-        const uint64_t dP = smem_desc_sw128(sbase + L::kP, kBlockT, 1024), dV = smem_desc_sw128(sbase + L::kV, kBlockT, 1024);
-        auto wait = [&](uint64_t *bar, uint32_t parity) {
-            const bool good = __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag));
-            tc_fence_after();
-            return good;
-        };
-        auto scores = [&](uint32_t j) {   // S^T(j), once K(j) (and a pair's Q) has arrived
-            const uint32_t buf = j & 1;
-            if (!wait(&k_full[buf], (j >> 1) & 1)) return false;
-            if (leader) {
+        const uint64_t dQ = smem_desc_sw128(sbase + L::kQ, 16, 1024), dP = smem_desc_sw128(sbase + L::kP, 16, 1024);
+        const uint64_t dV = smem_desc_sw128(sbase + L::kV, kBlockT, 1024);
+        bool ok = true;
+        uint32_t phase = 0, kb = 0;                  // kb: K's buffer
+        do {
+            const int t0 = it.t;
+            for (int t = t0 - 1; t < it.te; t++) {   // (t0 - 1: the pair's Q and its first K)
+                ok = __all_sync(0xffffffffu, wait_bar(ready, phase++ & 1, abort_flag));
+                tc_fence_after();
+                if (!ok) break;
+                if (leader) {
+                    if (t + 1 < it.te) {             // S^T of the next tile
 #pragma unroll
-                for (int kk = 0; kk < 8; kk++)
-                    tc_mma_bf16_tmem_a(tm + L::kColS + buf * N, tm + L::kColK + buf * 64 + kk * 8,
-                                       dQ + ((kk >> 2) * (L::kQBlock / 16) + (kk & 3) * 2), idesc_s, kk > 0);
-                tc_commit(&s_done[buf]);
-            }
-            return true;
-        };
-        bool fresh = true, ok = scores(0);
-        for (uint32_t j = 0; ok; j++) {
-            TreeIter nx = it;
-            next_tile(a, nx, r0);
-            const bool same = nx.left > 0 && nx.t > 0;      // the next tile belongs to the same pair
-            if (same) ok = scores(j + 1);
-            const uint32_t buf = j & 1;
-            ok = ok && wait(&p_full[buf], (j >> 1) & 1);
-            ok = ok && wait(&v_full[buf], (j >> 1) & 1);
-            if (!ok) break;
-            if (leader) {
-                const uint64_t v = dV + buf * (2 * kBlockT / 16), p = dP + buf * (L::kPBlocks * kBlockT / 16);
-                const uint32_t acc = fresh ? 0u : 1u;
+                        for (int kk = 0; kk < 8; kk++)
+                            tc_mma_bf16_tmem_a(tm + L::kColS, tm + L::kColK + kb * 64 + kk * 8,
+                                               dQ + ((kk >> 2) * (L::kQBlock / 16) + (kk & 3) * 2), idesc_s, kk > 0);
+                    }
+                    if (t >= t0) {
+                        const uint32_t acc = t == t0 ? 0u : 1u;
 #pragma unroll
-                for (int kk = 0; kk < 8; kk++)   // 16 tokens: 2,048 bytes of a column block, and of P
-                    tc_mma_bf16(tm, v + kk * 128, p + kk * 128, idesc_o, kk > 0 ? 1u : acc);
-                tc_commit(&pv_done[buf]);
+                        for (int kk = 0; kk < 8; kk++)   // 16 tokens: 2,048 bytes of a column block, and of P
+                            tc_mma_bf16(tm, dV + kk * 128, dP + kk * 128, idesc_o, kk > 0 ? 1u : acc);
+                    }
+                    tc_commit(done);
+                }
+                if (t + 1 < it.te) kb ^= 1u;
             }
-            it = nx;
-            fresh = !same;
-            if (it.left <= 0) break;
-            if (fresh) ok = scores(j + 1);
-        }
+        } while (ok && next_pair(a, it, r0));
         if (!ok && leader) {
             if (!*abort_flag) flag_error(a.err, kErrTimeout);
             *abort_flag = 1;
@@ -349,38 +341,38 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_kernel(TreeArgs a) {
             mbar_wait_bounded(drain, 0, kWaitLimitT, nullptr);
         }
         __syncwarp();
-    } else if (warp == 17) {
+    } else if (warp == kLoadWarp) {
         // ---------------- the load warp: lane g < 8 copies group g of each tile
-        uint32_t j = 0;
-        int32_t page = -1;
-        auto token = [&](const TreeIter &x) { return (x.s.t0 + x.t) * kTileT + 16 * lane; };
-        auto page_of = [&](const TreeIter &x) {
-            const int t = token(x);
-            return x.left > 0 && lane < 8 && t < x.s.n ? __ldg(a.block_table + (int64_t)x.b * a.max_pages + (t >> a.log2P)) : -1;
-        };
-        page = page_of(it);
-        for (; it.left > 0; j++) {
-            const uint32_t st = j % S, ph = (j / S) & 1;
-            if (j >= S && !__all_sync(0xffffffffu, wait_bar(&raw_free[st], ph ^ 1u, abort_flag))) {
-                if (lane == 0 && !*abort_flag) flag_error(a.err, kErrTimeout);
-                *abort_flag = 1;
-                break;
+        uint32_t j = 0, st = 0, ph = 0;
+        bool ok = true;
+        do {
+            const int32_t *table = a.block_table + (int64_t)it.b * a.max_pages;
+            const uint8_t *pool = a.pool + it.kv * a.slab;
+            int tok = (it.s.t0 + it.t) * kTileT + 16 * lane;
+            auto page_at = [&](int x) { return lane < 8 && x < it.s.n ? __ldg(table + (x >> a.log2P)) : -1; };
+            int32_t page = page_at(tok);
+            for (int t = it.t; t < it.te; t++, j++, tok += kTileT) {
+                const int32_t next = t + 1 < it.te ? page_at(tok + kTileT) : -1;
+                if (j >= S) ok = __all_sync(0xffffffffu, wait_bar(&raw_free[st], ph ^ 1u, abort_flag));
+                if (!ok) break;
+                const bool want = lane < 8 && tok < it.s.n, good = want && page >= 0 && page < a.num_pages;
+                if (want && !good) flag_error(a.err, kErrPage);
+                const unsigned mask = __ballot_sync(0xffffffffu, good);
+                if (lane == 0) {
+                    s_valid[st] = (int)mask;
+                    mbar_arrive_expect_tx(&raw_full[st], (uint32_t)__popc(mask) * kGroupT);
+                }
+                __syncwarp();
+                if (good)
+                    bulk_g2s(smem + L::kRaw + st * kRawT + lane * kGroupT,
+                             pool + (int64_t)page * a.Hkv * a.slab + ((tok & (a.P - 1)) >> 4) * kGroupT, kGroupT, &raw_full[st]);
+                page = next;
+                if (++st == S) st = 0, ph ^= 1u;
             }
-            const int t = token(it);
-            const bool want = lane < 8 && t < it.s.n, good = want && page >= 0 && page < a.num_pages;
-            if (want && !good) flag_error(a.err, kErrPage);
-            const unsigned mask = __ballot_sync(0xffffffffu, good);
-            if (lane == 0) {
-                s_valid[st] = (int)mask;
-                mbar_arrive_expect_tx(&raw_full[st], (uint32_t)__popc(mask) * kGroupT);
-            }
-            __syncwarp();
-            if (good)
-                bulk_g2s(smem + L::kRaw + st * kRawT + lane * kGroupT,
-                         a.pool + ((int64_t)page * a.Hkv + it.kv) * a.slab + (int64_t)((t & (a.P - 1)) >> 4) * kGroupT, kGroupT,
-                         &raw_full[st]);
-            next_tile(a, it, r0);
-            page = page_of(it);
+        } while (ok && next_pair(a, it, r0));
+        if (!ok) {
+            if (lane == 0 && !*abort_flag) flag_error(a.err, kErrTimeout);
+            *abort_flag = 1;
         }
         // no copy may still be writing when the CTA ends
         for (uint32_t i = j > S ? j - S : 0; i < j; i++)
@@ -397,113 +389,103 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_kernel(TreeArgs a) {
             }
             __syncwarp();
         };
-        const int wg = warp >> 2, row = 32 * (warp & 3) + lane;   // softmax: row quarter, token
-        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-        // expanding: group grp of the tile (its TMEM lanes are this warp's to reach), K or V
-        const int grp = 2 * (warp & 3) + (wg & 1), er = lane >> 2, eq = lane & 3;
-        const bool is_v = wg >> 1;
-        const uint32_t glanes = (uint32_t)(16 * grp) << 16;
+        const int wg = warp >> 2, quarter = warp & 3, row = 32 * quarter + lane;   // softmax: rows' half, token
+        const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+        const int er = lane >> 2, eq = lane & 3;
+        // expanding: 16-token group grp of the tile (its TMEM lanes are this warp's to reach)
+        const int grp = 2 * quarter + wg;
+        uint32_t ks = 0, ksp = 0, vs = 0, kb = 0;   // the raw stages whose K and V come next, K's parity and buffer
 
-        // The raw tile j -> K in TMEM or V in shared memory; returns the groups that it holds.
-        auto expand = [&](const TreeIter &x, uint32_t j) {
-            const uint32_t st = j % S, buf = j & 1;
-            wait(&raw_full[st], (j / S) & 1);
-            const int held = s_valid[st];
-            const bool landed = (held >> grp) & 1;
-            const int rows = landed ? x.s.n - ((x.s.t0 + x.t) * kTileT + 16 * grp) : 0;   // rows of the group that exist
-            const uint8_t *g = smem + L::kRaw + st * kRawT + grp * kGroupT;
-            if (!is_v) {
-                uint32_t f[2][16];
+        // 16 dims a word pair of 16-byte piece eq, times the scales of its two blocks
+        auto scaled = [&](const uint32_t (&w)[4], uint32_t s0, uint32_t s1, uint32_t (&f)[16]) {
 #pragma unroll
-                for (int e = 0; e < 2; e++) {
-                    const int r = er + 8 * e;
-                    const uint4 c = *reinterpret_cast<const uint4 *>(g + r * 64 + eq * 16);
-                    const uint32_t s = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(g + 1024 + r * 8 + eq * 2));
-                    const uint32_t s0 = __byte_perm(s, 0, 0x1010), s1 = __byte_perm(s, 0, 0x3232);
-                    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+            for (int m = 0; m < 4; m++) {
+                e2m1x8_to_f16x2x4(w[m], f[4 * m], f[4 * m + 1], f[4 * m + 2], f[4 * m + 3]);
 #pragma unroll
-                    for (int m = 0; m < 4; m++) {
-                        e2m1x8_to_f16x2x4(w[m], f[e][4 * m], f[e][4 * m + 1], f[e][4 * m + 2], f[e][4 * m + 3]);
-#pragma unroll
-                        for (int i = 0; i < 4; i++) f[e][4 * m + i] = hmul2(f[e][4 * m + i], m < 2 ? s0 : s1);
-                    }
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&raw_free[st]);
-                // (rows that do not exist: their scores are masked, whatever these values are)
-#pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    uint32_t v[16];
-#pragma unroll
-                    for (int k = 0; k < 4; k++) {
-                        v[4 * k] = f[0][8 * h + 2 * k];
-                        v[4 * k + 1] = f[0][8 * h + 2 * k + 1];
-                        v[4 * k + 2] = f[1][8 * h + 2 * k];
-                        v[4 * k + 3] = f[1][8 * h + 2 * k + 1];
-                    }
-                    tc_st_16x256_x4(tmem + glanes + L::kColK + 64 * buf + 32 * h, v);
-                }
-                tc_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&k_full[buf]);
-            } else {
-                if (lane == 0) mbar_arrive(&k_full[buf]);     // (a pair's Q, stored by all warps)
-                uint32_t f[2][16];
-#pragma unroll
-                for (int e = 0; e < 2; e++) {
-                    const int r = er + 8 * e;
-                    uint4 c = *reinterpret_cast<const uint4 *>(g + 1152 + r * 64 + eq * 16);
-                    uint32_t s = (uint32_t)g[2176 + (2 * eq) * 16 + r] | ((uint32_t)g[2176 + (2 * eq + 1) * 16 + r] << 8);
-                    if (r >= rows) {                          // may hold anything: zeros
-                        c = make_uint4(0, 0, 0, 0);
-                        s = 0;
-                    }
-                    s = e4m3x2_to_f16x2(s);
-                    uint32_t s0 = __byte_perm(s, 0, 0x1010), s1 = __byte_perm(s, 0, 0x3232);
-                    // lanes q >= 2 store their words 2, 3, 0, 1, so that a quarter warp meets all banks
-                    const bool sw = eq & 2;
-                    const uint32_t w[4] = {sw ? c.z : c.x, sw ? c.w : c.y, sw ? c.x : c.z, sw ? c.y : c.w};
-                    if (sw) {
-                        const uint32_t x0 = s0;
-                        s0 = s1;
-                        s1 = x0;
-                    }
-#pragma unroll
-                    for (int m = 0; m < 4; m++) {
-                        e2m1x8_to_f16x2x4(w[m], f[e][4 * m], f[e][4 * m + 1], f[e][4 * m + 2], f[e][4 * m + 3]);
-#pragma unroll
-                        for (int i = 0; i < 4; i++) f[e][4 * m + i] = hmul2(f[e][4 * m + i], m < 2 ? s0 : s1);
-                    }
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&raw_free[st]);
-                if (j >= 2) wait(&pv_done[buf], ((j >> 1) - 1) & 1);
-                uint8_t *blk = smem + L::kV + (2 * buf + (eq >> 1)) * kBlockT;
-#pragma unroll
-                for (int e = 0; e < 2; e++) {
-                    const int tr = 16 * grp + er + 8 * e;
-#pragma unroll
-                    for (int m = 0; m < 4; m++)
-                        *reinterpret_cast<uint4 *>(blk + sw128_off(tr, (eq & 1) * 4 + (m ^ (eq & 2)))) =
-                            make_uint4(f[e][4 * m], f[e][4 * m + 1], f[e][4 * m + 2], f[e][4 * m + 3]);
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&v_full[buf]);
+                for (int i = 0; i < 4; i++) f[4 * m + i] = hmul2(f[4 * m + i], m < 2 ? s0 : s1);
             }
+        };
+        // K of the next raw tile to TMEM; returns the groups that the tile holds.  (Rows that do
+        // not exist: their scores are masked.)
+        auto expand_k = [&]() {
+            wait(&raw_full[ks], ksp);
+            const int held = s_valid[ks];
+            const uint8_t *g = smem + L::kRaw + ks * kRawT + grp * kGroupT;
+            uint32_t f[2][16];
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                const int r = er + 8 * e;
+                const uint4 c = *reinterpret_cast<const uint4 *>(g + r * 64 + eq * 16);
+                const uint32_t s = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(g + 1024 + r * 8 + eq * 2));
+                const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+                scaled(w, __byte_perm(s, 0, 0x1010), __byte_perm(s, 0, 0x3232), f[e]);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const uint32_t v[16] = {f[0][8 * h], f[0][8 * h + 1], f[1][8 * h], f[1][8 * h + 1],
+                                        f[0][8 * h + 2], f[0][8 * h + 3], f[1][8 * h + 2], f[1][8 * h + 3],
+                                        f[0][8 * h + 4], f[0][8 * h + 5], f[1][8 * h + 4], f[1][8 * h + 5],
+                                        f[0][8 * h + 6], f[0][8 * h + 7], f[1][8 * h + 6], f[1][8 * h + 7]};
+                tc_st_16x256_x4(tmem + ((uint32_t)(16 * grp) << 16) + L::kColK + 64 * kb + 32 * h, v);
+            }
+            kb ^= 1u;
+            if (++ks == S) ks = 0, ksp ^= 1u;
             return held;
+        };
+        // V of the tile whose K was the last but one (or last) to shared memory; rows: those of the group that exist.
+        auto expand_v = [&](int rows) {
+            const uint8_t *g = smem + L::kRaw + vs * kRawT + grp * kGroupT + 1152;
+            uint8_t *blk = smem + L::kV + (eq >> 1) * kBlockT;
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                const int r = er + 8 * e;
+                uint4 c = *reinterpret_cast<const uint4 *>(g + r * 64 + eq * 16);
+                uint32_t s = (uint32_t)g[1024 + (2 * eq) * 16 + r] | ((uint32_t)g[1024 + (2 * eq + 1) * 16 + r] << 8);
+                if (r >= rows) {                          // may hold anything: zeros
+                    c = make_uint4(0, 0, 0, 0);
+                    s = 0;
+                }
+                // lanes q >= 2 store their words 2, 3, 0, 1, so that a quarter warp meets all banks
+                const bool sw = eq & 2;
+                s = e4m3x2_to_f16x2(s);
+                const uint32_t w[4] = {sw ? c.z : c.x, sw ? c.w : c.y, sw ? c.x : c.z, sw ? c.y : c.w};
+                uint32_t f[16];
+                scaled(w, __byte_perm(s, 0, sw ? 0x3232 : 0x1010), __byte_perm(s, 0, sw ? 0x1010 : 0x3232), f);
+                const int tr = 16 * grp + r;
+#pragma unroll
+                for (int m = 0; m < 4; m++)
+                    *reinterpret_cast<uint4 *>(blk + sw128_off(tr, (eq & 1) * 4 + (m ^ (eq & 2)))) =
+                        make_uint4(f[4 * m], f[4 * m + 1], f[4 * m + 2], f[4 * m + 3]);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&raw_free[vs]);
+            if (++vs == S) vs = 0;
+        };
+        // What this warp has put into TMEM and shared memory is the MMA warp's.
+        auto hand_over = [&]() {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ready);
         };
         // A pair's Q, the rows' factors and the tree.  (The previous pair's products and its
         // epilogue are done.)
         auto load_pair = [&](const TreeIter &x) {
             const int rows = x.s.d * a.G;
-#pragma unroll 2
-            for (int k = 0; k < N / 16; k++) {
-                const int c = warp + 16 * k, r = r0 + c;
-                const int i = r / a.G, h = x.kv * a.G + (r - i * a.G);
-                uint2 w = make_uint2(0, 0);
-                if (r < rows) w = __ldg(reinterpret_cast<const uint2 *>(a.q + ((int64_t)(x.s.q0 + i) * a.Hq + h) * kHeadDim) + lane);
+            uint2 qw[N / 8];
+            int at[N / 8];                      // a row of q, -1: none
+#pragma unroll
+            for (int k = 0; k < N / 8; k++) {
+                const int r = r0 + warp + 8 * k, i = r / a.G;
+                at[k] = r < rows ? (x.s.q0 + i) * a.Hq + x.kv * a.G + (r - i * a.G) : -1;
+                qw[k] = make_uint2(0, 0);
+                if (r < rows) qw[k] = __ldg(reinterpret_cast<const uint2 *>(a.q + (int64_t)at[k] * kHeadDim) + lane);
+            }
+#pragma unroll
+            for (int k = 0; k < N / 8; k++) {
+                const int c = warp + 8 * k;
+                const uint2 w = qw[k];
                 uint32_t m = max_u16x2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu);
                 m = __reduce_max_sync(0xffffffffu, max(m >> 16, m & 0xffffu));
                 // 2^kq puts the row's largest value into [2^14, 2^15)
@@ -515,12 +497,15 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_kernel(TreeArgs a) {
                     make_uint2(f32x2_to_f16x2(bf16_hi(w.x) * sc, bf16_lo(w.x) * sc),
                                f32x2_to_f16x2(bf16_hi(w.y) * sc, bf16_lo(w.y) * sc));
                 if (lane == 0) {
-                    s_fac[c] = (OPT && a.cap_log2 > 0.f ? a.cap_in : a.score_log2) * __uint_as_float((uint32_t)(127 - kq) << 23);
+                    const float fac = (OPT && a.cap_log2 > 0.f ? a.cap_in : a.score_log2) * __uint_as_float((uint32_t)(127 - kq) << 23);
+                    // (a positive factor stays one, so that minus infinity times it is minus infinity: no score
+                    // reaches 2^34, and 2^-92 is none)
+                    s_fac[c] = OPT ? fac : fmaxf(fac, 0x1p-126f);
                     s_m[c] = kNegInfT;
                     s_off[c] = kNoMaxT;
-                    s_row[c] = r < rows ? (x.s.q0 + i) * a.Hq + h : -1;
-                    s_draft[c] = min(i, 63);
-                    if (OPT) s_slope[c] = a.slopes && r < rows ? __ldg(a.slopes + h) * 1.4426950408889634f : 0.f;
+                    s_row[c] = at[k];
+                    s_draft[c] = min((r0 + c) / a.G, 63);
+                    if (OPT) s_slope[c] = a.slopes && at[k] >= 0 ? __ldg(a.slopes + at[k] % a.Hq) * 1.4426950408889634f : 0.f;
                 }
             }
             if (tid < 64) {
@@ -530,209 +515,199 @@ __global__ void __launch_bounds__(kThreadsT, 1) tree_kernel(TreeArgs a) {
                 s_mask[tid] = mk;
                 s_depth[tid] = __popcll(mk) - 1;
             }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // Q for the tensor core
             workers_sync();
             if (OPT) {
                 if (tid < N) s_dep[tid] = (float)s_depth[s_draft[tid]];
                 workers_sync();
             }
         };
-
-        bool fresh = true;                      // the range's first tile of its pair
-        int t_begin = it.t;
-        float l[CW];
-        load_pair(it);
-        int held = 0, held_next = expand(it, 0);
-        for (uint32_t j = 0; it.left > 0; j++) {
-            const uint32_t buf = j & 1;
-            if (fresh) {
-                if (j > 0) {
-                    load_pair(it);
-                    held_next = expand(it, j);
-                }
-#pragma unroll
-                for (int c = 0; c < CW; c++) l[c] = 0.f;
+        // Which of the warpgroup's rows do not see the thread's token (bit c: row c).
+        auto unseen = [&](const Seq &s, int tok, int held) {
+            const int rel = tok - s.base, jj = rel < 0 ? 0 : min(rel, 63), key = rel < 0 ? rel : s_depth[jj];
+            const bool there = tok < s.n && ((held >> (row >> 4)) & 1);
+            uint32_t gone = 0;
+#pragma unroll 1
+            for (int c = 0; c < CW; c++) {
+                const int i = s_draft[wg * CW + c];
+                const bool sees = there && (rel < 0 || (s_mask[i] >> jj) & 1) && (a.window <= 0 || key > s_depth[i] - a.window);
+                gone |= sees ? 0u : 1u << c;
             }
-            TreeIter nx = it;
-            next_tile(a, nx, r0);
-            const bool same = nx.left > 0 && nx.t > 0;
-            // (K's buffer of tile j + 1 is free: the scores of tile j - 1 were seen)
-            held = held_next;
-            if (same) held_next = expand(nx, j + 1);
+            return gone;
+        };
 
-            // ---- softmax of the token's scores for the warpgroup's rows
-            const int tok0 = (it.s.t0 + it.t) * kTileT, tok = tok0 + row;
-            // edge: a token of the tile that some row does not see
-            const bool edge = tok0 + kTileT > it.s.base || (a.window > 0 && tok0 <= it.s.n - 1 - a.window) ||
-                              held != 0xff;
-            uint32_t gone = 0;                  // bit c: row c of the warpgroup does not see the token
-            const int rel = tok - it.s.base;
-            int key = rel;                      // the token's position, from base on
-            if (edge || OPT) {
-                const int jj = rel < 0 ? 0 : min(rel, 63);
-                if (rel >= 0) key = s_depth[jj];
+        uint32_t phase = 0;
+        do {
+            load_pair(it);
+            float l[CW];
+#pragma unroll
+            for (int c = 0; c < CW; c++) l[c] = 0.f;
+            int held = 0, held_next = expand_k();   // the groups that a raw tile holds
+            hand_over();
+            int tok0 = (it.s.t0 + it.t) * kTileT;
+            for (int t = it.t; t < it.te; t++, tok0 += kTileT) {
+                // The products handed over last run while K of the next tile is unpacked.
+                held = held_next;
+                if (t + 1 < it.te) held_next = expand_k();
+                // This tile's scores are there, O^T holds the tiles before: V and P may be written.
+                wait(done, phase++ & 1);
+                tc_fence_after();
+                expand_v((held >> grp) & 1 ? it.s.n - (tok0 + 16 * grp) : 0);
+
+                // ---- softmax of the token's scores for the warpgroup's rows
+                const int tok = tok0 + row;
+                // edge: a token of the tile that some row does not see
+                const bool edge = tok0 + kTileT > it.s.base || (a.window > 0 && tok0 <= it.s.n - 1 - a.window) || held != 0xff;
+                const uint32_t tS = tmem + lanes + L::kColS + wg * CW, tO = tmem + lanes + wg * CW;
+                uint32_t gone = 0;
                 if (edge) {
-                    const bool there = tok < it.s.n && ((held >> (row >> 4)) & 1);
-#pragma unroll 4
-                    for (int c = 0; c < CW; c++) {
-                        const int i = s_draft[wg * CW + c];
-                        const bool sees = there && (rel < 0 || (s_mask[i] >> jj) & 1) &&
-                                          (a.window <= 0 || key > s_depth[i] - a.window);
-                        gone |= sees ? 0u : 1u << c;
-                    }
-                }
-            }
-            wait(&s_done[buf], (j >> 1) & 1);
-            tc_fence_after();
-            // d = z - m + 7 in base 2
-            float d[CW];
-            auto score = [&](uint32_t s, int c) {    // z (OPT), without the row's offset
-                float z = __uint_as_float(s) * s_fac[wg * CW + c];
-                if (OPT) {
-                    if (a.cap_log2 > 0.f) {          // cap tanh(x) = cap - 2 cap / (1 + e^(2 x))
-                        const float e = ex2(z) + 1.0f;
-                        z = fmaf(-2.0f * a.cap_log2, rcp_approx(e), a.cap_log2);
-                    }
-                    z = fmaf(s_slope[wg * CW + c], (float)key - s_dep[wg * CW + c], z);
-                }
-                return z;
-            };
-            auto load_scores = [&]() {
-                uint32_t sr[CW];
-                load_columns<CW>(tmem + lanes + L::kColS + buf * N + wg * CW, sr);
-                tc_wait_ld();
-                const float4 *fac = reinterpret_cast<const float4 *>(s_fac + wg * CW);
-                const float4 *off = reinterpret_cast<const float4 *>(s_off + wg * CW);
+                    gone = unseen(it.s, tok, held);
+                    if (!OPT) {                     // scores of what is not seen: minus infinity
+#pragma unroll 1
+                        for (int c0 = 0; c0 < CW; c0 += 8) {
+                            uint32_t x[8];
+                            tc_ld8(tS + c0, x);
+                            tc_wait_ld();
 #pragma unroll
-                for (int x = 0; x < CW / 4; x++) {
-                    const float4 o = off[x];
+                            for (int c = 0; c < 8; c++)
+                                if ((gone >> (c0 + c)) & 1) x[c] = 0xff800000u;
+                            tc_st8(tS + c0, x);
+                        }
+                        tc_wait_st();
+                    }
+                }
+                const int rel = tok - it.s.base;
+                const float key = OPT ? (float)(rel < 0 ? rel : s_depth[min(rel, 63)]) : 0.f;   // the token's position, from base on
+                auto score = [&](uint32_t x, int c) {        // z in base 2
+                    float z = __uint_as_float(x) * s_fac[wg * CW + c];
                     if (OPT) {
-                        d[4 * x] = score(sr[4 * x], 4 * x) + o.x;
-                        d[4 * x + 1] = score(sr[4 * x + 1], 4 * x + 1) + o.y;
-                        d[4 * x + 2] = score(sr[4 * x + 2], 4 * x + 2) + o.z;
-                        d[4 * x + 3] = score(sr[4 * x + 3], 4 * x + 3) + o.w;
-                    } else {
-                        const float4 f = fac[x];
-                        d[4 * x] = fmaf(__uint_as_float(sr[4 * x]), f.x, o.x);
-                        d[4 * x + 1] = fmaf(__uint_as_float(sr[4 * x + 1]), f.y, o.y);
-                        d[4 * x + 2] = fmaf(__uint_as_float(sr[4 * x + 2]), f.z, o.z);
-                        d[4 * x + 3] = fmaf(__uint_as_float(sr[4 * x + 3]), f.w, o.w);
+                        if (a.cap_log2 > 0.f) {              // cap tanh(x) = cap - 2 cap / (1 + e^(2 x))
+                            const float e = ex2(z) + 1.0f;
+                            z = fmaf(-2.0f * a.cap_log2, rcp_approx(e), a.cap_log2);
+                        }
+                        z = fmaf(s_slope[wg * CW + c], key - s_dep[wg * CW + c], z);
+                        if ((gone >> c) & 1) z = kNegInfT;
                     }
-                }
-                if (edge) {
-#pragma unroll
-                    for (int c = 0; c < CW; c++)
-                        if ((gone >> c) & 1) d[c] = kNegInfT;
-                }
-            };
-            load_scores();
-            float top = d[0];
-#pragma unroll
-            for (int c = 1; c < CW; c++) top = fmaxf(top, d[c]);
-            if (group_any(wg, top > kRescaleT + kPOffsetT)) {
-                float *wmax = reinterpret_cast<float *>(smem + L::kWarpMax) + wg * 4 * CW;
-                int mine = 0;
-                uint32_t sr[CW];
-                load_columns<CW>(tmem + lanes + L::kColS + buf * N + wg * CW, sr);
-                tc_wait_ld();
-#pragma unroll
-                for (int c = 0; c < CW; c++) {
-                    const float z = (gone >> c) & 1 ? kNegInfT : score(sr[c], c);
-                    const int mx = __reduce_max_sync(0xffffffffu, ordered(z));
-                    if (lane == c) mine = mx;
-                }
-                if (lane < CW) wmax[(warp & 3) * CW + lane] = unordered(mine);
-                group_sync(wg);
-                if ((warp & 3) == 0 && lane < CW) {
-                    const float mx = fmaxf(fmaxf(wmax[lane], wmax[CW + lane]), fmaxf(wmax[2 * CW + lane], wmax[3 * CW + lane]));
-                    const float mo = s_m[wg * CW + lane], mn = fmaxf(mo, mx);
-                    s_alpha[wg * CW + lane] = mo == kNegInfT ? 0.f : ex2(mo - mn);
-                    s_m[wg * CW + lane] = mn;
-                    s_off[wg * CW + lane] = mn == kNegInfT ? kNoMaxT : kPOffsetT - mn;
-                }
-                group_sync(wg);
-#pragma unroll
-                for (int c = 0; c < CW; c++) l[c] *= s_alpha[wg * CW + c];
-                if (!fresh) {   // O^T holds the earlier tiles: rescale the warpgroup's rows
-                    wait(&pv_done[buf ^ 1], ((j - 1) >> 1) & 1);
-                    tc_fence_after();
-                    uint32_t ov[CW];
-                    load_columns<CW>(tmem + lanes + wg * CW, ov);
+                    return z;
+                };
+                // d = z - m + 7
+                float d[CW];
+                auto load_scores = [&]() {
+                    uint32_t x[CW];
+                    load_columns<CW>(tS, x);
+                    const float4 *fac = reinterpret_cast<const float4 *>(s_fac + wg * CW);
+                    const float4 *off = reinterpret_cast<const float4 *>(s_off + wg * CW);
                     tc_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < CW; c++) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * s_alpha[wg * CW + c]);
-                    if constexpr (CW == 32) tc_st32(tmem + lanes + wg * CW, ov);
-                    else tc_st(tmem + lanes + wg * CW, ov);
-                    tc_wait_st();
-                }
+                    for (int i = 0; i < CW; i += 4) {
+                        const float4 o = off[i / 4], f = OPT ? make_float4(0.f, 0.f, 0.f, 0.f) : fac[i / 4];
+                        d[i] = OPT ? score(x[i], i) + o.x : fmaf(__uint_as_float(x[i]), f.x, o.x);
+                        d[i + 1] = OPT ? score(x[i + 1], i + 1) + o.y : fmaf(__uint_as_float(x[i + 1]), f.y, o.y);
+                        d[i + 2] = OPT ? score(x[i + 2], i + 2) + o.z : fmaf(__uint_as_float(x[i + 2]), f.z, o.z);
+                        d[i + 3] = OPT ? score(x[i + 3], i + 3) + o.w : fmaf(__uint_as_float(x[i + 3]), f.w, o.w);
+                    }
+                };
                 load_scores();
-            }
-            if (j >= 2) wait(&pv_done[buf], ((j >> 1) - 1) & 1);     // P's buffer is free
-            uint8_t *pt = smem + L::kP + (buf * L::kPBlocks + (wg * CW) / 64) * kBlockT;
+                float top = fmaxf(d[0], d[1]), top2 = fmaxf(d[2], d[3]);
 #pragma unroll
-            for (int c0 = 0; c0 < CW; c0 += CW < 8 ? CW : 8) {
-                uint32_t pw[4];
-#pragma unroll
-                for (int e = 0; e < (CW < 8 ? CW : 8) / 2; e++) {
-                    pw[e] = f32x2_to_f16x2(ex2(d[c0 + 2 * e + 1]), ex2(d[c0 + 2 * e]));
-                    add_f16x2(l[c0 + 2 * e], l[c0 + 2 * e + 1], pw[e]);
+                for (int c = 4; c < CW; c += 4) {
+                    top = max3(top, d[c], d[c + 1]);
+                    top2 = max3(top2, d[c + 2], d[c + 3]);
                 }
-                if (CW == 4)   // eight bytes a thread: two warpgroups share a 16-byte chunk
-                    *reinterpret_cast<uint2 *>(pt + sw128_off(row, wg >> 1) + (wg & 1) * 8) = make_uint2(pw[0], pw[1]);
-                else
-                    *reinterpret_cast<uint4 *>(pt + sw128_off(row, ((wg * CW + c0) & 63) / 8)) =
-                        make_uint4(pw[0], pw[1], pw[2], pw[3]);
+                if (group_any(wg, fmaxf(top, top2) > kRescaleT + kPOffsetT)) {
+                    float *wmax = reinterpret_cast<float *>(smem + L::kWarpMax) + wg * 4 * CW;
+                    int mine = 0;
+#pragma unroll 1
+                    for (int c0 = 0; c0 < CW; c0 += 8) {
+                        uint32_t x[8];
+                        tc_ld8(tS + c0, x);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 8; c++) {
+                            const int mx = __reduce_max_sync(0xffffffffu, ordered(score(x[c], c0 + c)));
+                            if (lane == c0 + c) mine = mx;
+                        }
+                    }
+                    if (lane < CW) wmax[quarter * CW + lane] = unordered(mine);
+                    group_sync(wg);
+                    if (quarter == 0 && lane < CW) {
+                        const float mx = fmaxf(fmaxf(wmax[lane], wmax[CW + lane]), fmaxf(wmax[2 * CW + lane], wmax[3 * CW + lane]));
+                        const float mo = s_m[wg * CW + lane], mn = fmaxf(mo, mx);
+                        s_alpha[wg * CW + lane] = mo == kNegInfT ? 0.f : ex2(mo - mn);
+                        s_m[wg * CW + lane] = mn;
+                        s_off[wg * CW + lane] = mn == kNegInfT ? kNoMaxT : kPOffsetT - mn;
+                    }
+                    group_sync(wg);
+#pragma unroll
+                    for (int c = 0; c < CW; c++) l[c] *= s_alpha[wg * CW + c];
+                    if (t > it.t) {                 // O^T holds the earlier tiles: rescale the warpgroup's rows
+#pragma unroll 1
+                        for (int c0 = 0; c0 < CW; c0 += 8) {
+                            uint32_t x[8];
+                            tc_ld8(tO + c0, x);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int c = 0; c < 8; c++)
+                                x[c] = __float_as_uint(__uint_as_float(x[c]) * s_alpha[wg * CW + c0 + c]);
+                            tc_st8(tO + c0, x);
+                        }
+                        tc_wait_st();
+                    }
+                    load_scores();
+                }
+                uint8_t *pt = smem + L::kP;
+#pragma unroll
+                for (int c0 = 0; c0 < CW; c0 += 8) {
+                    uint32_t pw[4];
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        pw[e] = f32x2_to_f16x2(ex2(d[c0 + 2 * e + 1]), ex2(d[c0 + 2 * e]));
+                        add_f16x2(l[c0 + 2 * e], l[c0 + 2 * e + 1], pw[e]);
+                    }
+                    *reinterpret_cast<uint4 *>(pt + sw128_off(row, (wg * CW + c0) / 8)) = make_uint4(pw[0], pw[1], pw[2], pw[3]);
+                }
+                hand_over();
             }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[buf]);
 
             // ---- the pair's last tile of this range: normalise, or leave the partial
-            const TreeIter cur = it;
-            it = nx;
-            fresh = !same;
-            if (!fresh) continue;
-            wait(&pv_done[buf], (j >> 1) & 1);
+            wait(done, phase++ & 1);
             tc_fence_after();
-            {
-                float *wsum = reinterpret_cast<float *>(smem + L::kWarpMax) + wg * 4 * CW;
-                const float s = column_sums<CW>(l, lane);
-                if (lane < CW) wsum[(warp & 3) * CW + lane] = s;
-                group_sync(wg);
-                const bool whole = t_begin == 0 && cur.t == cur.s.nt - 1;
-                const int64_t slot = (int64_t)blockIdx.y * ((int64_t)a.splits + (int64_t)a.B * a.Hkv) + blockIdx.x +
-                                     (int64_t)cur.b * a.Hkv + cur.kv;
-                auto sum = [&](int c) { return (wsum[c] + wsum[CW + c]) + (wsum[2 * CW + c] + wsum[3 * CW + c]); };
-                if (!whole && (warp & 3) == 0 && lane < CW) {
-                    const float m = s_m[wg * CW + lane];
-                    a.part_ml[slot * N + wg * CW + lane] = make_float2(m == kNegInfT ? m : m - kPOffsetT, sum(lane));
-                }
-                uint32_t ov[CW];
-                load_columns<CW>(tmem + lanes + wg * CW, ov);
-                tc_wait_ld();
-                if (whole) {
-#pragma unroll
-                    for (int c = 0; c < CW; c++) {
-                        const int at = s_row[wg * CW + c];
-                        const float t = sum(c), inv = t == 0.f ? 0.f : a.gv / t;   // (a row that sees nothing: zeros)
-                        if (at >= 0) a.out[(int64_t)at * kHeadDim + row] = __float2bfloat16_rn(__uint_as_float(ov[c]) * inv);
-                    }
-                } else {
-                    float *dst = a.part_acc + (slot * N + wg * CW) * kHeadDim + row;
-#pragma unroll
-                    for (int c = 0; c < CW; c++)
-                        if (s_row[wg * CW + c] >= 0) dst[c * kHeadDim] = __uint_as_float(ov[c]);
-                }
-                tc_fence_before();
-                workers_sync();   // sums, maxima and rows are read: the next pair may write them
+            float *wsum = reinterpret_cast<float *>(smem + L::kWarpMax) + wg * 4 * CW;
+            const float s = column_sums<CW>(l, lane);
+            if (lane < CW) wsum[quarter * CW + lane] = s;
+            group_sync(wg);
+            const bool whole = it.t == 0 && it.te == it.s.nt;
+            const int64_t slot = (int64_t)blockIdx.y * ((int64_t)a.splits + (int64_t)a.B * a.Hkv) + blockIdx.x +
+                                 (int64_t)it.b * a.Hkv + it.kv;
+            if (quarter == 0 && lane < CW) {
+                const float m = s_m[wg * CW + lane];
+                const float t = (wsum[lane] + wsum[CW + lane]) + (wsum[2 * CW + lane] + wsum[3 * CW + lane]);
+                if (!whole) a.part_ml[slot * N + wg * CW + lane] = make_float2(m == kNegInfT ? m : m - kPOffsetT, t);
+                s_alpha[wg * CW + lane] = t == 0.f ? 0.f : a.gv / t;      // (a row that sees nothing: zeros)
             }
-            t_begin = it.t;
-        }
+            group_sync(wg);
+            float *dst = a.part_acc + (slot * N + wg * CW) * kHeadDim + row;
+#pragma unroll 1
+            for (int c0 = 0; c0 < CW; c0 += 8) {
+                uint32_t x[8];
+                tc_ld8(tmem + lanes + wg * CW + c0, x);
+                tc_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 8; c++) {
+                    const int at = s_row[wg * CW + c0 + c];
+                    if (at < 0) continue;
+                    if (whole)
+                        a.out[(int64_t)at * kHeadDim + row] = __float2bfloat16_rn(__uint_as_float(x[c]) * s_alpha[wg * CW + c0 + c]);
+                    else
+                        dst[(c0 + c) * kHeadDim] = __uint_as_float(x[c]);
+                }
+            }
+            tc_fence_before();
+            workers_sync();   // sums, maxima and rows are read: the next pair may write them
+        } while (next_pair(a, it, r0));
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 16) tc_dealloc(tmem, L::kCols);
+    if (warp == kMmaWarp) tc_dealloc(tmem, L::kCols);
 }
 
 // Joins the partials of the pairs that several CTAs covered: one warp per row, a float4 a lane.
@@ -828,13 +803,13 @@ TreeFns fns_of() {
 }
 
 // Rows of a CTA's tile.
-int tile_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+int tile_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
-TreeFns tree_fns(int n) { return n == 16 ? fns_of<16>() : n == 32 ? fns_of<32>() : n == 64 ? fns_of<64>() : fns_of<128>(); }
+TreeFns tree_fns(int n) { return n == 16 ? fns_of<16>() : n == 32 ? fns_of<32>() : fns_of<64>(); }
 
 constexpr int kMaxDevicesT = 64;
 std::mutex g_mu_t;
-bool g_attr_t[kMaxDevicesT][4][2];
+bool g_attr_t[kMaxDevicesT][3][2];
 int g_sms_t[kMaxDevicesT];
 
 size_t align256t(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -854,7 +829,7 @@ int tree_auto_splits(int64_t rows, cudaError_t *status) {
     if (status) *status = e;
     if (e != cudaSuccess) return 0;
     const int64_t n = tile_rows(rows), tiles = (rows + n - 1) / n;
-    return sms / tiles > 0 ? (int)(sms / tiles) : 1;
+    return kCtasT * sms / tiles > 0 ? (int)(kCtasT * sms / tiles) : 1;
 }
 
 // Workspace: (m, l) partials | their O, one per row tile and (CTA of it, pair) that can meet
@@ -909,10 +884,10 @@ cudaError_t launch_tree(const nvfp4kv_cache &c, const void *q, const int32_t *cu
     const int64_t most = (int64_t)batch * a.Hkv * ((a.cap + kTileT - 1) / kTileT);
     a.splits = splits > most ? (int)most : splits;
     const TreeFns f = tree_fns(n);
-    const bool opt = softcap > 0.f || slopes;
+    const bool opt = softcap > 0.f || slopes || !(a.score_log2 > 0.f);
     {
         std::lock_guard<std::mutex> lock(g_mu_t);
-        bool &set = g_attr_t[dev][n == 16 ? 0 : n == 32 ? 1 : n == 64 ? 2 : 3][opt];
+        bool &set = g_attr_t[dev][n == 16 ? 0 : n == 32 ? 1 : 2][opt];
         if (!set) {
             e = cudaFuncSetAttribute(f.tree[opt], cudaFuncAttributeMaxDynamicSharedMemorySize, f.smem);
             if (e != cudaSuccess) return e;
