@@ -8,9 +8,11 @@
 // touched before it is quantised (quantize.cuh: the rounding of the exact quotients).
 //
 // Bound by bandwidth: a token reads (Hq + 2 Hkv) 256 bytes and writes Hq 256 + Hkv 144.
-// Eight threads hold a row, 16 values each (one block of the format); the partner of a
-// half-split pair comes by shuffle.  A thread takes up to kRows rows of one token, all
-// loaded first, so that the token's table row, 128 bytes a thread, is read once for them.
+// Eight threads hold a row, 16 values each: eight of the first rotated half and their eight
+// partners (or, for adjacent pairs and behind the rotated values, one block of the format), so
+// a thread needs eight cosines and sines.  Each warp takes rows of one kind of one token --
+// 4 J rows of Q, 4 of K, 4 or 8 of V -- and loads them all first.  Q's weights are multiplied into
+// the cosines and sines once a warp, and its rows go through packed FP32 operations.
 //
 // K's rounding to BF16 decides the codes: a value on the other side of a BF16 border may
 // move a block's scale.  So K is formed from two floats: products and sums with their
@@ -43,7 +45,6 @@ struct RopeArgs {
     const int64_t *slots;
     float gk, gv;
     int dtype;
-    int chunks;                                      // thread groups a token
     unsigned *err;
 };
 
@@ -67,12 +68,6 @@ __device__ __forceinline__ uint32_t bf16_of_pair(float hi, float lo) {
     return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(b)));
 }
 
-__device__ __forceinline__ float bf16_at(const uint32_t (&w)[8], int i) { return (i & 1) ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]); }
-
-__device__ __forceinline__ void unpack8(const uint4 &a, const uint4 &b, uint32_t (&w)[8]) {
-    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-}
-
 // 1 / sqrt(ssq / 128 + eps) as two floats: the hardware's estimate and one Newton step
 // whose residual 1 - m r^2 is formed exactly up to 2^-44.
 __device__ __forceinline__ Pair root(Pair ssq, float eps) {
@@ -84,173 +79,233 @@ __device__ __forceinline__ Pair root(Pair ssq, float eps) {
     return {r, 0.5f * r * e};
 }
 
-// One row's block: x (this thread's 16 values), xp (the partner block's, half-split) and
-// the weights -> 16 BF16 numbers.  c, s: the block's cosines and sines (adjacent pairs: 8
-// of each, half-split: 16, the sines negated for the first half).  EXACT: see above.
-template <bool EXACT>
-__device__ __forceinline__ void turn_block(const RopeArgs &a, const uint32_t (&x)[8], const uint4 *weight, int blk, int pblk,
-                                           unsigned group, int src, bool turned, const float (&c)[16], const float (&s)[16],
-                                           uint32_t (&out)[8]) {
-    uint32_t xp[8], w[8], wp[8];
-    const bool half = !a.adjacent;
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    return (uint64_t)__float_as_uint(lo) | ((uint64_t)__float_as_uint(hi) << 32);
+}
+__device__ __forceinline__ float low2(uint64_t x) { return __uint_as_float((uint32_t)x); }
+__device__ __forceinline__ float high2(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
+__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t bf16_pair(uint32_t w) { return pack2(bf16_lo(w), bf16_hi(w)); }
+
+__device__ __forceinline__ void words(const uint4 &x, uint32_t (&w)[4]) { w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w; }
+
+constexpr int kWarpsR = kThreadsR / 32;
+
+// JQ: passes of four rows a warp makes over Q (and JQ > 1: two over V).
+template <int JQ, bool kUnitScale>
+__global__ void __launch_bounds__(kThreadsR, 2) rope_append_kernel(RopeArgs a) {
+    pdl_wait();
+    pdl_launch_dependents();
+    constexpr int JV = JQ > 1 ? 2 : 1;
+    const int64_t id = (int64_t)blockIdx.x * kWarpsR + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, blk = lane & 7, g = lane >> 3;
+    const int nq = (a.Hq + 4 * JQ - 1) / (4 * JQ), nk = (a.Hkv + 3) / 4, nv = (a.Hkv + 4 * JV - 1) / (4 * JV);
+    const int64_t t = id / (nq + nk + nv);
+    const int sub = (int)(id - t * (nq + nk + nv));
+    if (t >= a.num_tokens) return;                            // (the whole warp)
+    const bool is_q = sub < nq, is_k = !is_q && sub < nq + nk;
+    // The thread's two chunks of eight values: ca in the first rotated half and its partner cb, or a block's
+    // (2 blk, 2 blk + 1).
+    const int half8 = a.rot >> 4;                             // chunks of half the rotated values (even)
+    const bool turned = is_q || is_k ? (a.adjacent ? 2 * blk < 2 * half8 : blk < half8) : false;
+    const bool split = turned && !a.adjacent;
+    const int ca = split ? blk : 2 * blk, cb = split ? blk + half8 : 2 * blk + 1;
+    // ---- the rows
+    constexpr int JM = JQ > JV ? JQ : JV;
+    const int row0 = is_q ? sub * 4 * JQ : is_k ? (sub - nq) * 4 : (sub - nq - nk) * 4 * JV;
+    const int nrows = is_q ? a.Hq : a.Hkv, passes = is_q ? JQ : is_k ? 1 : JV;
+    const uint4 *base = is_q ? a.q + t * a.q_stride16 : (is_k ? a.k : a.v) + t * a.kv_stride16;
+    uint4 xa[JM], xb[JM];
 #pragma unroll
-    for (int i = 0; i < 8; i++) xp[i] = x[i];
-    if (half && a.rot) {
-#pragma unroll
-        for (int i = 0; i < 8; i++) xp[i] = __shfl_sync(group, x[i], src);
+    for (int j = 0; j < JM; j++) {
+        const int row = row0 + 4 * j + g;
+        xa[j] = xb[j] = make_uint4(0, 0, 0, 0);
+        if (j < passes && row < nrows) {
+            xa[j] = __ldg(base + row * 16 + ca);
+            xb[j] = __ldg(base + row * 16 + cb);
+        }
     }
+    const int64_t slot = is_q ? 0 : __ldg(a.slots + t);
+    // ---- the positions (all of the token's: any warp skips it), and the pairs' row of the table
+    bool ok = true;
+    if (a.rot > 0) {
+        const int axes = a.sec1 >= kHeadDim ? 1 : a.sec2 >= kHeadDim ? 2 : 3;
+        for (int x = 0; x < axes; x++) {
+            const int32_t pos = __ldg(a.positions + x * a.num_tokens + t);
+            ok = ok && pos >= 0 && pos < a.num_positions;
+        }
+    }
+    if (sub == 0 && lane == 0) {
+        const int64_t s0 = __ldg(a.slots + t);
+        if (!ok) flag_error(a.err, kErrPosition);
+        if (s0 >= a.num_slots) flag_error(a.err, kErrSlot);
+    }
+    if (!ok) return;
+    float c[8], s[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) c[i] = 1.f, s[i] = 0.f;
+    if (turned) {
+#pragma unroll
+        for (int i = 0; i < 2; i++) {                         // (four pairs lie in one section)
+            const int pair = 8 * blk + 4 * i, axis = pair < a.sec1 ? 0 : pair < a.sec2 ? 1 : 2;
+            const int32_t pos = __ldg(a.positions + axis * a.num_tokens + t);
+            const float4 *at = reinterpret_cast<const float4 *>(a.table + (int64_t)pos * a.rot + pair);
+            const float4 x = __ldg(at), y = __ldg(at + (a.rot >> 3));
+            c[4 * i] = x.x, c[4 * i + 1] = x.y, c[4 * i + 2] = x.z, c[4 * i + 3] = x.w;
+            s[4 * i] = y.x, s[4 * i + 1] = y.y, s[4 * i + 2] = y.z, s[4 * i + 3] = y.w;
+        }
+    }
+    const uint4 *weight = is_q ? a.wq : is_k ? a.wk : nullptr;
+    uint32_t wa[4], wb[4];
+    words(weight ? __ldg(weight + ca) : make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u), wa);
+    words(weight ? __ldg(weight + cb) : make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u), wb);
+    if (is_q) {
+        // y = x p + (its partner) m, for the pairs of values of chunk a and chunk b
+        uint64_t pa[4], ma[4], pb[4], mb[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const uint64_t ua = bf16_pair(wa[i]), ub = bf16_pair(wb[i]);
+            if (a.adjacent) {
+                const float c0 = c[i], c1 = c[4 + i], s0 = s[i], s1 = s[4 + i];
+                pa[i] = mul_pair(ua, pack2(c0, c0));
+                ma[i] = mul_pair(pack2(high2(ua), low2(ua)), pack2(-s0, s0));
+                pb[i] = mul_pair(ub, pack2(c1, c1));
+                mb[i] = mul_pair(pack2(high2(ub), low2(ub)), pack2(-s1, s1));
+            } else {
+                const uint64_t cc = pack2(c[2 * i], c[2 * i + 1]), ss = pack2(s[2 * i], s[2 * i + 1]);
+                pa[i] = mul_pair(ua, cc);
+                ma[i] = mul_pair(ub, pack2(-s[2 * i], -s[2 * i + 1]));
+                pb[i] = mul_pair(ub, cc);
+                mb[i] = mul_pair(ua, ss);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < JQ; j++) {
+            const int row = row0 + 4 * j + g;
+            uint32_t va[4], vb[4];
+            words(xa[j], va);
+            words(xb[j], vb);
+            uint64_t ya[4], yb[4], q = 0;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const uint64_t x = bf16_pair(va[i]), z = bf16_pair(vb[i]);
+                const uint64_t px = a.adjacent ? pack2(bf16_hi(va[i]), bf16_lo(va[i])) : z;
+                const uint64_t pz = a.adjacent ? pack2(bf16_hi(vb[i]), bf16_lo(vb[i])) : x;
+                ya[i] = fma_pair(x, pa[i], mul_pair(px, ma[i]));
+                yb[i] = fma_pair(z, pb[i], mul_pair(pz, mb[i]));
+                q = fma_pair(z, z, fma_pair(x, x, q));
+            }
+            if (weight) {
+                float sum = low2(q) + high2(q);
+#pragma unroll
+                for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                const float r = rsqrtf(fmaf(sum, 0.0078125f, a.eps));
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    ya[i] = mul_pair(ya[i], pack2(r, r));
+                    yb[i] = mul_pair(yb[i], pack2(r, r));
+                }
+            }
+            if (row < nrows) {
+                uint4 *dst = a.q_out + t * a.out_stride16 + row * 16;
+                dst[ca] = make_uint4(f32x2_to_bf16x2(high2(ya[0]), low2(ya[0])), f32x2_to_bf16x2(high2(ya[1]), low2(ya[1])),
+                                     f32x2_to_bf16x2(high2(ya[2]), low2(ya[2])), f32x2_to_bf16x2(high2(ya[3]), low2(ya[3])));
+                dst[cb] = make_uint4(f32x2_to_bf16x2(high2(yb[0]), low2(yb[0])), f32x2_to_bf16x2(high2(yb[1]), low2(yb[1])),
+                                     f32x2_to_bf16x2(high2(yb[2]), low2(yb[2])), f32x2_to_bf16x2(high2(yb[3]), low2(yb[3])));
+            }
+        }
+        return;
+    }
+    if (slot < 0 || slot >= a.num_slots) return;
+    const int64_t page = slot >> a.log2P;
+    const int in_page = (int)(slot & (a.P - 1));
+    const uint64_t policy = l2_policy_evict_last();           // of scale bytes, as in the plain append
+    if (!is_k) {
+#pragma unroll
+        for (int j = 0; j < JV; j++) {
+            const int row = row0 + 4 * j + g;
+            if (row < nrows)
+                store_block_values<kUnitScale, true>(a.pool + (page * a.Hkv + row) * a.slab, a.dtype, in_page, 1, blk, xa[j],
+                                                     xb[j], a.gv, policy);
+        }
+        return;
+    }
+    const int row = row0 + g;
+    uint32_t va[4], vb[4], ya[4], yb[4];
+    words(xa[0], va);
+    words(xb[0], vb);
     Pair r = {1.0f, 0.0f};
     if (weight) {
-        unpack8(__ldg(weight + 2 * blk), __ldg(weight + 2 * blk + 1), w);
-        unpack8(__ldg(weight + 2 * pblk), __ldg(weight + 2 * pblk + 1), wp);
         Pair q = {0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < 16; i++) {
-            const float v = bf16_at(x, i);
-            if (EXACT) {                                    // (a BF16 number's square is exact)
-                const Pair n = two_sum(q.hi, __fmul_rn(v, v));
+        for (int i = 0; i < 4; i++) {
+            const float v[4] = {bf16_lo(va[i]), bf16_hi(va[i]), bf16_lo(vb[i]), bf16_hi(vb[i])};
+#pragma unroll
+            for (int e = 0; e < 4; e++) {                     // (a BF16 number's square is exact)
+                const Pair n = two_sum(q.hi, __fmul_rn(v[e], v[e]));
                 q = {n.hi, q.lo + n.lo};
-            } else {
-                q.hi = fmaf(v, v, q.hi);
             }
         }
 #pragma unroll
         for (int d = 1; d < 8; d <<= 1) {
-            const float h = __shfl_xor_sync(group, q.hi, d);
-            if (EXACT) {
-                const float l = __shfl_xor_sync(group, q.lo, d);
-                const Pair n = two_sum(q.hi, h);
-                q = {n.hi, (q.lo + l) + n.lo};
-            } else {
-                q.hi += h;
-            }
+            const float h = __shfl_xor_sync(0xffffffffu, q.hi, d), lo = __shfl_xor_sync(0xffffffffu, q.lo, d);
+            const Pair n = two_sum(q.hi, h);
+            q = {n.hi, (q.lo + lo) + n.lo};
         }
-        if (EXACT) r = root(q, a.eps);
-        else r.hi = rsqrtf(fmaf(q.hi, 0.0078125f, a.eps));
+        r = root(q, a.eps);
     }
-    auto value = [&](int i) { return weight ? bf16_at(x, i) * bf16_at(w, i) : bf16_at(x, i); };      // exact: 16 bits
-    auto partner = [&](int i) { return weight ? bf16_at(xp, i) * bf16_at(wp, i) : bf16_at(xp, i); };
+    // r (u cc + p ss) rounded to BF16, u and p exact products of 16 bits
+    auto exact = [&](float u, float cc, float p, float ss) {
+        Pair d = {u, 0.0f};
+        if (turned) {
+            const float h = __fmul_rn(u, cc), k = __fmul_rn(p, ss);
+            const Pair z = two_sum(h, k);
+            d = {z.hi, z.lo + (__fmaf_rn(u, cc, -h) + __fmaf_rn(p, ss, -k))};
+        }
+        if (weight) {
+            const float h = __fmul_rn(d.hi, r.hi);
+            d = {h, __fmaf_rn(d.lo, r.hi, __fmaf_rn(d.hi, r.lo, __fmaf_rn(d.hi, r.hi, -h)))};
+        }
+        return bf16_of_pair(d.hi, d.lo);
+    };
 #pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-        float u[2] = {value(i), value(i + 1)}, p[2], cc[2], ss[2];
-        if (half) {
-#pragma unroll
-            for (int e = 0; e < 2; e++) p[e] = partner(i + e), cc[e] = c[i + e], ss[e] = s[i + e];
+    for (int i = 0; i < 4; i++) {
+        const float a0 = bf16_lo(va[i]) * bf16_lo(wa[i]), a1 = bf16_hi(va[i]) * bf16_hi(wa[i]);
+        const float b0 = bf16_lo(vb[i]) * bf16_lo(wb[i]), b1 = bf16_hi(vb[i]) * bf16_hi(wb[i]);
+        if (a.adjacent) {
+            ya[i] = exact(a0, c[i], a1, -s[i]) | (exact(a1, c[i], a0, s[i]) << 16);
+            yb[i] = exact(b0, c[4 + i], b1, -s[4 + i]) | (exact(b1, c[4 + i], b0, s[4 + i]) << 16);
         } else {
-            p[0] = u[1], p[1] = u[0];
-            cc[0] = cc[1] = c[i >> 1];
-            ss[0] = -s[i >> 1], ss[1] = s[i >> 1];
-        }
-        uint32_t y[2];
-#pragma unroll
-        for (int e = 0; e < 2; e++) {
-            if (EXACT) {
-                Pair d = {u[e], 0.0f};
-                if (turned) {
-                    const float h = __fmul_rn(u[e], cc[e]), g = __fmul_rn(p[e], ss[e]);
-                    const Pair z = two_sum(h, g);
-                    d = {z.hi, z.lo + (__fmaf_rn(u[e], cc[e], -h) + __fmaf_rn(p[e], ss[e], -g))};
-                }
-                if (weight) {
-                    const float h = __fmul_rn(d.hi, r.hi);
-                    d = {h, __fmaf_rn(d.lo, r.hi, __fmaf_rn(d.hi, r.lo, __fmaf_rn(d.hi, r.hi, -h)))};
-                }
-                y[e] = bf16_of_pair(d.hi, d.lo);
-            } else {
-                float d = turned ? fmaf(u[e], cc[e], p[e] * ss[e]) : u[e];
-                if (weight) d *= r.hi;
-                y[e] = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(d));
-            }
-        }
-        out[i >> 1] = y[0] | (y[1] << 16);
-    }
-}
-
-// Thread group g of eight (one row at a time) takes rows chunk + j * chunks of its token
-// (rows: Hq of Q, then Hkv of K, then Hkv of V), j < kRows.
-template <int kRows, bool kUnitScale>
-__global__ void __launch_bounds__(kThreadsR) rope_append_kernel(RopeArgs a) {
-    pdl_wait();
-    pdl_launch_dependents();
-    const int64_t id = (int64_t)blockIdx.x * (kThreadsR / 8) + (threadIdx.x >> 3);
-    const int blk = threadIdx.x & 7, lane = threadIdx.x & 31;
-    const unsigned group = 0xffu << (lane & 24);
-    if (id >= a.num_tokens * a.chunks) return;               // (a whole group at a time)
-    const int64_t t = id / a.chunks;
-    const int chunk = (int)(id - t * a.chunks), rows = a.Hq + 2 * a.Hkv;
-    uint4 x0[kRows], x1[kRows];
-#pragma unroll
-    for (int j = 0; j < kRows; j++) {
-        const int row = chunk + j * a.chunks;
-        if (row >= rows) continue;
-        const uint4 *src = row < a.Hq ? a.q + t * a.q_stride16 + row * 16
-                           : row < a.Hq + a.Hkv ? a.k + t * a.kv_stride16 + (row - a.Hq) * 16
-                                                : a.v + t * a.kv_stride16 + (row - a.Hq - a.Hkv) * 16;
-        x0[j] = __ldg(src + 2 * blk);
-        x1[j] = __ldg(src + 2 * blk + 1);
-    }
-    const int64_t slot = __ldg(a.slots + t);
-    // ---- the block's pairs, and their row of the table (a float4 of pairs lies in one section)
-    const int half16 = a.rot >> 5;                           // blocks of half the rotated values
-    const bool turned = blk < (a.rot >> 4);
-    const bool second = !a.adjacent && blk >= half16;
-    const int pblk = !turned || a.adjacent ? blk : second ? blk - half16 : blk + half16;
-    float c[16], s[16];
-    bool ok = true;
-    if (turned) {
-        const int first = a.adjacent ? 8 * blk : 16 * (second ? blk - half16 : blk), n4 = a.adjacent ? 2 : 4;
-        const float4 *at[4];
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            if (i >= n4) continue;
-            const int pair = first + 4 * i, axis = pair < a.sec1 ? 0 : pair < a.sec2 ? 1 : 2;
-            const int32_t pos = __ldg(a.positions + axis * a.num_tokens + t);
-            const bool in = pos >= 0 && pos < a.num_positions;
-            ok = ok && in;
-            at[i] = reinterpret_cast<const float4 *>(a.table + (in ? (int64_t)pos * a.rot : 0) + pair);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            if (i >= n4) continue;
-            const float4 x = __ldg(at[i]), y = __ldg(at[i] + (a.rot >> 3));
-            const float f = !a.adjacent && !second ? -1.0f : 1.0f;
-            c[4 * i] = x.x, c[4 * i + 1] = x.y, c[4 * i + 2] = x.z, c[4 * i + 3] = x.w;
-            s[4 * i] = f * y.x, s[4 * i + 1] = f * y.y, s[4 * i + 2] = f * y.z, s[4 * i + 3] = f * y.w;
+            ya[i] = exact(a0, c[2 * i], b0, -s[2 * i]) | (exact(a1, c[2 * i + 1], b1, -s[2 * i + 1]) << 16);
+            yb[i] = exact(b0, c[2 * i], a0, s[2 * i]) | (exact(b1, c[2 * i + 1], a1, s[2 * i + 1]) << 16);
         }
     }
-    ok = __all_sync(group, ok);
-    if (!ok && blk == 0 && chunk == 0) flag_error(a.err, kErrPosition);
-    if (slot >= a.num_slots && blk == 0 && chunk == 0) flag_error(a.err, kErrSlot);
-    const bool write = slot >= 0 && slot < a.num_slots;
-    if (!ok) return;
-    const int64_t page = write ? slot >> a.log2P : 0;
-    const int in_page = (int)(slot & (a.P - 1));
-    const int src = (lane & 24) + pblk;
-    const uint64_t policy = l2_policy_evict_last();          // of scale bytes, as in the plain append
+    // Two threads of a half-split pair of chunks exchange one each: the even one quantises the block of the
+    // first half, the odd one that of the second.
+    const bool odd = blk & 1;
+    int at = blk;
 #pragma unroll
-    for (int j = 0; j < kRows; j++) {
-        const int row = chunk + j * a.chunks;
-        if (row >= rows) continue;
-        uint32_t x[8], y[8];
-        unpack8(x0[j], x1[j], x);
-        if (row < a.Hq) {
-            turn_block<false>(a, x, a.wq, blk, pblk, group, src, turned, c, s, y);
-            uint4 *dst = a.q_out + t * a.out_stride16 + row * 16 + 2 * blk;
-            dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
-            dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
-        } else if (write) {
-            const int which = row >= a.Hq + a.Hkv;
-            uint4 y0 = x0[j], y1 = x1[j];
-            if (!which) {
-                turn_block<true>(a, x, a.wk, blk, pblk, group, src, turned, c, s, y);
-                y0 = make_uint4(y[0], y[1], y[2], y[3]);
-                y1 = make_uint4(y[4], y[5], y[6], y[7]);
-            }
-            const int h = row - a.Hq - which * a.Hkv;
-            store_block_values<kUnitScale, true>(a.pool + (page * a.Hkv + h) * a.slab, a.dtype, in_page, which, blk, y0, y1,
-                                                 which ? a.gv : a.gk, policy);
+    for (int i = 0; i < 4; i++) {
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? ya[i] : yb[i], 1);
+        if (split) {
+            if (odd) ya[i] = other;
+            else yb[i] = other;
         }
     }
+    if (split) at = odd ? (blk - 1 + half8) >> 1 : blk >> 1;
+    if (row < nrows)
+        store_block_values<kUnitScale, true>(a.pool + (page * a.Hkv + row) * a.slab, a.dtype, in_page, 0, at,
+                                             make_uint4(ya[0], ya[1], ya[2], ya[3]), make_uint4(yb[0], yb[1], yb[2], yb[3]),
+                                             a.gk, policy);
 }
 
 }  // namespace
@@ -290,11 +345,11 @@ cudaError_t launch_rope_append(const nvfp4kv_cache &c, const nvfp4kv_rope &rope,
     a.gv = c.v_global_scale;
     a.dtype = c.dtype;
     a.err = err;
-    // One row a thread while that does not fill the GPU (152 SMs of 2,048 threads), four beyond.
-    const int rows = a.Hq + 2 * a.Hkv;
-    const bool many = num_tokens * rows * 8 > 152 * 2048;
-    a.chunks = many ? (rows + 3) / 4 : rows;
-    const int64_t grid = ceil_div64(num_tokens * a.chunks, kThreadsR / 8);
+    // Four rows a warp while that does not fill the GPU (two CTAs on each of 152 SMs), more beyond.
+    const bool many = num_tokens * (a.Hq + 2 * a.Hkv) > 4 * 152 * 2 * kWarpsR;
+    const int jq = many ? 4 : 1, jv = many ? 2 : 1;
+    const int64_t warps = (a.Hq + 4 * jq - 1) / (4 * jq) + (a.Hkv + 3) / 4 + (a.Hkv + 4 * jv - 1) / (4 * jv);
+    const int64_t grid = ceil_div64(num_tokens * warps, kWarpsR);
     const bool unit = c.k_global_scale == 1.0f && c.v_global_scale == 1.0f;
     void *args[] = {&a};
     const void *fn = many ? (unit ? reinterpret_cast<const void *>(&rope_append_kernel<4, true>)
