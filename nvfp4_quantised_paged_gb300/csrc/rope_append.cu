@@ -20,6 +20,9 @@
 // reciprocal root as well, and the BF16 rounding breaks ties by the low part; it is the
 // rounding of the exact value up to a relative 2^-40 of the pair's larger product.  Q is formed in FP32
 // (a value within 2^-21 of a tie may round to the other neighbour).
+#include <algorithm>
+#include <mutex>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "quantize.cuh"
@@ -100,151 +103,97 @@ __device__ __forceinline__ void words(const uint4 &x, uint32_t (&w)[4]) { w[0] =
 
 constexpr int kWarpsR = kThreadsR / 32;
 
-// JQ: passes of four rows a warp makes over Q (and JQ > 1: two over V).
-template <int JQ, bool kUnitScale>
-__global__ void __launch_bounds__(kThreadsR, 2) rope_append_kernel(RopeArgs a) {
-    pdl_wait();
-    pdl_launch_dependents();
-    constexpr int JV = JQ > 1 ? 2 : 1;
-    const int64_t id = (int64_t)blockIdx.x * kWarpsR + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31, blk = lane & 7, g = lane >> 3;
-    const int nq = (a.Hq + 4 * JQ - 1) / (4 * JQ), nk = (a.Hkv + 3) / 4, nv = (a.Hkv + 4 * JV - 1) / (4 * JV);
-    const int64_t t = id / (nq + nk + nv);
-    const int sub = (int)(id - t * (nq + nk + nv));
-    if (t >= a.num_tokens) return;                            // (the whole warp)
-    const bool is_q = sub < nq, is_k = !is_q && sub < nq + nk;
-    // The thread's two chunks of eight values: ca in the first rotated half and its partner cb, or a block's
-    // (2 blk, 2 blk + 1).
-    const int half8 = a.rot >> 4;                             // chunks of half the rotated values (even)
-    const bool turned = is_q || is_k ? (a.adjacent ? 2 * blk < 2 * half8 : blk < half8) : false;
-    const bool split = turned && !a.adjacent;
-    const int ca = split ? blk : 2 * blk, cb = split ? blk + half8 : 2 * blk + 1;
-    // ---- the rows
-    constexpr int JM = JQ > JV ? JQ : JV;
-    const int row0 = is_q ? sub * 4 * JQ : is_k ? (sub - nq) * 4 : (sub - nq - nk) * 4 * JV;
-    const int nrows = is_q ? a.Hq : a.Hkv, passes = is_q ? JQ : is_k ? 1 : JV;
-    const uint4 *base = is_q ? a.q + t * a.q_stride16 : (is_k ? a.k : a.v) + t * a.kv_stride16;
-    uint4 xa[JM], xb[JM];
+// Where a thread's 16 values of a rotated row lie: chunk ca of eight in the first rotated half and its partner cb,
+// or the two chunks of block blk.
+struct Place {
+    bool turned, split;
+    int half8, ca, cb;    // half8: chunks of half the rotated values (even)
+};
+
+template <bool kAdj>
+__device__ __forceinline__ Place place_of(const RopeArgs &a, int blk) {
+    Place p;
+    p.half8 = a.rot >> 4;
+    p.turned = blk < p.half8;
+    p.split = p.turned && !kAdj;
+    p.ca = p.split ? blk : 2 * blk;
+    p.cb = p.split ? blk + p.half8 : 2 * blk + 1;
+    return p;
+}
+
+__device__ __forceinline__ uint4 weight_chunk(const uint4 *w, int chunk) {
+    return w ? __ldg(w + chunk) : make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);   // ones
+}
+
+// Q: y = x p + (its partner) m, for the pairs of values of the chunks a and b.
+struct Turn {
+    uint64_t pa[4], ma[4], pb[4], mb[4];
+};
+
+template <bool kAdj>
+__device__ __forceinline__ void make_turn(const RopeArgs &a, const float (&c)[8], const float (&s)[8], const uint32_t (&wa)[4],
+                                          const uint32_t (&wb)[4], Turn &u) {
 #pragma unroll
-    for (int j = 0; j < JM; j++) {
-        const int row = row0 + 4 * j + g;
-        xa[j] = xb[j] = make_uint4(0, 0, 0, 0);
-        if (j < passes && row < nrows) {
-            xa[j] = __ldg(base + row * 16 + ca);
-            xb[j] = __ldg(base + row * 16 + cb);
+    for (int i = 0; i < 4; i++) {
+        const uint64_t ua = bf16_pair(wa[i]), ub = bf16_pair(wb[i]);
+        if (kAdj) {
+            const float c0 = c[i], c1 = c[4 + i], s0 = s[i], s1 = s[4 + i];
+            u.pa[i] = mul_pair(ua, pack2(c0, c0));
+            u.ma[i] = mul_pair(pack2(high2(ua), low2(ua)), pack2(-s0, s0));
+            u.pb[i] = mul_pair(ub, pack2(c1, c1));
+            u.mb[i] = mul_pair(pack2(high2(ub), low2(ub)), pack2(-s1, s1));
+        } else {
+            const uint64_t cc = pack2(c[2 * i], c[2 * i + 1]), ss = pack2(s[2 * i], s[2 * i + 1]);
+            u.pa[i] = mul_pair(ua, cc);
+            u.ma[i] = mul_pair(ub, pack2(-s[2 * i], -s[2 * i + 1]));
+            u.pb[i] = mul_pair(ub, cc);
+            u.mb[i] = mul_pair(ua, ss);
         }
     }
-    const int64_t slot = is_q ? 0 : __ldg(a.slots + t);
-    // ---- the positions (all of the token's: any warp skips it), and the pairs' row of the table
-    bool ok = true;
-    if (a.rot > 0) {
-        const int axes = a.sec1 >= kHeadDim ? 1 : a.sec2 >= kHeadDim ? 2 : 3;
-        for (int x = 0; x < axes; x++) {
-            const int32_t pos = __ldg(a.positions + x * a.num_tokens + t);
-            ok = ok && pos >= 0 && pos < a.num_positions;
-        }
-    }
-    if (sub == 0 && lane == 0) {
-        const int64_t s0 = __ldg(a.slots + t);
-        if (!ok) flag_error(a.err, kErrPosition);
-        if (s0 >= a.num_slots) flag_error(a.err, kErrSlot);
-    }
-    if (!ok) return;
-    float c[8], s[8];
+}
+
+// The eight threads of a row call it together (as do the four rows of the warp).
+template <bool kAdj>
+__device__ __forceinline__ void turn_q(const RopeArgs &a, const Turn &u, uint4 &xa, uint4 &xb) {
+    uint32_t va[4], vb[4];
+    words(xa, va);
+    words(xb, vb);
+    uint64_t ya[4], yb[4], q = 0;
 #pragma unroll
-    for (int i = 0; i < 8; i++) c[i] = 1.f, s[i] = 0.f;
-    if (turned) {
-#pragma unroll
-        for (int i = 0; i < 2; i++) {                         // (four pairs lie in one section)
-            const int pair = 8 * blk + 4 * i, axis = pair < a.sec1 ? 0 : pair < a.sec2 ? 1 : 2;
-            const int32_t pos = __ldg(a.positions + axis * a.num_tokens + t);
-            const float4 *at = reinterpret_cast<const float4 *>(a.table + (int64_t)pos * a.rot + pair);
-            const float4 x = __ldg(at), y = __ldg(at + (a.rot >> 3));
-            c[4 * i] = x.x, c[4 * i + 1] = x.y, c[4 * i + 2] = x.z, c[4 * i + 3] = x.w;
-            s[4 * i] = y.x, s[4 * i + 1] = y.y, s[4 * i + 2] = y.z, s[4 * i + 3] = y.w;
-        }
+    for (int i = 0; i < 4; i++) {
+        const uint64_t x = bf16_pair(va[i]), z = bf16_pair(vb[i]);
+        const uint64_t px = kAdj ? pack2(bf16_hi(va[i]), bf16_lo(va[i])) : z;
+        const uint64_t pz = kAdj ? pack2(bf16_hi(vb[i]), bf16_lo(vb[i])) : x;
+        ya[i] = fma_pair(x, u.pa[i], mul_pair(px, u.ma[i]));
+        yb[i] = fma_pair(z, u.pb[i], mul_pair(pz, u.mb[i]));
+        q = fma_pair(z, z, fma_pair(x, x, q));
     }
-    const uint4 *weight = is_q ? a.wq : is_k ? a.wk : nullptr;
-    uint32_t wa[4], wb[4];
-    words(weight ? __ldg(weight + ca) : make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u), wa);
-    words(weight ? __ldg(weight + cb) : make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u), wb);
-    if (is_q) {
-        // y = x p + (its partner) m, for the pairs of values of chunk a and chunk b
-        uint64_t pa[4], ma[4], pb[4], mb[4];
+    if (a.wq) {
+        float sum = low2(q) + high2(q);
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        const float r = rsqrtf(fmaf(sum, 0.0078125f, a.eps));
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-            const uint64_t ua = bf16_pair(wa[i]), ub = bf16_pair(wb[i]);
-            if (a.adjacent) {
-                const float c0 = c[i], c1 = c[4 + i], s0 = s[i], s1 = s[4 + i];
-                pa[i] = mul_pair(ua, pack2(c0, c0));
-                ma[i] = mul_pair(pack2(high2(ua), low2(ua)), pack2(-s0, s0));
-                pb[i] = mul_pair(ub, pack2(c1, c1));
-                mb[i] = mul_pair(pack2(high2(ub), low2(ub)), pack2(-s1, s1));
-            } else {
-                const uint64_t cc = pack2(c[2 * i], c[2 * i + 1]), ss = pack2(s[2 * i], s[2 * i + 1]);
-                pa[i] = mul_pair(ua, cc);
-                ma[i] = mul_pair(ub, pack2(-s[2 * i], -s[2 * i + 1]));
-                pb[i] = mul_pair(ub, cc);
-                mb[i] = mul_pair(ua, ss);
-            }
+            ya[i] = mul_pair(ya[i], pack2(r, r));
+            yb[i] = mul_pair(yb[i], pack2(r, r));
         }
-#pragma unroll
-        for (int j = 0; j < JQ; j++) {
-            const int row = row0 + 4 * j + g;
-            uint32_t va[4], vb[4];
-            words(xa[j], va);
-            words(xb[j], vb);
-            uint64_t ya[4], yb[4], q = 0;
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const uint64_t x = bf16_pair(va[i]), z = bf16_pair(vb[i]);
-                const uint64_t px = a.adjacent ? pack2(bf16_hi(va[i]), bf16_lo(va[i])) : z;
-                const uint64_t pz = a.adjacent ? pack2(bf16_hi(vb[i]), bf16_lo(vb[i])) : x;
-                ya[i] = fma_pair(x, pa[i], mul_pair(px, ma[i]));
-                yb[i] = fma_pair(z, pb[i], mul_pair(pz, mb[i]));
-                q = fma_pair(z, z, fma_pair(x, x, q));
-            }
-            if (weight) {
-                float sum = low2(q) + high2(q);
-#pragma unroll
-                for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                const float r = rsqrtf(fmaf(sum, 0.0078125f, a.eps));
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    ya[i] = mul_pair(ya[i], pack2(r, r));
-                    yb[i] = mul_pair(yb[i], pack2(r, r));
-                }
-            }
-            if (row < nrows) {
-                uint4 *dst = a.q_out + t * a.out_stride16 + row * 16;
-                dst[ca] = make_uint4(f32x2_to_bf16x2(high2(ya[0]), low2(ya[0])), f32x2_to_bf16x2(high2(ya[1]), low2(ya[1])),
-                                     f32x2_to_bf16x2(high2(ya[2]), low2(ya[2])), f32x2_to_bf16x2(high2(ya[3]), low2(ya[3])));
-                dst[cb] = make_uint4(f32x2_to_bf16x2(high2(yb[0]), low2(yb[0])), f32x2_to_bf16x2(high2(yb[1]), low2(yb[1])),
-                                     f32x2_to_bf16x2(high2(yb[2]), low2(yb[2])), f32x2_to_bf16x2(high2(yb[3]), low2(yb[3])));
-            }
-        }
-        return;
     }
-    if (slot < 0 || slot >= a.num_slots) return;
-    const int64_t page = slot >> a.log2P;
-    const int in_page = (int)(slot & (a.P - 1));
-    const uint64_t policy = l2_policy_evict_last();           // of scale bytes, as in the plain append
-    if (!is_k) {
-#pragma unroll
-        for (int j = 0; j < JV; j++) {
-            const int row = row0 + 4 * j + g;
-            if (row < nrows)
-                store_block_values<kUnitScale, true>(a.pool + (page * a.Hkv + row) * a.slab, a.dtype, in_page, 1, blk, xa[j],
-                                                     xb[j], a.gv, policy);
-        }
-        return;
-    }
-    const int row = row0 + g;
+    xa = make_uint4(f32x2_to_bf16x2(high2(ya[0]), low2(ya[0])), f32x2_to_bf16x2(high2(ya[1]), low2(ya[1])),
+                    f32x2_to_bf16x2(high2(ya[2]), low2(ya[2])), f32x2_to_bf16x2(high2(ya[3]), low2(ya[3])));
+    xb = make_uint4(f32x2_to_bf16x2(high2(yb[0]), low2(yb[0])), f32x2_to_bf16x2(high2(yb[1]), low2(yb[1])),
+                    f32x2_to_bf16x2(high2(yb[2]), low2(yb[2])), f32x2_to_bf16x2(high2(yb[3]), low2(yb[3])));
+}
+
+// K: the chunks' exact values rounded to BF16, then exchanged so that the thread holds a whole block; returns which.
+template <bool kAdj>
+__device__ __forceinline__ int turn_k(const RopeArgs &a, const Place &p, int blk, const float (&c)[8], const float (&s)[8],
+                                      const uint32_t (&wa)[4], const uint32_t (&wb)[4], uint4 &xa, uint4 &xb) {
     uint32_t va[4], vb[4], ya[4], yb[4];
-    words(xa[0], va);
-    words(xb[0], vb);
+    words(xa, va);
+    words(xb, vb);
     Pair r = {1.0f, 0.0f};
-    if (weight) {
+    if (a.wk) {
         Pair q = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < 4; i++) {
@@ -263,15 +212,15 @@ __global__ void __launch_bounds__(kThreadsR, 2) rope_append_kernel(RopeArgs a) {
         }
         r = root(q, a.eps);
     }
-    // r (u cc + p ss) rounded to BF16, u and p exact products of 16 bits
-    auto exact = [&](float u, float cc, float p, float ss) {
+    // r (u cc + z ss) rounded to BF16, u and z exact products of 16 bits
+    auto exact = [&](float u, float cc, float z, float ss) {
         Pair d = {u, 0.0f};
-        if (turned) {
-            const float h = __fmul_rn(u, cc), k = __fmul_rn(p, ss);
-            const Pair z = two_sum(h, k);
-            d = {z.hi, z.lo + (__fmaf_rn(u, cc, -h) + __fmaf_rn(p, ss, -k))};
+        if (p.turned) {
+            const float h = __fmul_rn(u, cc), k = __fmul_rn(z, ss);
+            const Pair n = two_sum(h, k);
+            d = {n.hi, n.lo + (__fmaf_rn(u, cc, -h) + __fmaf_rn(z, ss, -k))};
         }
-        if (weight) {
+        if (a.wk) {
             const float h = __fmul_rn(d.hi, r.hi);
             d = {h, __fmaf_rn(d.lo, r.hi, __fmaf_rn(d.hi, r.lo, __fmaf_rn(d.hi, r.hi, -h)))};
         }
@@ -281,7 +230,7 @@ __global__ void __launch_bounds__(kThreadsR, 2) rope_append_kernel(RopeArgs a) {
     for (int i = 0; i < 4; i++) {
         const float a0 = bf16_lo(va[i]) * bf16_lo(wa[i]), a1 = bf16_hi(va[i]) * bf16_hi(wa[i]);
         const float b0 = bf16_lo(vb[i]) * bf16_lo(wb[i]), b1 = bf16_hi(vb[i]) * bf16_hi(wb[i]);
-        if (a.adjacent) {
+        if (kAdj) {
             ya[i] = exact(a0, c[i], a1, -s[i]) | (exact(a1, c[i], a0, s[i]) << 16);
             yb[i] = exact(b0, c[4 + i], b1, -s[4 + i]) | (exact(b1, c[4 + i], b0, s[4 + i]) << 16);
         } else {
@@ -292,21 +241,292 @@ __global__ void __launch_bounds__(kThreadsR, 2) rope_append_kernel(RopeArgs a) {
     // Two threads of a half-split pair of chunks exchange one each: the even one quantises the block of the
     // first half, the odd one that of the second.
     const bool odd = blk & 1;
-    int at = blk;
 #pragma unroll
     for (int i = 0; i < 4; i++) {
         const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? ya[i] : yb[i], 1);
-        if (split) {
+        if (p.split) {
             if (odd) ya[i] = other;
             else yb[i] = other;
         }
     }
-    if (split) at = odd ? (blk - 1 + half8) >> 1 : blk >> 1;
-    if (row < nrows)
-        store_block_values<kUnitScale, true>(a.pool + (page * a.Hkv + row) * a.slab, a.dtype, in_page, 0, at,
-                                             make_uint4(ya[0], ya[1], ya[2], ya[3]), make_uint4(yb[0], yb[1], yb[2], yb[3]),
-                                             a.gk, policy);
+    xa = make_uint4(ya[0], ya[1], ya[2], ya[3]);
+    xb = make_uint4(yb[0], yb[1], yb[2], yb[3]);
+    return !p.split ? blk : odd ? (blk - 1 + p.half8) >> 1 : blk >> 1;
 }
+
+// A thread's cosines and sines from a row of the table (cosines, then sines) of its pair groups x (two of four pairs).
+__device__ __forceinline__ void take4(float (&v)[8], int i, const float4 &x) {
+    v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
+}
+
+__device__ __forceinline__ int axis_of(const RopeArgs &a, int pair) { return pair < a.sec1 ? 0 : pair < a.sec2 ? 1 : 2; }
+__device__ __forceinline__ int axes_of(const RopeArgs &a) { return a.sec1 >= kHeadDim ? 1 : a.sec2 >= kHeadDim ? 2 : 3; }
+
+// Few tokens: a warp takes four rows of one kind of a token, everything straight from global memory.
+template <bool kUnitScale, bool kAdj>
+__global__ void __launch_bounds__(kThreadsR) rope_append_kernel(RopeArgs a) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t id = (int64_t)blockIdx.x * kWarpsR + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, blk = lane & 7, g = lane >> 3;
+    const int nq = (a.Hq + 3) / 4, nk = (a.Hkv + 3) / 4;
+    const int64_t t = id / (nq + 2 * nk);
+    const int sub = (int)(id - t * (nq + 2 * nk));
+    if (t >= a.num_tokens) return;                            // (the whole warp)
+    const bool is_q = sub < nq, is_k = !is_q && sub < nq + nk;
+    Place p = place_of<kAdj>(a, blk);
+    if (!is_q && !is_k) p.turned = p.split = false, p.ca = 2 * blk, p.cb = 2 * blk + 1;
+    const int row = 4 * (is_q ? sub : is_k ? sub - nq : sub - nq - nk) + g, nrows = is_q ? a.Hq : a.Hkv;
+    const uint4 *base = (is_q ? a.q + t * a.q_stride16 : (is_k ? a.k : a.v) + t * a.kv_stride16) + row * 16;
+    uint4 xa = make_uint4(0, 0, 0, 0), xb = xa;
+    if (row < nrows) {
+        xa = __ldg(base + p.ca);
+        xb = __ldg(base + p.cb);
+    }
+    const int64_t slot = __ldg(a.slots + t);
+    bool ok = true;                                           // (all of the token's positions: any warp skips it)
+    if (a.rot > 0) {
+        for (int x = 0; x < axes_of(a); x++) {
+            const int32_t pos = __ldg(a.positions + x * a.num_tokens + t);
+            ok = ok && pos >= 0 && pos < a.num_positions;
+        }
+    }
+    if (sub == 0 && lane == 0) {
+        if (!ok) flag_error(a.err, kErrPosition);
+        if (slot >= a.num_slots) flag_error(a.err, kErrSlot);
+    }
+    if (!ok) return;
+    float c[8], s[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) c[i] = 1.f, s[i] = 0.f;
+    if (p.turned) {
+#pragma unroll
+        for (int i = 0; i < 2; i++) {                         // (four pairs lie in one section)
+            const int pair = 8 * blk + 4 * i;
+            const int32_t pos = __ldg(a.positions + axis_of(a, pair) * a.num_tokens + t);
+            const float4 *at = reinterpret_cast<const float4 *>(a.table + (int64_t)pos * a.rot + pair);
+            take4(c, i, __ldg(at));
+            take4(s, i, __ldg(at + (a.rot >> 3)));
+        }
+    }
+    if (is_q) {
+        uint32_t wa[4], wb[4];
+        words(weight_chunk(a.wq, p.ca), wa);
+        words(weight_chunk(a.wq, p.cb), wb);
+        Turn u;
+        make_turn<kAdj>(a, c, s, wa, wb, u);
+        turn_q<kAdj>(a, u, xa, xb);
+        if (row < nrows) {
+            uint4 *dst = a.q_out + t * a.out_stride16 + row * 16;
+            dst[p.ca] = xa;
+            dst[p.cb] = xb;
+        }
+        return;
+    }
+    if (slot < 0 || slot >= a.num_slots) return;
+    int at = blk;
+    if (is_k) {
+        uint32_t wa[4], wb[4];
+        words(weight_chunk(a.wk, p.ca), wa);
+        words(weight_chunk(a.wk, p.cb), wb);
+        at = turn_k<kAdj>(a, p, blk, c, s, wa, wb, xa, xb);
+    }
+    if (row < nrows)
+        store_block_values<kUnitScale, true>(a.pool + ((slot >> a.log2P) * a.Hkv + row) * a.slab, a.dtype, (int)(slot & (a.P - 1)),
+                                             !is_k, at, xa, xb, is_k ? a.gk : a.gv, l2_policy_evict_last());
+}
+
+// Many tokens: persistent CTAs.  One warp copies whole tokens (rows of Q, K and V, the pieces of the table) into a ring
+// in shared memory, eight warps work on four rows at a time from there.  The direct form's loads, a chain of position,
+// table row and use, left DRAM idle: 32,768 tokens of 64 + 8 heads with norms took it 355 us.
+constexpr int kThreadsS = kThreadsR + 32;
+constexpr int kStreamBytes = 110 * 1024;          // of a CTA's ring, two CTAs an SM
+constexpr int kMaxStages = 8, kMaxTps = 32;
+constexpr uint32_t kWaitLimitR = 1u << 22;
+
+struct StreamPlan {
+    int tps, stages;       // tokens a stage, stages
+    int token_bytes;       // rows and table pieces of a token
+};
+
+struct StreamMisc {
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    int64_t slot[kMaxStages][kMaxTps];            // -1: K and V are skipped; kNoToken: all of it
+    int abort;
+};
+constexpr int64_t kNoToken = -2;
+
+template <bool kUnitScale, bool kAdj>
+__global__ void __launch_bounds__(kThreadsS, 2) rope_stream_kernel(RopeArgs a, StreamPlan plan) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    StreamMisc &m = *reinterpret_cast<StreamMisc *>(smem + plan.stages * plan.tps * plan.token_bytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < plan.stages; i++) {
+            mbar_init(&m.full[i], 1);
+            mbar_init(&m.empty[i], kWarpsR);
+        }
+        m.abort = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    pdl_wait();
+    pdl_launch_dependents();
+    volatile int *abort_flag = &m.abort;
+    const int64_t tiles = (a.num_tokens + plan.tps - 1) / plan.tps;
+    const int q_bytes = a.Hq * 256, kv_bytes = a.Hkv * 256;
+    int st = 0;
+    uint32_t ph = 0;
+    bool good = true;
+    if (warp == kWarpsR) {
+        // ---------------- the copying warp: lane i < tps takes token i of a stage
+        const int axes = a.rot > 0 ? axes_of(a) : 0;
+        int32_t pos[3] = {0, 0, 0};
+        int64_t slot = 0;
+        auto fetch = [&](int64_t tile) {
+            const int64_t t = tile * plan.tps + lane;
+            if (lane >= plan.tps || t >= a.num_tokens) return;
+            for (int x = 0; x < 3; x++)
+                if (x < axes) pos[x] = __ldg(a.positions + x * a.num_tokens + t);
+            slot = __ldg(a.slots + t);
+        };
+        fetch(blockIdx.x);
+        int64_t done = 0;
+        for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, done++) {
+            if (done >= plan.stages) good = __all_sync(0xffffffffu, mbar_wait_bounded(&m.empty[st], ph ^ 1u, kWaitLimitR, abort_flag));
+            if (!good) break;
+            const int64_t t = tile * plan.tps + lane;
+            const bool there = lane < plan.tps && t < a.num_tokens;
+            bool ok = there;
+#pragma unroll
+            for (int x = 0; x < 3; x++) ok = ok && (x >= axes || (pos[x] >= 0 && pos[x] < a.num_positions));
+            if (there && !ok) flag_error(a.err, kErrPosition);
+            if (there && slot >= a.num_slots) flag_error(a.err, kErrSlot);
+            const bool write = ok && slot >= 0 && slot < a.num_slots;
+            if (lane < plan.tps) m.slot[st][lane] = !ok ? kNoToken : write ? slot : -1;
+            const uint32_t bytes = ok ? q_bytes + 4 * a.rot + (write ? 2 * kv_bytes : 0) : 0;
+            const uint32_t total = __reduce_add_sync(0xffffffffu, bytes);
+            __syncwarp();
+            if (lane == 0) mbar_arrive_expect_tx(&m.full[st], total);
+            __syncwarp();
+            if (ok) {
+                uint8_t *dst = smem + (st * plan.tps + lane) * plan.token_bytes;
+                if (q_bytes) bulk_g2s(dst, a.q + t * a.q_stride16, q_bytes, &m.full[st]);
+                if (write) {
+                    bulk_g2s(dst + q_bytes, a.k + t * a.kv_stride16, kv_bytes, &m.full[st]);
+                    bulk_g2s(dst + q_bytes + kv_bytes, a.v + t * a.kv_stride16, kv_bytes, &m.full[st]);
+                }
+                dst += q_bytes + 2 * kv_bytes;
+                for (int x = 0; x < axes; x++) {              // the pairs of axis x: cosines and sines
+                    const int first = x == 0 ? 0 : x == 1 ? a.sec1 : a.sec2;
+                    const int end = min(a.rot / 2, x == 0 ? a.sec1 : x == 1 ? a.sec2 : kHeadDim);
+                    if (end <= first) continue;
+                    const float *row = a.table + (int64_t)pos[x] * a.rot;
+                    if (axes == 1) {
+                        bulk_g2s(dst, row, 4 * a.rot, &m.full[st]);
+                    } else {
+                        bulk_g2s(dst + 4 * first, row + first, 4 * (end - first), &m.full[st]);
+                        bulk_g2s(dst + 2 * a.rot + 4 * first, row + a.rot / 2 + first, 4 * (end - first), &m.full[st]);
+                    }
+                }
+            }
+            fetch(tile + gridDim.x);
+            if (++st == plan.stages) st = 0, ph ^= 1u;
+        }
+        // no copy may still be writing when the CTA ends
+        for (int64_t i = done > plan.stages ? done - plan.stages : 0; i < done; i++)
+            mbar_wait_bounded(&m.full[i % plan.stages], (uint32_t)(i / plan.stages) & 1, kWaitLimitR, nullptr);
+    } else {
+        const int blk = lane & 7, g = lane >> 3;
+        const Place p = place_of<kAdj>(a, blk);
+        // A token's units: four rows of K, four of V, eight of Q.  Those of K take longest, so the warps take turns.
+        const int nq = (a.Hq + 7) / 8, nk = (a.Hkv + 3) / 4, per = nq + 2 * nk;
+        const uint64_t policy = l2_policy_evict_last();
+        int turn = warp;
+        for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+            good = __all_sync(0xffffffffu, mbar_wait_bounded(&m.full[st], ph, kWaitLimitR, abort_flag));
+            if (!good) break;
+            const int n = (int)min((int64_t)plan.tps, a.num_tokens - tile * plan.tps);
+            int unit = turn;
+            for (; unit < n * per; unit += kWarpsR) {
+                const int i = unit / per, sub = unit - i * per;
+                const int64_t slot = m.slot[st][i], t = tile * plan.tps + i;
+                if (slot == kNoToken || (sub < 2 * nk && slot < 0)) continue;
+                const uint8_t *src = smem + (st * plan.tps + i) * plan.token_bytes;
+                float c[8], s[8];
+                if (sub < nk || sub >= 2 * nk) {
+                    const float *table = reinterpret_cast<const float *>(src + q_bytes + 2 * kv_bytes);
+#pragma unroll
+                    for (int x = 0; x < 8; x++) c[x] = 1.f, s[x] = 0.f;
+                    if (p.turned) {
+#pragma unroll
+                        for (int x = 0; x < 2; x++) {
+                            take4(c, x, *reinterpret_cast<const float4 *>(table + 8 * blk + 4 * x));
+                            take4(s, x, *reinterpret_cast<const float4 *>(table + (a.rot >> 1) + 8 * blk + 4 * x));
+                        }
+                    }
+                }
+                uint32_t wa[4], wb[4];                        // (from L1: registers are short)
+                if (sub < 2 * nk) {
+                    const bool is_k = sub < nk;
+                    const int row = 4 * (is_k ? sub : sub - nk) + g;
+                    uint4 xa = make_uint4(0, 0, 0, 0), xb = xa;
+                    if (row < a.Hkv) {
+                        const uint4 *x = reinterpret_cast<const uint4 *>(src + q_bytes + (is_k ? 0 : kv_bytes) + row * 256);
+                        xa = x[is_k ? p.ca : 2 * blk];
+                        xb = x[is_k ? p.cb : 2 * blk + 1];
+                    }
+                    int at = blk;
+                    if (is_k) {
+                        words(weight_chunk(a.wk, p.ca), wa);
+                        words(weight_chunk(a.wk, p.cb), wb);
+                        at = turn_k<kAdj>(a, p, blk, c, s, wa, wb, xa, xb);
+                    }
+                    if (row < a.Hkv)
+                        store_block_values<kUnitScale, true>(a.pool + ((slot >> a.log2P) * a.Hkv + row) * a.slab, a.dtype,
+                                                             (int)(slot & (a.P - 1)), !is_k, at, xa, xb, is_k ? a.gk : a.gv, policy);
+                } else {
+                    const int row = 8 * (sub - 2 * nk) + g;
+                    uint4 xa[2], xb[2];
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {
+                        const uint4 *x = reinterpret_cast<const uint4 *>(src + (row + 4 * e) * 256);
+                        xa[e] = xb[e] = make_uint4(0, 0, 0, 0);
+                        if (row + 4 * e < a.Hq) {
+                            xa[e] = x[p.ca];
+                            xb[e] = x[p.cb];
+                        }
+                    }
+                    words(weight_chunk(a.wq, p.ca), wa);
+                    words(weight_chunk(a.wq, p.cb), wb);
+                    Turn u;
+                    make_turn<kAdj>(a, c, s, wa, wb, u);
+#pragma unroll
+                    for (int e = 0; e < 2; e++) turn_q<kAdj>(a, u, xa[e], xb[e]);
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {
+                        if (row + 4 * e >= a.Hq) continue;
+                        uint4 *dst = a.q_out + t * a.out_stride16 + (row + 4 * e) * 16;
+                        dst[p.ca] = xa[e];
+                        dst[p.cb] = xb[e];
+                    }
+                }
+            }
+            turn = unit - n * per;                            // the next stage's units go on behind this one's
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&m.empty[st]);
+            if (++st == plan.stages) st = 0, ph ^= 1u;
+        }
+    }
+    if (!good) {
+        if (lane == 0 && !*abort_flag) flag_error(a.err, kErrTimeout);
+        *abort_flag = 1;
+    }
+}
+
+constexpr int kMaxDevicesR = 64;
+std::mutex g_mu_r;
+int g_sms_r[kMaxDevicesR];      // 0: not set up yet
 
 }  // namespace
 
@@ -345,18 +565,46 @@ cudaError_t launch_rope_append(const nvfp4kv_cache &c, const nvfp4kv_rope &rope,
     a.gv = c.v_global_scale;
     a.dtype = c.dtype;
     a.err = err;
-    // Four rows a warp while that does not fill the GPU (two CTAs on each of 152 SMs), more beyond.
-    const bool many = num_tokens * (a.Hq + 2 * a.Hkv) > 4 * 152 * 2 * kWarpsR;
-    const int jq = many ? 4 : 1, jv = many ? 2 : 1;
-    const int64_t warps = (a.Hq + 4 * jq - 1) / (4 * jq) + (a.Hkv + 3) / 4 + (a.Hkv + 4 * jv - 1) / (4 * jv);
-    const int64_t grid = ceil_div64(num_tokens * warps, kWarpsR);
     const bool unit = c.k_global_scale == 1.0f && c.v_global_scale == 1.0f;
-    void *args[] = {&a};
-    const void *fn = many ? (unit ? reinterpret_cast<const void *>(&rope_append_kernel<4, true>)
-                                  : reinterpret_cast<const void *>(&rope_append_kernel<4, false>))
-                          : (unit ? reinterpret_cast<const void *>(&rope_append_kernel<1, true>)
-                                  : reinterpret_cast<const void *>(&rope_append_kernel<1, false>));
-    return launch_pdl(fn, dim3((unsigned)grid), kThreadsR, 0, stream, args);
+    const int64_t groups = (a.Hq + 3) / 4 + 2 * ((a.Hkv + 3) / 4);
+    StreamPlan plan;
+    plan.token_bytes = (a.Hq + 2 * a.Hkv) * 256 + 4 * a.rot;
+    plan.tps = std::max(1, std::min(kMaxTps, 16 * 1024 / plan.token_bytes));
+    plan.stages = std::min(kMaxStages, (int)((kStreamBytes - sizeof(StreamMisc)) / ((size_t)plan.tps * plan.token_bytes)));
+    // A ring of two stages at least, and more groups of rows than the GPU's warps at once.
+    if (plan.stages < 2 || num_tokens * groups <= 152 * 2 * kWarpsR * 2) {
+        void *args[] = {&a};
+        const void *few[2][2] = {{reinterpret_cast<const void *>(&rope_append_kernel<false, false>),
+                                  reinterpret_cast<const void *>(&rope_append_kernel<false, true>)},
+                                 {reinterpret_cast<const void *>(&rope_append_kernel<true, false>),
+                                  reinterpret_cast<const void *>(&rope_append_kernel<true, true>)}};
+        return launch_pdl(few[unit][a.adjacent], dim3((unsigned)ceil_div64(num_tokens * groups, kWarpsR)), kThreadsR, 0, stream,
+                          args);
+    }
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && (dev < 0 || dev >= kMaxDevicesR)) e = cudaErrorInvalidDevice;
+    if (e != cudaSuccess) return e;
+    const void *fn[2][2] = {{reinterpret_cast<const void *>(&rope_stream_kernel<false, false>),
+                             reinterpret_cast<const void *>(&rope_stream_kernel<false, true>)},
+                            {reinterpret_cast<const void *>(&rope_stream_kernel<true, false>),
+                             reinterpret_cast<const void *>(&rope_stream_kernel<true, true>)}};
+    {
+        std::lock_guard<std::mutex> lock(g_mu_r);
+        if (!g_sms_r[dev]) {
+            for (int i = 0; i < 4; i++) {
+                e = cudaFuncSetAttribute(fn[i >> 1][i & 1], cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamBytes);
+                if (e != cudaSuccess) return e;
+            }
+            e = cudaDeviceGetAttribute(&g_sms_r[dev], cudaDevAttrMultiProcessorCount, dev);
+            if (e != cudaSuccess) return e;
+        }
+        sms = g_sms_r[dev];
+    }
+    void *args[] = {&a, &plan};
+    const int64_t grid = std::min((int64_t)2 * sms, (num_tokens + plan.tps - 1) / plan.tps);
+    return launch_pdl(fn[unit][a.adjacent], dim3((unsigned)grid), kThreadsS,
+                      (size_t)plan.stages * plan.tps * plan.token_bytes + sizeof(StreamMisc), stream, args);
 }
 
 }  // namespace nvfp4kv
