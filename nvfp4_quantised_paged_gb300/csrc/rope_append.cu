@@ -15,11 +15,13 @@
 // the cosines and sines once a warp, and its rows go through packed FP32 operations.
 //
 // K's rounding to BF16 decides the codes: a value on the other side of a BF16 border may
-// move a block's scale.  So K is formed from two floats: products and sums with their
-// rounding errors (fused multiply-adds, Knuth's two-sum), the sum of squares and the
-// reciprocal root as well, and the BF16 rounding breaks ties by the low part; it is the
-// rounding of the exact value up to a relative 2^-40 of the pair's larger product.  Q is formed in FP32
-// (a value within 2^-21 of a tie may round to the other neighbour).
+// move a block's scale.  So K's FP32 value is rounded twice, at both ends of its error bound,
+// and where they differ for some value of the warp (1 warp in 25, 1 in 8 with norms) its rows are formed
+// again from two floats: products and sums with their rounding errors (fused multiply-adds,
+// Knuth's two-sum), the sum of squares and the reciprocal root as well, and the BF16 rounding
+// breaks ties by the low part: the rounding of the exact value up to a relative 2^-40 of
+// the pair's larger product.  Q is formed in FP32 (a value within 2^-21 of a tie may round to the other
+// neighbour).
 #include <algorithm>
 #include <mutex>
 
@@ -192,50 +194,99 @@ __device__ __forceinline__ int turn_k(const RopeArgs &a, const Place &p, int blk
     uint32_t va[4], vb[4], ya[4], yb[4];
     words(xa, va);
     words(xb, vb);
-    Pair r = {1.0f, 0.0f};
-    if (a.wk) {
-        Pair q = {0.f, 0.f};
+    // FP32: y = r (u c + z s) is off by at most 2^-24 (|z s| + |y|), and with a norm by 2^-20.9 |y| more (a sum of
+    // squares of nine steps, 2^-21.8 in the root, its Newton step, the product); a rounding of the ends is allowed for.
+    uint32_t differ = 0;
+    {
+        float r = 1.0f, dm = 0x1p-23f, dy = 0x1p-23f;
+        if (a.wk) {
+            uint64_t qa = 0, qb = 0;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const uint64_t x = bf16_pair(va[i]), z = bf16_pair(vb[i]);
+                qa = fma_pair(x, x, qa);
+                qb = fma_pair(z, z, qb);
+            }
+            float sum = (low2(qa) + high2(qa)) + (low2(qb) + high2(qb));
+#pragma unroll
+            for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            const float m = fmaf(sum, 0.0078125f, a.eps), r0 = rsqrtf(m);
+            r = fmaf(0.5f * r0, fmaf(-m * r0, r0, 1.0f), r0);
+            dm *= r;
+            dy = 0x1.6p-21f;
+        }
+        auto both = [&](uint64_t u, uint64_t cc, uint64_t z, uint64_t ss) {
+            const uint64_t m = mul_pair(z, ss);
+            uint64_t y = fma_pair(u, cc, m);
+            if (a.wk) y = mul_pair(y, pack2(r, r));
+            const float e0 = fmaf(fabsf(low2(m)), dm, fabsf(low2(y)) * dy), e1 = fmaf(fabsf(high2(m)), dm, fabsf(high2(y)) * dy);
+            const uint32_t lo = f32x2_to_bf16x2(high2(y) - e1, low2(y) - e0), hi = f32x2_to_bf16x2(high2(y) + e1, low2(y) + e0);
+            differ |= lo ^ hi;
+            return lo;
+        };
+        if (p.turned || a.wk) {
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const uint64_t ua = mul_pair(bf16_pair(va[i]), bf16_pair(wa[i])), ub = mul_pair(bf16_pair(vb[i]), bf16_pair(wb[i]));
+                if (kAdj) {
+                    ya[i] = both(ua, pack2(c[i], c[i]), pack2(high2(ua), low2(ua)), pack2(-s[i], s[i]));
+                    yb[i] = both(ub, pack2(c[4 + i], c[4 + i]), pack2(high2(ub), low2(ub)), pack2(-s[4 + i], s[4 + i]));
+                } else {
+                    ya[i] = both(ua, pack2(c[2 * i], c[2 * i + 1]), ub, pack2(-s[2 * i], -s[2 * i + 1]));
+                    yb[i] = both(ub, pack2(c[2 * i], c[2 * i + 1]), ua, pack2(s[2 * i], s[2 * i + 1]));
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; i++) ya[i] = va[i], yb[i] = vb[i];
+        }
+    }
+    if (__any_sync(0xffffffffu, differ != 0)) {
+        Pair r = {1.0f, 0.0f};
+        if (a.wk) {
+            Pair q = {0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const float v[4] = {bf16_lo(va[i]), bf16_hi(va[i]), bf16_lo(vb[i]), bf16_hi(vb[i])};
+#pragma unroll
+                for (int e = 0; e < 4; e++) {                     // (a BF16 number's square is exact)
+                    const Pair n = two_sum(q.hi, __fmul_rn(v[e], v[e]));
+                    q = {n.hi, q.lo + n.lo};
+                }
+            }
+#pragma unroll
+            for (int d = 1; d < 8; d <<= 1) {
+                const float h = __shfl_xor_sync(0xffffffffu, q.hi, d), lo = __shfl_xor_sync(0xffffffffu, q.lo, d);
+                const Pair n = two_sum(q.hi, h);
+                q = {n.hi, (q.lo + lo) + n.lo};
+            }
+            r = root(q, a.eps);
+        }
+        // r (u cc + z ss) rounded to BF16, u and z exact products of 16 bits
+        auto exact = [&](float u, float cc, float z, float ss) {
+            Pair d = {u, 0.0f};
+            if (p.turned) {
+                const float h = __fmul_rn(u, cc), k = __fmul_rn(z, ss);
+                const Pair n = two_sum(h, k);
+                d = {n.hi, n.lo + (__fmaf_rn(u, cc, -h) + __fmaf_rn(z, ss, -k))};
+            }
+            if (a.wk) {
+                const float h = __fmul_rn(d.hi, r.hi);
+                d = {h, __fmaf_rn(d.lo, r.hi, __fmaf_rn(d.hi, r.lo, __fmaf_rn(d.hi, r.hi, -h)))};
+            }
+            return bf16_of_pair(d.hi, d.lo);
+        };
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-            const float v[4] = {bf16_lo(va[i]), bf16_hi(va[i]), bf16_lo(vb[i]), bf16_hi(vb[i])};
-#pragma unroll
-            for (int e = 0; e < 4; e++) {                     // (a BF16 number's square is exact)
-                const Pair n = two_sum(q.hi, __fmul_rn(v[e], v[e]));
-                q = {n.hi, q.lo + n.lo};
+            const float a0 = bf16_lo(va[i]) * bf16_lo(wa[i]), a1 = bf16_hi(va[i]) * bf16_hi(wa[i]);
+            const float b0 = bf16_lo(vb[i]) * bf16_lo(wb[i]), b1 = bf16_hi(vb[i]) * bf16_hi(wb[i]);
+            if (kAdj) {
+                ya[i] = exact(a0, c[i], a1, -s[i]) | (exact(a1, c[i], a0, s[i]) << 16);
+                yb[i] = exact(b0, c[4 + i], b1, -s[4 + i]) | (exact(b1, c[4 + i], b0, s[4 + i]) << 16);
+            } else {
+                ya[i] = exact(a0, c[2 * i], b0, -s[2 * i]) | (exact(a1, c[2 * i + 1], b1, -s[2 * i + 1]) << 16);
+                yb[i] = exact(b0, c[2 * i], a0, s[2 * i]) | (exact(b1, c[2 * i + 1], a1, s[2 * i + 1]) << 16);
             }
-        }
-#pragma unroll
-        for (int d = 1; d < 8; d <<= 1) {
-            const float h = __shfl_xor_sync(0xffffffffu, q.hi, d), lo = __shfl_xor_sync(0xffffffffu, q.lo, d);
-            const Pair n = two_sum(q.hi, h);
-            q = {n.hi, (q.lo + lo) + n.lo};
-        }
-        r = root(q, a.eps);
-    }
-    // r (u cc + z ss) rounded to BF16, u and z exact products of 16 bits
-    auto exact = [&](float u, float cc, float z, float ss) {
-        Pair d = {u, 0.0f};
-        if (p.turned) {
-            const float h = __fmul_rn(u, cc), k = __fmul_rn(z, ss);
-            const Pair n = two_sum(h, k);
-            d = {n.hi, n.lo + (__fmaf_rn(u, cc, -h) + __fmaf_rn(z, ss, -k))};
-        }
-        if (a.wk) {
-            const float h = __fmul_rn(d.hi, r.hi);
-            d = {h, __fmaf_rn(d.lo, r.hi, __fmaf_rn(d.hi, r.lo, __fmaf_rn(d.hi, r.hi, -h)))};
-        }
-        return bf16_of_pair(d.hi, d.lo);
-    };
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const float a0 = bf16_lo(va[i]) * bf16_lo(wa[i]), a1 = bf16_hi(va[i]) * bf16_hi(wa[i]);
-        const float b0 = bf16_lo(vb[i]) * bf16_lo(wb[i]), b1 = bf16_hi(vb[i]) * bf16_hi(wb[i]);
-        if (kAdj) {
-            ya[i] = exact(a0, c[i], a1, -s[i]) | (exact(a1, c[i], a0, s[i]) << 16);
-            yb[i] = exact(b0, c[4 + i], b1, -s[4 + i]) | (exact(b1, c[4 + i], b0, s[4 + i]) << 16);
-        } else {
-            ya[i] = exact(a0, c[2 * i], b0, -s[2 * i]) | (exact(a1, c[2 * i + 1], b1, -s[2 * i + 1]) << 16);
-            yb[i] = exact(b0, c[2 * i], a0, s[2 * i]) | (exact(b1, c[2 * i + 1], a1, s[2 * i + 1]) << 16);
         }
     }
     // Two threads of a half-split pair of chunks exchange one each: the even one quantises the block of the
@@ -447,9 +498,12 @@ __global__ void __launch_bounds__(kThreadsS, 2) rope_stream_kernel(RopeArgs a, S
             good = __all_sync(0xffffffffu, mbar_wait_bounded(&m.full[st], ph, kWaitLimitR, abort_flag));
             if (!good) break;
             const int n = (int)min((int64_t)plan.tps, a.num_tokens - tile * plan.tps);
-            int unit = turn;
-            for (; unit < n * per; unit += kWarpsR) {
-                const int i = unit / per, sub = unit - i * per;
+            for (int sub = turn, i = 0;; sub += kWarpsR) {
+                for (; sub >= per && i < n; i++) sub -= per;
+                if (i >= n) {
+                    turn = sub;                               // the next stage's units go on behind this one's
+                    break;
+                }
                 const int64_t slot = m.slot[st][i], t = tile * plan.tps + i;
                 if (slot == kNoToken || (sub < 2 * nk && slot < 0)) continue;
                 const uint8_t *src = smem + (st * plan.tps + i) * plan.token_bytes;
@@ -512,7 +566,6 @@ __global__ void __launch_bounds__(kThreadsS, 2) rope_stream_kernel(RopeArgs a, S
                     }
                 }
             }
-            turn = unit - n * per;                            // the next stage's units go on behind this one's
             __syncwarp();
             if (lane == 0) mbar_arrive(&m.empty[st]);
             if (++st == plan.stages) st = 0, ph ^= 1u;
