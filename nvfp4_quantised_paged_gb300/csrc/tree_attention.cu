@@ -433,28 +433,27 @@ __global__ void __launch_bounds__(kThreadsT, kCtasT) tree_kernel(TreeArgs a) {
             return held;
         };
         // V of the tile whose K was the last but one (or last) to shared memory; rows: those of the group that exist.
+        // Lanes q >= 2 take rows r ^ 2, so that a quarter warp's stores meet all banks.
         auto expand_v = [&](int rows) {
+            const int r0v = er ^ (eq & 2);
             const uint8_t *g = smem + L::kRaw + vs * kRawT + grp * kGroupT + 1152;
-            uint8_t *blk = smem + L::kV + (eq >> 1) * kBlockT;
+            uint8_t *blk = smem + L::kV + (eq >> 1) * kBlockT + (16 * grp + r0v) * 128;
 #pragma unroll
             for (int e = 0; e < 2; e++) {
-                const int r = er + 8 * e;
+                const int r = r0v + 8 * e;
                 uint4 c = *reinterpret_cast<const uint4 *>(g + r * 64 + eq * 16);
                 uint32_t s = (uint32_t)g[1024 + (2 * eq) * 16 + r] | ((uint32_t)g[1024 + (2 * eq + 1) * 16 + r] << 8);
-                if (r >= rows) {                          // may hold anything: zeros
+                if (rows < 16 && r >= rows) {             // may hold anything: zeros
                     c = make_uint4(0, 0, 0, 0);
                     s = 0;
                 }
-                // lanes q >= 2 store their words 2, 3, 0, 1, so that a quarter warp meets all banks
-                const bool sw = eq & 2;
                 s = e4m3x2_to_f16x2(s);
-                const uint32_t w[4] = {sw ? c.z : c.x, sw ? c.w : c.y, sw ? c.x : c.z, sw ? c.y : c.w};
+                const uint32_t w[4] = {c.x, c.y, c.z, c.w};
                 uint32_t f[16];
-                scaled(w, __byte_perm(s, 0, sw ? 0x3232 : 0x1010), __byte_perm(s, 0, sw ? 0x1010 : 0x3232), f);
-                const int tr = 16 * grp + r;
+                scaled(w, __byte_perm(s, 0, 0x1010), __byte_perm(s, 0, 0x3232), f);
 #pragma unroll
                 for (int m = 0; m < 4; m++)
-                    *reinterpret_cast<uint4 *>(blk + sw128_off(tr, (eq & 1) * 4 + (m ^ (eq & 2)))) =
+                    *reinterpret_cast<uint4 *>(blk + e * 1024 + ((((eq & 1) * 4 + m) ^ (r0v & 7)) << 4)) =
                         make_uint4(f[4 * m], f[4 * m + 1], f[4 * m + 2], f[4 * m + 3]);
             }
             __syncwarp();
