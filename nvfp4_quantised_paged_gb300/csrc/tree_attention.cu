@@ -588,29 +588,34 @@ __global__ void __launch_bounds__(kThreadsT, kCtasT) tree_kernel(TreeArgs a) {
                     }
                     return z;
                 };
-                // d = z - m + 7
-                float d[CW];
-                auto load_scores = [&]() {
-                    uint32_t x[CW];
-                    load_columns<CW>(tS, x);
-                    const float4 *fac = reinterpret_cast<const float4 *>(s_fac + wg * CW);
-                    const float4 *off = reinterpret_cast<const float4 *>(s_off + wg * CW);
+                // d = z - m + 7, CH rows at a time: with 32 rows a warpgroup once to see whether a maximum must
+                // move and again to form P (held in registers they spill: %(m)s)
+                constexpr int CH = CW < 16 ? CW : 16;
+                float d[CH];
+                auto load_scores = [&](int c0) {
+                    uint32_t x[CH];
+                    load_columns<CH>(tS + c0, x);
+                    const float4 *fac = reinterpret_cast<const float4 *>(s_fac + wg * CW + c0);
+                    const float4 *off = reinterpret_cast<const float4 *>(s_off + wg * CW + c0);
                     tc_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < CW; i += 4) {
+                    for (int i = 0; i < CH; i += 4) {
                         const float4 o = off[i / 4], f = OPT ? make_float4(0.f, 0.f, 0.f, 0.f) : fac[i / 4];
-                        d[i] = OPT ? score(x[i], i) + o.x : fmaf(__uint_as_float(x[i]), f.x, o.x);
-                        d[i + 1] = OPT ? score(x[i + 1], i + 1) + o.y : fmaf(__uint_as_float(x[i + 1]), f.y, o.y);
-                        d[i + 2] = OPT ? score(x[i + 2], i + 2) + o.z : fmaf(__uint_as_float(x[i + 2]), f.z, o.z);
-                        d[i + 3] = OPT ? score(x[i + 3], i + 3) + o.w : fmaf(__uint_as_float(x[i + 3]), f.w, o.w);
+                        d[i] = OPT ? score(x[i], c0 + i) + o.x : fmaf(__uint_as_float(x[i]), f.x, o.x);
+                        d[i + 1] = OPT ? score(x[i + 1], c0 + i + 1) + o.y : fmaf(__uint_as_float(x[i + 1]), f.y, o.y);
+                        d[i + 2] = OPT ? score(x[i + 2], c0 + i + 2) + o.z : fmaf(__uint_as_float(x[i + 2]), f.z, o.z);
+                        d[i + 3] = OPT ? score(x[i + 3], c0 + i + 3) + o.w : fmaf(__uint_as_float(x[i + 3]), f.w, o.w);
                     }
                 };
-                load_scores();
-                float top = fmaxf(d[0], d[1]), top2 = fmaxf(d[2], d[3]);
+                float top = kNegInfT, top2 = kNegInfT;
 #pragma unroll
-                for (int c = 4; c < CW; c += 4) {
-                    top = max3(top, d[c], d[c + 1]);
-                    top2 = max3(top2, d[c + 2], d[c + 3]);
+                for (int c0 = 0; c0 < CW; c0 += CH) {
+                    load_scores(c0);
+#pragma unroll
+                    for (int c = 0; c < CH; c += 4) {
+                        top = max3(top, d[c], d[c + 1]);
+                        top2 = max3(top2, d[c + 2], d[c + 3]);
+                    }
                 }
                 if (group_any(wg, fmaxf(top, top2) > kRescaleT + kPOffsetT)) {
                     float *wmax = reinterpret_cast<float *>(smem + L::kWarpMax) + wg * 4 * CW;
@@ -651,15 +656,16 @@ __global__ void __launch_bounds__(kThreadsT, kCtasT) tree_kernel(TreeArgs a) {
                         }
                         tc_wait_st();
                     }
-                    load_scores();
+                    if (CW == CH) load_scores(0);
                 }
                 uint8_t *pt = smem + L::kP;
 #pragma unroll
                 for (int c0 = 0; c0 < CW; c0 += 8) {
+                    if (CW > CH && c0 % CH == 0) load_scores(c0);
                     uint32_t pw[4];
 #pragma unroll
                     for (int e = 0; e < 4; e++) {
-                        pw[e] = f32x2_to_f16x2(ex2(d[c0 + 2 * e + 1]), ex2(d[c0 + 2 * e]));
+                        pw[e] = f32x2_to_f16x2(ex2(d[c0 % CH + 2 * e + 1]), ex2(d[c0 % CH + 2 * e]));
                         add_f16x2(l[c0 + 2 * e], l[c0 + 2 * e + 1], pw[e]);
                     }
                     *reinterpret_cast<uint4 *>(pt + sw128_off(row, (wg * CW + c0) / 8)) = make_uint4(pw[0], pw[1], pw[2], pw[3]);
