@@ -53,10 +53,15 @@ namespace nvfp4kv {
 
 namespace {
 
-constexpr int kWorkersT = 256;                // warps 0 .. 7
-constexpr int kThreadsT = kWorkersT + 64;     // + the MMA warp (8) and the load warp (9)
-constexpr int kMmaWarp = kWorkersT / 32, kLoadWarp = kMmaWarp + 1;
-constexpr int kCtasT = 2;                     // CTAs an SM
+// Up to 64 rows a tile: eight workers, two CTAs an SM.  With 128: sixteen workers, one CTA.
+template <int N>
+constexpr bool kWide = N == 128;
+template <int N>
+constexpr int kWorkersT = kWide<N> ? 512 : 256;
+template <int N>
+constexpr int kThreadsT = kWorkersT<N> + 64;  // + the MMA warp and the load warp
+template <int N>
+constexpr int kCtasT = kWide<N> ? 1 : 2;      // CTAs an SM
 constexpr int kTileT = 128;                   // tokens a tile
 constexpr int kBlockT = kTileT * 128;         // bytes of a column block: 64 dims (or rows of P) of 128 tokens
 constexpr int kGroupT = 2304;                 // bytes of a 16-token group
@@ -70,26 +75,28 @@ constexpr int kPairUnits = 1;                 // what a pair's start costs a CTA
 
 template <int N>
 struct TSmem {
+    static constexpr bool kW = kWide<N>;
     static constexpr int kStages = N == 64 ? 2 : 3;
     static constexpr int kQBlock = N * 128;                       // a column block of Q, [N][64]
     static constexpr int kQ = 0;
     static constexpr int kV = 2 * kQBlock;                        // two column blocks
-    static constexpr int kP = kV + 2 * kBlockT;                   // FP16 [128 tokens][64], N rows used
-    static constexpr int kRaw = kP + kBlockT;
+    static constexpr int kP = kV + (kW ? 3 : 1) * 2 * kBlockT;    // FP16 [N / 64][128 tokens][64]
+    static constexpr int kRaw = kP + (kW ? 2 : 1) * kBlockT;
     static constexpr int kBar = kRaw + kStages * kRawT;
-    static constexpr int kNumBars = 3 + 2 * kStages;              // ready done drain raw_full[] raw_free[]
+    static constexpr int kFirstRaw = kW ? 8 : 3;                  // ready done drain; 128 rows: k_ready[2] scored[2] pv_odd too
+    static constexpr int kNumBars = kFirstRaw + 2 * kStages;      // raw_full[] raw_free[]
     static constexpr int kMisc = kBar + 8 * kNumBars;             // tmem base, abort, valid[kStages]
-    static constexpr int kM = (kMisc + 8 + 4 * kStages + 15) & ~15;   // float m[N], fac[N], alpha[N], off[N], slope[N], depth[N]
-    static constexpr int kRow = kM + 6 * N * 4;                   // int row[N] (-1: none), draft[N]
-    static constexpr int kWarpMax = kRow + 2 * N * 4;             // float [2][4][N / 2]
+    static constexpr int kM = (kMisc + 8 + 4 * kStages + 15) & ~15;   // float m[N], fac[N], alpha[N], off[N], slope[N], depth[N], in[N]
+    static constexpr int kRow = kM + 7 * N * 4;                   // int row[N] (-1: none), draft[N]
+    static constexpr int kWarpMax = kRow + 2 * N * 4;             // float [warpgroups][4][rows of one]
     static constexpr int kMask = kWarpMax + 4 * N * 4;            // u64 mask[64], int depth[64]
     static constexpr int kBytes = kMask + 64 * 12;
-    // TMEM columns: O at 0, S, K[2]
-    static constexpr uint32_t kColS = N, kColK = 2 * N, kCols = 256;
-    static_assert(kColK + 128 <= kCols && kCtasT * kCols <= 512, "TMEM columns");
+    // TMEM columns: O at 0, S (two with 128 rows), K[2]
+    static constexpr uint32_t kColS = N, kColK = (kW ? 3 : 2) * N, kCols = kW ? 512 : 256;
+    static_assert(kColK + 128 <= kCols && kCtasT<N> * kCols <= 512, "TMEM columns");
     static_assert(kV % 1024 == 0 && kP % 1024 == 0 && kRaw % 1024 == 0 && kBar % 16 == 0 && kMask % 8 == 0, "alignment");
-    static_assert(kCtasT * (kBytes + 1024) <= 228 * 1024, "shared memory of an SM");
-    static_assert(sizeof(FlatScratch<kThreadsT>) <= 2 * kBlockT, "the plan's scratch lies in the V tile");
+    static_assert(kCtasT<N> * (kBytes + 1024) <= 228 * 1024, "shared memory of an SM");
+    static_assert(sizeof(FlatScratch<kThreadsT<N>>) <= 2 * kBlockT, "the plan's scratch lies in the V tile");
 };
 
 struct TreeArgs {
@@ -181,9 +188,10 @@ __device__ __forceinline__ void add_f16x2(float &s0, float &s1, uint32_t w) {
         : "r"(w), "h"(one));
 }
 
-// Barriers 1, 2: the working warpgroups; 3: both of them.
+// Barriers 1 .. 4: the working warpgroups; 5: all of them.
 __device__ __forceinline__ void group_sync(int wg) { asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory"); }
-__device__ __forceinline__ void workers_sync() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void workers_sync() { asm volatile("bar.sync 5, %0;" ::"n"(kWorkersT<N>) : "memory"); }
 
 __device__ __forceinline__ bool group_any(int wg, bool p) {
     uint32_t r;
@@ -228,18 +236,24 @@ __device__ __forceinline__ void load_columns(uint32_t taddr, uint32_t (&r)[C]) {
 
 // OPT: the scores are capped or biased, or their factor is not positive.
 template <int N, bool OPT>
-__global__ void __launch_bounds__(kThreadsT, kCtasT) tree_kernel(TreeArgs a) {
+__global__ void __launch_bounds__(kThreadsT<N>, kCtasT<N>) tree_kernel(TreeArgs a) {
     using L = TSmem<N>;
-    constexpr int CW = N / 2;                     // rows per warpgroup
+    constexpr bool W = kWide<N>;
+    constexpr int kWarps = kWorkersT<N> / 32, kMmaWarp = kWarps, kLoadWarp = kWarps + 1;
+    constexpr int CW = N / (kWarps / 4);          // rows per warpgroup
     constexpr int S = L::kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBar);
-    uint64_t *ready = bars, *done = bars + 1, *drain = bars + 2, *raw_full = bars + 3, *raw_free = raw_full + S;
+    uint64_t *ready = bars, *done = bars + 1, *drain = bars + 2, *raw_full = bars + L::kFirstRaw, *raw_free = raw_full + S;
+    // 128 rows: pairs of barriers, by the tile's parity -- the first waits of a tile may follow the next one's arrivals
+    auto k_ready = [&](uint32_t j) { return bars + 3 + (j & 1); };
+    auto scored = [&](uint32_t j) { return bars + 5 + (j & 1); };
+    auto pv_done = [&](uint32_t j) { return j & 1 ? bars + 7 : done; };
     uint32_t &tmem_base = *reinterpret_cast<uint32_t *>(smem + L::kMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 4);
     volatile int *s_valid = abort_flag + 1;
     float *s_m = reinterpret_cast<float *>(smem + L::kM), *s_fac = s_m + N, *s_alpha = s_fac + N, *s_off = s_alpha + N;
-    float *s_slope = s_off + N, *s_dep = s_slope + N;
+    float *s_slope = s_off + N, *s_dep = s_slope + N, *s_in = s_dep + N;
     int *s_row = reinterpret_cast<int *>(smem + L::kRow), *s_draft = s_row + N;
     uint64_t *s_mask = reinterpret_cast<uint64_t *>(smem + L::kMask);
     int *s_depth = reinterpret_cast<int *>(s_mask + 64);
@@ -247,7 +261,7 @@ __global__ void __launch_bounds__(kThreadsT, kCtasT) tree_kernel(TreeArgs a) {
     const int r0 = blockIdx.y * N;
     if (tid == 0) {
         for (int i = 0; i < L::kNumBars; i++)
-            mbar_init(&bars[i], i == 0 || i >= 3 + S ? kWorkersT / 32 : 1);
+            mbar_init(&bars[i], i == 0 || i >= L::kFirstRaw + S ? kWarps : W && (i == 3 || i == 4) ? kWarps / 2 : 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -257,8 +271,8 @@ __global__ void __launch_bounds__(kThreadsT, kCtasT) tree_kernel(TreeArgs a) {
 
     int b0;
     unsigned first, u0 = 0, u1 = 0;
-    flat_locate<kThreadsT>(
-        *reinterpret_cast<FlatScratch<kThreadsT> *>(smem + L::kV), a.B,
+    flat_locate<kThreadsT<N>>(
+        *reinterpret_cast<FlatScratch<kThreadsT<N>> *>(smem + L::kV), a.B,
         [&](int b) { return (unsigned)a.Hkv * pair_units(a, seq_of(a, b), r0); },
         [&](unsigned total) {
             const FlatCut cut(total, a.splits);
@@ -306,34 +320,64 @@ __global__ void __launch_bounds__(kThreadsT, kCtasT) tree_kernel(TreeArgs a) {
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         const bool leader = elect_one();
         // operand descriptors; a step adds its byte offset / 16 to the address field
-        const uint64_t dQ = smem_desc_sw128(sbase + L::kQ, 16, 1024), dP = smem_desc_sw128(sbase + L::kP, 16, 1024);
+        const uint64_t dQ = smem_desc_sw128(sbase + L::kQ, 16, 1024), dP = smem_desc_sw128(sbase + L::kP, kBlockT, 1024);
         const uint64_t dV = smem_desc_sw128(sbase + L::kV, kBlockT, 1024);
+        auto scores = [&](uint32_t kb, uint32_t sb) {      // S^T from K's buffer kb
+#pragma unroll
+            for (int kk = 0; kk < 8; kk++)
+                tc_mma_bf16_tmem_a(tm + L::kColS + sb * N, tm + L::kColK + kb * 64 + kk * 8,
+                                   dQ + ((kk >> 2) * (L::kQBlock / 16) + (kk & 3) * 2), idesc_s, kk > 0);
+        };
+        auto output = [&](uint32_t vb, uint32_t acc) {     // O^T (+)= V^T P^T; 16 tokens: 2,048 bytes of a column block, and of P
+            const uint64_t v = dV + vb * (2 * kBlockT / 16);
+#pragma unroll
+            for (int kk = 0; kk < 8; kk++) tc_mma_bf16(tm, v + kk * 128, dP + kk * 128, idesc_o, kk > 0 ? 1u : acc);
+        };
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            const bool good = __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag));
+            tc_fence_after();
+            return good;
+        };
         bool ok = true;
-        uint32_t phase = 0, kb = 0;                  // kb: K's buffer
-        do {
-            const int t0 = it.t;
-            for (int t = t0 - 1; t < it.te; t++) {   // (t0 - 1: the pair's Q and its first K)
-                ok = __all_sync(0xffffffffu, wait_bar(ready, phase++ & 1, abort_flag));
-                tc_fence_after();
-                if (!ok) break;
-                if (leader) {
-                    if (t + 1 < it.te) {             // S^T of the next tile
-#pragma unroll
-                        for (int kk = 0; kk < 8; kk++)
-                            tc_mma_bf16_tmem_a(tm + L::kColS, tm + L::kColK + kb * 64 + kk * 8,
-                                               dQ + ((kk >> 2) * (L::kQBlock / 16) + (kk & 3) * 2), idesc_s, kk > 0);
+        if constexpr (W) {
+            uint32_t j = 0, kp = 0, vb = 0;                // tile, K tiles taken, V's buffer
+            do {
+                for (int t = it.t - 1; ok && t < it.te; t++) {   // (t = it.t - 1: the pair's Q and its first K)
+                    if (t + 1 < it.te) {
+                        ok = wait(k_ready(kp), (kp >> 1) & 1);
+                        if (!ok) break;
+                        if (leader) {
+                            scores(kp & 1, kp & 1);
+                            tc_commit(scored(kp));
+                        }
+                        kp++;
                     }
-                    if (t >= t0) {
-                        const uint32_t acc = t == t0 ? 0u : 1u;
-#pragma unroll
-                        for (int kk = 0; kk < 8; kk++)   // 16 tokens: 2,048 bytes of a column block, and of P
-                            tc_mma_bf16(tm, dV + kk * 128, dP + kk * 128, idesc_o, kk > 0 ? 1u : acc);
+                    if (t < it.t) continue;
+                    ok = wait(ready, j & 1);
+                    if (!ok) break;
+                    if (leader) {
+                        output(vb, t == it.t ? 0u : 1u);
+                        tc_commit(pv_done(j));
                     }
-                    tc_commit(done);
+                    vb = vb == 2 ? 0 : vb + 1;
+                    j++;
                 }
-                if (t + 1 < it.te) kb ^= 1u;
-            }
-        } while (ok && next_pair(a, it, r0));
+            } while (ok && next_pair(a, it, r0));
+        } else {
+            uint32_t phase = 0, kb = 0;                    // kb: K's buffer
+            do {
+                for (int t = it.t - 1; t < it.te; t++) {   // (t = it.t - 1: the pair's Q and its first K)
+                    ok = wait(ready, phase++ & 1);
+                    if (!ok) break;
+                    if (leader) {
+                        if (t + 1 < it.te) scores(kb, 0);  // of the next tile
+                        if (t >= it.t) output(0, t == it.t ? 0u : 1u);
+                        tc_commit(done);
+                    }
+                    if (t + 1 < it.te) kb ^= 1u;
+                }
+            } while (ok && next_pair(a, it, r0));
+        }
         if (!ok && leader) {
             if (!*abort_flag) flag_error(a.err, kErrTimeout);
             *abort_flag = 1;
@@ -389,11 +433,11 @@ __global__ void __launch_bounds__(kThreadsT, kCtasT) tree_kernel(TreeArgs a) {
             }
             __syncwarp();
         };
-        const int wg = warp >> 2, quarter = warp & 3, row = 32 * quarter + lane;   // softmax: rows' half, token
+        const int wg = warp >> 2, quarter = warp & 3, row = 32 * quarter + lane;   // softmax: rows' part, token
         const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
         const int er = lane >> 2, eq = lane & 3;
         // expanding: 16-token group grp of the tile (its TMEM lanes are this warp's to reach)
-        const int grp = 2 * quarter + wg;
+        const int grp = 2 * quarter + (wg & 1);
         uint32_t ks = 0, ksp = 0, vs = 0, kb = 0;   // the raw stages whose K and V come next, K's parity and buffer
 
         // 16 dims a word pair of 16-byte piece eq, times the scales of its two blocks
@@ -404,6 +448,10 @@ __global__ void __launch_bounds__(kThreadsT, kCtasT) tree_kernel(TreeArgs a) {
 #pragma unroll
                 for (int i = 0; i < 4; i++) f[4 * m + i] = hmul2(f[4 * m + i], m < 2 ? s0 : s1);
             }
+        };
+        auto free_stage = [&](uint32_t st) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&raw_free[st]);
         };
         // K of the next raw tile to TMEM; returns the groups that the tile holds.  (Rows that do
         // not exist: their scores are masked.)
@@ -429,15 +477,16 @@ __global__ void __launch_bounds__(kThreadsT, kCtasT) tree_kernel(TreeArgs a) {
                 tc_st_16x256_x4(tmem + ((uint32_t)(16 * grp) << 16) + L::kColK + 64 * kb + 32 * h, v);
             }
             kb ^= 1u;
+            if (W) free_stage(ks);
             if (++ks == S) ks = 0, ksp ^= 1u;
             return held;
         };
-        // V of the tile whose K was the last but one (or last) to shared memory; rows: those of the group that exist.
+        // V of the tile of stage vs to shared memory, buffer vb; rows: those of the group that exist.
         // Lanes q >= 2 take rows r ^ 2, so that a quarter warp's stores meet all banks.
-        auto expand_v = [&](int rows) {
+        auto expand_v = [&](int rows, uint32_t vb) {
             const int r0v = er ^ (eq & 2);
             const uint8_t *g = smem + L::kRaw + vs * kRawT + grp * kGroupT + 1152;
-            uint8_t *blk = smem + L::kV + (eq >> 1) * kBlockT + (16 * grp + r0v) * 128;
+            uint8_t *blk = smem + L::kV + (2 * vb + (eq >> 1)) * kBlockT + (16 * grp + r0v) * 128;
 #pragma unroll
             for (int e = 0; e < 2; e++) {
                 const int r = r0v + 8 * e;
@@ -456,9 +505,28 @@ __global__ void __launch_bounds__(kThreadsT, kCtasT) tree_kernel(TreeArgs a) {
                     *reinterpret_cast<uint4 *>(blk + e * 1024 + ((((eq & 1) * 4 + m) ^ (r0v & 7)) << 4)) =
                         make_uint4(f[4 * m], f[4 * m + 1], f[4 * m + 2], f[4 * m + 3]);
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&raw_free[vs]);
+            free_stage(vs);
             if (++vs == S) vs = 0;
+        };
+        // 128 rows: K by the first two warpgroups, V by the others, of tile j (from tok0 on).  V's buffer was read last by
+        // the product of tile j - 3 (which is done where the tile is its pair's first).
+        uint32_t vb = 0;
+        auto expand_wide = [&](int n, int tok0, uint32_t j, bool first) {
+            if (wg < 2) {
+                const int held = expand_k();
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(k_ready(j));
+                return held;
+            }
+            wait(&raw_full[vs], ksp);
+            const int held = s_valid[vs];
+            if (!first && j >= 3) wait(pv_done(j - 3), ((j - 3) >> 1) & 1);
+            expand_v((held >> grp) & 1 ? n - (tok0 + 16 * grp) : 0, vb);
+            vb = vb == 2 ? 0 : vb + 1;
+            if (vs == 0) ksp ^= 1u;
+            return held;
         };
         // What this warp has put into TMEM and shared memory is the MMA warp's.
         auto hand_over = [&]() {
@@ -472,18 +540,18 @@ __global__ void __launch_bounds__(kThreadsT, kCtasT) tree_kernel(TreeArgs a) {
         // epilogue are done.)
         auto load_pair = [&](const TreeIter &x) {
             const int rows = x.s.d * a.G;
-            uint2 qw[N / 8];
-            int at[N / 8];                      // a row of q, -1: none
+            uint2 qw[N / kWarps];
+            int at[N / kWarps];                 // a row of q, -1: none
 #pragma unroll
-            for (int k = 0; k < N / 8; k++) {
-                const int r = r0 + warp + 8 * k, i = r / a.G;
+            for (int k = 0; k < N / kWarps; k++) {
+                const int r = r0 + warp + kWarps * k, i = r / a.G;
                 at[k] = r < rows ? (x.s.q0 + i) * a.Hq + x.kv * a.G + (r - i * a.G) : -1;
                 qw[k] = make_uint2(0, 0);
                 if (r < rows) qw[k] = __ldg(reinterpret_cast<const uint2 *>(a.q + (int64_t)at[k] * kHeadDim) + lane);
             }
 #pragma unroll
-            for (int k = 0; k < N / 8; k++) {
-                const int c = warp + 8 * k;
+            for (int k = 0; k < N / kWarps; k++) {
+                const int c = warp + kWarps * k;
                 const uint2 w = qw[k];
                 uint32_t m = max_u16x2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu);
                 m = __reduce_max_sync(0xffffffffu, max(m >> 16, m & 0xffffu));
@@ -499,7 +567,8 @@ __global__ void __launch_bounds__(kThreadsT, kCtasT) tree_kernel(TreeArgs a) {
                     const float fac = (OPT && a.cap_log2 > 0.f ? a.cap_in : a.score_log2) * __uint_as_float((uint32_t)(127 - kq) << 23);
                     // (a positive factor stays one, so that minus infinity times it is minus infinity: no score
                     // reaches 2^34, and 2^-92 is none)
-                    s_fac[c] = OPT ? fac : fmaxf(fac, 0x1p-126f);
+                    s_fac[c] = OPT ? 1.f : fmaxf(fac, 0x1p-126f);
+                    if (OPT) s_in[c] = fac;
                     s_m[c] = kNegInfT;
                     s_off[c] = kNoMaxT;
                     s_row[c] = at[k];
@@ -514,10 +583,11 @@ __global__ void __launch_bounds__(kThreadsT, kCtasT) tree_kernel(TreeArgs a) {
                 s_mask[tid] = mk;
                 s_depth[tid] = __popcll(mk) - 1;
             }
-            workers_sync();
+            if (W) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // Q, before any warp reports K
+            workers_sync<N>();
             if (OPT) {
                 if (tid < N) s_dep[tid] = (float)s_depth[s_draft[tid]];
-                workers_sync();
+                workers_sync<N>();
             }
         };
         // Which of the warpgroup's rows do not see the thread's token (bit c: row c).
@@ -534,60 +604,72 @@ __global__ void __launch_bounds__(kThreadsT, kCtasT) tree_kernel(TreeArgs a) {
             return gone;
         };
 
-        uint32_t phase = 0;
+        uint32_t phase = 0;                         // up to 64 rows: products awaited; 128: tiles
         do {
             load_pair(it);
             float l[CW];
 #pragma unroll
             for (int c = 0; c < CW; c++) l[c] = 0.f;
-            int held = 0, held_next = expand_k();   // the groups that a raw tile holds
-            hand_over();
             int tok0 = (it.s.t0 + it.t) * kTileT;
+            int held = 0, held_next;                // the groups that a raw tile holds
+            if constexpr (W) {
+                held_next = expand_wide(it.s.n, tok0, phase, true);
+            } else {
+                held_next = expand_k();
+                hand_over();
+            }
             for (int t = it.t; t < it.te; t++, tok0 += kTileT) {
-                // The products handed over last run while K of the next tile is unpacked.
                 held = held_next;
-                if (t + 1 < it.te) held_next = expand_k();
-                // This tile's scores are there, O^T holds the tiles before: V and P may be written.
-                wait(done, phase++ & 1);
-                tc_fence_after();
-                expand_v((held >> grp) & 1 ? it.s.n - (tok0 + 16 * grp) : 0);
+                if constexpr (W) {
+                    if (t + 1 < it.te) held_next = expand_wide(it.s.n, tok0 + kTileT, phase + 1, false);
+                    wait(scored(phase), (phase >> 1) & 1);
+                    tc_fence_after();
+                } else {
+                    // The products handed over last run while K of the next tile is unpacked.
+                    if (t + 1 < it.te) held_next = expand_k();
+                    // This tile's scores are there, O^T holds the tiles before: V and P may be written.
+                    wait(done, phase++ & 1);
+                    tc_fence_after();
+                    expand_v((held >> grp) & 1 ? it.s.n - (tok0 + 16 * grp) : 0, 0);
+                }
 
                 // ---- softmax of the token's scores for the warpgroup's rows
                 const int tok = tok0 + row;
                 // edge: a token of the tile that some row does not see
                 const bool edge = tok0 + kTileT > it.s.base || (a.window > 0 && tok0 <= it.s.n - 1 - a.window) || held != 0xff;
-                const uint32_t tS = tmem + lanes + L::kColS + wg * CW, tO = tmem + lanes + wg * CW;
-                uint32_t gone = 0;
-                if (edge) {
-                    gone = unseen(it.s, tok, held);
-                    if (!OPT) {                     // scores of what is not seen: minus infinity
+                const uint32_t tS = tmem + lanes + L::kColS + (W ? (phase & 1) * N : 0) + wg * CW, tO = tmem + lanes + wg * CW;
+                if (OPT || edge) {                  // in place: the capped and biased scores, minus infinity where nothing is seen
+                    const uint32_t gone = edge ? unseen(it.s, tok, held) : 0u;
+                    const int rel = tok - it.s.base;
+                    const float key = OPT ? (float)(rel < 0 ? rel : s_depth[min(rel, 63)]) : 0.f;   // the token's position, from base on
 #pragma unroll 1
-                        for (int c0 = 0; c0 < CW; c0 += 8) {
-                            uint32_t x[8];
-                            tc_ld8(tS + c0, x);
-                            tc_wait_ld();
+                    for (int c0 = 0; c0 < CW; c0 += 8) {
+                        uint32_t x[8];
+                        tc_ld8(tS + c0, x);
+                        tc_wait_ld();
+                        if (OPT) {
+                            float in[8], slope[8], dep[8];
 #pragma unroll
-                            for (int c = 0; c < 8; c++)
-                                if ((gone >> (c0 + c)) & 1) x[c] = 0xff800000u;
-                            tc_st8(tS + c0, x);
+                            for (int i = 0; i < 2; i++) {
+                                *reinterpret_cast<float4 *>(in + 4 * i) = reinterpret_cast<const float4 *>(s_in + wg * CW + c0)[i];
+                                *reinterpret_cast<float4 *>(slope + 4 * i) = reinterpret_cast<const float4 *>(s_slope + wg * CW + c0)[i];
+                                *reinterpret_cast<float4 *>(dep + 4 * i) = reinterpret_cast<const float4 *>(s_dep + wg * CW + c0)[i];
+                            }
+#pragma unroll
+                            for (int c = 0; c < 8; c++) {
+                                float z = __uint_as_float(x[c]) * in[c];
+                                if (a.cap_log2 > 0.f)        // cap tanh(x) = cap - 2 cap / (1 + e^(2 x))
+                                    z = fmaf(-2.0f * a.cap_log2, rcp_approx(ex2(z) + 1.0f), a.cap_log2);
+                                x[c] = __float_as_uint(fmaf(slope[c], key - dep[c], z));
+                            }
                         }
-                        tc_wait_st();
+#pragma unroll
+                        for (int c = 0; c < 8; c++)
+                            if ((gone >> (c0 + c)) & 1) x[c] = 0xff800000u;
+                        tc_st8(tS + c0, x);
                     }
+                    tc_wait_st();
                 }
-                const int rel = tok - it.s.base;
-                const float key = OPT ? (float)(rel < 0 ? rel : s_depth[min(rel, 63)]) : 0.f;   // the token's position, from base on
-                auto score = [&](uint32_t x, int c) {        // z in base 2
-                    float z = __uint_as_float(x) * s_fac[wg * CW + c];
-                    if (OPT) {
-                        if (a.cap_log2 > 0.f) {              // cap tanh(x) = cap - 2 cap / (1 + e^(2 x))
-                            const float e = ex2(z) + 1.0f;
-                            z = fmaf(-2.0f * a.cap_log2, rcp_approx(e), a.cap_log2);
-                        }
-                        z = fmaf(s_slope[wg * CW + c], key - s_dep[wg * CW + c], z);
-                        if ((gone >> c) & 1) z = kNegInfT;
-                    }
-                    return z;
-                };
                 // d = z - m + 7, CH rows at a time: with 32 rows a warpgroup once to see whether a maximum must
                 // move and again to form P (held in registers they spill: %(m)s)
                 constexpr int CH = CW < 16 ? CW : 16;
@@ -600,11 +682,11 @@ __global__ void __launch_bounds__(kThreadsT, kCtasT) tree_kernel(TreeArgs a) {
                     tc_wait_ld();
 #pragma unroll
                     for (int i = 0; i < CH; i += 4) {
-                        const float4 o = off[i / 4], f = OPT ? make_float4(0.f, 0.f, 0.f, 0.f) : fac[i / 4];
-                        d[i] = OPT ? score(x[i], c0 + i) + o.x : fmaf(__uint_as_float(x[i]), f.x, o.x);
-                        d[i + 1] = OPT ? score(x[i + 1], c0 + i + 1) + o.y : fmaf(__uint_as_float(x[i + 1]), f.y, o.y);
-                        d[i + 2] = OPT ? score(x[i + 2], c0 + i + 2) + o.z : fmaf(__uint_as_float(x[i + 2]), f.z, o.z);
-                        d[i + 3] = OPT ? score(x[i + 3], c0 + i + 3) + o.w : fmaf(__uint_as_float(x[i + 3]), f.w, o.w);
+                        const float4 o = off[i / 4], f = fac[i / 4];
+                        d[i] = fmaf(__uint_as_float(x[i]), f.x, o.x);
+                        d[i + 1] = fmaf(__uint_as_float(x[i + 1]), f.y, o.y);
+                        d[i + 2] = fmaf(__uint_as_float(x[i + 2]), f.z, o.z);
+                        d[i + 3] = fmaf(__uint_as_float(x[i + 3]), f.w, o.w);
                     }
                 };
                 float top = kNegInfT, top2 = kNegInfT;
@@ -627,7 +709,7 @@ __global__ void __launch_bounds__(kThreadsT, kCtasT) tree_kernel(TreeArgs a) {
                         tc_wait_ld();
 #pragma unroll
                         for (int c = 0; c < 8; c++) {
-                            const int mx = __reduce_max_sync(0xffffffffu, ordered(score(x[c], c0 + c)));
+                            const int mx = __reduce_max_sync(0xffffffffu, ordered(__uint_as_float(x[c]) * s_fac[wg * CW + c0 + c]));
                             if (lane == c0 + c) mine = mx;
                         }
                     }
@@ -644,6 +726,10 @@ __global__ void __launch_bounds__(kThreadsT, kCtasT) tree_kernel(TreeArgs a) {
 #pragma unroll
                     for (int c = 0; c < CW; c++) l[c] *= s_alpha[wg * CW + c];
                     if (t > it.t) {                 // O^T holds the earlier tiles: rescale the warpgroup's rows
+                        if (W) {
+                            wait(pv_done(phase - 1), ((phase - 1) >> 1) & 1);
+                            tc_fence_after();
+                        }
 #pragma unroll 1
                         for (int c0 = 0; c0 < CW; c0 += 8) {
                             uint32_t x[8];
@@ -658,7 +744,8 @@ __global__ void __launch_bounds__(kThreadsT, kCtasT) tree_kernel(TreeArgs a) {
                     }
                     if (CW == CH) load_scores(0);
                 }
-                uint8_t *pt = smem + L::kP;
+                if (W && phase > 0) wait(pv_done(phase - 1), ((phase - 1) >> 1) & 1);    // P is read
+                uint8_t *pt = smem + L::kP + (wg * CW / 64) * kBlockT;
 #pragma unroll
                 for (int c0 = 0; c0 < CW; c0 += 8) {
                     if (CW > CH && c0 % CH == 0) load_scores(c0);
@@ -668,13 +755,15 @@ __global__ void __launch_bounds__(kThreadsT, kCtasT) tree_kernel(TreeArgs a) {
                         pw[e] = f32x2_to_f16x2(ex2(d[c0 % CH + 2 * e + 1]), ex2(d[c0 % CH + 2 * e]));
                         add_f16x2(l[c0 + 2 * e], l[c0 + 2 * e + 1], pw[e]);
                     }
-                    *reinterpret_cast<uint4 *>(pt + sw128_off(row, (wg * CW + c0) / 8)) = make_uint4(pw[0], pw[1], pw[2], pw[3]);
+                    *reinterpret_cast<uint4 *>(pt + sw128_off(row, ((wg * CW + c0) & 63) / 8)) = make_uint4(pw[0], pw[1], pw[2], pw[3]);
                 }
                 hand_over();
+                if (W) phase++;
             }
 
             // ---- the pair's last tile of this range: normalise, or leave the partial
-            wait(done, phase++ & 1);
+            if (W) wait(pv_done(phase - 1), ((phase - 1) >> 1) & 1);
+            else wait(done, phase++ & 1);
             tc_fence_after();
             float *wsum = reinterpret_cast<float *>(smem + L::kWarpMax) + wg * 4 * CW;
             const float s = column_sums<CW>(l, lane);
@@ -707,7 +796,7 @@ __global__ void __launch_bounds__(kThreadsT, kCtasT) tree_kernel(TreeArgs a) {
                 }
             }
             tc_fence_before();
-            workers_sync();   // sums, maxima and rows are read: the next pair may write them
+            workers_sync<N>();   // sums, maxima and rows are read: the next pair may write them
         } while (next_pair(a, it, r0));
     }
     tc_fence_before();
@@ -798,23 +887,23 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(TreeArgs a) 
 
 struct TreeFns {
     const void *tree[2], *join;
-    int smem;
+    int smem, threads;
 };
 
 template <int N>
 TreeFns fns_of() {
     return {{reinterpret_cast<const void *>(&tree_kernel<N, false>), reinterpret_cast<const void *>(&tree_kernel<N, true>)},
-            reinterpret_cast<const void *>(&tree_join_kernel<N>), TSmem<N>::kBytes};
+            reinterpret_cast<const void *>(&tree_join_kernel<N>), TSmem<N>::kBytes, kThreadsT<N>};
 }
 
 // Rows of a CTA's tile.
-int tile_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+int tile_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
 
-TreeFns tree_fns(int n) { return n == 16 ? fns_of<16>() : n == 32 ? fns_of<32>() : fns_of<64>(); }
+TreeFns tree_fns(int n) { return n == 16 ? fns_of<16>() : n == 32 ? fns_of<32>() : n == 64 ? fns_of<64>() : fns_of<128>(); }
 
 constexpr int kMaxDevicesT = 64;
 std::mutex g_mu_t;
-bool g_attr_t[kMaxDevicesT][3][2];
+bool g_attr_t[kMaxDevicesT][4][2];
 int g_sms_t[kMaxDevicesT];
 
 size_t align256t(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -834,7 +923,8 @@ int tree_auto_splits(int64_t rows, cudaError_t *status) {
     if (status) *status = e;
     if (e != cudaSuccess) return 0;
     const int64_t n = tile_rows(rows), tiles = (rows + n - 1) / n;
-    return kCtasT * sms / tiles > 0 ? (int)(kCtasT * sms / tiles) : 1;
+    const int64_t ctas = (n == 128 ? kCtasT<128> : kCtasT<64>) * (int64_t)sms / tiles;
+    return ctas > 0 ? (int)ctas : 1;
 }
 
 // Workspace: (m, l) partials | their O, one per row tile and (CTA of it, pair) that can meet
@@ -892,7 +982,7 @@ cudaError_t launch_tree(const nvfp4kv_cache &c, const void *q, const int32_t *cu
     const bool opt = softcap > 0.f || slopes || !(a.score_log2 > 0.f);
     {
         std::lock_guard<std::mutex> lock(g_mu_t);
-        bool &set = g_attr_t[dev][n == 16 ? 0 : n == 32 ? 1 : 2][opt];
+        bool &set = g_attr_t[dev][n == 16 ? 0 : n == 32 ? 1 : n == 64 ? 2 : 3][opt];
         if (!set) {
             e = cudaFuncSetAttribute(f.tree[opt], cudaFuncAttributeMaxDynamicSharedMemorySize, f.smem);
             if (e != cudaSuccess) return e;
@@ -900,7 +990,7 @@ cudaError_t launch_tree(const nvfp4kv_cache &c, const void *q, const int32_t *cu
         }
     }
     void *args[] = {&a};
-    e = launch_pdl(f.tree[opt], dim3((unsigned)a.splits, (unsigned)tiles), kThreadsT, (size_t)f.smem, stream, args);
+    e = launch_pdl(f.tree[opt], dim3((unsigned)a.splits, (unsigned)tiles), (unsigned)f.threads, (size_t)f.smem, stream, args);
     if (e != cudaSuccess || a.splits == 1 || a.cap <= kTileT) return e;   // no pair can have been split
     return launch_pdl(f.join, dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps), (unsigned)a.Hkv, (unsigned)batch),
                       32 * kJoinWarps, 0, stream, args);
