@@ -153,16 +153,25 @@ def _check(rc: int, what: str):
         raise NVFP4KVError(rc, what)
 
 
-def _stream(stream: Optional[torch.cuda.Stream]) -> ctypes.c_void_p:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+# (a call's time on the host counts where few tokens are in flight: these helpers and checks are written to cost little)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
-def _ptr(t: Optional[torch.Tensor]) -> ctypes.c_void_p:
-    return ctypes.c_void_p(t.data_ptr() if t is not None else 0)
+def _stream(stream: Optional[torch.cuda.Stream]) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    torch.cuda._lazy_init()
+    return _raw_stream(_current_device())
+
+
+def _ptr(t: Optional[torch.Tensor]) -> int:
+    return t.data_ptr() if t is not None else 0
 
 
 def _require(t: torch.Tensor, name: str, dtype: torch.dtype):
+    if t.is_cuda and t.dtype is dtype and t.is_contiguous():
+        return
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
     if t.dtype != dtype:
@@ -190,10 +199,7 @@ class PagedCache:
         self.pool = pool
         self._desc = _CacheDesc(pool.data_ptr(), self.num_pages, self.page_size, self.num_kv_heads, HEAD_DIM,
                                 self.dtype, self.k_global_scale, self.v_global_scale)
-
-    @property
-    def desc(self):
-        return ctypes.byref(self._desc)
+        self.desc = ctypes.byref(self._desc)
 
     @property
     def num_slots(self) -> int:
@@ -208,6 +214,15 @@ def slab_bytes(dtype: int, page_size: int, num_kv_heads: int = 1) -> int:
     return int(n)
 
 
+def _whole_tokens(x: torch.Tensor, row: int) -> bool:
+    """Whether each x[t] holds `row` contiguous values (tokens may be strided)."""
+    if x.dim() == 3:
+        st, (_, h, d) = x.stride(), x.shape
+        if h * d == row and d > 1 and st[2] == 1 and (h == 1 or st[1] == d):
+            return True
+    return x[0].is_contiguous() and x[0].numel() == row
+
+
 def quantize_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor,
                     stream: Optional[torch.cuda.Stream] = None):
     """k, v: BF16 [T][Hkv][128] or [T][stride >= Hkv*128]; slot_mapping: int64 [T]."""
@@ -220,7 +235,7 @@ def quantize_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, slot_ma
         if x.shape[0] != T:
             raise ValueError("%s has %d tokens, slot_mapping %d" % (name, x.shape[0], T))
         # each token's Hkv*128 values contiguous; tokens may be strided (a view of a wider QKV buffer)
-        if T > 0 and (not x[0].is_contiguous() or x[0].numel() != row):
+        if T > 0 and not _whole_tokens(x, row):
             raise ValueError("%s: each token must hold %d contiguous values" % (name, row))
     stride = int(k.stride(0)) if T > 0 else row
     if T > 0 and int(v.stride(0)) != stride:
@@ -241,7 +256,7 @@ def calibrate_global_scales(k: torch.Tensor, v: torch.Tensor, num_kv_heads: int,
             raise ValueError("%s must be a CUDA bfloat16 tensor" % name)
         if x.shape[0] != T:
             raise ValueError("k and v must have the same number of tokens")
-        if T > 0 and (not x[0].is_contiguous() or x[0].numel() != row):
+        if T > 0 and not _whole_tokens(x, row):
             raise ValueError("%s: each token must hold %d contiguous values" % (name, row))
     stride = int(k.stride(0)) if T > 0 else row
     if T > 0 and int(v.stride(0)) != stride:
@@ -319,7 +334,7 @@ def paged_decode_attention_append(cache: PagedCache, k_new: torch.Tensor, v_new:
     for name, x in (("k_new", k_new), ("v_new", v_new)):
         if not x.is_cuda or x.dtype != torch.bfloat16 or x.shape[0] != B:
             raise ValueError("%s must be a CUDA bfloat16 tensor with one row per sequence" % name)
-        if B > 0 and (not x[0].is_contiguous() or x[0].numel() != row):
+        if B > 0 and not _whole_tokens(x, row):
             raise ValueError("%s: each row must hold %d contiguous values" % (name, row))
     stride = int(k_new.stride(0)) if B > 0 else row
     if B > 0 and int(v_new.stride(0)) != stride:
@@ -412,10 +427,12 @@ def prefix_dequant(cache: PagedCache, block_table: torch.Tensor, prefix_lens: to
     dev = cache.pool.device
     if k_ws is None:
         k_ws = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _require(k_ws, "k_ws", torch.bfloat16)
     if v_ws is None:
         v_ws = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-    _require(k_ws, "k_ws", torch.bfloat16)
-    _require(v_ws, "v_ws", torch.bfloat16)
+    else:
+        _require(v_ws, "v_ws", torch.bfloat16)
     rc = _lib.nvfp4_prefix_dequant(cache.desc, _ptr(block_table), int(block_table.shape[1]), _ptr(prefix_lens),
                                    _ptr(cu_prefix_lens), int(prefix_lens.shape[0]), int(total_prefix_tokens),
                                    _ptr(k_ws), _ptr(v_ws), _stream(stream))
@@ -521,11 +538,6 @@ def extend_attention_paged(cache: PagedCache, q: torch.Tensor, block_table: torc
 
 
 # ---------------------------------------------------------------- latent cache and eviction
-
-# (the calls below are short: their checks are written to cost little on the host)
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
-
 
 def _complain(t, name: str, dtype: torch.dtype, shape, dev: int):
     """The error that the failed check of _want describes."""
@@ -950,7 +962,7 @@ def rope_quantize_append(cache: PagedCache, q: Optional[torch.Tensor], k: torch.
         Hq = q.shape[1]
         qp, qs = _head_rows(q, "q", T, Hq, dev)
         if q_out is None:
-            q_out = torch.empty((T, Hq, HEAD_DIM), dtype=torch.bfloat16, device=cache.pool.device)
+            q_out = q.new_empty((T, Hq, HEAD_DIM))
             op, os_ = q_out.data_ptr(), Hq * HEAD_DIM
             if stream is not None:
                 _keep_until_done(stream, q_out)
