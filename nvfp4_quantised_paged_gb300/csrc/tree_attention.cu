@@ -71,7 +71,7 @@ constexpr float kNegInfT = -__builtin_huge_valf();
 constexpr float kRescaleT = 8.0f;
 constexpr float kPOffsetT = 7.0f;             // P = 2^(z - m + 7): at most 2^15
 constexpr float kNoMaxT = 3.402823466e38f;    // the offset while every score was -inf
-constexpr int kPairUnits = 1;                 // what a pair's start costs a CTA, in tiles
+constexpr int kPairUnits = 2;                 // what a pair's start costs a CTA, in tiles
 
 template <int N>
 struct TSmem {
@@ -511,13 +511,16 @@ __global__ void __launch_bounds__(kThreadsT<N>, kCtasT<N>) tree_kernel(TreeArgs 
         // 128 rows: K by the first two warpgroups, V by the others, of tile j (from tok0 on).  V's buffer was read last by
         // the product of tile j - 3 (which is done where the tile is its pair's first).
         uint32_t vb = 0;
+        auto report_k = [&](uint32_t j) {
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(k_ready(j));
+        };
         auto expand_wide = [&](int n, int tok0, uint32_t j, bool first) {
             if (wg < 2) {
                 const int held = expand_k();
-                tc_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(k_ready(j));
+                if (!first) report_k(j);
                 return held;
             }
             wait(&raw_full[vs], ksp);
@@ -536,12 +539,13 @@ __global__ void __launch_bounds__(kThreadsT<N>, kCtasT<N>) tree_kernel(TreeArgs 
             __syncwarp();
             if (lane == 0) mbar_arrive(ready);
         };
-        // A pair's Q, the rows' factors and the tree.  (The previous pair's products and its
-        // epilogue are done.)
-        auto load_pair = [&](const TreeIter &x) {
+        // A pair's Q, the rows' factors and the tree: requested before the pair's first tile is expanded, laid out
+        // after it.  (The previous pair's products and its epilogue are done.)
+        uint2 qw[N / kWarps];
+        int at[N / kWarps];                     // a row of q, -1: none
+        uint64_t tree = 0;
+        auto fetch_pair = [&](const TreeIter &x) {
             const int rows = x.s.d * a.G;
-            uint2 qw[N / kWarps];
-            int at[N / kWarps];                 // a row of q, -1: none
 #pragma unroll
             for (int k = 0; k < N / kWarps; k++) {
                 const int r = r0 + warp + kWarps * k, i = r / a.G;
@@ -549,39 +553,51 @@ __global__ void __launch_bounds__(kThreadsT<N>, kCtasT<N>) tree_kernel(TreeArgs 
                 qw[k] = make_uint2(0, 0);
                 if (r < rows) qw[k] = __ldg(reinterpret_cast<const uint2 *>(a.q + (int64_t)at[k] * kHeadDim) + lane);
             }
+            tree = 0;
+            if (tid < x.s.d) {
+                const uint64_t all = x.s.d >= 64 ? ~0ull : (1ull << x.s.d) - 1;
+                tree = (a.mask ? __ldg(reinterpret_cast<const unsigned long long *>(a.mask) + x.s.q0 + tid) : (2ull << tid) - 1) & all;
+            }
+        };
+        auto store_pair = [&]() {
+            constexpr int R = N / kWarps;       // rows a warp: their scalars are lanes 0 .. R - 1's
+            int my_kq = 0, my_at = -1;
+            uint32_t m[R];
 #pragma unroll
-            for (int k = 0; k < N / kWarps; k++) {
+            for (int k = 0; k < R; k++) {
+                const uint32_t x = max_u16x2(qw[k].x & 0x7fff7fffu, qw[k].y & 0x7fff7fffu);
+                m[k] = __reduce_max_sync(0xffffffffu, max(x >> 16, x & 0xffffu));
+            }
+#pragma unroll
+            for (int k = 0; k < R; k++) {
                 const int c = warp + kWarps * k;
                 const uint2 w = qw[k];
-                uint32_t m = max_u16x2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu);
-                m = __reduce_max_sync(0xffffffffu, max(m >> 16, m & 0xffffu));
                 // 2^kq puts the row's largest value into [2^14, 2^15)
-                const int kq = m ? min(126, max(-126, 14 - ((int)(m >> 7) - 127))) : 0;
+                const int kq = m[k] ? min(126, max(-126, 14 - ((int)(m[k] >> 7) - 127))) : 0;
                 const float sc = __uint_as_float((uint32_t)(kq + 127) << 23);
                 // dims 4 lane .. + 3 = 32 q + 4 a + e lie at position 16 a + 4 q + e
                 const int pos = 16 * (lane & 7) + 4 * (lane >> 3);
                 *reinterpret_cast<uint2 *>(smem + L::kQ + (pos >> 6) * L::kQBlock + sw128_off(c, (pos & 63) >> 3) + (pos & 7) * 2) =
                     make_uint2(f32x2_to_f16x2(bf16_hi(w.x) * sc, bf16_lo(w.x) * sc),
                                f32x2_to_f16x2(bf16_hi(w.y) * sc, bf16_lo(w.y) * sc));
-                if (lane == 0) {
-                    const float fac = (OPT && a.cap_log2 > 0.f ? a.cap_in : a.score_log2) * __uint_as_float((uint32_t)(127 - kq) << 23);
-                    // (a positive factor stays one, so that minus infinity times it is minus infinity: no score
-                    // reaches 2^34, and 2^-92 is none)
-                    s_fac[c] = OPT ? 1.f : fmaxf(fac, 0x1p-126f);
-                    if (OPT) s_in[c] = fac;
-                    s_m[c] = kNegInfT;
-                    s_off[c] = kNoMaxT;
-                    s_row[c] = at[k];
-                    s_draft[c] = min((r0 + c) / a.G, 63);
-                    if (OPT) s_slope[c] = a.slopes && at[k] >= 0 ? __ldg(a.slopes + at[k] % a.Hq) * 1.4426950408889634f : 0.f;
-                }
+                if (lane == k) my_kq = kq, my_at = at[k];
+            }
+            if (lane < R) {
+                const int c = warp + kWarps * lane;
+                const float fac = (OPT && a.cap_log2 > 0.f ? a.cap_in : a.score_log2) * __uint_as_float((uint32_t)(127 - my_kq) << 23);
+                // (a positive factor stays one, so that minus infinity times it is minus infinity: no score
+                // reaches 2^34, and 2^-92 is none)
+                s_fac[c] = OPT ? 1.f : fmaxf(fac, 0x1p-126f);
+                if (OPT) s_in[c] = fac;
+                s_m[c] = kNegInfT;
+                s_off[c] = kNoMaxT;
+                s_row[c] = my_at;
+                s_draft[c] = min((r0 + c) / a.G, 63);
+                if (OPT) s_slope[c] = a.slopes && my_at >= 0 ? __ldg(a.slopes + my_at % a.Hq) * 1.4426950408889634f : 0.f;
             }
             if (tid < 64) {
-                const uint64_t all = x.s.d >= 64 ? ~0ull : (1ull << x.s.d) - 1;
-                uint64_t mk = 0;
-                if (tid < x.s.d) mk = (a.mask ? a.mask[x.s.q0 + tid] : (2ull << tid) - 1) & all;
-                s_mask[tid] = mk;
-                s_depth[tid] = __popcll(mk) - 1;
+                s_mask[tid] = tree;
+                s_depth[tid] = __popcll(tree) - 1;
             }
             if (W) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // Q, before any warp reports K
             workers_sync<N>();
@@ -606,18 +622,21 @@ __global__ void __launch_bounds__(kThreadsT<N>, kCtasT<N>) tree_kernel(TreeArgs 
 
         uint32_t phase = 0;                         // up to 64 rows: products awaited; 128: tiles
         do {
-            load_pair(it);
-            float l[CW];
-#pragma unroll
-            for (int c = 0; c < CW; c++) l[c] = 0.f;
+            fetch_pair(it);
             int tok0 = (it.s.t0 + it.t) * kTileT;
             int held = 0, held_next;                // the groups that a raw tile holds
             if constexpr (W) {
                 held_next = expand_wide(it.s.n, tok0, phase, true);
+                store_pair();
+                if (wg < 2) report_k(phase);
             } else {
                 held_next = expand_k();
+                store_pair();
                 hand_over();
             }
+            float l[CW];
+#pragma unroll
+            for (int c = 0; c < CW; c++) l[c] = 0.f;
             for (int t = it.t; t < it.te; t++, tok0 += kTileT) {
                 held = held_next;
                 if constexpr (W) {
