@@ -631,8 +631,8 @@ NVFP4KV_API size_t nvfp4kv_tree_workspace_bytes(const nvfp4kv_cache *cache, int 
  *   num_splits    CTAs that share the tokens of a row tile (128 rows of drafts x heads of a kv
  *                 head); 0 = auto.
  * NVFP4 pools only; at most 128 query heads a kv head.  Queries are FP16 under a power of two
- * per row, the probabilities FP16, the sums FP32.  A NaN among a sequence's cached value rows
- * may reach all of its drafts (a probability of 0 times it is a NaN).
+ * per row, the probabilities FP16, the sums FP32.  A NaN in a cached row reaches the drafts
+ * that see the row, and no others.
  */
 NVFP4KV_API int nvfp4_tree_attention(const nvfp4kv_cache *cache, const void *q, const int32_t *cu_q_lens,
                                      int64_t total_q_tokens, int batch, int max_q_len, int num_q_heads,

@@ -90,7 +90,8 @@ struct TSmem {
     static constexpr int kRow = kM + 7 * N * 4;                   // int row[N] (-1: none), draft[N]
     static constexpr int kWarpMax = kRow + 2 * N * 4;             // float [warpgroups][4][rows of one]
     static constexpr int kMask = kWarpMax + 4 * N * 4;            // u64 mask[64], int depth[64]
-    static constexpr int kBytes = kMask + 64 * 12;
+    static constexpr int kNan = kMask + 64 * 12;                  // u32 nan[1 + 64 + 64]: of all rows, of drafts, of the window's edge
+    static constexpr int kBytes = kNan + 4 * 129;
     // TMEM columns: O at 0, S (two with 128 rows), K[2]
     static constexpr uint32_t kColS = N, kColK = (kW ? 3 : 2) * N, kCols = kW ? 512 : 256;
     static_assert(kColK + 128 <= kCols && kCtasT<N> * kCols <= 512, "TMEM columns");
@@ -257,6 +258,9 @@ __global__ void __launch_bounds__(kThreadsT<N>, kCtasT<N>) tree_kernel(TreeArgs 
     int *s_row = reinterpret_cast<int *>(smem + L::kRow), *s_draft = s_row + N;
     uint64_t *s_mask = reinterpret_cast<uint64_t *>(smem + L::kMask);
     int *s_depth = reinterpret_cast<int *>(s_mask + 64);
+    // A value block that is NaN would reach every row (0 times NaN is NaN): it is multiplied as zeros, noted here
+    // (bit b: block b) and put into the outputs of the rows that see its token.
+    unsigned *s_nan = reinterpret_cast<unsigned *>(smem + L::kNan);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int r0 = blockIdx.y * N;
     if (tid == 0) {
@@ -265,6 +269,7 @@ __global__ void __launch_bounds__(kThreadsT<N>, kCtasT<N>) tree_kernel(TreeArgs 
         *abort_flag = 0;
         fence_mbar_init();
     }
+    if (tid < 129) s_nan[tid] = 0;
     pdl_wait();               // everything read or written may belong to earlier work of the stream
     pdl_launch_dependents();
     if (warp == kMmaWarp) tc_alloc(&tmem_base, L::kCols);
@@ -483,7 +488,7 @@ __global__ void __launch_bounds__(kThreadsT<N>, kCtasT<N>) tree_kernel(TreeArgs 
         };
         // V of the tile of stage vs to shared memory, buffer vb; rows: those of the group that exist.
         // Lanes q >= 2 take rows r ^ 2, so that a quarter warp's stores meet all banks.
-        auto expand_v = [&](int rows, uint32_t vb) {
+        auto expand_v = [&](int rows, uint32_t vb, const Seq &sq) {
             const int r0v = er ^ (eq & 2);
             const uint8_t *g = smem + L::kRaw + vs * kRawT + grp * kGroupT + 1152;
             uint8_t *blk = smem + L::kV + (2 * vb + (eq >> 1)) * kBlockT + (16 * grp + r0v) * 128;
@@ -495,6 +500,17 @@ __global__ void __launch_bounds__(kThreadsT<N>, kCtasT<N>) tree_kernel(TreeArgs 
                 if (rows < 16 && r >= rows) {             // may hold anything: zeros
                     c = make_uint4(0, 0, 0, 0);
                     s = 0;
+                }
+                const uint32_t nan = ((s & 0x7f7fu) + 0x0101u) & 0x8080u;   // of a scale that is NaN: its byte's top bit
+                if (nan) {
+                    const int rel = sq.n - rows + r - sq.base;              // the token's index, from base on
+                    const unsigned bits = ((nan >> 7 & 1u) | (nan >> 14 & 2u)) << (2 * eq);
+                    const int edge = rel + a.window;                        // from the window of the first draft on
+                    if (rel >= 0) atomicOr(s_nan + 1 + min(rel, 63), bits);
+                    else if (a.window <= 0 || edge >= 64) atomicOr(s_nan, bits);
+                    else if (edge >= 0) atomicOr(s_nan + 65 + edge, bits);
+                    if (nan & 0x80u) s &= 0xff00u;
+                    if (nan & 0x8000u) s &= 0x00ffu;
                 }
                 s = e4m3x2_to_f16x2(s);
                 const uint32_t w[4] = {c.x, c.y, c.z, c.w};
@@ -517,7 +533,7 @@ __global__ void __launch_bounds__(kThreadsT<N>, kCtasT<N>) tree_kernel(TreeArgs 
             __syncwarp();
             if (lane == 0) mbar_arrive(k_ready(j));
         };
-        auto expand_wide = [&](int n, int tok0, uint32_t j, bool first) {
+        auto expand_wide = [&](const Seq &sq, int tok0, uint32_t j, bool first) {
             if (wg < 2) {
                 const int held = expand_k();
                 if (!first) report_k(j);
@@ -526,7 +542,7 @@ __global__ void __launch_bounds__(kThreadsT<N>, kCtasT<N>) tree_kernel(TreeArgs 
             wait(&raw_full[vs], ksp);
             const int held = s_valid[vs];
             if (!first && j >= 3) wait(pv_done(j - 3), ((j - 3) >> 1) & 1);
-            expand_v((held >> grp) & 1 ? n - (tok0 + 16 * grp) : 0, vb);
+            expand_v((held >> grp) & 1 ? sq.n - (tok0 + 16 * grp) : 0, vb, sq);
             vb = vb == 2 ? 0 : vb + 1;
             if (vs == 0) ksp ^= 1u;
             return held;
@@ -626,7 +642,7 @@ __global__ void __launch_bounds__(kThreadsT<N>, kCtasT<N>) tree_kernel(TreeArgs 
             int tok0 = (it.s.t0 + it.t) * kTileT;
             int held = 0, held_next;                // the groups that a raw tile holds
             if constexpr (W) {
-                held_next = expand_wide(it.s.n, tok0, phase, true);
+                held_next = expand_wide(it.s, tok0, phase, true);
                 store_pair();
                 if (wg < 2) report_k(phase);
             } else {
@@ -640,7 +656,7 @@ __global__ void __launch_bounds__(kThreadsT<N>, kCtasT<N>) tree_kernel(TreeArgs 
             for (int t = it.t; t < it.te; t++, tok0 += kTileT) {
                 held = held_next;
                 if constexpr (W) {
-                    if (t + 1 < it.te) held_next = expand_wide(it.s.n, tok0 + kTileT, phase + 1, false);
+                    if (t + 1 < it.te) held_next = expand_wide(it.s, tok0 + kTileT, phase + 1, false);
                     wait(scored(phase), (phase >> 1) & 1);
                     tc_fence_after();
                 } else {
@@ -649,7 +665,7 @@ __global__ void __launch_bounds__(kThreadsT<N>, kCtasT<N>) tree_kernel(TreeArgs 
                     // This tile's scores are there, O^T holds the tiles before: V and P may be written.
                     wait(done, phase++ & 1);
                     tc_fence_after();
-                    expand_v((held >> grp) & 1 ? it.s.n - (tok0 + 16 * grp) : 0, 0);
+                    expand_v((held >> grp) & 1 ? it.s.n - (tok0 + 16 * grp) : 0, 0, it.s);
                 }
 
                 // ---- softmax of the token's scores for the warpgroup's rows
@@ -797,7 +813,26 @@ __global__ void __launch_bounds__(kThreadsT<N>, kCtasT<N>) tree_kernel(TreeArgs 
                 if (!whole) a.part_ml[slot * N + wg * CW + lane] = make_float2(m == kNegInfT ? m : m - kPOffsetT, t);
                 s_alpha[wg * CW + lane] = t == 0.f ? 0.f : a.gv / t;      // (a row that sees nothing: zeros)
             }
-            group_sync(wg);
+            workers_sync<N>();
+            // NaN blocks: rows' bits into s_draft (which the pair needs no more)
+            bool any_nan = false;
+            for (int i = lane; i < 129; i += 32) any_nan = any_nan || s_nan[i] != 0;
+            any_nan = __any_sync(0xffffffffu, any_nan);
+            if (any_nan) {
+                unsigned bits = 0;
+                if (tid < N) {
+                    const int i = s_draft[tid];
+                    bits = s_nan[0];
+                    for (int x = 0; x < 64; x++) {
+                        if ((s_mask[i] >> x & 1) && (a.window <= 0 || s_depth[x] > s_depth[i] - a.window)) bits |= s_nan[1 + x];
+                        if (x > s_depth[i]) bits |= s_nan[65 + x];
+                    }
+                }
+                workers_sync<N>();
+                if (tid < N) s_draft[tid] = (int)bits;
+                if (tid < 129) s_nan[tid] = 0;
+                workers_sync<N>();
+            }
             float *dst = a.part_acc + (slot * N + wg * CW) * kHeadDim + row;
 #pragma unroll 1
             for (int c0 = 0; c0 < CW; c0 += 8) {
@@ -808,6 +843,7 @@ __global__ void __launch_bounds__(kThreadsT<N>, kCtasT<N>) tree_kernel(TreeArgs 
                 for (int c = 0; c < 8; c++) {
                     const int at = s_row[wg * CW + c0 + c];
                     if (at < 0) continue;
+                    if (any_nan && (s_draft[wg * CW + c0 + c] >> (row >> 4) & 1)) x[c] = 0x7fc00000u;
                     if (whole)
                         a.out[(int64_t)at * kHeadDim + row] = __float2bfloat16_rn(__uint_as_float(x[c]) * s_alpha[wg * CW + c0 + c]);
                     else
@@ -887,9 +923,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(TreeArgs a) 
         acc.x *= f0, acc.y *= f0, acc.z *= f0, acc.w *= f0;
 #pragma unroll
         for (int k = 0; k < U; k++) {
-            // (a partial without a maximum counts nothing, unless its sum is NaN)
-            const float f = ml[k].x == kNegInfT ? (ml[k].y == 0.f ? 0.f : ml[k].y) : ex2(ml[k].x - mx);
-            if (f == 0.f) continue;
+            if (ml[k].x == kNegInfT && ml[k].y == 0.f) continue;      // it saw nothing
+            const float f = ml[k].x == kNegInfT ? ml[k].y : ex2(ml[k].x - mx);   // (no maximum, but a sum: NaN)
             l = fmaf(f, ml[k].y, l);
             acc.x = fmaf(f, v[k].x, acc.x);
             acc.y = fmaf(f, v[k].y, acc.y);

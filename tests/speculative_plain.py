@@ -118,6 +118,9 @@ def tree(q, k, v, masks, n, scale, cap=0.0, window=0, slopes=None, gone=()):
         z = z.masked_fill(~sees, -math.inf)
         w = torch.nan_to_num(torch.softmax(z, -1), nan=0.0) if not sees.any(1).all() else torch.softmax(z, -1)
         w = torch.where(sees.any(1, keepdim=True), w, 0.0)
+        if torch.isnan(v[h // g]).any():     # (0 times the NaN of a token that is not seen would be one)
+            out[:, h] = torch.stack([w[i][sees[i]] @ v[h // g][sees[i]] for i in range(d)])
+            continue
         out[:, h] = w @ v[h // g]
         spread[:, h] = torch.einsum("dn,dnc->dc", w, (v[h // g][None] - out[:, h][:, None]).abs()) if d * n <= 20000 else \
             torch.stack([(w[i][:, None] * (v[h // g] - out[i, h]).abs()).sum(0) for i in range(d)])

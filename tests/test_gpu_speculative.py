@@ -150,6 +150,36 @@ def test_rope_append_skips_what_is_out_of_range(m):
     assert same == [i in (4, 5) for i in range(T)]
 
 
+@pytest.mark.parametrize("sections", [None, (8, 12, 12)])
+def test_rope_append_long_skips_what_is_out_of_range(m, sections):
+    """The same through the form for many tokens: negative and too large slots, positions on each axis."""
+    T, hq, hkv, page = 6000, 20, 4, 64
+    x, pos, table, (wq, wk) = write_inputs(T, hq, hkv, 64, sections, True, 13, rows=300)
+    slots = torch.randperm(100 * page, generator=gen(1))[:T]
+    bad_pos, bad_slot = list(range(3, T, 501)), list(range(5, T, 700))
+    first = pos[len(sections) - 1] if sections else pos
+    first[bad_pos] = torch.tensor([300, -1] * len(bad_pos))[:len(bad_pos)].int()
+    slots[bad_slot] = torch.tensor([-1, 100 * page] * len(bad_slot))[:len(bad_slot)]
+    a, b = m.PagedCache(100, page, hkv), m.PagedCache(100, page, hkv)
+    q, k, v = x.cuda().unflatten(-1, (-1, HEAD)).split([hq, hkv, hkv], 1)
+    out = torch.full((T, hq, HEAD), 3.0, dtype=torch.bfloat16, device="cuda")
+    m.rope_quantize_append(a, q, k, v, pos.cuda(), table.cuda(), slots.cuda(), q_norm=wq.cuda(), k_norm=wk.cuda(),
+                           sections=sections, q_out=out)
+    assert m.check_device_errors() == -4 and m.check_device_errors() == 0
+    fine = torch.ones(T, dtype=torch.bool)
+    fine[bad_pos] = False
+    assert (out[~fine.cuda()] == 3.0).all()
+    some = pos[:, fine] if sections else pos[fine]
+    rows = x.unflatten(-1, (-1, HEAD))[fine]
+    rq, size = plain.turned(rows[:, :hq], wq, some, table, 1e-6, False, sections)
+    rk, _ = plain.turned(rows[:, hq:hq + hkv], wk, some, table, 1e-6, False, sections)
+    err = (out.cpu().double()[fine] - rq).abs()
+    assert (err <= 2.0**-8 * rq.abs() + 2.0**-16 * size + 1e-30).all()
+    kept = torch.where(slots < 100 * page, slots, torch.full_like(slots, -1))[fine]
+    m.quantize_append(b, plain.bf16_rounded(rk).cuda(), packed(rows[:, hq + hkv:]), kept.cuda())
+    assert torch.equal(a.pool, b.pool) and m.check_device_errors() == 0
+
+
 def test_rope_append_zero_rows_and_no_tokens(m):
     cache, ref = m.PagedCache(1, 16, 1), m.PagedCache(1, 16, 1)
     z = torch.zeros((3, 1, HEAD), dtype=torch.bfloat16, device="cuda")
@@ -331,6 +361,66 @@ def test_tree_attention_many_sequences(m):
     g = gen(8)
     lens = [int(x) for x in torch.randint(1, 60, (300,), generator=g)]
     run_tree(m, lens, [min(n, 1 + i % 3) for i, n in enumerate(lens)], 4, 1, 16, seed=5)
+
+
+@pytest.mark.parametrize("window", [0, 20])
+@pytest.mark.parametrize("hq", [4, 24, 64])
+def test_tree_attention_nan_reaches_the_drafts_that_see_it(m, window, hq):
+    """NaN scales in the rows of a draft, of a token at the window's edge, and behind the sequence."""
+    g = gen(51)
+    hkv, page, n, d = 2, 16, 333, 6
+    base = n - d
+    table, pages = table_of([n + 3], page, g)
+    masks = plain.masks_of([-1, 0, 0, 1, 2, 4])
+    q = torch.randn((d, hq, HEAD), generator=g).to(torch.bfloat16)
+
+    def poisoned(tokens):
+        pool = random_pool(pages, hkv, page, 4)
+        grp = pool.view(pages, hkv, page // 16, GROUP)
+        for t, head, block, is_k in tokens:
+            row = grp[table[0, t // page].long(), head, (t % page) // 16]
+            row[1024 + (t % 16) * 8 + block if is_k else 2176 + block * 16 + t % 16] = 0x7f
+        return pool
+
+    for tokens in ([(base + 2, 0, 3, False)], [(base + 4, 1, 0, False), (base + 1, 1, 7, False)], [(base + 3, 0, 5, True)],
+                   [(base - 18, 0, 1, False)], [(base - 19, 1, 6, False), (base - 20, 0, 6, False)], [(7, 0, 2, False)],
+                   [(n, 0, 2, False), (n + 2, 1, 2, True)]):
+        pool = poisoned(tokens)
+        cache = m.PagedCache(pages, page, hkv, pool=pool.cuda())
+        got = m.tree_attention(cache, q.cuda(), sums([d]), d, table.cuda(), ints([n]), window=window,
+                               tree_mask=torch.tensor(masks, device="cuda")).cpu()
+        k, v = plain.rows_of(pool, page, table[0], n)
+        ref = plain.tree(q, k, v, masks, n, 1 / math.sqrt(HEAD), window=window)[0]
+        assert torch.equal(torch.isnan(got), torch.isnan(ref)), tokens
+        fine = ~torch.isnan(ref)
+        assert (got.double()[fine] - ref[fine]).abs().max() < 0.05 * ref[fine].abs().max(), tokens
+    assert m.check_device_errors() == 0
+
+
+def test_pages_beyond_four_gigabytes(m):
+    g = gen(61)
+    hkv, page, pages = 8, 128, 40000                 # 5.9 GB
+    cache = m.PagedCache(pages, page, hkv)
+    lens, drafts, hq = [300, 129], [5, 1], 16
+    table = torch.tensor([[39999, 31000, 29500], [39998, 30999, -1]], dtype=torch.int32)
+    small = random_pool(6, hkv, page, 2)
+    for i, p in enumerate([39999, 31000, 29500, 39998, 30999]):
+        cache.pool[p] = small[i].cuda()
+    near = torch.tensor([[0, 1, 2], [3, 4, -1]], dtype=torch.int32)
+    other = m.PagedCache(6, page, hkv, pool=small.cuda())
+    q = torch.randn((6, hq, HEAD), generator=g).to(torch.bfloat16).cuda()
+    x = torch.randn((6, 2 * hkv, HEAD), generator=g).to(torch.bfloat16).cuda()
+    at = [(0, t) for t in range(295, 300)] + [(1, 128)]
+    outs = []
+    for c, t in ((cache, table), (other, near)):
+        slots = torch.tensor([int(t[b, p // page]) * page + p % page for b, p in at]).cuda()
+        m.rope_quantize_append(c, None, x[:, :hkv], x[:, hkv:], ints([p for _, p in at]), rotation(400, 128).cuda(), slots)
+        outs.append(m.tree_attention(c, q, sums(drafts), 5, t.cuda(), ints(lens)))
+        new = m.accept_tokens(c, t.cuda(), ints(lens), sums(drafts), ints([[0, 3], [0, 0]]), ints([2, 1]))
+        assert new.tolist() == [297, 129]
+        outs.append(m.paged_decode_attention(c, q[:2], t.cuda(), new))
+    assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[3])
+    assert m.check_device_errors() == 0
 
 
 # --------------------------------------------------------------------------------- acceptance
