@@ -180,6 +180,21 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
+// Two scale bytes of a token and of the token eight behind it (rel: its index, from the base of the drafts on), some
+// NaN: those are noted and set to zero.  See s_nan.
+__device__ __noinline__ uint32_t without_nan(uint32_t scales, unsigned *s_nan, int rel, int window, int eq) {
+    for (int i = 0; i < 4; i++) {
+        if (((scales >> (8 * i)) & 0x7fu) != 0x7fu) continue;
+        const unsigned bit = 1u << (2 * eq + (i & 1));
+        const int at = rel + 8 * (i >> 1), edge = at + window;   // edge: from the window of the first draft on
+        if (at >= 0) atomicOr(s_nan + 1 + min(at, 63), bit);
+        else if (window <= 0 || edge >= 64) atomicOr(s_nan, bit);
+        else if (edge >= 0) atomicOr(s_nan + 65 + edge, bit);
+        scales &= ~(0xffu << (8 * i));
+    }
+    return scales;
+}
+
 // s0 += low FP16 of w, s1 += high FP16 of w
 __device__ __forceinline__ void add_f16x2(float &s0, float &s1, uint32_t w) {
     const unsigned short one = 0x3c00;
@@ -492,26 +507,19 @@ __global__ void __launch_bounds__(kThreadsT<N>, kCtasT<N>) tree_kernel(TreeArgs 
             const int r0v = er ^ (eq & 2);
             const uint8_t *g = smem + L::kRaw + vs * kRawT + grp * kGroupT + 1152;
             uint8_t *blk = smem + L::kV + (2 * vb + (eq >> 1)) * kBlockT + (16 * grp + r0v) * 128;
+            const uint8_t *gs = g + 1024 + 2 * eq * 16 + r0v;
+            uint32_t scales = gs[0] | (uint32_t)gs[16] << 8 | (uint32_t)gs[8] << 16 | (uint32_t)gs[24] << 24;   // of rows r0v, r0v + 8
+            if (rows < 16) {                              // rows that do not exist may hold anything: zeros
+                if (r0v >= rows) scales &= 0xffff0000u;
+                if (r0v + 8 >= rows) scales &= 0x0000ffffu;
+            }
+            if (((scales & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u)
+                scales = without_nan(scales, s_nan, sq.n - rows + r0v - sq.base, a.window, eq);
 #pragma unroll
             for (int e = 0; e < 2; e++) {
                 const int r = r0v + 8 * e;
                 uint4 c = *reinterpret_cast<const uint4 *>(g + r * 64 + eq * 16);
-                uint32_t s = (uint32_t)g[1024 + (2 * eq) * 16 + r] | ((uint32_t)g[1024 + (2 * eq + 1) * 16 + r] << 8);
-                if (rows < 16 && r >= rows) {             // may hold anything: zeros
-                    c = make_uint4(0, 0, 0, 0);
-                    s = 0;
-                }
-                const uint32_t nan = ((s & 0x7f7fu) + 0x0101u) & 0x8080u;   // of a scale that is NaN: its byte's top bit
-                if (nan) {
-                    const int rel = sq.n - rows + r - sq.base;              // the token's index, from base on
-                    const unsigned bits = ((nan >> 7 & 1u) | (nan >> 14 & 2u)) << (2 * eq);
-                    const int edge = rel + a.window;                        // from the window of the first draft on
-                    if (rel >= 0) atomicOr(s_nan + 1 + min(rel, 63), bits);
-                    else if (a.window <= 0 || edge >= 64) atomicOr(s_nan, bits);
-                    else if (edge >= 0) atomicOr(s_nan + 65 + edge, bits);
-                    if (nan & 0x80u) s &= 0xff00u;
-                    if (nan & 0x8000u) s &= 0x00ffu;
-                }
+                uint32_t s = scales >> (16 * e);
                 s = e4m3x2_to_f16x2(s);
                 const uint32_t w[4] = {c.x, c.y, c.z, c.w};
                 uint32_t f[16];
