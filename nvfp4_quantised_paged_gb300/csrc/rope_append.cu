@@ -65,8 +65,12 @@ __device__ __forceinline__ Pair two_sum(float a, float b) {
     return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb))};
 }
 
-// hi + lo (lo small beside hi) rounded to BF16, ties of hi broken by lo
+constexpr float kInfR = __builtin_huge_valf();
+
+// hi + lo (lo small beside hi) rounded to BF16, ties of hi broken by lo; hi alone where lo is zero (a zero keeps its
+// sign) or hi no finite number
 __device__ __forceinline__ uint32_t bf16_of_pair(float hi, float lo) {
+    if (lo == 0.0f || !(fabsf(hi) < kInfR)) return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(hi));
     const float t = __fadd_rn(hi, lo), rest = __fsub_rn(lo, __fsub_rn(t, hi));
     uint32_t b = __float_as_uint(t);
     if ((b & 0xffffu) == 0x8000u && rest != 0.0f) b += (rest > 0.0f) == (t > 0.0f) ? 1u : 0xffffffffu;
@@ -76,6 +80,7 @@ __device__ __forceinline__ uint32_t bf16_of_pair(float hi, float lo) {
 // 1 / sqrt(ssq / 128 + eps) as two floats: the hardware's estimate and one Newton step
 // whose residual 1 - m r^2 is formed exactly up to 2^-44.
 __device__ __forceinline__ Pair root(Pair ssq, float eps) {
+    if (ssq.hi == kInfR) return {0.0f, 0.0f};
     const Pair m0 = two_sum(ssq.hi * 0.0078125f, eps);
     const float lo = m0.lo + ssq.lo * 0.0078125f;
     const float m = m0.hi + lo, ml = lo - (m - m0.hi);
@@ -211,7 +216,7 @@ __device__ __forceinline__ int turn_k(const RopeArgs &a, const Place &p, int blk
 #pragma unroll
             for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
             const float m = fmaf(sum, 0.0078125f, a.eps), r0 = rsqrtf(m);
-            r = fmaf(0.5f * r0, fmaf(-m * r0, r0, 1.0f), r0);
+            r = m == kInfR ? 0.0f : fmaf(0.5f * r0, fmaf(-m * r0, r0, 1.0f), r0);
             dm *= r;
             dy = 0x1.6p-21f;
         }

@@ -180,6 +180,44 @@ def test_rope_append_long_skips_what_is_out_of_range(m, sections):
     assert torch.equal(a.pool, b.pool) and m.check_device_errors() == 0
 
 
+@pytest.mark.parametrize("T", [8, 6000])
+@pytest.mark.parametrize("norms", [False, True])
+def test_rope_append_infinities_and_nan(m, T, norms):
+    """Rows with an infinity or a NaN give what FP32 gives (the rotation by angles whose cosine and sine are 0 or 1, so
+    that every other product is exact); their neighbours are not touched."""
+    hq, hkv = 4, 4
+    g = gen(2)
+    x = torch.randint(-8, 9, (T, hq + 2 * hkv, HEAD), generator=g).float()
+    x[::5, 1, 3], x[1::7, 2, 70], x[2::9, hq, 100], x[3::8, hq + 1, 5] = math.inf, math.nan, -math.inf, math.nan
+    table = torch.tensor([[1.0] * 64 + [0.0] * 64, [0.0] * 64 + [1.0] * 64])
+    pos = torch.randint(0, 2, (T,), generator=g, dtype=torch.int32)
+    w = torch.ones(HEAD, dtype=torch.bfloat16)
+    slots = torch.arange(T)
+    pages = -(-T // 64)
+    a, b = m.PagedCache(pages, 64, hkv), m.PagedCache(pages, 64, hkv)
+    q, k, v = x.to(torch.bfloat16).cuda().split([hq, hkv, hkv], 1)
+    on = w.cuda() if norms else None
+    out = m.rope_quantize_append(a, q, k, v, pos.cuda(), table.cuda(), slots.cuda(), q_norm=on, k_norm=on, eps=0.0).cpu()
+    y = x.double()
+    if norms:
+        y = y / torch.sqrt((y * y).mean(-1, keepdim=True))
+    c, s = (table[pos.long(), i:i + 64].double()[:, None] for i in (0, 64))
+    y = torch.cat([y[..., :64] * c - y[..., 64:] * s, y[..., 64:] * c + y[..., :64] * s], -1)
+    for h in range(hq):
+        fine = torch.isfinite(y[:, h])
+        assert torch.equal(torch.isnan(out[:, h]), torch.isnan(y[:, h]))
+        assert torch.equal(out[:, h].double()[~fine & ~torch.isnan(y[:, h])], y[:, h][~fine & ~torch.isnan(y[:, h])])
+        assert ((out[:, h].double() - y[:, h])[fine].abs() <= 2.0**-8 * y[:, h][fine].abs()).all()
+    rk = y[:, hq:hq + hkv]
+    rounded = torch.where(torch.isfinite(rk), plain.bf16_rounded(torch.where(torch.isfinite(rk), rk, 1.0)).double(), rk)
+    m.quantize_append(b, packed(rounded.to(torch.bfloat16)), packed(x[:, hq + hkv:].to(torch.bfloat16)), slots.cuda())
+    # (as values: where an infinity makes a row's norm infinite, the order of rotation and norm decides a zero's sign)
+    for ours, other in zip(*(plain.rows_of(c.pool.cpu(), 64, torch.arange(pages), T) for c in (a, b))):
+        assert torch.equal(torch.isnan(ours), torch.isnan(other))
+        assert torch.equal(torch.nan_to_num(ours), torch.nan_to_num(other))
+    assert m.check_device_errors() == 0
+
+
 def test_rope_append_zero_rows_and_no_tokens(m):
     cache, ref = m.PagedCache(1, 16, 1), m.PagedCache(1, 16, 1)
     z = torch.zeros((3, 1, HEAD), dtype=torch.bfloat16, device="cuda")
@@ -357,10 +395,32 @@ def test_tree_attention_device_checks(m):
         assert torch.isfinite(out).all()
 
 
-def test_tree_attention_many_sequences(m):
+@pytest.mark.parametrize("hq,drafts", [(4, 3), (16, 12)])
+def test_tree_attention_many_sequences(m, hq, drafts):
     g = gen(8)
     lens = [int(x) for x in torch.randint(1, 60, (300,), generator=g)]
-    run_tree(m, lens, [min(n, 1 + i % 3) for i, n in enumerate(lens)], 4, 1, 16, seed=5)
+    run_tree(m, lens, [min(n, 1 + i % drafts) for i, n in enumerate(lens)], hq, 1, 16, seed=5)
+
+
+def test_tree_attention_on_two_streams_at_once(m):
+    """Two calls that may overlap, each with its workspace."""
+    g = gen(71)
+    table, pages = table_of([3000, 2500], 64, g)
+    cache = m.PagedCache(pages, 64, 2, pool=random_pool(pages, 2, 64, 2).cuda())
+    t, n, cu = table.cuda(), ints([3000, 2500]), sums([9, 3])
+    q = [torch.randn((12, 16, HEAD), generator=g).to(torch.bfloat16).cuda() for _ in range(2)]
+    want = [m.tree_attention(cache, x, cu, 9, t, n) for x in q]
+    ws = [m.alloc_tree_workspace(cache, 2, 16, 9) for _ in range(2)]
+    outs = [[torch.empty_like(q[0]) for _ in range(20)] for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for j in range(2):
+            m.tree_attention(cache, q[j], cu, 9, t, n, workspace=ws[j], out=outs[j][i], stream=streams[j])
+    torch.cuda.synchronize()
+    for j in range(2):
+        assert all(torch.equal(o, want[j]) for o in outs[j])
+    assert m.check_device_errors() == 0
 
 
 @pytest.mark.parametrize("window", [0, 20])

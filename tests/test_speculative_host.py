@@ -2,8 +2,11 @@
 refusals (a rejected call launches nothing, so plain numbers stand in for device pointers)."""
 
 import ctypes
+import os
 
 import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 P = ctypes.c_void_p
 OK, EINVAL, EUNSUPPORTED = 0, -1, -2
@@ -118,3 +121,33 @@ def test_accept_refusals(m, kw, status):
 def test_accept_refuses_the_cache_and_takes_nothing(m):
     assert accept(m, cache=desc(m, num_pages=0)) == EINVAL
     assert accept(m, batch=0, bt=None, lens=None, cu=None, acc=None, num=None, new=None) == OK
+
+
+# ------------------------------------------------------------------ the sources: what no output shows
+
+def _source(name):
+    with open(os.path.join(ROOT, "nvfp4_quantised_paged_gb300", "csrc", name)) as f:
+        return f.read()
+
+
+def test_what_the_tree_products_read_is_fenced_before_it_is_reported():
+    src = _source("tree_attention.cu")
+    over = src[src.index("auto hand_over"):]
+    over = over[:over.index("};")]
+    assert over.index("fence.proxy.async.shared::cta") < over.index("tc_wait_st") < over.index("tc_fence_before") \
+        < over.index("__syncwarp") < over.index("mbar_arrive(ready)")
+    # with 128 rows the scores start at the report of K: Q has to be fenced before the barrier that precedes it
+    store = src[src.index("auto store_pair"):]
+    assert store.index("if (W) asm volatile(\"fence.proxy.async.shared::cta") < store.index("workers_sync<N>()")
+    report = src[src.index("auto report_k"):]
+    assert report.index("tc_wait_st") < report.index("tc_fence_before") < report.index("mbar_arrive(k_ready(j))")
+
+
+@pytest.mark.parametrize("name", ["tree_attention.cu", "rope_append.cu"])
+def test_copies_in_flight_are_waited_for_at_the_end(name):
+    src = _source(name)
+    tail = src[src.index("no copy may still be writing when the CTA ends"):]
+    assert "mbar_wait_bounded(" in tail[:400] and "nullptr" in tail[:400]
+    if name == "tree_attention.cu":
+        drain = src[src.index("tc_commit(drain)"):]
+        assert "mbar_wait_bounded(drain" in drain[:200]
