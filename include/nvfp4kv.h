@@ -572,7 +572,8 @@ typedef struct {
 /*
  * Normalise and rotate Q and K a head, and quantise K and V into the pool, in one pass.
  * For every head x of Q (and K), with u = x w r, w = the norm's weights and
- * r = 1 / sqrt(mean(x^2) + eps) (u = x without a norm), and for every rotated pair (a, b) of
+ * r = 1 / sqrt(mean(x^2) + eps) (u = x without a norm; r = 0 where the FP32 sum of squares
+ * overflows), and for every rotated pair (a, b) of
  * angle row (c, s) at the token's position on the pair's axis:
  *   y_a = u_a c - u_b s,  y_b = u_b c + u_a s;   y = u elsewhere,
  * rounded to BF16 once.  Q's y goes to q_out; K's y and V as they would by

@@ -32,6 +32,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -909,6 +910,9 @@ def _head_rows(t, name: str, T: int, H: int, dev: int):
     return t.data_ptr(), st[0] if T > 1 else H * HEAD_DIM
 
 
+_ROPE = struct.Struct("@PqiiiiiiPPf4x")   # nvfp4kv_rope
+
+
 def rope_quantize_append(cache: PagedCache, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
                          positions: Optional[torch.Tensor], cos_sin: Optional[torch.Tensor],
                          slot_mapping: torch.Tensor, q_norm: Optional[torch.Tensor] = None,
@@ -931,29 +935,27 @@ def rope_quantize_append(cache: PagedCache, q: Optional[torch.Tensor], k: torch.
     vp, vs = _head_rows(v, "v", T, Hkv, dev)
     if ks != vs:
         raise ValueError("k and v must share a token stride")
-    rope = _RopeDesc(num_axes=1, adjacent=int(bool(adjacent)), eps=float(eps))
-    pp = 0
+    pp = tp = rows = rot = s0 = s1 = s2 = 0
+    axes = 1
     if cos_sin is not None:
-        rope.cos_sin = _want(cos_sin, "cos_sin", torch.float32, None, dev)
+        tp = _want(cos_sin, "cos_sin", torch.float32, None, dev)
         if cos_sin.dim() != 2:
             raise ValueError("cos_sin must be [positions][rotated values]")
-        rope.num_positions, rope.rot_dim = cos_sin.shape
+        rows, rot = cos_sin.shape
         if sections is None:
             pp = _want(positions, "positions", torch.int32, None, dev)
             if positions.numel() != T:
                 raise ValueError("positions must have %d entries" % T)
         else:
-            rope.num_axes = len(sections)
-            if not 1 <= len(sections) <= 3 or sum(sections) * 2 != rope.rot_dim:
+            axes = len(sections)
+            if not 1 <= axes <= 3 or sum(sections) * 2 != rot:
                 raise ValueError("sections must be one to three counts that sum up to half the rotated values")
-            rope.sections[:len(sections)] = [int(x) for x in sections]
-            pp = _want(positions, "positions", torch.int32, (len(sections), T), dev)
+            s0, s1, s2 = (*(int(x) for x in sections), 0, 0)[:3]
+            pp = _want(positions, "positions", torch.int32, (axes, T), dev)
     elif sections is not None:
         raise ValueError("sections need cos_sin")
-    if q_norm is not None:
-        rope.q_norm = _want(q_norm, "q_norm", torch.bfloat16, (HEAD_DIM,), dev)
-    if k_norm is not None:
-        rope.k_norm = _want(k_norm, "k_norm", torch.bfloat16, (HEAD_DIM,), dev)
+    wq = _want(q_norm, "q_norm", torch.bfloat16, (HEAD_DIM,), dev) if q_norm is not None else 0
+    wk = _want(k_norm, "k_norm", torch.bfloat16, (HEAD_DIM,), dev) if k_norm is not None else 0
     s = _launch_stream(dev, stream)
     Hq = qp = qs = op = os_ = 0
     if q is not None:
@@ -970,7 +972,8 @@ def rope_quantize_append(cache: PagedCache, q: Optional[torch.Tensor], k: torch.
             op, os_ = _head_rows(q_out, "q_out", T, Hq, dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    rc = _lib.nvfp4_rope_quantize_append(cache.desc, ctypes.addressof(rope), qp, qs, op, os_, Hq, kp, vp, ks, T, pp, sp, s)
+    rope = _ROPE.pack(tp, rows, rot, 1 if adjacent else 0, axes, s0, s1, s2, wq, wk, eps)
+    rc = _lib.nvfp4_rope_quantize_append(cache.desc, rope, qp, qs, op, os_, Hq, kp, vp, ks, T, pp, sp, s)
     if rc:
         _check(rc, "nvfp4_rope_quantize_append")
     return q_out

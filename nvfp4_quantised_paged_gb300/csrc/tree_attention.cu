@@ -12,7 +12,7 @@
 // A token costs 144 bytes a kv head and 512 flops a row: the cache's bytes bound it up to some
 // 128 rows, the tensor cores beyond.
 //
-// Tokens sit on the tensor core's M dimension in both products, rows on N (16, 32 or 64),
+// Tokens sit on the tensor core's M dimension in both products, rows on N (16, 32, 64 or 128),
 // so few rows cost little:
 //   S^T (128 tokens x N) = K Q^T     8 steps of M 128 x N x K 16, K as the A operand in TMEM
 //   O^T (128 dims x N) += V^T P^T    8 steps, V and P in shared memory, both MN-major
@@ -20,27 +20,39 @@
 // above 2^-29 of the row's largest value); the tensor scales go into the score's factor and
 // into the output.
 //
-// Two CTAs per SM, ten warps each:
-//   * eight workers expand a tile and run its softmax.  The first warpgroup expands K of the
-//     tile after this one, the second V of this one, a warp two 16-token groups; lane (r, q)
-//     holds the q-th 16 bytes of rows r and r + 8.  K goes to TMEM (the store takes a quad's
-//     registers as four columns each, so the dims lie there in another order: position 16 a +
-//     4 q + e holds dim 32 q + 4 a + e, and Q's with them), V to a swizzled tile in shared
-//     memory.  Softmax: one token (= TMEM lane) a thread, half of the rows a warpgroup; a lazily
-//     moved maximum per row (a vote over the warpgroup; O^T is rescaled only when a score exceeds
-//     it by 2^8), P = 2^(z - m + 7) in FP16, the sums of the rounded P in registers until the
-//     pair ends.
+// Warps:
+//   * eight workers (sixteen with 128 rows) expand a tile and run its softmax.  Expanding: a
+//     warp takes a 16-token group, K and V (with 128 rows one of them); lane (r, q) holds the
+//     q-th 16 bytes of rows r and r + 8.  K goes to TMEM (the store takes a quad's registers as
+//     four columns each, so the dims lie there in another order: position 16 a + 4 q + e holds
+//     dim 32 q + 4 a + e, and Q's with them), V to a swizzled tile in shared memory.  Softmax:
+//     one token (= TMEM lane) a thread, the warpgroups sharing the rows; a lazily moved maximum
+//     per row (a vote over the warpgroup; O^T is rescaled only when a score exceeds it by 2^8),
+//     P = 2^(z - m + 7) in FP16 (the offset uses FP16's upper range), the sums of the rounded P
+//     in registers until the pair ends.  Options and masks change the scores in TMEM before
+//     that, in tiles that have any.
 //   * one warp copies raw tiles (8 groups of 2,304 bytes) into a ring, ahead of everything;
-//   * one warp issues the products: O^T += V^T P^T of a tile and S^T of the next, handed over
-//     together and awaited together, so that a tile costs two waits and one vote.
-// The chain of a tile (wait, expand, softmax, products) is long beside its instructions: the
-// other CTA of the SM fills the gaps.  (One CTA of sixteen workers, with K, V and P double or
-// triple: 61 us for 32 sequences of up to 4,096 tokens, 32 query heads and 8 drafts.)
+//   * one warp issues the products.
+// Up to 64 rows two CTAs share an SM.  K of tile j + 1 is expanded while the products of tile j
+// - 1 run; O^T += V^T P^T of a tile and S^T of the next are handed over together and awaited
+// together, so that a tile costs two waits and one vote.  The chain of a tile (K, wait, V,
+// softmax, products) is long beside its instructions: the other CTA fills the gaps.  With 128
+// rows O^T and S^T leave no TMEM for a second CTA: one, with S double and V triple, so
+// that S^T of tile j + 1 runs during the softmax of tile j.
 //
-// Split: all pairs' 128-token tiles form one flat range (a pair's start counts as one tile
-// more), cut equally over the CTAs of a row tile.  A pair that lies in one CTA is normalised
-// and written there; others leave (m, l, O) partials that a second kernel joins.  Tiles wholly
-// before the window of every row are left out.  Every wait is bounded.
+// Measured (ragged lengths up to n, 64 query and 8 kv heads, cold L2): 16 sequences, n 32,768, 1
+// draft (8 rows) 115 us, 4 drafts (32 rows) 130, 8 (64 rows) 188, 16 (128 rows) 293 to 300: 500
+// TFLOP/s.  A tile takes an SM some 1,250, 1,350, 2,150 and 3,700 clocks (its bytes 780, its
+// products 1,024 with 128 rows): half the issue slots are used, by 3,600 (8 rows) to 10,300
+// (128) warp instructions a tile -- conversions and packed multiplies of 32,768 values, per
+// score a multiply-add, a power of two, a rounding and a sum -- and the rest are latencies of
+// shared memory, TMEM and the waits.  128 rows as two tiles of 64: 327 us.  One CTA of sixteen
+// workers up to 64 rows too: 61 instead of 50 us for 32 sequences, n 4,096, 32 rows.
+//
+// Split: all pairs' 128-token tiles form one flat range (a pair's start and end count as two
+// tiles more), cut equally over the CTAs of a row tile.  A pair that lies in one CTA is
+// normalised and written there; others leave (m, l, O) partials that a second kernel joins.
+// Tiles wholly before the window of every row are left out.  Every wait is bounded.
 #include <mutex>
 
 #include "common.cuh"
@@ -71,7 +83,7 @@ constexpr float kNegInfT = -__builtin_huge_valf();
 constexpr float kRescaleT = 8.0f;
 constexpr float kPOffsetT = 7.0f;             // P = 2^(z - m + 7): at most 2^15
 constexpr float kNoMaxT = 3.402823466e38f;    // the offset while every score was -inf
-constexpr int kPairUnits = 2;                 // what a pair's start costs a CTA, in tiles
+constexpr int kPairUnits = 2;                 // what a pair's start and end cost a CTA, in tiles
 
 template <int N>
 struct TSmem {
@@ -714,7 +726,7 @@ __global__ void __launch_bounds__(kThreadsT<N>, kCtasT<N>) tree_kernel(TreeArgs 
                     tc_wait_st();
                 }
                 // d = z - m + 7, CH rows at a time: with 32 rows a warpgroup once to see whether a maximum must
-                // move and again to form P (held in registers they spill: %(m)s)
+                // move and again to form P (32 of them held in registers beside the sums spill: 336 against 327 us)
                 constexpr int CH = CW < 16 ? CW : 16;
                 float d[CH];
                 auto load_scores = [&](int c0) {

@@ -123,6 +123,13 @@ def test_accept_refuses_the_cache_and_takes_nothing(m):
     assert accept(m, batch=0, bt=None, lens=None, cu=None, acc=None, num=None, new=None) == OK
 
 
+def test_the_packed_rotation_is_the_struct(m):
+    at, r = rope(m, cos_sin=4096, num_positions=7, rot_dim=64, adjacent=1, num_axes=3, sections=(8, 12, 12), q_norm=8192,
+                 k_norm=16384, eps=0.5)
+    assert m._ROPE.size == ctypes.sizeof(r)
+    assert m._ROPE.pack(4096, 7, 64, 1, 3, 8, 12, 12, 8192, 16384, 0.5) == bytes(r)
+
+
 # ------------------------------------------------------------------ the sources: what no output shows
 
 def _source(name):
