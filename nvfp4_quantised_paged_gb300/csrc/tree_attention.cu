@@ -186,6 +186,11 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, const v
     return false;
 }
 
+// Brings `bytes` (a multiple of 16) at p, 16-byte aligned, to L2.
+__device__ __forceinline__ void prefetch_l2(const void *p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -439,9 +444,13 @@ __global__ void __launch_bounds__(kThreadsT<N>, kCtasT<N>) tree_kernel(TreeArgs 
                     mbar_arrive_expect_tx(&raw_full[st], (uint32_t)__popc(mask) * kGroupT);
                 }
                 __syncwarp();
-                if (good)
-                    bulk_g2s(smem + L::kRaw + st * kRawT + lane * kGroupT,
-                             pool + (int64_t)page * a.Hkv * a.slab + ((tok & (a.P - 1)) >> 4) * kGroupT, kGroupT, &raw_full[st]);
+                auto group_at = [&](int32_t pg, int x) {
+                    return pool + (int64_t)pg * a.Hkv * a.slab + ((x & (a.P - 1)) >> 4) * kGroupT;
+                };
+                if (good) bulk_g2s(smem + L::kRaw + st * kRawT + lane * kGroupT, group_at(page, tok), kGroupT, &raw_full[st]);
+                // With two stages the tile after it comes to L2 while its place in the ring is still in use (64 rows: 188
+                // us without, 183 so; with three stages nothing).
+                if (N == 64 && next >= 0 && next < a.num_pages) prefetch_l2(group_at(next, tok + kTileT), kGroupT);
                 page = next;
                 if (++st == S) st = 0, ph ^= 1u;
             }
