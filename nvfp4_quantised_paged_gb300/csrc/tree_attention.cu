@@ -734,11 +734,14 @@ __global__ void __launch_bounds__(kThreadsT<N>, kCtasT<N>) tree_kernel(TreeArgs 
                     }
                     tc_wait_st();
                 }
-                // d = z - m + 7, CH rows at a time: with 32 rows a warpgroup once to see whether a maximum must
-                // move and again to form P (32 of them held in registers beside the sums spill: 336 against 327 us)
+                // P = 2^d, d = z - m + 7, CH rows at a time.  Up to 64 rows by the maxima as they stand, and again where
+                // one has to move; with 128 rows, whose warps have fewer registers to spare, P is formed after the
+                // vote from the scores in TMEM (64 rows: 176 us so, 183 after the vote; 128 rows, 8 sequences of up to 2,000:
+                // 44 us before, 40 after).
                 constexpr int CH = CW < 16 ? CW : 16;
-                float d[CH];
-                auto load_scores = [&](int c0) {
+                uint32_t pw[W ? CH / 2 : CW / 2];
+                float top, top2;
+                auto scan = [&](int c0, auto use) {     // use(c, d of rows c .. c + 3)
                     uint32_t x[CH];
                     load_columns<CH>(tS + c0, x);
                     const float4 *fac = reinterpret_cast<const float4 *>(s_fac + wg * CW + c0);
@@ -747,23 +750,29 @@ __global__ void __launch_bounds__(kThreadsT<N>, kCtasT<N>) tree_kernel(TreeArgs 
 #pragma unroll
                     for (int i = 0; i < CH; i += 4) {
                         const float4 o = off[i / 4], f = fac[i / 4];
-                        d[i] = fmaf(__uint_as_float(x[i]), f.x, o.x);
-                        d[i + 1] = fmaf(__uint_as_float(x[i + 1]), f.y, o.y);
-                        d[i + 2] = fmaf(__uint_as_float(x[i + 2]), f.z, o.z);
-                        d[i + 3] = fmaf(__uint_as_float(x[i + 3]), f.w, o.w);
+                        use(i, fmaf(__uint_as_float(x[i]), f.x, o.x), fmaf(__uint_as_float(x[i + 1]), f.y, o.y),
+                            fmaf(__uint_as_float(x[i + 2]), f.z, o.z), fmaf(__uint_as_float(x[i + 3]), f.w, o.w));
                     }
                 };
-                float top = kNegInfT, top2 = kNegInfT;
+                auto form = [&]() {
+                    top = top2 = kNegInfT;
 #pragma unroll
-                for (int c0 = 0; c0 < CW; c0 += CH) {
-                    load_scores(c0);
-#pragma unroll
-                    for (int c = 0; c < CH; c += 4) {
-                        top = max3(top, d[c], d[c + 1]);
-                        top2 = max3(top2, d[c + 2], d[c + 3]);
-                    }
+                    for (int c0 = 0; c0 < CW; c0 += CH)
+                        scan(c0, [&](int i, float d0, float d1, float d2, float d3) {
+                            top = max3(top, d0, d1);
+                            top2 = max3(top2, d2, d3);
+                            if (!W) {
+                                pw[(c0 + i) / 2] = f32x2_to_f16x2(ex2(d1), ex2(d0));
+                                pw[(c0 + i) / 2 + 1] = f32x2_to_f16x2(ex2(d3), ex2(d2));
+                            }
+                        });
+                };
+                bool moves = t == it.t;             // (a pair's first tile sets them)
+                if (!moves) {
+                    form();
+                    moves = group_any(wg, fmaxf(top, top2) > kRescaleT + kPOffsetT);
                 }
-                if (group_any(wg, fmaxf(top, top2) > kRescaleT + kPOffsetT)) {
+                if (moves) {
                     float *wmax = reinterpret_cast<float *>(smem + L::kWarpMax) + wg * 4 * CW;
                     int mine = 0;
 #pragma unroll 1
@@ -806,20 +815,21 @@ __global__ void __launch_bounds__(kThreadsT<N>, kCtasT<N>) tree_kernel(TreeArgs 
                         }
                         tc_wait_st();
                     }
-                    if (CW == CH) load_scores(0);
+                    if (!W) form();
                 }
                 if (W && phase > 0) wait(pv_done(phase - 1), ((phase - 1) >> 1) & 1);    // P is read
                 uint8_t *pt = smem + L::kP + (wg * CW / 64) * kBlockT;
 #pragma unroll
                 for (int c0 = 0; c0 < CW; c0 += 8) {
-                    if (CW > CH && c0 % CH == 0) load_scores(c0);
-                    uint32_t pw[4];
+                    if (W && c0 % CH == 0)
+                        scan(c0, [&](int i, float d0, float d1, float d2, float d3) {
+                            pw[i / 2] = f32x2_to_f16x2(ex2(d1), ex2(d0));
+                            pw[i / 2 + 1] = f32x2_to_f16x2(ex2(d3), ex2(d2));
+                        });
+                    const uint32_t *w = pw + (W ? c0 % CH : c0) / 2;
 #pragma unroll
-                    for (int e = 0; e < 4; e++) {
-                        pw[e] = f32x2_to_f16x2(ex2(d[c0 % CH + 2 * e + 1]), ex2(d[c0 % CH + 2 * e]));
-                        add_f16x2(l[c0 + 2 * e], l[c0 + 2 * e + 1], pw[e]);
-                    }
-                    *reinterpret_cast<uint4 *>(pt + sw128_off(row, ((wg * CW + c0) & 63) / 8)) = make_uint4(pw[0], pw[1], pw[2], pw[3]);
+                    for (int e = 0; e < 4; e++) add_f16x2(l[c0 + 2 * e], l[c0 + 2 * e + 1], w[e]);
+                    *reinterpret_cast<uint4 *>(pt + sw128_off(row, ((wg * CW + c0) & 63) / 8)) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
                 hand_over();
                 if (W) phase++;
