@@ -41,13 +41,15 @@
 // that S^T of tile j + 1 runs during the softmax of tile j.
 //
 // Measured (ragged lengths up to n, 64 query and 8 kv heads, cold L2): 16 sequences, n 32,768, 1
-// draft (8 rows) 115 us, 4 drafts (32 rows) 130, 8 (64 rows) 188, 16 (128 rows) 293 to 300: 500
-// TFLOP/s.  A tile takes an SM some 1,250, 1,350, 2,150 and 3,700 clocks (its bytes 780, its
-// products 1,024 with 128 rows): half the issue slots are used, by 3,600 (8 rows) to 10,300
-// (128) warp instructions a tile -- conversions and packed multiplies of 32,768 values, per
-// score a multiply-add, a power of two, a rounding and a sum -- and the rest are latencies of
-// shared memory, TMEM and the waits.  128 rows as two tiles of 64: 327 us.  One CTA of sixteen
-// workers up to 64 rows too: 61 instead of 50 us for 32 sequences, n 4,096, 32 rows.
+// draft (8 rows) 115 us, 4 drafts (32 rows) 129, 8 (64 rows) 176, 16 (128 rows) 302: 470
+// TFLOP/s.  A tile takes an SM some 1,250, 1,350, 2,000 and 3,700 clocks (its bytes 780, its
+// products 1,024 with 128 rows).  Few rows: shared memory's 128 bytes a clock, some 80% taken (V
+// written 256 clocks and read by the products 256 to 300, the raw tile written and read 300, Q, P,
+// scales and factors the rest).  Many rows: the chain of a tile, at half the issue slots, of 3,600 (8
+// rows) to 10,300 (128) warp instructions -- conversions and packed multiplies of 32,768 values,
+// per score a multiply-add, a power of two, a rounding and a sum.  (Without the powers of two: 2%
+// less.)  128 rows as two tiles of 64: 327 us.  One CTA of sixteen workers up to 64 rows too: 61
+// instead of 50 us for 32 sequences, n 4,096, 32 rows.
 //
 // Split: all pairs' 128-token tiles form one flat range (a pair's start and end count as two
 // tiles more), cut equally over the CTAs of a row tile.  A pair that lies in one CTA is
