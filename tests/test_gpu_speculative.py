@@ -644,3 +644,40 @@ def test_calls_on_another_stream(m):
         side.synchronize()
         assert torch.equal(got, want)
         del junk
+
+
+def test_wrong_tensors_are_refused(m):
+    """The binding's own checks: types, shapes, devices."""
+    cache = m.PagedCache(2, 16, 2)
+    k = torch.zeros((3, 2, HEAD), dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros((3, 4, HEAD), dtype=torch.bfloat16, device="cuda")
+    slots, pos, turn = torch.arange(3, device="cuda"), ints([0, 1, 2]), rotation(8, 128).cuda()
+    ok = dict(q=q, k=k, v=k, positions=pos, cos_sin=turn, slot_mapping=slots)
+    m.rope_quantize_append(cache, **ok)
+    for bad in (dict(k=k.float()), dict(k=k[:2]), dict(v=k[..., :64]), dict(q=q[:, :, ::2]), dict(q=q.cpu()), dict(positions=pos.long()),
+                dict(positions=pos[:2]), dict(positions=None), dict(cos_sin=turn.double()), dict(cos_sin=turn[0]),
+                dict(slot_mapping=slots.int()), dict(sections=(16, 24)), dict(sections=(16, 24, 24)), dict(cos_sin=None, sections=(64,)),
+                dict(q_norm=turn[0]), dict(k_norm=k[0, 0, :64]), dict(q=None, q_out=q), dict(q_out=q[:2]),
+                dict(k=torch.zeros((3, 4, HEAD), dtype=torch.bfloat16, device="cuda")[:, ::2])):
+        with pytest.raises(ValueError):
+            m.rope_quantize_append(cache, **{**ok, **bad})
+    t, n, cu = ints([[0, 1]]), ints([20]), ints([0, 3])
+    ok = dict(q=q, cu_q_lens=cu, max_q_len=3, block_table=t, seq_lens=n)
+    m.tree_attention(cache, **ok)
+    for bad in (dict(q=q.float()), dict(q=q[0]), dict(cu_q_lens=cu[:1]), dict(cu_q_lens=cu.long()), dict(block_table=t[0]),
+                dict(seq_lens=n.long()), dict(tree_mask=ints([1, 3, 7])), dict(tree_mask=slots[:2]), dict(slopes=turn[0]),
+                dict(out=k), dict(workspace=turn)):
+        with pytest.raises(ValueError):
+            m.tree_attention(cache, **{**ok, **bad})
+    for bad in (dict(max_q_len=0), dict(max_q_len=65), dict(window=-1), dict(softcap=-1.0), dict(out=q),
+                dict(workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(m.NVFP4KVError):
+            m.tree_attention(cache, **{**ok, **bad})
+    ok = dict(block_table=t, seq_lens=n, cu_q_lens=cu, accepted=ints([[0, 1]]), num_accepted=ints([2]))
+    m.accept_tokens(cache, **ok)
+    for bad in (dict(accepted=ints([0, 1])), dict(num_accepted=ints([2, 2])), dict(cu_q_lens=n), dict(new_lens=n.long())):
+        with pytest.raises(ValueError):
+            m.accept_tokens(cache, **{**ok, **bad})
+    with pytest.raises(m.NVFP4KVError):
+        m.accept_tokens(cache, **ok, new_lens=n)
+    assert m.check_device_errors() == 0

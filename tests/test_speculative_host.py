@@ -27,11 +27,18 @@ def desc(m, **kw):
                                      d["k"], d["v"]))
 
 
+class Rope(ctypes.Structure):
+    """nvfp4kv_rope of the header."""
+    _fields_ = [("cos_sin", P), ("num_positions", ctypes.c_int64), ("rot_dim", ctypes.c_int32), ("adjacent", ctypes.c_int32),
+                ("num_axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 3), ("q_norm", P), ("k_norm", P),
+                ("eps", ctypes.c_float)]
+
+
 def rope(m, **kw):
     d = dict(cos_sin=4096, num_positions=10, rot_dim=128, adjacent=0, num_axes=1, sections=(0, 0, 0), q_norm=None, k_norm=None,
              eps=1e-6)
     d.update(kw)
-    r = m._RopeDesc(d["cos_sin"], d["num_positions"], d["rot_dim"], d["adjacent"], d["num_axes"])
+    r = Rope(d["cos_sin"], d["num_positions"], d["rot_dim"], d["adjacent"], d["num_axes"])
     r.sections[:] = d["sections"]
     r.q_norm, r.k_norm, r.eps = d["q_norm"], d["k_norm"], d["eps"]
     return ctypes.addressof(r), r
