@@ -631,8 +631,11 @@ cudaError_t launch_rope_append(const nvfp4kv_cache &c, const nvfp4kv_rope &rope,
     plan.token_bytes = (a.Hq + 2 * a.Hkv) * 256 + 4 * a.rot;
     plan.tps = std::max(1, std::min(kMaxTps, 16 * 1024 / plan.token_bytes));
     plan.stages = std::min(kMaxStages, (int)((kStreamBytes - sizeof(StreamMisc)) / ((size_t)plan.tps * plan.token_bytes)));
-    // A ring of two stages at least, and more groups of rows than the GPU's warps at once.
-    if (plan.stages < 2 || num_tokens * groups <= 152 * 2 * kWarpsR * 2) {
+    // The ring (of two stages at least) from 12,000 groups of four rows on.  Direct form and ring, with norms: 64 + 8
+    // heads 13.0 and 13.0 us for 256 tokens (5,000 groups), 21.2 and 19.2 for 1,024, 219.8 and 142.0 for 16,384; 32 + 8
+    // heads 17.1 and 19.1 for 1,024 (12,000 groups), 43.7 and 41.6 for 4,096; 4 + 1 heads 10.9 and 13.0 for 1,024, 25.2
+    // and 21.2 for 4,096 (12,000 groups).
+    if (plan.stages < 2 || num_tokens * groups < 12000) {
         void *args[] = {&a};
         const void *few[2][2] = {{reinterpret_cast<const void *>(&rope_append_kernel<false, false>),
                                   reinterpret_cast<const void *>(&rope_append_kernel<false, true>)},

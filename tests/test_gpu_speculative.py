@@ -77,7 +77,10 @@ WRITE = [  # tokens, q heads, kv heads, page, rot, adjacent, sections, norms, sc
     (50, 4, 4, 16, 128, True, (4, 40, 20), False, 0.6, False),
     (41, 4, 2, 16, 64, False, (0, 32), True, 1.0, True),
     (20, 7, 1, 16, 0, False, None, True, 1.0, False),
-    (1500, 32, 8, 64, 128, False, None, True, 1.0, False),
+    (999, 32, 8, 64, 128, False, None, True, 1.0, False),
+    (1000, 32, 8, 64, 128, False, None, True, 1.0, False),
+    (1500, 33, 7, 64, 128, True, None, True, 1.0, True),
+    (1300, 40, 8, 64, 96, False, None, False, 1.0, False),
     (4097, 16, 4, 64, 128, False, None, True, 0.75, False),
 ]
 
