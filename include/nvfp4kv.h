@@ -575,7 +575,8 @@ typedef struct {
  * r = 1 / sqrt(mean(x^2) + eps) (u = x without a norm; r = 0 where the FP32 sum of squares
  * overflows), and for every rotated pair (a, b) of
  * angle row (c, s) at the token's position on the pair's axis:
- *   y_a = u_a c - u_b s,  y_b = u_b c + u_a s;   y = u elsewhere,
+ *   y_a = u_a c - u_b s,  y_b = u_b c + u_a s;   y = u elsewhere (an infinity or a NaN there stays where
+ *   it is; with r = 0 it gives a NaN and the row's finite values zeros),
  * rounded to BF16 once.  Q's y goes to q_out; K's y and V as they would by
  * nvfp4_kv_quantize_append of that y (K's rounding to BF16 is the exact value's up to 2^-40
  * of the pair's larger product, as a code may hang on it; Q's is formed in FP32).

@@ -161,37 +161,50 @@ __device__ __forceinline__ void make_turn(const RopeArgs &a, const float (&c)[8]
     }
 }
 
-// The eight threads of a row call it together (as do the four rows of the warp).
+// The eight threads of a row call it together (as do the four rows of the warp).  Behind the rotation the partner is
+// multiplied by a sine of zero, which adds nothing while the row is finite: a row whose norm is not, and one without a
+// norm, goes without.
 template <bool kAdj>
-__device__ __forceinline__ void turn_q(const RopeArgs &a, const Turn &u, uint4 &xa, uint4 &xb) {
-    uint32_t va[4], vb[4];
+__device__ __forceinline__ void turn_q(const RopeArgs &a, bool turned, const Turn &u, uint4 &xa, uint4 &xb) {
+    uint32_t va[4], vb[4], ya[4], yb[4];
     words(xa, va);
     words(xb, vb);
-    uint64_t ya[4], yb[4], q = 0;
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const uint64_t x = bf16_pair(va[i]), z = bf16_pair(vb[i]);
-        const uint64_t px = kAdj ? pack2(bf16_hi(va[i]), bf16_lo(va[i])) : z;
-        const uint64_t pz = kAdj ? pack2(bf16_hi(vb[i]), bf16_lo(vb[i])) : x;
-        ya[i] = fma_pair(x, u.pa[i], mul_pair(px, u.ma[i]));
-        yb[i] = fma_pair(z, u.pb[i], mul_pair(pz, u.mb[i]));
-        q = fma_pair(z, z, fma_pair(x, x, q));
-    }
+    float r = 1.0f;
     if (a.wq) {
+        uint64_t q = 0;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const uint64_t x = bf16_pair(va[i]), z = bf16_pair(vb[i]);
+            q = fma_pair(z, z, fma_pair(x, x, q));
+        }
         float sum = low2(q) + high2(q);
 #pragma unroll
         for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        const float r = rsqrtf(fmaf(sum, 0.0078125f, a.eps));
+        r = rsqrtf(fmaf(sum, 0.0078125f, a.eps));
+    }
+    auto rounded = [&](uint64_t y) {
+        if (a.wq) y = mul_pair(y, pack2(r, r));
+        return f32x2_to_bf16x2(high2(y), low2(y));
+    };
+    if (!turned && !(a.wq && r > 0.0f)) {
+        if (!a.wq) return;
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-            ya[i] = mul_pair(ya[i], pack2(r, r));
-            yb[i] = mul_pair(yb[i], pack2(r, r));
+            ya[i] = rounded(mul_pair(bf16_pair(va[i]), u.pa[i]));
+            yb[i] = rounded(mul_pair(bf16_pair(vb[i]), u.pb[i]));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const uint64_t x = bf16_pair(va[i]), z = bf16_pair(vb[i]);
+            const uint64_t px = kAdj ? pack2(bf16_hi(va[i]), bf16_lo(va[i])) : z;
+            const uint64_t pz = kAdj ? pack2(bf16_hi(vb[i]), bf16_lo(vb[i])) : x;
+            ya[i] = rounded(fma_pair(x, u.pa[i], mul_pair(px, u.ma[i])));
+            yb[i] = rounded(fma_pair(z, u.pb[i], mul_pair(pz, u.mb[i])));
         }
     }
-    xa = make_uint4(f32x2_to_bf16x2(high2(ya[0]), low2(ya[0])), f32x2_to_bf16x2(high2(ya[1]), low2(ya[1])),
-                    f32x2_to_bf16x2(high2(ya[2]), low2(ya[2])), f32x2_to_bf16x2(high2(ya[3]), low2(ya[3])));
-    xb = make_uint4(f32x2_to_bf16x2(high2(yb[0]), low2(yb[0])), f32x2_to_bf16x2(high2(yb[1]), low2(yb[1])),
-                    f32x2_to_bf16x2(high2(yb[2]), low2(yb[2])), f32x2_to_bf16x2(high2(yb[3]), low2(yb[3])));
+    xa = make_uint4(ya[0], ya[1], ya[2], ya[3]);
+    xb = make_uint4(yb[0], yb[1], yb[2], yb[3]);
 }
 
 // K: the chunks' exact values rounded to BF16, then exchanged so that the thread holds a whole block; returns which.
@@ -222,16 +235,18 @@ __device__ __forceinline__ int turn_k(const RopeArgs &a, const Place &p, int blk
             dm *= r;
             dy = 0x1.6p-21f;
         }
-        auto both = [&](uint64_t u, uint64_t cc, uint64_t z, uint64_t ss) {
-            const uint64_t m = mul_pair(z, ss);
-            uint64_t y = fma_pair(u, cc, m);
-            if (a.wk) y = mul_pair(y, pack2(r, r));
-            const float e0 = fmaf(fabsf(low2(m)), dm, fabsf(low2(y)) * dy), e1 = fmaf(fabsf(high2(m)), dm, fabsf(high2(y)) * dy);
+        auto ends = [&](uint64_t y, float e0, float e1) {
             const uint32_t lo = f32x2_to_bf16x2(high2(y) - e1, low2(y) - e0), hi = f32x2_to_bf16x2(high2(y) + e1, low2(y) + e0);
             differ |= lo ^ hi;
             return lo;
         };
-        if (p.turned || a.wk) {
+        auto both = [&](uint64_t u, uint64_t cc, uint64_t z, uint64_t ss) {
+            const uint64_t m = mul_pair(z, ss);
+            uint64_t y = fma_pair(u, cc, m);
+            if (a.wk) y = mul_pair(y, pack2(r, r));
+            return ends(y, fmaf(fabsf(low2(m)), dm, fabsf(low2(y)) * dy), fmaf(fabsf(high2(m)), dm, fabsf(high2(y)) * dy));
+        };
+        if (p.turned) {
 #pragma unroll
             for (int i = 0; i < 4; i++) {
                 const uint64_t ua = mul_pair(bf16_pair(va[i]), bf16_pair(wa[i])), ub = mul_pair(bf16_pair(vb[i]), bf16_pair(wb[i]));
@@ -242,6 +257,14 @@ __device__ __forceinline__ int turn_k(const RopeArgs &a, const Place &p, int blk
                     ya[i] = both(ua, pack2(c[2 * i], c[2 * i + 1]), ub, pack2(-s[2 * i], -s[2 * i + 1]));
                     yb[i] = both(ub, pack2(c[2 * i], c[2 * i + 1]), ua, pack2(s[2 * i], s[2 * i + 1]));
                 }
+            }
+        } else if (a.wk) {                      // (no partner: see turn_q)
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const uint64_t y = mul_pair(mul_pair(bf16_pair(va[i]), bf16_pair(wa[i])), pack2(r, r));
+                const uint64_t z = mul_pair(mul_pair(bf16_pair(vb[i]), bf16_pair(wb[i])), pack2(r, r));
+                ya[i] = ends(y, fabsf(low2(y)) * dy, fabsf(high2(y)) * dy);
+                yb[i] = ends(z, fabsf(low2(z)) * dy, fabsf(high2(z)) * dy);
             }
         } else {
 #pragma unroll
@@ -373,7 +396,7 @@ __global__ void __launch_bounds__(kThreadsR) rope_append_kernel(RopeArgs a) {
         words(weight_chunk(a.wq, p.cb), wb);
         Turn u;
         make_turn<kAdj>(a, c, s, wa, wb, u);
-        turn_q<kAdj>(a, u, xa, xb);
+        turn_q<kAdj>(a, p.turned, u, xa, xb);
         if (row < nrows) {
             uint4 *dst = a.q_out + t * a.out_stride16 + row * 16;
             dst[p.ca] = xa;
@@ -414,7 +437,9 @@ struct StreamMisc {
 };
 constexpr int64_t kNoToken = -2;
 
-template <bool kUnitScale, bool kAdj>
+// kAll: all 128 values are rotated, a form of its own for adjacent pairs (32,768 tokens of 64 + 8 heads with norms: 285 us
+// without it, 271 so; half-split pairs 270 without, 304 so).
+template <bool kUnitScale, bool kAdj, bool kAll>
 __global__ void __launch_bounds__(kThreadsS, 2) rope_stream_kernel(RopeArgs a, StreamPlan plan) {
     extern __shared__ __align__(128) uint8_t smem[];
     StreamMisc &m = *reinterpret_cast<StreamMisc *>(smem + plan.stages * plan.tps * plan.token_bytes);
@@ -496,7 +521,8 @@ __global__ void __launch_bounds__(kThreadsS, 2) rope_stream_kernel(RopeArgs a, S
             mbar_wait_bounded(&m.full[i % plan.stages], (uint32_t)(i / plan.stages) & 1, kWaitLimitR, nullptr);
     } else {
         const int blk = lane & 7, g = lane >> 3;
-        const Place p = place_of<kAdj>(a, blk);
+        Place p = place_of<kAdj>(a, blk);
+        if (kAll) p.turned = true, p.split = !kAdj;
         // A token's units: four rows of K, four of V, eight of Q.  Those of K take longest, so the warps take turns.
         const int nq = (a.Hq + 7) / 8, nk = (a.Hkv + 3) / 4, per = nq + 2 * nk;
         const uint64_t policy = l2_policy_evict_last();
@@ -563,7 +589,7 @@ __global__ void __launch_bounds__(kThreadsS, 2) rope_stream_kernel(RopeArgs a, S
                     Turn u;
                     make_turn<kAdj>(a, c, s, wa, wb, u);
 #pragma unroll
-                    for (int e = 0; e < 2; e++) turn_q<kAdj>(a, u, xa[e], xb[e]);
+                    for (int e = 0; e < 2; e++) turn_q<kAdj>(a, p.turned, u, xa[e], xb[e]);
 #pragma unroll
                     for (int e = 0; e < 2; e++) {
                         if (row + 4 * e >= a.Hq) continue;
@@ -648,15 +674,17 @@ cudaError_t launch_rope_append(const nvfp4kv_cache &c, const nvfp4kv_rope &rope,
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess && (dev < 0 || dev >= kMaxDevicesR)) e = cudaErrorInvalidDevice;
     if (e != cudaSuccess) return e;
-    const void *fn[2][2] = {{reinterpret_cast<const void *>(&rope_stream_kernel<false, false>),
-                             reinterpret_cast<const void *>(&rope_stream_kernel<false, true>)},
-                            {reinterpret_cast<const void *>(&rope_stream_kernel<true, false>),
-                             reinterpret_cast<const void *>(&rope_stream_kernel<true, true>)}};
+    const void *fn[2][3] = {{reinterpret_cast<const void *>(&rope_stream_kernel<false, false, false>),
+                             reinterpret_cast<const void *>(&rope_stream_kernel<false, true, false>),
+                             reinterpret_cast<const void *>(&rope_stream_kernel<false, true, true>)},
+                            {reinterpret_cast<const void *>(&rope_stream_kernel<true, false, false>),
+                             reinterpret_cast<const void *>(&rope_stream_kernel<true, true, false>),
+                             reinterpret_cast<const void *>(&rope_stream_kernel<true, true, true>)}};
     {
         std::lock_guard<std::mutex> lock(g_mu_r);
         if (!g_sms_r[dev]) {
-            for (int i = 0; i < 4; i++) {
-                e = cudaFuncSetAttribute(fn[i >> 1][i & 1], cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamBytes);
+            for (int i = 0; i < 6; i++) {
+                e = cudaFuncSetAttribute(fn[i / 3][i % 3], cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamBytes);
                 if (e != cudaSuccess) return e;
             }
             e = cudaDeviceGetAttribute(&g_sms_r[dev], cudaDevAttrMultiProcessorCount, dev);
@@ -666,7 +694,7 @@ cudaError_t launch_rope_append(const nvfp4kv_cache &c, const nvfp4kv_rope &rope,
     }
     void *args[] = {&a, &plan};
     const int64_t grid = std::min((int64_t)2 * sms, (num_tokens + plan.tps - 1) / plan.tps);
-    return launch_pdl(fn[unit][a.adjacent], dim3((unsigned)grid), kThreadsS,
+    return launch_pdl(fn[unit][!a.adjacent ? 0 : a.rot < kHeadDim ? 1 : 2], dim3((unsigned)grid), kThreadsS,
                       (size_t)plan.stages * plan.tps * plan.token_bytes + sizeof(StreamMisc), stream, args);
 }
 

@@ -1,0 +1,89 @@
+"""Edges of the speculative decoding calls on the GPU: values behind the rotation, large caps, scales that are not
+positive, many heads, and what stays as it was where a call flags its inputs."""
+
+import math
+
+import pytest
+import torch
+
+import speculative_plain as plain
+from speculative_plain import HEAD
+from test_gpu_speculative import gen, packed, rotation
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def m():
+    import nvfp4_quantised_paged_gb300 as mod
+    return mod
+
+
+def finite_rounded(y):
+    """64-bit numbers rounded to BF16 once, infinities and NaN as they are."""
+    fine = torch.isfinite(y)
+    return torch.where(fine, plain.bf16_rounded(torch.where(fine, y, 1.0)).double(), y).to(torch.bfloat16)
+
+
+# --------------------------------------------------------------------------------- rotated append
+
+@pytest.mark.parametrize("T", [8, 6000])
+@pytest.mark.parametrize("rot", [0, 32, 64])
+@pytest.mark.parametrize("adjacent", [False, True])
+@pytest.mark.parametrize("norms", [False, True])
+def test_infinities_behind_the_rotation_stay_where_they_are(m, T, rot, adjacent, norms):
+    """Infinities and NaN at rotated and at other values: y = u behind the rotation, and a norm that is infinite gives
+    zeros (the rotation by angles whose cosine and sine are 0 or 1, so that every other product is exact)."""
+    hq, hkv = 4, 4
+    g = gen(rot + T)
+    x = torch.randint(-8, 9, (T, hq + 2 * hkv, HEAD), generator=g).float()
+    x[::5, 1, 127], x[1::7, 2, 100], x[2::9, 0, 70], x[3::4, 3, 3] = math.inf, math.nan, -math.inf, math.inf
+    x[::3, hq, 127], x[1::7, hq + 1, 99], x[2::5, hq + 2, 66], x[3::4, hq + 3, 3] = -math.inf, math.nan, math.inf, math.inf
+    half = rot // 2
+    table = torch.tensor([[1.0] * half + [0.0] * half, [0.0] * half + [1.0] * half]) if rot else None
+    pos = torch.randint(0, 2, (T,), generator=g, dtype=torch.int32)
+    w = torch.exp2(torch.randint(-1, 2, (HEAD,), generator=g).float()).to(torch.bfloat16) if norms else None
+    slots = torch.arange(T)
+    pages = -(-T // 64)
+    a, b = m.PagedCache(pages, 64, hkv), m.PagedCache(pages, 64, hkv)
+    x = x.to(torch.bfloat16)
+    q, k, v = x.cuda().split([hq, hkv, hkv], 1)
+    on = lambda t: None if t is None else t.cuda()  # noqa: E731
+    out = m.rope_quantize_append(a, q, k, v, pos.cuda(), on(table), slots.cuda(), q_norm=on(w), k_norm=on(w), eps=0.0,
+                                 adjacent=adjacent).cpu()
+    rq, _ = plain.turned(x[:, :hq], w, pos, table, 0.0, adjacent, None)
+    rk, _ = plain.turned(x[:, hq:hq + hkv], w, pos, table, 0.0, adjacent, None)
+    fine = torch.isfinite(rq)
+    assert torch.equal(torch.isnan(out), torch.isnan(rq))
+    assert torch.equal(torch.isinf(out), torch.isinf(rq))
+    assert ((out.double() - rq)[fine].abs() <= (2.0**-8 + 2.0**-18) * rq[fine].abs()).all()   # half a step, and FP32's
+    if not norms:
+        assert torch.equal(torch.nan_to_num(out[..., rot:], nan=3.0), torch.nan_to_num(x[:, :hq, rot:], nan=3.0))
+    m.quantize_append(b, packed(finite_rounded(rk)), packed(x[:, hq + hkv:]), slots.cuda())
+    # (as values: where a row's norm is infinite, the order of rotation and norm decides a zero's sign)
+    for ours, other in zip(*(plain.rows_of(c.pool.cpu(), 64, torch.arange(pages), T) for c in (a, b))):
+        assert torch.equal(torch.isnan(ours), torch.isnan(other))
+        assert torch.equal(torch.nan_to_num(ours), torch.nan_to_num(other))
+    assert m.check_device_errors() == 0
+
+
+@pytest.mark.parametrize("T", [9, 6000])
+@pytest.mark.parametrize("rot,adjacent", [(0, False), (64, False), (64, True), (128, True)])
+@pytest.mark.parametrize("norms", [False, True])
+def test_zeros_keep_their_signs_in_the_pages(m, T, rot, adjacent, norms):
+    hkv = 4
+    g = gen(T + rot)
+    x = torch.randint(-3, 4, (T, 2 * hkv, HEAD), generator=g).float()
+    x = torch.where((x == 0) & (torch.rand(x.shape, generator=g) < 0.5), -x, x).to(torch.bfloat16)
+    assert torch.signbit(x[x == 0]).any() and not torch.signbit(x[x == 0]).all()
+    table = rotation(50, rot) if rot else None
+    pos = torch.randint(0, 50, (T,), generator=g, dtype=torch.int32)
+    w = (torch.randn(HEAD, generator=g) * 0.3 + 1).to(torch.bfloat16) if norms else None
+    slots = torch.arange(T).cuda()
+    a, b = m.PagedCache(-(-T // 64), 64, hkv), m.PagedCache(-(-T // 64), 64, hkv)
+    on = lambda t: None if t is None else t.cuda()  # noqa: E731
+    k, v = x.cuda().split([hkv, hkv], 1)
+    m.rope_quantize_append(a, None, k, v, pos.cuda(), on(table), slots, k_norm=on(w), adjacent=adjacent)
+    rk, _ = plain.turned(x[:, :hkv], w, pos, table, 1e-6, adjacent, None)
+    m.quantize_append(b, packed(plain.bf16_rounded(rk)), packed(x[:, hkv:]), slots)
+    assert torch.equal(a.pool, b.pool) and m.check_device_errors() == 0
