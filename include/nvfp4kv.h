@@ -625,7 +625,9 @@ NVFP4KV_API size_t nvfp4kv_tree_workspace_bytes(const nvfp4kv_cache *cache, int 
  *                 draft i sees drafts 0..i
  *   block_table, seq_lens  as nvfp4_paged_decode_attention; d > n > 0 is flagged and yields
  *                 zeros; tokens of a page outside the pool are flagged and not seen
- *   softcap >= 0 (0: none), window >= 0 (0: none), slopes device float [num_q_heads] or NULL
+ *   softcap >= 0 (0: none; capped scores are off by at most 2^-20 of themselves or, with caps from
+ *                 2^-10 to 128, 2^-14.6), window >= 0 (0: none), slopes device float [num_q_heads]
+ *                 or NULL
  *   out           device BF16 [total_q][num_q_heads][128], not q; rows of no sequence are left
  *                 as they are
  *   workspace     device, >= nvfp4kv_tree_workspace_bytes(...), 256-byte aligned; calls that

@@ -55,6 +55,8 @@
 // tiles more), cut equally over the CTAs of a row tile.  A pair that lies in one CTA is
 // normalised and written there; others leave (m, l, O) partials that a second kernel joins.
 // Tiles wholly before the window of every row are left out.  Every wait is bounded.
+#include <algorithm>
+#include <cfloat>
 #include <mutex>
 
 #include "common.cuh"
@@ -125,7 +127,8 @@ struct TreeArgs {
     const float *slopes;      // [Hq] or nullptr
     float score_log2;         // sm_scale * g_K * log2(e)
     float cap_log2;           // cap * log2(e), 0: none
-    float cap_in;             // 2 log2(e) / cap * sm_scale * g_K
+    float cap_in;             // 2 log2(e) / cap * sm_scale * g_K for a cap of kCapFrom to kCapTo, 0 for others
+    float cap_rcp;            // 1 / (cap * log2(e))
     int window;               // 0: none
     float gv;
     __nv_bfloat16 *out;
@@ -212,6 +215,42 @@ __device__ __noinline__ uint32_t without_nan(uint32_t scales, unsigned *s_nan, i
         scales &= ~(0xffu << (8 * i));
     }
     return scales;
+}
+
+// cap tanh(x) of e2x = 2 x log2(e).  Each step is off by some 2^-23 of the cap, together 1.3 2^-22 of it: of a score
+// up to kCapTo that moves its weight by 2^-14.6 at most.
+constexpr double kCapFrom = 0x1p-10, kCapTo = 128.0;
+
+__device__ __forceinline__ float capped(float e2x, float cap) { return fmaf(-2.0f * cap, rcp_approx(ex2(e2x) + 1.0f), cap); }
+
+// z = cap tanh(z / cap) of any cap (rcp: 1 / cap), off by at most 2^-20 of itself.  With x = z / cap: below 1/2, z
+// tanh(x) / x by a polynomial in x^2 (off by 2^-26; coefficients solved for the least largest relative error); above,
+// as before, off by 2^-22 of the cap, which is 2.2 z at most there.
+__device__ __forceinline__ void any_cap(float (&z)[4], float cap, float rcp) {
+    float t[4];
+    bool large = false;
+#pragma unroll
+    for (int c = 0; c < 4; c++) {
+        const float x = z[c] * rcp, y = x * x;
+        large = large || !(y < 0.25f);
+        const float p = fmaf(fmaf(fmaf(0.017135007f, y, -0.052986074f), y, 0.13324779f), y, -0.3333307f);
+        t[c] = fmaf(z[c], p * y, z[c]);
+    }
+    if (large) {
+#pragma unroll
+        for (int c = 0; c < 4; c++) {
+            const float x = z[c] * rcp;
+            if (!(x * x < 0.25f)) t[c] = capped(2.8853900817779268f * x, cap);
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < 4; c++) z[c] = t[c];
+}
+
+__device__ __noinline__ float4 any_cap_called(float4 z, float cap, float rcp) {
+    float v[4] = {z.x, z.y, z.z, z.w};
+    any_cap(v, cap, rcp);
+    return make_float4(v[0], v[1], v[2], v[3]);
 }
 
 // s0 += low FP16 of w, s1 += high FP16 of w
@@ -631,7 +670,7 @@ __global__ void __launch_bounds__(kThreadsT<N>, kCtasT<N>) tree_kernel(TreeArgs 
             }
             if (lane < R) {
                 const int c = warp + kWarps * lane;
-                const float fac = (OPT && a.cap_log2 > 0.f ? a.cap_in : a.score_log2) * __uint_as_float((uint32_t)(127 - my_kq) << 23);
+                const float fac = (OPT && a.cap_in != 0.f ? a.cap_in : a.score_log2) * __uint_as_float((uint32_t)(127 - my_kq) << 23);
                 // (a positive factor stays one, so that minus infinity times it is minus infinity: no score
                 // reaches 2^34, and 2^-92 is none)
                 s_fac[c] = OPT ? 1.f : fmaxf(fac, 0x1p-126f);
@@ -722,12 +761,26 @@ __global__ void __launch_bounds__(kThreadsT<N>, kCtasT<N>) tree_kernel(TreeArgs 
                                 *reinterpret_cast<float4 *>(dep + 4 * i) = reinterpret_cast<const float4 *>(s_dep + wg * CW + c0)[i];
                             }
 #pragma unroll
-                            for (int c = 0; c < 8; c++) {
-                                float z = __uint_as_float(x[c]) * in[c];
-                                if (a.cap_log2 > 0.f)        // cap tanh(x) = cap - 2 cap / (1 + e^(2 x))
-                                    z = fmaf(-2.0f * a.cap_log2, rcp_approx(ex2(z) + 1.0f), a.cap_log2);
-                                x[c] = __float_as_uint(fmaf(slope[c], key - dep[c], z));
+                            for (int c = 0; c < 8; c++) in[c] *= __uint_as_float(x[c]);
+                            if (a.cap_in != 0.f) {
+#pragma unroll
+                                for (int c = 0; c < 8; c++) in[c] = capped(in[c], a.cap_log2);
+                            } else if (a.cap_log2 > 0.f) {   // (in line up to 64 rows it costs the other caps registers:
+                                // 32 sequences of n 4,096, 32 rows, 68 us instead of 66; called with 128, 16 of n 32,768
+                                // take 477 us instead of 457)
+#pragma unroll
+                                for (int i = 0; i < 2; i++) {
+                                    float (&v)[4] = reinterpret_cast<float (&)[4]>(in[4 * i]);
+                                    if (W) {
+                                        any_cap(v, a.cap_log2, a.cap_rcp);
+                                    } else {
+                                        const float4 t = any_cap_called(make_float4(v[0], v[1], v[2], v[3]), a.cap_log2, a.cap_rcp);
+                                        v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
+                                    }
+                                }
                             }
+#pragma unroll
+                            for (int c = 0; c < 8; c++) x[c] = __float_as_uint(fmaf(slope[c], key - dep[c], in[c]));
                         }
 #pragma unroll
                         for (int c = 0; c < 8; c++)
@@ -1058,8 +1111,10 @@ cudaError_t launch_tree(const nvfp4kv_cache &c, const void *q, const int32_t *cu
     a.slopes = slopes;
     const double scale = (double)sm_scale * c.k_global_scale, log2e = 1.4426950408889634;
     a.score_log2 = (float)(scale * log2e);
-    a.cap_log2 = (float)(softcap * log2e);
-    a.cap_in = softcap > 0.f ? (float)(2.0 * log2e * scale / softcap) : 0.f;
+    // (in FP32's range whatever the cap: a very large one is none, a very small one leaves nothing of the scores)
+    a.cap_log2 = (float)std::min(softcap * log2e, (double)FLT_MAX);
+    a.cap_rcp = softcap > 0.f ? (float)std::min(1.0 / (softcap * log2e), (double)FLT_MAX) : 0.f;
+    a.cap_in = softcap >= kCapFrom && softcap <= kCapTo ? (float)(2.0 * log2e * scale / softcap) : 0.f;
     a.window = window;
     a.gv = c.v_global_scale;
     a.out = static_cast<__nv_bfloat16 *>(out);

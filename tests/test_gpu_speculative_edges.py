@@ -8,7 +8,7 @@ import torch
 
 import speculative_plain as plain
 from speculative_plain import HEAD
-from test_gpu_speculative import gen, packed, rotation
+from test_gpu_speculative import gen, ints, packed, random_pool, random_tree, rotation, run_tree, sums, table_of
 
 pytestmark = pytest.mark.gpu
 
@@ -87,3 +87,24 @@ def test_zeros_keep_their_signs_in_the_pages(m, T, rot, adjacent, norms):
     rk, _ = plain.turned(x[:, :hkv], w, pos, table, 1e-6, adjacent, None)
     m.quantize_append(b, packed(plain.bf16_rounded(rk)), packed(x[:, hkv:]), slots)
     assert torch.equal(a.pool, b.pool) and m.check_device_errors() == 0
+
+
+# --------------------------------------------------------------------------------- tree attention
+
+@pytest.mark.parametrize("cap", [1e-42, 1e-4, 0.02, 2.0, 30.0, 50.0, 128.0, 129.0, 1e3, 2e4, 1e6, 1e30, 3e38])
+@pytest.mark.parametrize("lens,drafts,hq,hkv,page", [([300, 900, 20], [1, 1, 1], 8, 2, 16), ([300, 900, 20], [5, 12, 20], 8, 2, 16),
+                                                     ([600, 410], [40, 64], 8, 2, 32)])
+def test_caps_of_any_size(m, cap, lens, drafts, hq, hkv, page):
+    """The tolerance of the other caps: a capped score is off by 2^-20 of itself, and scores stay below 32 here, so its
+    weight by 2^-15; with caps from 2^-10 to 128 by 1.3 x 2^-22 of the cap, its weight by 2^-14.6: inside the 2^-14 of the
+    bound, whatever the cap."""
+    run_tree(m, lens, drafts, hq, hkv, page, seed=3, cap=cap, qscale=2.0)
+
+
+def test_a_cap_far_above_the_scores_is_none(m):
+    """Both within their bound of the same numbers, and of each other: scores z off by z^3 / (3 cap^2) at most."""
+    args = ([300, 900, 20], [5, 12, 20], 8, 2, 16)
+    a = run_tree(m, *args, seed=3, qscale=2.0)
+    b = run_tree(m, *args, seed=3, qscale=2.0, cap=1e6)
+    # 2^-20 of scores below 32 moves a weight by 2^-15 and may round it (FP16, 2^-11) and the output (BF16, 2^-8) elsewhere
+    assert ((a - b).abs() <= 2.0**-7 * a.abs() + 2.0**-10 * float(a.abs().max())).all()
