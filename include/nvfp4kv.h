@@ -655,7 +655,7 @@ NVFP4KV_API int nvfp4_tree_attention(const nvfp4kv_cache *cache, const void *q, 
  *                 max_accepted)
  *   num_accepted  device int32 [batch]
  *   max_accepted  1..NVFP4KV_MAX_DRAFTS
- *   new_lens      device int32 [batch], must not overlap seq_lens
+ *   new_lens      device int32 [batch], must overlap no other array of the call
  * A sequence with d < 0, d > NVFP4KV_MAX_DRAFTS or d > seq_lens[b] is flagged and left as it is.
  * A row with a page outside the pool is flagged and not moved.  NVFP4 and FP8 pools;
  * batch <= 65535.

@@ -1037,7 +1037,7 @@ def accept_tokens(cache: PagedCache, block_table: torch.Tensor, seq_lens: torch.
                   stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """Moves the accepted drafts' rows together behind each sequence's prefix: draft accepted[b][k]
     (int32 [B][at most 64]) becomes the k-th token after it, k < num_accepted[b] (int32 [B]).
-    seq_lens and cu_q_lens as in tree_attention.  Returns new_lens, int32 [B]."""
+    seq_lens and cu_q_lens as in tree_attention.  Returns new_lens, int32 [B], which overlaps no input."""
     dev = cache.pool.get_device()
     lp = _want(seq_lens, "seq_lens", torch.int32, None, dev)
     B = seq_lens.numel()

@@ -55,6 +55,12 @@ static_assert(kMaxDrafts == NVFP4KV_MAX_DRAFTS, "one mask bit a draft");
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Whether the bytes [p, p + m) and [q, q + n) share one.
+bool overlap(const void *p, uint64_t m, const void *q, uint64_t n) {
+    const uint64_t x = reinterpret_cast<uintptr_t>(p), y = reinterpret_cast<uintptr_t>(q);
+    return x < y + n && y < x + m;
+}
+
 // A tensor scale is a positive normal FP32 number (the exact-rounding argument of
 // the g != 1 quantiser needs g >= 2^-126).
 bool normal_positive(float x) { return isfinite(x) && x >= 0x1p-126f; }
@@ -650,9 +656,13 @@ int nvfp4_accept_tokens(const nvfp4kv_cache *cache, const int32_t *block_table, 
     if (!aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(cu_q_lens, 4) || !aligned(accepted, 4) ||
         !aligned(num_accepted, 4) || !aligned(new_lens, 4))
         return NVFP4KV_EINVAL;
-    const uintptr_t x = reinterpret_cast<uintptr_t>(new_lens), y = reinterpret_cast<uintptr_t>(seq_lens);
-    if (x < y + 4 * (uintptr_t)batch && y < x + 4 * (uintptr_t)batch) return NVFP4KV_EINVAL;
     if ((int64_t)max_pages_per_seq * cache->page_size > kMaxRows) return NVFP4KV_EUNSUPPORTED;
+    // a sequence's first warp writes its length while others still read what the call is given
+    const uint64_t n = (uint64_t)batch, lens = 4 * n;
+    if (overlap(new_lens, lens, seq_lens, lens) || overlap(new_lens, lens, num_accepted, lens) ||
+        overlap(new_lens, lens, cu_q_lens, lens + 4) || overlap(new_lens, lens, accepted, lens * max_accepted) ||
+        overlap(new_lens, lens, block_table, lens * max_pages_per_seq))
+        return NVFP4KV_EINVAL;
     cudaError_t e;
     unsigned *err = error_word(&e);
     if (!err) return NVFP4KV_ECUDA;

@@ -1,0 +1,18 @@
+"""CPU checks of refusals of the speculative decoding calls (a refused call launches nothing, so plain numbers stand
+in for device pointers; every call here is refused)."""
+
+import pytest
+
+from test_speculative_host import EINVAL, EUNSUPPORTED, accept, desc, m, tree  # noqa: F401  (m: the fixture)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(num=8192), dict(num=8188), dict(num=8196),              # of 2 sequences: 8 bytes
+    dict(cu=8192), dict(cu=8184), dict(cu=8196),                 # 12 bytes
+    dict(acc=8192), dict(acc=8164), dict(acc=8196),              # 2 lists of 4: 32 bytes
+    dict(bt=8192), dict(bt=8180), dict(bt=8196),                 # 2 rows of 2 pages: 16 bytes
+    dict(lens=8188), dict(lens=8196),
+])
+def test_accept_refuses_lengths_over_what_it_reads(m, kw):  # noqa: F811
+    """The new lengths are written while other warps read the lists, counts, bounds and tables."""
+    assert accept(m, **kw) == EINVAL
