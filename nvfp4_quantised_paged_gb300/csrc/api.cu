@@ -629,8 +629,8 @@ int nvfp4_tree_attention(const nvfp4kv_cache *cache, const void *q, const int32_
         return NVFP4KV_EINVAL;
     const int64_t cap = (int64_t)max_pages_per_seq * cache->page_size, most = ((int64_t)1 << 31) - 1;
     if (cap > kMaxRows || total_q_tokens > most / num_q_heads) return NVFP4KV_EUNSUPPORTED;
-    // tiles, counted in 32 bits
-    if ((int64_t)batch * cache->num_kv_heads > most / ((cap + 127) / 128 + 1)) return NVFP4KV_EUNSUPPORTED;
+    // units of the plan, counted in 32 bits
+    if ((int64_t)batch * cache->num_kv_heads > most / ((cap + kTreeTile - 1) / kTreeTile + kTreePairUnits)) return NVFP4KV_EUNSUPPORTED;
     cudaError_t e = cudaSuccess;
     const int64_t rows = (int64_t)max_q_len * G;
     const int splits = num_splits ? num_splits : tree_auto_splits(rows, &e);

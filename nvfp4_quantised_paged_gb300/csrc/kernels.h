@@ -121,6 +121,9 @@ cudaError_t launch_rope_append(const nvfp4kv_cache &c, const nvfp4kv_rope &rope,
                                int64_t kv_stride, int64_t num_tokens, const int32_t *positions,
                                const int64_t *slot_mapping, unsigned *err, cudaStream_t stream);
 
+// The tree attention's plan: tokens a tile (one unit), and what a (sequence, kv head) pair's start and end cost a CTA, in units.
+constexpr int kTreeTile = 128, kTreePairUnits = 2;
+
 // Attention of the drafted tokens: CTAs per row tile of an auto split for `rows` = max_q_len x
 // group rows a pair (0 on an error), workspace bytes for `splits` of them, and the launch.
 int tree_auto_splits(int64_t rows, cudaError_t *status);

@@ -78,7 +78,7 @@ template <int N>
 constexpr int kThreadsT = kWorkersT<N> + 64;  // + the MMA warp and the load warp
 template <int N>
 constexpr int kCtasT = kWide<N> ? 1 : 2;      // CTAs an SM
-constexpr int kTileT = 128;                   // tokens a tile
+constexpr int kTileT = kTreeTile;             // tokens a tile
 constexpr int kBlockT = kTileT * 128;         // bytes of a column block: 64 dims (or rows of P) of 128 tokens
 constexpr int kGroupT = 2304;                 // bytes of a 16-token group
 constexpr int kRawT = 8 * kGroupT;            // a raw tile
@@ -87,7 +87,7 @@ constexpr float kNegInfT = -__builtin_huge_valf();
 constexpr float kRescaleT = 8.0f;
 constexpr float kPOffsetT = 7.0f;             // P = 2^(z - m + 7): at most 2^15
 constexpr float kNoMaxT = 3.402823466e38f;    // the offset while every score was -inf
-constexpr int kPairUnits = 2;                 // what a pair's start and end cost a CTA, in tiles
+constexpr int kPairUnits = kTreePairUnits;    // what a pair's start and end cost a CTA, in tiles
 
 template <int N>
 struct TSmem {

@@ -16,3 +16,17 @@ from test_speculative_host import EINVAL, EUNSUPPORTED, accept, desc, m, tree  #
 def test_accept_refuses_lengths_over_what_it_reads(m, kw):  # noqa: F811
     """The new lengths are written while other warps read the lists, counts, bounds and tables."""
     assert accept(m, **kw) == EINVAL
+
+
+def test_tree_attention_refuses_what_its_plan_cannot_count(m):  # noqa: F811
+    """A pair's units are its tiles of 128 tokens and two more: 2^31 of them are refused.  (The workspace is too small in
+    every call, which is found later: what the plan can count is refused for that.)"""
+    def status(batch, heads, tiles):
+        return tree(m, cache=desc(m, num_kv_heads=heads), hq=heads, total=batch, most=1, batch=batch, pages=8 * tiles, size=1)
+
+    assert 65535 * 8 * 4096 < 2**31 <= 65535 * 8 * 4097
+    assert status(65535, 8, 4094) == EINVAL
+    assert status(65535, 8, 4095) == EUNSUPPORTED
+    assert 65535 * 32 * 1024 < 2**31 <= 65535 * 32 * 1025
+    assert status(65535, 32, 1022) == EINVAL
+    assert status(65535, 32, 1023) == EUNSUPPORTED
