@@ -628,8 +628,8 @@ NVFP4KV_API size_t nvfp4kv_tree_workspace_bytes(const nvfp4kv_cache *cache, int 
  *   softcap >= 0 (0: none; capped scores are off by at most 2^-20 of themselves or, with caps from
  *                 2^-10 to 128, 2^-14.6), window >= 0 (0: none), slopes device float [num_q_heads]
  *                 or NULL
- *   out           device BF16 [total_q][num_q_heads][128], not q; rows of no sequence are left
- *                 as they are
+ *   out           device BF16 [total_q][num_q_heads][128], must not overlap q; rows of no sequence
+ *                 are left as they are
  *   workspace     device, >= nvfp4kv_tree_workspace_bytes(...), 256-byte aligned; calls that
  *                 may overlap need one each
  *   num_splits    CTAs that share the tokens of a row tile (128 rows of drafts x heads of a kv

@@ -623,7 +623,6 @@ int nvfp4_tree_attention(const nvfp4kv_cache *cache, const void *q, const int32_
         return NVFP4KV_EUNSUPPORTED;
     if (batch == 0 || total_q_tokens == 0) return NVFP4KV_OK;
     if (!q || !cu_q_lens || !block_table || !seq_lens || !out || !workspace || max_pages_per_seq < 1) return NVFP4KV_EINVAL;
-    if (out == q) return NVFP4KV_EINVAL;   // several CTAs read a query
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 256) || !aligned(block_table, 4) ||
         !aligned(seq_lens, 4) || !aligned(cu_q_lens, 4) || !aligned(tree_mask, 8) || !aligned(slopes, 4))
         return NVFP4KV_EINVAL;
@@ -631,6 +630,8 @@ int nvfp4_tree_attention(const nvfp4kv_cache *cache, const void *q, const int32_
     if (cap > kMaxRows || total_q_tokens > most / num_q_heads) return NVFP4KV_EUNSUPPORTED;
     // units of the plan, counted in 32 bits
     if ((int64_t)batch * cache->num_kv_heads > most / ((cap + kTreeTile - 1) / kTreeTile + kTreePairUnits)) return NVFP4KV_EUNSUPPORTED;
+    const uint64_t bytes = (uint64_t)total_q_tokens * num_q_heads * (2 * kHeadDim);
+    if (overlap(out, bytes, q, bytes)) return NVFP4KV_EINVAL;   // several CTAs read a query, at any time
     cudaError_t e = cudaSuccess;
     const int64_t rows = (int64_t)max_q_len * G;
     const int splits = num_splits ? num_splits : tree_auto_splits(rows, &e);

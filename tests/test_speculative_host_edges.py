@@ -30,3 +30,9 @@ def test_tree_attention_refuses_what_its_plan_cannot_count(m):  # noqa: F811
     assert 65535 * 32 * 1024 < 2**31 <= 65535 * 32 * 1025
     assert status(65535, 32, 1022) == EINVAL
     assert status(65535, 32, 1023) == EUNSUPPORTED
+
+
+@pytest.mark.parametrize("out", [4096, 16, 4080, 4112, 8176])
+def test_tree_attention_refuses_an_output_over_its_queries(m, out):  # noqa: F811
+    """4 queries of 4 heads: 4,096 bytes from address 4,096 on."""
+    assert tree(m, out=out) == EINVAL
