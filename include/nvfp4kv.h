@@ -582,7 +582,8 @@ typedef struct {
  * of the pair's larger product, as a code may hang on it; Q's is formed in FP32).
  *   q              device BF16 [num_tokens][q_stride], head h at h*128; NULL with num_q_heads 0
  *   q_out          device BF16 [num_tokens][q_out_stride]; may be q itself with its stride,
- *                  must not overlap q, k or v otherwise
+ *                  must not overlap q, k or v otherwise (with the same stride its rows may lie
+ *                  between theirs)
  *   k, v           device BF16 [num_tokens][kv_stride]; q, k and v may be views of one row
  *   positions      device int32 [num_axes][num_tokens]; a token with one outside
  *                  [0, num_positions) is skipped and flagged

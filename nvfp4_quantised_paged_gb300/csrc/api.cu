@@ -61,6 +61,16 @@ bool overlap(const void *p, uint64_t m, const void *q, uint64_t n) {
     return x < y + n && y < x + m;
 }
 
+// Whether one of the t rows of m bytes, `sp` apart, from p on shares a byte with one of the t rows of n, `sq` apart, from
+// q on.  (Rows with the same stride may lie between each other, as those of one projection do; with another they may not.)
+bool rows_overlap(const void *p, uint64_t m, uint64_t sp, const void *q, uint64_t n, uint64_t sq, uint64_t t) {
+    if (!overlap(p, (t - 1) * sp + m, q, (t - 1) * sq + n)) return false;
+    if (sp != sq || t == 1) return true;
+    const int64_t apart = (int64_t)(reinterpret_cast<uintptr_t>(p) - reinterpret_cast<uintptr_t>(q));
+    const uint64_t at = (uint64_t)((apart % (int64_t)sp + (int64_t)sp) % (int64_t)sp);   // of p's rows, from q's on
+    return at < n || at + m > sp;
+}
+
 // A tensor scale is a positive normal FP32 number (the exact-rounding argument of
 // the g != 1 quantiser needs g >= 2^-126).
 bool normal_positive(float x) { return isfinite(x) && x >= 0x1p-126f; }
@@ -588,6 +598,13 @@ int nvfp4_rope_quantize_append(const nvfp4kv_cache *cache, const nvfp4kv_rope *r
         if (q_out == q && q_out_stride != q_stride) return NVFP4KV_EINVAL;
     }
     if (num_tokens > (((int64_t)1 << 31) - 1) / (num_q_heads + 2 * (int64_t)cache->num_kv_heads)) return NVFP4KV_EUNSUPPORTED;
+    if (num_q_heads > 0) {   // rows are read and written at any time: only a query's own may be its output's
+        const uint64_t t = (uint64_t)num_tokens, row = (uint64_t)num_q_heads * (2 * kHeadDim), so = 2 * (uint64_t)q_out_stride;
+        const uint64_t kv_row = (uint64_t)cache->num_kv_heads * (2 * kHeadDim), skv = 2 * (uint64_t)kv_stride;
+        if ((q_out != q && rows_overlap(q_out, row, so, q, row, 2 * (uint64_t)q_stride, t)) ||
+            rows_overlap(q_out, row, so, k, kv_row, skv, t) || rows_overlap(q_out, row, so, v, kv_row, skv, t))
+            return NVFP4KV_EINVAL;
+    }
     cudaError_t e;
     unsigned *err = error_word(&e);
     if (!err) return NVFP4KV_ECUDA;

@@ -89,6 +89,30 @@ def test_zeros_keep_their_signs_in_the_pages(m, T, rot, adjacent, norms):
     assert torch.equal(a.pool, b.pool) and m.check_device_errors() == 0
 
 
+
+@pytest.mark.parametrize("T", [1, 5, 6000])
+def test_queries_written_between_the_rows_they_come_from(m, T):
+    """An output of the same stride beside q, k and v in one row, and q itself; rows over others are refused."""
+    hq, hkv = 4, 4
+    g = gen(T)
+    rows = torch.randn((T + 1, 2 * hq + 2 * hkv, HEAD), generator=g).to(torch.bfloat16).cuda()
+    kept = rows.clone()
+    q, k, v, out = rows[:T].split([hq, hkv, hkv, hq], 1)
+    table, pos, slots = rotation(T, 128).cuda(), ints(list(range(T))), torch.arange(T, device="cuda")
+    pages = -(-T // 64)
+    a, b, c = (m.PagedCache(pages, 64, hkv) for _ in range(3))
+    want = m.rope_quantize_append(a, q, k, v, pos, table, slots)
+    assert m.rope_quantize_append(b, q, k, v, pos, table, slots, q_out=out).data_ptr() == out.data_ptr()
+    assert torch.equal(out, want) and torch.equal(rows[:T, :-hq], kept[:T, :-hq]) and torch.equal(rows[T:], kept[T:])
+    for bad in (k, v, rows[:T, 1:hq + 1], rows[:T, hq - 1:2 * hq - 1], rows[1:, :hq] if T > 1 else k, rows[1:, 2:hq + 2] if T > 1 else v):
+        with pytest.raises(m.NVFP4KVError):
+            m.rope_quantize_append(c, q, k, v, pos, table, slots, q_out=bad)
+    assert not c.pool.any()
+    m.rope_quantize_append(c, q, k, v, pos, table, slots, q_out=q)
+    assert torch.equal(q, want) and torch.equal(rows[:T, hq:3 * hq], kept[:T, hq:3 * hq])
+    assert torch.equal(a.pool, b.pool) and torch.equal(a.pool, c.pool) and m.check_device_errors() == 0
+
+
 # --------------------------------------------------------------------------------- tree attention
 
 @pytest.mark.parametrize("cap", [1e-42, 1e-4, 0.02, 2.0, 30.0, 50.0, 128.0, 129.0, 1e3, 2e4, 1e6, 1e30, 3e38])

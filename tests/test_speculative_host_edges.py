@@ -3,7 +3,7 @@ in for device pointers; every call here is refused)."""
 
 import pytest
 
-from test_speculative_host import EINVAL, EUNSUPPORTED, accept, desc, m, tree  # noqa: F401  (m: the fixture)
+from test_speculative_host import EINVAL, EUNSUPPORTED, accept, append, desc, m, tree  # noqa: F401  (m: the fixture)
 
 
 @pytest.mark.parametrize("kw", [
@@ -36,3 +36,22 @@ def test_tree_attention_refuses_what_its_plan_cannot_count(m):  # noqa: F811
 def test_tree_attention_refuses_an_output_over_its_queries(m, out):  # noqa: F811
     """4 queries of 4 heads: 4,096 bytes from address 4,096 on."""
     assert tree(m, out=out) == EINVAL
+
+
+# 3 tokens of 4 query heads (1,024 bytes) and 2 kv heads (512); q, k, v are one projection's rows of 2,048 bytes from 4,096 on
+ROWS = dict(q=4096, qs=1024, k=5120, v=5632, ks=1024, hq=4, t=3)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(qo=6144, qos=1024), dict(qo=2048, qos=1024), dict(qo=4112, qos=1024), dict(qo=4080, qos=1024),     # q, shifted
+    dict(qo=5120, qos=1024), dict(qo=5632, qos=1024), dict(qo=5104, qos=1024), dict(qo=6128, qos=1024),     # k, v
+    dict(qo=9216, qos=512), dict(qo=4096, qos=512), dict(qo=8192, qos=2048), dict(qo=16, qos=2048),         # other strides
+])
+def test_rope_append_refuses_an_output_over_what_it_reads(m, kw):  # noqa: F811
+    assert append(m, **{**ROWS, **kw}) == EINVAL
+
+
+def test_rope_append_refuses_a_single_token_over_another(m):  # noqa: F811
+    one = dict(q=4096, qs=512, k=8192, v=8704, ks=256, hq=4, t=1)
+    for qo in (3088, 5104, 7184, 8688, 9200):
+        assert append(m, **{**one, "qo": qo, "qos": 512}) == EINVAL
