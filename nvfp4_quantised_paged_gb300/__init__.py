@@ -973,8 +973,17 @@ def rope_quantize_append(cache: PagedCache, q: Optional[torch.Tensor], k: torch.
     return q_out
 
 
+def _int32(x, name: str) -> int:
+    """x for an int32 argument (ctypes would take the low 32 bits of a larger one)."""
+    x = int(x)
+    if not -1 << 31 <= x < 1 << 31:
+        raise ValueError("%s must fit 32 bits, got %d" % (name, x))
+    return x
+
+
 def tree_workspace_bytes(cache: PagedCache, batch: int, num_q_heads: int, max_q_len: int, num_splits: int = 0) -> int:
-    n = _lib.nvfp4kv_tree_workspace_bytes(cache.desc, int(batch), int(num_q_heads), int(max_q_len), int(num_splits))
+    n = _lib.nvfp4kv_tree_workspace_bytes(cache.desc, _int32(batch, "batch"), _int32(num_q_heads, "num_q_heads"),
+                                          _int32(max_q_len, "max_q_len"), _int32(num_splits, "num_splits"))
     if n == 0:
         raise NVFP4KVError(-1, "tree_workspace_bytes")
     return int(n)
@@ -1010,6 +1019,7 @@ def tree_attention(cache: PagedCache, q: torch.Tensor, cu_q_lens: torch.Tensor, 
     bp = _want_table(block_table, "block_table", B, dev)
     mp = _want(tree_mask, "tree_mask", torch.int64, (TQ,), dev) if tree_mask is not None else 0
     ap = _want(slopes, "slopes", torch.float32, (Hq,), dev) if slopes is not None else 0
+    max_q_len, window, num_splits = _int32(max_q_len, "max_q_len"), _int32(window, "window"), _int32(num_splits, "num_splits")
     s = _launch_stream(dev, stream)
     made = []
     if out is None:
@@ -1024,9 +1034,9 @@ def tree_attention(cache: PagedCache, q: torch.Tensor, cu_q_lens: torch.Tensor, 
     wp = _want(workspace, "workspace", torch.uint8, None, dev)
     if stream is not None:
         _keep_until_done(stream, *made)
-    rc = _lib.nvfp4_tree_attention(cache.desc, qp, cp, TQ, B, int(max_q_len), Hq, mp, bp, block_table.shape[1], lp,
-                                   _HEAD_SCALE if sm_scale is None else float(sm_scale), float(softcap), int(window), ap,
-                                   op, wp, workspace.numel(), int(num_splits), s)
+    rc = _lib.nvfp4_tree_attention(cache.desc, qp, cp, TQ, B, max_q_len, Hq, mp, bp, block_table.shape[1], lp,
+                                   _HEAD_SCALE if sm_scale is None else float(sm_scale), float(softcap), window, ap,
+                                   op, wp, workspace.numel(), num_splits, s)
     if rc:
         _check(rc, "nvfp4_tree_attention")
     return out

@@ -132,3 +132,17 @@ def test_a_cap_far_above_the_scores_is_none(m):
     b = run_tree(m, *args, seed=3, qscale=2.0, cap=1e6)
     # 2^-20 of scores below 32 moves a weight by 2^-15 and may round it (FP16, 2^-11) and the output (BF16, 2^-8) elsewhere
     assert ((a - b).abs() <= 2.0**-7 * a.abs() + 2.0**-10 * float(a.abs().max())).all()
+
+
+def test_windows_and_counts_beyond_32_bits(m):
+    """2^32 + 5 is no window of 5; the largest number that fits limits nothing."""
+    g = gen(5)
+    table, pages = table_of([300], 16, g)
+    cache = m.PagedCache(pages, 16, 2, pool=random_pool(pages, 2, 16, 5).cuda())
+    args = (cache, torch.randn((3, 8, HEAD), generator=g).to(torch.bfloat16).cuda(), sums([3]), 3, table.cuda(), ints([300]))
+    for kw in (dict(window=2**32 + 5), dict(window=2**31), dict(num_splits=2**32 + 1)):
+        with pytest.raises(ValueError):
+            m.tree_attention(*args, **kw)
+    with pytest.raises(ValueError):
+        m.tree_attention(*args[:3], 2**32 + 3, *args[4:])
+    assert torch.equal(m.tree_attention(*args, window=2**31 - 1), m.tree_attention(*args)) and m.check_device_errors() == 0

@@ -55,3 +55,18 @@ def test_rope_append_refuses_a_single_token_over_another(m):  # noqa: F811
     one = dict(q=4096, qs=512, k=8192, v=8704, ks=256, hq=4, t=1)
     for qo in (3088, 5104, 7184, 8688, 9200):
         assert append(m, **{**one, "qo": qo, "qos": 512}) == EINVAL
+
+
+def test_numbers_beyond_32_bits_are_refused_by_the_binding(m):  # noqa: F811
+    assert [m._int32(x, "window") for x in (0, -1, 2**31 - 1, -2**31, 5.0)] == [0, -1, 2**31 - 1, -2**31, 5]
+    for x in (2**31, 2**32 + 5, -2**31 - 1, 1 << 70):
+        with pytest.raises(ValueError, match="window"):
+            m._int32(x, "window")
+
+    class Cache:
+        desc = desc(m)
+
+    assert m.tree_workspace_bytes(Cache, 3, 4, 1, 7) == (13 * 16 * 8 + 255) // 256 * 256 + 13 * 16 * 512
+    for args in ((2**32 + 3, 4, 1, 7), (3, 2**32 + 4, 1, 7), (3, 4, 2**32 + 1, 7), (3, 4, 1, 2**32 + 7)):
+        with pytest.raises(ValueError):
+            m.tree_workspace_bytes(Cache, *args)
