@@ -146,3 +146,131 @@ def test_windows_and_counts_beyond_32_bits(m):
     with pytest.raises(ValueError):
         m.tree_attention(*args[:3], 2**32 + 3, *args[4:])
     assert torch.equal(m.tree_attention(*args, window=2**31 - 1), m.tree_attention(*args)) and m.check_device_errors() == 0
+
+
+def check_rows(got, q, pool, page, pages, masks, n, scale=1 / math.sqrt(HEAD), **kw):
+    """The drafts' outputs of one sequence against the formula, within its bound."""
+    k, v = plain.rows_of(pool, page, pages, n)
+    ref, spread, size = plain.tree(q, k, v, masks, n, scale, **kw)
+    err = (got.cpu().double() - ref).abs()
+    assert (err <= plain.tree_bound(ref, spread, size, n, float(v.abs().max()))).all()
+
+
+@pytest.mark.parametrize("scale", [-0.11, 0.0, 1e-30])
+@pytest.mark.parametrize("kw", [{}, dict(cap=30.0), dict(cap=1e5), dict(window=70), dict(cap=3.0, window=5, sloped=True)])
+@pytest.mark.parametrize("d,hq", [(1, 8), (9, 8), (33, 16)])
+def test_scales_that_are_not_positive(m, scale, kw, d, hq):
+    g = gen(d)
+    n, page, hkv = 310, 16, 2
+    table, pages = table_of([n], page, g)
+    pool = random_pool(pages, hkv, page, 9)
+    q = torch.randn((d, hq, HEAD), generator=g).to(torch.bfloat16)
+    masks = plain.masks_of(random_tree(d, g))
+    slopes = torch.exp2(-torch.arange(1, hq + 1) * 8.0 / hq) if kw.get("sloped") else None
+    cap, window = kw.get("cap", 0.0), kw.get("window", 0)
+    got = m.tree_attention(m.PagedCache(pages, page, hkv, pool=pool.cuda()), q.cuda(), sums([d]), d, table.cuda(), ints([n]),
+                           tree_mask=torch.tensor([plain.signed(x) for x in masks]).cuda(), sm_scale=scale, softcap=cap,
+                           window=window, slopes=None if slopes is None else slopes.cuda())
+    assert m.check_device_errors() == 0
+    check_rows(got, q, pool, page, table[0], masks, n, scale, cap=cap, window=window, slopes=slopes)
+
+
+@pytest.mark.parametrize("d", [1, 3, 64])
+def test_128_query_heads_a_kv_head(m, d):
+    g = gen(d)
+    n, page = 200 + d, 32
+    table, pages = table_of([n], page, g)
+    pool = random_pool(pages, 1, page, 9)
+    q = torch.randn((d, 128, HEAD), generator=g).to(torch.bfloat16)
+    masks = plain.masks_of(random_tree(d, g))
+    got = m.tree_attention(m.PagedCache(pages, page, 1, pool=pool.cuda()), q.cuda(), sums([d]), d, table.cuda(), ints([n]),
+                           tree_mask=torch.tensor([plain.signed(x) for x in masks]).cuda())
+    assert m.check_device_errors() == 0
+    check_rows(got, q, pool, page, table[0], masks, n)
+
+
+@pytest.mark.parametrize("hq", [2, 40])
+def test_sequences_beside_one_that_does_not_fit(m, hq):
+    """What each flagged sequence gives, and the others' outputs."""
+    g = gen(6)
+    page = 16
+    table, pages = table_of([64, 64, 64], page, g)
+    pool = random_pool(pages, 1, page, 1)
+    cache = m.PagedCache(pages, page, 1, pool=pool.cuda())
+    q = torch.randn((7, hq, HEAD), generator=g).to(torch.bfloat16)
+
+    def run(lens, cu, bound):
+        out = torch.full((7, hq, HEAD), 7.0, dtype=torch.bfloat16, device="cuda")
+        m.tree_attention(cache, q.cuda(), ints(cu), bound, table.cuda(), ints(lens), out=out)
+        assert m.check_device_errors() == -4
+        return out
+
+    def fine(out, b, rows, n):
+        check_rows(out[rows], q[rows], pool, page, table[b], [(2 << i) - 1 for i in range(rows.stop - rows.start)], n)
+
+    kept = lambda x: bool((x == 7.0).all())  # noqa: E731
+    a, b, c, rest = slice(0, 2), slice(2, 4), slice(4, 6), slice(6, 7)
+    out = run([64, 1, 60], [0, 2, 4, 6], 2)          # more drafts than tokens: zeros
+    fine(out, 0, a, 64), fine(out, 2, c, 60)
+    assert not out[b].any() and kept(out[rest])
+    out = run([64, 70, 60], [0, 2, 4, 6], 2)         # longer than the table: cut to it
+    fine(out, 0, a, 64), fine(out, 1, b, 64), fine(out, 2, c, 60)
+    assert kept(out[rest])
+    out = run([64, -3, 60], [0, 2, 4, 6], 2)         # a negative length: none
+    fine(out, 0, a, 64), fine(out, 2, c, 60)
+    assert not out[b].any() and kept(out[rest])
+    out = run([64, 63, 64], [0, 2, 4, 9], 2)         # rows that there are not
+    fine(out, 0, a, 64), fine(out, 1, b, 63)
+    assert kept(out[4:])
+    out = run([64, 63, 62], [0, 2, -1, 2], 2)        # bounds that fall, and one that begins before the first row
+    fine(out, 0, a, 64)
+    assert kept(out[2:])
+    out = run([64, 63, 62], [0, 2, 5, 7], 2)         # more drafts than the call's bound: the first ones, as the last tokens
+    fine(out, 0, a, 64), fine(out, 1, b, 63), fine(out, 2, slice(5, 7), 62)
+    assert kept(out[4:5])
+
+
+# --------------------------------------------------------------------------------- acceptance
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_what_an_acceptance_flags_stays_as_it_was(m, fp8):
+    """The pool's bytes after calls with one inconsistent sequence or entry: the intact sequence's rows moved, no others."""
+    g = gen(7)
+    hkv, page = 3, 16
+    dtype = m.DTYPE_FP8_E4M3 if fp8 else m.DTYPE_NVFP4
+    pool = torch.randint(0, 256, (4, hkv, m.slab_bytes(dtype, page)), generator=g, dtype=torch.int32).to(torch.uint8)
+
+    def parts(p, t):      # of token t of a sequence whose pages are p: page, bytes [heads][...]
+        r, x = t % 16, p[0][p[1][t // page]]
+        if fp8:
+            return [x[:, r * 128:(r + 1) * 128], x[:, 2048 + r * 128:2048 + (r + 1) * 128]]
+        return [x[:, r * 64:(r + 1) * 64], x[:, 1024 + r * 8:1024 + (r + 1) * 8],
+                x[:, 1152 + r * 64:1152 + (r + 1) * 64], x[:, 2176 + r::16]]
+
+    tables = [[0, 1], [2, 3]]
+
+    def run(lens, cu, lists, counts, moved, want, bad=None):
+        cache = m.PagedCache(4, page, hkv, dtype=dtype, pool=pool.clone().cuda())
+        given = [list(x) for x in tables]
+        if bad is not None:
+            given[bad[0]][bad[1]] = bad[2]
+        new = m.accept_tokens(cache, ints(given), ints(lens), ints(cu), ints(lists), ints(counts))
+        assert m.check_device_errors() == -4 and new.tolist() == want
+        after = pool.clone()
+        for b, s, t in moved:
+            for x, y in zip(parts((pool, tables[b]), s), parts((after, tables[b]), t)):
+                y.copy_(x)
+        assert torch.equal(cache.pool.cpu(), after)
+
+    fit = [(1, 17, 16), (1, 19, 17)]                                             # the second sequence's, where intact
+    run([20, 20], [0, 4, 8], [[2, 9, 0], [1, 3, 0]], [3, 2], [(0, 18, 16)] + fit, [17, 18])     # an entry that is no draft
+    run([20, 20], [0, 4, 8], [[2, 0, 1], [1, 3, 0]], [4, 2], [(0, 18, 16), (0, 16, 17), (0, 17, 18)] + fit, [19, 18])
+    run([20, 20], [0, 4, 8], [[2, 0, 1], [1, 3, 0]], [-1, 2], fit, [16, 18])                    # a negative count
+    run([3, 20], [0, 4, 8], [[2, 0, 1], [1, 3, 0]], [2, 2], fit, [3, 18])                       # more drafts than tokens
+    run([20, 20], [0, -4, 0], [[2, 0, 1], [1, 3, 0]], [2, 2], fit, [20, 18])                    # bounds that fall
+    run([20, 20], [0, 65, 69], [[2, 0, 1], [1, 3, 0]], [2, 2], fit, [20, 18])                   # more than 64 drafts
+    run([40, 20], [0, 4, 8], [[1, 0, 0], [1, 3, 0]], [1, 2], [(0, 29, 28)] + fit, [29, 18])     # longer than the table: cut
+    for page_id in (4, -1, 1 << 30):
+        # drafts of the first sequence on both of its pages (12 .. 19): rows from or to the one out of range stay
+        run([20, 20], [0, 8, 12], [[1, 6, 3], [1, 3, 0]], [3, 2], [(0, 13, 12), (0, 15, 14)] + fit, [15, 18], bad=(0, 1, page_id))
+        run([20, 20], [0, 8, 12], [[5, 6, 2], [1, 3, 0]], [3, 2], fit, [15, 18], bad=(0, 0, page_id))
