@@ -579,7 +579,9 @@ typedef struct {
  *   it is; with r = 0 it gives a NaN and the row's finite values zeros),
  * rounded to BF16 once.  Q's y goes to q_out; K's y and V as they would by
  * nvfp4_kv_quantize_append of that y (K's rounding to BF16 is the exact value's up to 2^-40
- * of the pair's larger product, as a code may hang on it; Q's is formed in FP32).
+ * of the pair's larger product, as a code may hang on it; Q's is formed in FP32).  Both within FP32's
+ * range: what FP32 loses of x w above 2^128, of products below 2^-100 and of rows whose mean(x^2) +
+ * eps is below 2^-100 (an eps of 10^-30 or more rules those out) is lost.
  *   q              device BF16 [num_tokens][q_stride], head h at h*128; NULL with num_q_heads 0
  *   q_out          device BF16 [num_tokens][q_out_stride]; may be q itself with its stride,
  *                  must not overlap q, k or v otherwise (with the same stride its rows may lie

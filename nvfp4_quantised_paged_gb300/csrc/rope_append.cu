@@ -3,18 +3,20 @@
 // Per token and head x[128] of Q and K, with a weight w (or 1) and the token's table row (c, s):
 //   r = 1 / sqrt(mean(x^2) + eps)  (1 without norms),   u = x w,
 //   y_a = r (u_a c - u_b s),  y_b = r (u_b c + u_a s)   for each rotated pair (a, b),  y = r u elsewhere,
-// rounded to BF16 once (a user who rotates first hands such a row to the append, and the
-// chunk attention reads the same K).  Q goes to q_out, K to the pool like V, which is not
-// touched before it is quantised (quantize.cuh: the rounding of the exact quotients).
+// rounded to BF16 once (a user who rotates first hands such a row to the append).  Q goes to q_out,
+// K to the pool like V, which is not touched before it is quantised (quantize.cuh: the rounding of the
+// exact quotients).  The rotated K leaves the kernel quantised alone: a chunk attention that takes
+// the chunk's own BF16 rows needs them rotated by its caller.
 //
 // Bound by bandwidth: a token reads (Hq + 2 Hkv) 256 bytes and writes Hq 256 + Hkv 144.
 // Eight threads hold a row, 16 values each: eight of the first rotated half and their eight
 // partners (or, for adjacent pairs and behind the rotated values, one block of the format), so
 // a thread needs eight cosines and sines.  Four or eight rows of one kind of one token are a
 // warp's unit; Q's weights are multiplied into the cosines and sines, and its rows go through
-// packed FP32 operations.  Measured: 32,768 tokens of 64 + 8 heads with norms 265 us (4.8 TB/s, 70% of the copy
-// bandwidth: 5,100 warp instructions a token at half the issue slots), 5,003 of 40 + 8 with three
-// axes 44 us, 8 tokens 6.8 us (latency).
+// packed FP32 operations.  Measured, cold caches, a call alone: 32,768 tokens of 64 + 8 heads with norms 270 us (4.7
+// TB/s, 69% of the copy bandwidth: 5,100 warp instructions a token at half the issue slots, the warps waiting for
+// memory), the same to an FP8 pool 258, with 64 of 128 values rotated 282; 5,003 of 40 + 8 with norms, three axes and
+// tensor scales 50 us, 2,048 of 32 + 2 without norms 20, 8 tokens 6.3 (latency).
 //
 // K's rounding to BF16 decides the codes: a value on the other side of a BF16 border may
 // move a block's scale.  So K's FP32 value is rounded twice, at both ends of its error bound,
@@ -22,7 +24,8 @@
 // again from two floats: products and sums with their rounding errors (fused multiply-adds,
 // Knuth's two-sum), the sum of squares and the reciprocal root as well, and the BF16 rounding
 // breaks ties by the low part: the rounding of the exact value up to a relative 2^-40 of
-// the pair's larger product.  Q is formed in FP32 (a value within 2^-21 of a tie may round to the other
+// the pair's larger product (of one above 2^-100, and of rows whose mean square plus eps is: below, FP32's
+// subnormals lose the low parts).  Q is formed in FP32 (a value within 2^-21 of a tie may round to the other
 // neighbour).
 #include <algorithm>
 #include <mutex>
@@ -419,7 +422,7 @@ __global__ void __launch_bounds__(kThreadsR) rope_append_kernel(RopeArgs a) {
 
 // Many tokens: persistent CTAs.  One warp copies whole tokens (rows of Q, K and V, the pieces of the table) into a ring
 // in shared memory, eight warps work on four rows at a time from there.  The direct form's loads, a chain of position,
-// table row and use, left DRAM idle: 32,768 tokens of 64 + 8 heads with norms took it 355 us.
+// table row and use, leaves DRAM idle: 32,768 tokens of 64 + 8 heads with norms take it 372 us, the ring 270.
 constexpr int kThreadsS = kThreadsR + 32;
 constexpr int kStreamBytes = 110 * 1024;          // of a CTA's ring, two CTAs an SM
 constexpr int kMaxStages = 8, kMaxTps = 32;
@@ -657,11 +660,16 @@ cudaError_t launch_rope_append(const nvfp4kv_cache &c, const nvfp4kv_rope &rope,
     plan.token_bytes = (a.Hq + 2 * a.Hkv) * 256 + 4 * a.rot;
     plan.tps = std::max(1, std::min(kMaxTps, 16 * 1024 / plan.token_bytes));
     plan.stages = std::min(kMaxStages, (int)((kStreamBytes - sizeof(StreamMisc)) / ((size_t)plan.tps * plan.token_bytes)));
-    // The ring (of two stages at least) from 12,000 groups of four rows on.  Direct form and ring, with norms: 64 + 8
-    // heads 13.0 and 13.0 us for 256 tokens (5,000 groups), 21.2 and 19.2 for 1,024, 219.8 and 142.0 for 16,384; 32 + 8
-    // heads 17.1 and 19.1 for 1,024 (12,000 groups), 43.7 and 41.6 for 4,096; 4 + 1 heads 10.9 and 13.0 for 1,024, 25.2
-    // and 21.2 for 4,096 (12,000 groups).
-    if (plan.stages < 2 || num_tokens * groups < 12000) {
+    // The ring (of two stages at least) from 18,000 groups of four rows on, a compromise: it gains earlier without norms
+    // and with more rows of Q beside those of K.  Direct form and ring in us, with norms | without, adjacent pairs:
+    //   64 + 8 heads   256 tokens (5,000 groups) 11.4, 12.3;   1,024 (20,000) 20.3, 20.0 | 20.3, 16.6;   2,048 31.0, 28.6 |
+    //                  32.6, 24.0;   16,384 190.5, 142;   32,768 372, 270
+    //   32 + 8         1,024 (12,000) 15.6, 18.7;   1,500 (18,000) 18.6, 21.8 | 18.3, 18.2;   2,048 22.5, 26.4 | 22.8, 20.8;
+    //                  4,096 38.4, 39.8
+    //   32 + 2         2,048 (20,000) 22.4, 21.4 | 22.3, 18.5
+    //   4 + 1          1,024 (3,000) 10.1, 12.7;   4,096 (12,000) 20.4, 20.5;   6,000 (18,000) 26.0, 26.4 | 26.5, 22.6;
+    //                  8,192 32.5, 30.5 | 34.5, 26.4
+    if (plan.stages < 2 || num_tokens * groups < 18000) {
         void *args[] = {&a};
         const void *few[2][2] = {{reinterpret_cast<const void *>(&rope_append_kernel<false, false>),
                                   reinterpret_cast<const void *>(&rope_append_kernel<false, true>)},

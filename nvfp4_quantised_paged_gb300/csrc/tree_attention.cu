@@ -48,7 +48,8 @@
 // scales and factors the rest).  Many rows: the chain of a tile, at half the issue slots, of 3,600 (8
 // rows) to 10,300 (128) warp instructions -- conversions and packed multiplies of 32,768 values,
 // per score a multiply-add, a power of two, a rounding and a sum.  (Without the powers of two: 2%
-// less.)  128 rows as two tiles of 64: 327 us.  One CTA of sixteen workers up to 64 rows too: 61
+// less.)  The registers are all taken: with 64 and 128 rows some 30 bytes a thread are spilled, 70 to 120 with options.
+// 128 rows as two tiles of 64: 327 us.  One CTA of sixteen workers up to 64 rows too: 61
 // instead of 50 us for 32 sequences, n 4,096, 32 rows.
 //
 // Split: all pairs' 128-token tiles form one flat range (a pair's start and end count as two

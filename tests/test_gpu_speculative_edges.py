@@ -90,6 +90,27 @@ def test_zeros_keep_their_signs_in_the_pages(m, T, rot, adjacent, norms):
 
 
 
+@pytest.mark.parametrize("T", [9, 3000])
+@pytest.mark.parametrize("size,scale,norms", [(2.0**-90, 2.0**-90, False), (2.0**-45, 1.0, True), (2.0**60, 1.0, True), (2.0**100, 2.0**98, False)])
+def test_rows_far_from_one(m, T, size, scale, norms):
+    """Products down to 2^-100, mean squares down to 2^-100 without an eps, and large ones: K's bytes are the formula's."""
+    hq, hkv = 2, 8
+    g = gen(T)
+    x = (torch.randn((T, hq + 2 * hkv, HEAD), generator=g).clamp(-2.5, 2.5) * size).to(torch.bfloat16)
+    table, pos = rotation(50, 64), torch.randint(0, 50, (T,), generator=g, dtype=torch.int32)
+    w = (torch.rand(HEAD, generator=g) + 0.5).to(torch.bfloat16) if norms else None
+    slots = torch.arange(T).cuda()
+    a, b = (m.PagedCache(-(-T // 64), 64, hkv, k_global_scale=scale, v_global_scale=scale) for _ in range(2))
+    on = lambda t: None if t is None else t.cuda()  # noqa: E731
+    q, k, v = x.cuda().split([hq, hkv, hkv], 1)
+    out = m.rope_quantize_append(a, q, k, v, pos.cuda(), table.cuda(), slots, q_norm=on(w), k_norm=on(w), eps=0.0)
+    rq, top = plain.turned(x[:, :hq], w, pos, table, 0.0, False, None)
+    rk, _ = plain.turned(x[:, hq:hq + hkv], w, pos, table, 0.0, False, None)
+    m.quantize_append(b, packed(plain.bf16_rounded(rk)), packed(x[:, hq + hkv:]), slots)
+    assert torch.equal(a.pool, b.pool) and bool((a.pool != 0).any()) and m.check_device_errors() == 0
+    assert ((out.cpu().double() - rq).abs() <= 2.0**-8 * rq.abs() + 2.0**-16 * top).all()
+
+
 @pytest.mark.parametrize("T", [1, 5, 6000])
 def test_queries_written_between_the_rows_they_come_from(m, T):
     """An output of the same stride beside q, k and v in one row, and q itself; rows over others are refused."""
