@@ -226,7 +226,7 @@ __device__ __forceinline__ float capped(float e2x, float cap) { return fmaf(-2.0
 
 // z = cap tanh(z / cap) of any cap (rcp: 1 / cap), off by at most 2^-20 of itself.  With x = z / cap: below 1/2, z
 // tanh(x) / x by a polynomial in x^2 (off by 2^-26; coefficients solved for the least largest relative error); above,
-// as before, off by 2^-22 of the cap, which is 2.2 z at most there.
+// capped(), off by 2^-22 of the cap, which is 2.2 z at most there.
 __device__ __forceinline__ void any_cap(float (&z)[4], float cap, float rcp) {
     float t[4];
     bool large = false;
